@@ -306,6 +306,104 @@ pcf_status pcf_fused_attention_timed(const pcf_layout* layout, const uint16_t* q
 pcf_status pcf_score_noalloc(const pcf_layout* layout, const uint16_t* q_query, const uint16_t* k_pool,
                              const float* rope, float* importance, void* stream);
 
+/* ---------------------------------------------------------------- continuing on the page pool
+ * After the fused prefill a request goes on from its pages: it generates tokens one by one, or
+ * brings the next chunk of a prompt.  The calls below grow the requests of a batch on the GPU, from
+ * lengths that the host does not know, write the new tokens' keys and values into pages and attend
+ * from the new tokens over them (MiniPIC section 2.1: keys stay unrotated, attention applies RoPE
+ * at use from per-request positions; QCFuse Phase 4: the merged cache a request continues on).
+ *
+ * A request b holds seq_len[b] tokens in the pages block_table[b][0 ..]; token 16 p + r sits in slot
+ * r of page block_table[b][p] at logical position page_pos[b][p] + r.  Pages of different requests
+ * may be the same physical page at different positions, as in a layout.  A chunk brings new_len[b]
+ * tokens (0: the request is idle), which take the slots behind.  The rows of a chunk call are the
+ * new tokens, request after request: row row_base[b] + t is token seq_len[b] + t.
+ *
+ * Every buffer has the size the dims give, whatever the lengths turn out to be, so that calls can
+ * be captured in a CUDA graph and replayed while the lengths change.  None of the calls
+ * synchronises, allocates or keeps anything between calls. */
+typedef struct pcf_chunk_dims {
+    int32_t n_reqs;          /* requests (rows of the tables), 1 .. 4096 */
+    int32_t max_pages;       /* columns of the tables: pages one request can hold, 1 .. 65536 */
+    int32_t max_rows;        /* rows of a chunk, all requests together, 1 .. 1<<22 */
+    int32_t max_chunk;       /* new tokens of one request, 1 .. max_rows */
+    int32_t max_total_pages; /* pages all requests hold together (a shared page counts once for each
+                                request), 1 .. 1<<26 */
+    int32_t n_q_heads;       /* Hq, at most 1024 */
+    int32_t n_kv_heads;      /* Hkv, divides Hq; Hq/Hkv must divide 128 */
+    int32_t head_dim;        /* d in {64, 128} */
+    int32_t n_phys_pages;    /* pages in the pool; n_phys_pages * Hkv * 16 < 1<<31 */
+    int32_t max_pos;         /* rows of the rope table, 16 .. 1<<20 */
+    int32_t n_sms;           /* SMs of the device; <= 0 selects 152, GB300's count; at most 4096 */
+} pcf_chunk_dims;
+
+/* Host-only.  int32 words of the device plan pcf_chunk_tables writes and the calls after it read.
+ * PCF_ERR_INVALID_ARG / PCF_ERR_UNSUPPORTED for dims outside the limits above. */
+pcf_status pcf_chunk_plan_words(const pcf_chunk_dims* dims, int64_t* n_words);
+
+/* Block tables, page positions and slot maps of a chunk, built on the GPU.
+ *   in      seq_len, new_len [n_reqs] int32: tokens held and new tokens of every request
+ *           next_pos [n_reqs] int32 or NULL: position of each request's first new token; a request
+ *             whose last page has room left goes on at the position behind its last token, and
+ *             next_pos must say the same.  NULL: every request goes on there (at 0 without tokens)
+ *           free_pages [n_free] int32, free_head [1]: physical pages to start new pages on, taken
+ *             from free_pages[free_head[0]] on, request after request
+ *   in/out  block_table, page_pos [n_reqs][max_pages] int32: the entries of pages already held are
+ *             read, those of the pages a chunk starts are written, the others are left alone
+ *   out     slot_map [max_rows] int32: page * 16 + slot of every row; -1 behind the last row
+ *           row_pos [max_rows] int32: logical position of every row; -1 behind the last row
+ *           row_base [n_reqs + 1] int32: first row of every request, then the number of rows
+ *           seq_len_out [n_reqs] = seq_len + new_len, free_head_out [1]: may be the same buffers as
+ *             seq_len and free_head, so that a captured step moves itself on
+ *           plan [pcf_chunk_plan_words] int32
+ * Refused on the device, with PCF_ERR_DEVICE_BOUNDS from the next pcf_check_device_error: a negative
+ * length, one beyond the dims, positions outside the rope table (of any slot of a page a request
+ * writes to), a next_pos that breaks a started page, a free list that runs out or names a page
+ * outside the pool.  Then no table entry is written, the lengths and the list's head stay, slot_map
+ * and row_pos are all -1, and calls that use the plan do nothing.
+ * One block scans the lengths; a second launch writes the rows. */
+pcf_status pcf_chunk_tables(const pcf_chunk_dims* dims, const int32_t* seq_len, const int32_t* new_len,
+                            const int32_t* next_pos, const int32_t* free_pages, int32_t n_free,
+                            const int32_t* free_head, int32_t* block_table, int32_t* page_pos, int32_t* slot_map,
+                            int32_t* row_pos, int32_t* row_base, int32_t* seq_len_out, int32_t* free_head_out,
+                            int32_t* plan, void* stream);
+
+/* Writes the rows' keys and values into the pools: row i into slot slot_map[i] (rows at -1 are
+ * passed over; slots must differ).  k_new, v_new: [max_rows][Hkv][d] bf16 with k_row_stride and
+ * v_row_stride elements from row to row (multiples of 8, at least Hkv * d: columns of a wider
+ * product are fine).  Keys are stored unrotated.  With row_pos (NULL: none) a row sits at logical
+ * position row_pos[i] although its slot's is slot_pos[i] (pcf_chunk_tables' row_pos): its key is
+ * stored turned by the difference, R_{row_pos - slot_pos} k rounded to bf16, so that attention,
+ * which rotates a slot's key to the slot's position, sees R_{row_pos} k; where the two agree the key
+ * is copied bit for bit.  This keeps the recomputed tokens of a fused prefill (their fresh keys at
+ * positions inside the shared spans) in pages of the request's own, while `excl` of
+ * pcf_chunk_attention hides the stale copies.  slot_pos and rope are read only with row_pos.
+ * A slot or position out of range raises PCF_ERR_DEVICE_BOUNDS and the row is not written. */
+pcf_status pcf_append_kv(const pcf_chunk_dims* dims, const uint16_t* k_new, int64_t k_row_stride,
+                         const uint16_t* v_new, int64_t v_row_stride, const int32_t* slot_map, const int32_t* slot_pos,
+                         const int32_t* row_pos, const float* rope, uint16_t* k_pool, uint16_t* v_pool, void* stream);
+
+/* Bytes of device workspace pcf_chunk_attention needs for these dims. */
+pcf_status pcf_chunk_attention_workspace_bytes(const pcf_chunk_dims* dims, size_t* bytes);
+
+/* Attention of the chunk's rows over the pages of their requests (the new tokens' keys and values
+ * appended before).  For row i, token s + t of request b (s = seq_len before the chunk), and q head h:
+ *   out[i][h] = sum_j softmax_j((R_{row_pos[i]} q_{i,h}) . (R_{pos(j)} k_j) / sqrt(d)) v_j
+ * over the slots j <= s + t of b whose bit in excl is clear; pos(16 p + r) = page_pos[b][p] + r.
+ * excl [n_reqs][max_pages] uint16 (bit r of word p: slot 16 p + r takes no part) or NULL.  A row with
+ * no slot left gives zeros.  Order is that of the slots, not of the positions.  Slots behind a
+ * request's last token and excluded slots may hold anything, infinities and NaN included.
+ * q: [max_rows][Hq][d] bf16, q_row_stride elements from row to row (a multiple of 8); out
+ * [max_rows][Hq][d] bf16, rows behind the last one left as they are.  ws: device workspace of >=
+ * pcf_chunk_attention_workspace_bytes, contents need not be initialised; two calls that may overlap
+ * need one each.  Deterministic.  A page outside the pool or a position outside the rope table raises
+ * PCF_ERR_DEVICE_BOUNDS, a rotated query or key beyond fp16 PCF_ERR_DEVICE_RANGE; the call's results
+ * must then be discarded. */
+pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, const int32_t* plan, const uint16_t* q, int64_t q_row_stride,
+                               const uint16_t* k_pool, const uint16_t* v_pool, const int32_t* block_table,
+                               const int32_t* page_pos, const uint16_t* excl, const int32_t* row_pos,
+                               const float* rope, uint16_t* out, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronizes `stream`, then reads and clears the device error word: PCF_OK,
  * PCF_ERR_DEVICE_TIMEOUT, PCF_ERR_DEVICE_BOUNDS or PCF_ERR_DEVICE_RANGE (the first error raised
  * since the last check; PCF_ERR_CUDA if the sync itself failed).  The rotated queries and keys

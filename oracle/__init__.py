@@ -23,10 +23,13 @@ What it computes, and from which passage:
   over the cached keys minus the recomputed tokens plus the fresh rows, every key rotated at its
   logical position (QCFuse section 2C / Phase 4 "discrete recomputation", causal constraints of
   the sparse-attention kernel; MiniPIC section 2.1 score equation).
+* ``chunk.tables`` / ``chunk.appended`` / ``chunk.attention``  a request that goes on from its pages:
+  new pages and slots, keys stored for a slot's position, attention of new tokens over the merged
+  cache (MiniPIC section 2.1; QCFuse Phase 4).
 * ``method.full_prefill``  plain causal prefill over given rows, written separately as the
   100 %-recompute reference.
 
 Parity pins live in ``tests/test_oracle_pins.py``.  Every function above has at least one pin that
 does not go through the oracle itself.
 """
-from . import rope, method  # noqa: F401
+from . import chunk, method, rope  # noqa: F401

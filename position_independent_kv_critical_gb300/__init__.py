@@ -10,6 +10,11 @@ Hot path for one batch at the critical layer:
   ``select_topk``    per-span top-k tokens to recompute, exclusion bits, row positions
   ``gather_rows``    rows of the selected tokens (input of the recomputation)
   ``fused_attention`` recomputed + query rows over cached-minus-selected + fresh KV
+
+Going on from there, one token or a chunk of tokens at a time, with lengths that live on the GPU:
+  ``chunk_tables``    block tables, positions and slot map of the new tokens
+  ``append_kv``       their keys and values into the pages
+  ``chunk_attention`` attention from the new tokens over their requests' pages
 """
 from __future__ import annotations
 
@@ -24,7 +29,7 @@ from ._lib import PcfError  # noqa: F401
 __all__ = ["Layout", "CacheFusion", "PcfError", "k_from_percent", "rope_table", "score", "select_topk",
            "gather_rows", "fused_attention", "check_device_error", "load_library", "score_noalloc",
            "select_topn_global", "key_norms", "pack_anchor_pages", "prefetch_pool_pages",
-           "wait_limit_check", "score_layers"]
+           "wait_limit_check", "score_layers", "ChunkLayout", "chunk_tables", "append_kv", "chunk_attention"]
 
 
 def load_library():
@@ -267,6 +272,168 @@ def fused_attention(layout: Layout, q_fresh, k_fresh, v_fresh, k_pool, v_pool, e
         handles.append(ctypes.c_void_p(ev.cuda_event))
     _lib.check("pcf_fused_attention_timed", _lib.load().pcf_fused_attention_timed(
         *args, handles[0], handles[1], int(bool(paged)), _stream(stream)))
+
+
+class ChunkLayout:
+    """Tables of a batch of requests that go on from the page pool, and the sizes their calls are
+    made for (``pcf_chunk_dims``).  ``block_table`` and ``page_pos`` [n_reqs, max_pages] list the
+    physical page and the first position of every page a request holds: the caller fills them for
+    what is cached (or starts from ``from_layout``), ``chunk_tables`` adds the pages new tokens start.
+    ``slot_map``, ``row_pos`` [max_rows] and ``row_base`` [n_reqs + 1] describe the rows of the last
+    ``chunk_tables``, ``plan`` is what the calls after it read.  All are int32 tensors on ``device``
+    with fixed addresses, so that a captured step can be replayed."""
+
+    def __init__(self, n_reqs: int, hq: int, hkv: int, d: int, n_phys_pages: int, max_pos: int, max_pages: int,
+                 max_rows: int, max_chunk: int, max_total_pages: Optional[int] = None, device: str = "cuda"):
+        lib = _lib.load()
+        self.n_reqs, self.hq, self.hkv, self.d = n_reqs, hq, hkv, d
+        self.max_pages, self.max_rows, self.max_chunk = max_pages, max_rows, max_chunk
+        dev = torch.device(device)
+        n_sms = 0
+        if dev.type == "cuda":
+            if dev.index is None:
+                dev = torch.device("cuda", torch.cuda.current_device())
+            n_sms = torch.cuda.get_device_properties(dev).multi_processor_count
+        self.device = dev
+        total = n_reqs * max_pages if max_total_pages is None else max_total_pages
+        self.dims = _lib.ChunkDims(n_reqs, max_pages, max_rows, max_chunk, total, hq, hkv, d, n_phys_pages, max_pos,
+                                   n_sms)
+        n = ctypes.c_int64(0)
+        _lib.check("pcf_chunk_plan_words", lib.pcf_chunk_plan_words(ctypes.byref(self.dims), ctypes.byref(n)))
+        ints = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)
+        self.block_table, self.page_pos = ints(n_reqs, max_pages), ints(n_reqs, max_pages)
+        self.slot_map, self.row_pos, self.row_base = ints(max_rows), ints(max_rows), ints(n_reqs + 1)
+        self.plan = ints(n.value)
+
+    @classmethod
+    def from_layout(cls, layout: Layout, max_pages: int, max_rows: int, max_chunk: int, max_pos: int,
+                    n_phys_pages: Optional[int] = None, excl: Optional[torch.Tensor] = None, **kw):
+        """The tables of a batch after its fused prefill: every request holds its cached spans' pages
+        at their positions.  With ``excl`` (the layout's exclusion bits, as ``select_topk`` leaves
+        them) also returns them as [n_reqs, max_pages] words for ``chunk_attention``."""
+        self = cls(len(layout.requests), layout.hq, layout.hkv, layout.d,
+                   layout.field("n_phys_pages") if n_phys_pages is None else n_phys_pages, max_pos, max_pages,
+                   max_rows, max_chunk, **kw)
+        table = torch.zeros((self.n_reqs, max_pages), dtype=torch.int32)
+        pos = torch.zeros_like(table)
+        words = None if excl is None else torch.zeros((self.n_reqs, max_pages), dtype=torch.int16, device=self.device)
+        base = 0
+        for b, r in enumerate(layout.requests):
+            at = 0
+            for s in r.spans:
+                n = int(s.n_pages)
+                if at + n > max_pages:
+                    raise ValueError("max_pages: a request's cached pages do not fit")
+                table[b, at: at + n] = int(s.phys_first_page) + torch.arange(n, dtype=torch.int32)
+                pos[b, at: at + n] = int(s.pos0) + 16 * torch.arange(n, dtype=torch.int32)
+                at += n
+            if words is not None:
+                words[b, :at] = excl[base: base + at]
+            base += at
+        self.block_table.copy_(table)
+        self.page_pos.copy_(pos)
+        return self if words is None else (self, words)
+
+    def attention_workspace_bytes(self) -> int:
+        v = ctypes.c_size_t(0)
+        _lib.check("pcf_chunk_attention_workspace_bytes", _lib.load().pcf_chunk_attention_workspace_bytes(
+            ctypes.byref(self.dims), ctypes.byref(v)))
+        return int(v.value)
+
+
+def _chunk_ints(L: ChunkLayout, t: Optional[torch.Tensor], name: str, n: Optional[int] = None, dtype=torch.int32):
+    if t is None:
+        return
+    _need(t, dtype, name)
+    if t.device != L.device:
+        raise ValueError(f"{name}: on {t.device}, the layout is on {L.device}")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+
+
+def _chunk_rows(L: ChunkLayout, t: torch.Tensor, heads: int, name: str) -> int:
+    """Checks a [max_rows, heads, d] bf16 tensor whose rows may be columns of wider ones; elements
+    from row to row."""
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (L.max_rows, heads, L.d):
+        raise ValueError(f"{name}: expected bfloat16 [{L.max_rows}, {heads}, {L.d}], got {t.dtype} {tuple(t.shape)}")
+    if t.device != L.device:
+        raise ValueError(f"{name}: on {t.device}, the layout is on {L.device}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != L.d):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    if L.max_rows == 1:
+        return heads * L.d
+    if t.stride(0) < heads * L.d:
+        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)})")
+    return t.stride(0)
+
+
+def _chunk_pool(L: ChunkLayout, t: torch.Tensor, name: str):
+    _need(t, torch.bfloat16, name)
+    if t.device != L.device:
+        raise ValueError(f"{name}: on {t.device}, the layout is on {L.device}")
+    if t.numel() < L.dims.n_phys_pages * L.hkv * 16 * L.d:
+        raise ValueError(f"{name}: smaller than the {L.dims.n_phys_pages} pages of the layout")
+
+
+def _chunk_rope(L: ChunkLayout, t: Optional[torch.Tensor]):
+    if t is not None:
+        _need(t, torch.float32, "rope")
+        if t.device != L.device or t.numel() < L.dims.max_pos * L.d:
+            raise ValueError(f"rope: expected {L.dims.max_pos} rows on {L.device}")
+
+
+def _chunk_call(L: ChunkLayout, fn: str, stream, *args):
+    """The call on the layout's device, on its current stream unless one is named."""
+    with torch.cuda.device(L.device):
+        _lib.check(fn, getattr(_lib.load(), fn)(ctypes.byref(L.dims), *args, _stream(stream)))
+
+
+def chunk_tables(layout: ChunkLayout, seq_len, new_len, free_pages, free_head, seq_len_out, free_head_out,
+                 next_pos=None, stream=None):
+    """Grow every request by ``new_len`` tokens: starts the pages they need (taken from
+    ``free_pages[free_head:]``) in the layout's tables and fills its slot map, row positions and plan.
+    ``seq_len_out`` / ``free_head_out`` may be ``seq_len`` / ``free_head`` themselves."""
+    L = layout
+    for t, n, k in ((seq_len, "seq_len", L.n_reqs), (new_len, "new_len", L.n_reqs), (next_pos, "next_pos", L.n_reqs),
+                    (seq_len_out, "seq_len_out", L.n_reqs), (free_head, "free_head", 1),
+                    (free_head_out, "free_head_out", 1), (free_pages, "free_pages", None)):
+        _chunk_ints(L, t, n, k)
+    _chunk_call(L, "pcf_chunk_tables", stream, _p(seq_len), _p(new_len), _p(next_pos), _p(free_pages),
+                free_pages.numel(), _p(free_head), _p(L.block_table), _p(L.page_pos), _p(L.slot_map), _p(L.row_pos),
+                _p(L.row_base), _p(seq_len_out), _p(free_head_out), _p(L.plan))
+
+
+def append_kv(layout: ChunkLayout, k_new, v_new, k_pool, v_pool, rope=None, row_pos=None, stream=None):
+    """Write the rows' keys and values ([max_rows, hkv, d] each, rows may be strided) into the slots of
+    the last ``chunk_tables``.  ``row_pos`` (with ``rope``): positions of rows that differ from their
+    slots', whose keys are stored turned by the difference."""
+    L = layout
+    ks, vs = _chunk_rows(L, k_new, L.hkv, "k_new"), _chunk_rows(L, v_new, L.hkv, "v_new")
+    _chunk_pool(L, k_pool, "k_pool")
+    _chunk_pool(L, v_pool, "v_pool")
+    _chunk_ints(L, row_pos, "row_pos", L.max_rows)
+    _chunk_rope(L, rope)
+    _chunk_call(L, "pcf_append_kv", stream, _p(k_new), ks, _p(v_new), vs, _p(L.slot_map), _p(L.row_pos), _p(row_pos),
+                _p(rope), _p(k_pool), _p(v_pool))
+
+
+def chunk_attention(layout: ChunkLayout, q, k_pool, v_pool, rope, out, ws, excl=None, stream=None):
+    """Attention of the rows of the last ``chunk_tables`` ([max_rows, hq, d], rows may be strided) over
+    their requests' pages, into ``out``.  ``excl``: [n_reqs, max_pages] int16 words of slots that take
+    no part.  ``ws`` sized by ``ChunkLayout.attention_workspace_bytes``."""
+    L = layout
+    qs = _chunk_rows(L, q, L.hq, "q")
+    _chunk_pool(L, k_pool, "k_pool")
+    _chunk_pool(L, v_pool, "v_pool")
+    _chunk_ints(L, excl, "excl", L.n_reqs * L.max_pages, torch.int16)
+    _chunk_rope(L, rope)
+    if out.shape != (L.max_rows, L.hq, L.d) or out.device != L.device:
+        raise ValueError(f"out: expected [{L.max_rows}, {L.hq}, {L.d}] on {L.device}")
+    _need(out, torch.bfloat16, "out")
+    if ws.device != L.device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on {L.device}")
+    _chunk_call(L, "pcf_chunk_attention", stream, _p(L.plan), _p(q), qs, _p(k_pool), _p(v_pool), _p(L.block_table),
+                _p(L.page_pos), _p(excl), _p(L.row_pos), _p(rope), _p(out), _p(ws), ws.numel() * ws.element_size())
 
 
 def wait_limit_check(limit_cycles: int, flag, stream=None):

@@ -33,6 +33,8 @@ EXPORTS = (
     "pcf_key_norms", "pcf_pack_anchor_pages", "pcf_prefetch_pool_pages", "pcf_fused_attention_timed",
     "pcf_wait_limit_check", "pcf_score_layers", "pcf_fused_attention_paged",
     "pcf_attention_paged_workspace_bytes", "pcf_score_paged", "pcf_score_paged_workspace_bytes",
+    "pcf_chunk_plan_words", "pcf_chunk_tables", "pcf_append_kv", "pcf_chunk_attention_workspace_bytes",
+    "pcf_chunk_attention",
 )
 
 
@@ -48,6 +50,12 @@ class RequestDesc(ctypes.Structure):
 class Dims(ctypes.Structure):
     _fields_ = [("n_q_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
                 ("n_phys_pages", c_int32), ("max_pos", c_int32), ("n_sms", c_int32)]
+
+
+class ChunkDims(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in (
+        "n_reqs", "max_pages", "max_rows", "max_chunk", "max_total_pages", "n_q_heads", "n_kv_heads", "head_dim",
+        "n_phys_pages", "max_pos", "n_sms")]
 
 
 class LayoutRef(ctypes.Structure):
@@ -113,6 +121,16 @@ def _declare(lib):
     lib.pcf_check_device_error.argtypes = [c_void_p]
     lib.pcf_wait_limit_check.restype = c_int32
     lib.pcf_wait_limit_check.argtypes = [c_int64, c_void_p, c_void_p]
+    lib.pcf_chunk_plan_words.restype = c_int32
+    lib.pcf_chunk_plan_words.argtypes = [P(ChunkDims), P(c_int64)]
+    lib.pcf_chunk_attention_workspace_bytes.restype = c_int32
+    lib.pcf_chunk_attention_workspace_bytes.argtypes = [P(ChunkDims), P(c_size_t)]
+    lib.pcf_chunk_tables.restype = c_int32
+    lib.pcf_chunk_tables.argtypes = [P(ChunkDims)] + [c_void_p] * 4 + [c_int32] + [c_void_p] * 10
+    lib.pcf_append_kv.restype = c_int32
+    lib.pcf_append_kv.argtypes = [P(ChunkDims), c_void_p, c_int64, c_void_p, c_int64] + [c_void_p] * 7
+    lib.pcf_chunk_attention.restype = c_int32
+    lib.pcf_chunk_attention.argtypes = ([P(ChunkDims), c_void_p, c_void_p, c_int64] + [c_void_p] * 9 + [c_size_t, c_void_p])
     lib.pcf_copy_async.restype = c_int32
     lib.pcf_copy_async.argtypes = [c_int32, c_void_p, c_void_p, c_void_p, c_void_p]
 

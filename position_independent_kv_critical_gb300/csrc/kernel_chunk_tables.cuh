@@ -1,0 +1,298 @@
+// Growing the requests of a batch by a chunk of new tokens: block tables, page positions and slot
+// maps from lengths that only the GPU knows, and the write of the chunk's keys and values into the
+// pages they name.
+#pragma once
+#include "chunk_format.h"
+#include "ptx.cuh"
+
+namespace pcf {
+
+struct TablesParams {
+    const int32_t* seq;        // [n] tokens held
+    const int32_t* add;        // [n] new tokens
+    const int32_t* next_pos;   // [n] position of the first new token, or null: behind the last one
+    const int32_t* free_pages; // [n_free]
+    const int32_t* free_head;  // [1]
+    int32_t* block_table;      // [n][max_pages], new entries written
+    int32_t* page_pos;         // [n][max_pages], likewise
+    int32_t* slot_map;         // [max_rows]
+    int32_t* row_pos;          // [max_rows]
+    int32_t* row_base;         // [n + 1]
+    int32_t* seq_out;          // [n], may be seq
+    int32_t* head_out;         // [1], may be free_head
+    int32_t* plan;
+    int32_t n, max_pages, max_rows, max_chunk, max_total_pages, n_phys, max_pos, n_free, hq, hkv, d;
+};
+
+constexpr int kTablesThreads = 1024;
+
+// One block reads the lengths, checks them and leaves the plan.  Request b holds s tokens on
+// ceil(s / 16) pages and grows by n: the pages behind are taken from the free list in request
+// order, so a prefix sum of ceil((s + n) / 16) - ceil(s / 16) gives every request its first one;
+// a prefix sum of n gives its first row.  Thread t takes a run of consecutive requests, so one
+// block scan of per-thread sums is enough for any batch size.
+// (Sums of refused lengths may be as large as 4096 x 2^22: they stop at 2^29, above every limit.)
+__device__ __forceinline__ int32_t pages_of(int32_t tokens) { return (tokens + kPage - 1) / kPage; }
+__device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) { return min(a + b, 1 << 29); }
+
+__global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const TablesParams p) {
+    __shared__ int s_warp[3][kTablesThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int per = (p.n + kTablesThreads - 1) / kTablesThreads;
+    const int b0 = min(p.n, tid * per), b1 = min(p.n, b0 + per);
+    int32_t* plan = p.plan;
+    int32_t* o_seq = plan + plan_array(CA_SEQ, p.n);
+    int32_t* o_new = plan + plan_array(CA_NEW, p.n);
+    int32_t* o_row = plan + plan_array(CA_ROW, p.n);
+    int32_t* o_take = plan + plan_array(CA_TAKE, p.n);
+    int32_t* o_start = plan + plan_array(CA_START, p.n);
+    const int32_t head = p.free_head[0];
+    bool bad = head < 0 || head > p.n_free;
+    int sum[3] = {0, 0, 0};   // rows, pages taken, pages held afterwards
+    for (int b = b0; b < b1; ++b) {
+        const int32_t s = p.seq[b], n = p.add[b];
+        if (s < 0 || s > p.max_pages * kPage || n < 0 || n > p.max_chunk || s + n > p.max_pages * kPage) {
+            bad = true;
+            continue;
+        }
+        const int32_t before = pages_of(s), after = pages_of(s + n);
+        int32_t start = 0;
+        if (n > 0) {
+            // a page's slots sit at consecutive positions, so a started page fixes the next one
+            const int32_t last = s > 0 ? p.page_pos[(int64_t)b * p.max_pages + before - 1] : -kPage;
+            start = last < -kPage || last > p.max_pos ? -1 : last + (s % kPage ? s % kPage : kPage);
+            if (p.next_pos) {
+                const int32_t want = p.next_pos[b];
+                if (s % kPage && want != start) bad = true;
+                start = want;
+            }
+            // every slot of the last page has a row in the cos/sin table
+            if (start < 0 || start > p.max_pos || start + (after * kPage - s) > p.max_pos) bad = true;
+        }
+        sum[0] = sat_add(sum[0], n);
+        sum[1] = sat_add(sum[1], after - before);
+        sum[2] = sat_add(sum[2], after);
+        o_seq[b] = s;
+        o_new[b] = n;
+        o_start[b] = start;
+    }
+    const bool any_bad = __syncthreads_or(bad);
+    int pre[3], tot[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        int x = any_bad ? 0 : sum[i];
+        sum[i] = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x = sat_add(x, y);
+        }
+        pre[i] = x;
+        if (lane == 31) s_warp[i][warp] = x;
+    }
+    __syncthreads();
+    if (warp < 3) {
+        int x = s_warp[warp][lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x = sat_add(x, y);
+        }
+        s_warp[warp][lane] = x;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        tot[i] = s_warp[i][31];
+        pre[i] += (warp ? s_warp[i][warp - 1] : 0) - sum[i];
+    }
+    bad = any_bad || tot[0] > p.max_rows || tot[2] > p.max_total_pages || tot[1] > p.n_free - head;
+    if (!bad) {   // the pages about to be taken exist
+        bool out = false;
+        for (int i = tid; i < tot[1]; i += kTablesThreads) {
+            const int32_t ph = p.free_pages[head + i];
+            out |= ph < 0 || ph >= p.n_phys;
+        }
+        bad = out;
+    }
+    bad = __syncthreads_or(bad);
+    int32_t row = pre[0], take = pre[1];
+    for (int b = b0; b < b1; ++b) {
+        if (bad) {
+            o_seq[b] = p.seq[b];
+            o_new[b] = 0;
+            o_start[b] = 0;
+        }
+        o_row[b] = bad ? 0 : row;
+        o_take[b] = bad ? 0 : take;
+        if (!bad) {
+            row += o_new[b];
+            take += pages_of(o_seq[b] + o_new[b]) - pages_of(o_seq[b]);
+        }
+    }
+    if (tid == 0) {
+        plan[C_MAGIC] = kPlanMagic;
+        plan[C_N_REQS] = p.n;
+        plan[C_MAX_PAGES] = p.max_pages;
+        plan[C_MAX_ROWS] = p.max_rows;
+        plan[C_HQ] = p.hq;
+        plan[C_HKV] = p.hkv;
+        plan[C_D] = p.d;
+        plan[C_N_PHYS] = p.n_phys;
+        plan[C_MAX_POS] = p.max_pos;
+        plan[C_ROWS] = bad ? 0 : tot[0];
+        plan[C_HEAD] = head;
+        plan[C_TAKEN] = bad ? 0 : tot[1];
+        plan[C_BAD] = bad ? 1 : 0;
+        o_row[p.n] = bad ? 0 : tot[0];
+        o_take[p.n] = bad ? 0 : tot[1];
+        if (bad) set_dev_error(kDevErrBounds);
+    }
+}
+
+// The plan of another batch's dims, or of no pcf_chunk_tables call at all, is refused.
+__device__ __forceinline__ bool plan_fits(const int32_t* plan, int32_t n, int32_t max_pages, int32_t max_rows,
+                                          int32_t hkv) {
+    const bool ok = plan[C_MAGIC] == kPlanMagic && plan[C_N_REQS] == n && plan[C_MAX_PAGES] == max_pages &&
+                    plan[C_MAX_ROWS] == max_rows && plan[C_HKV] == hkv;
+    if (!ok) set_dev_error(kDevErrBounds);
+    return ok;
+}
+
+// Request of row i: the last b with base[b] <= i (requests without rows are passed over).
+__device__ __forceinline__ int row_request(const int32_t* __restrict__ base, int n, int32_t i) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (base[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// The tables from the plan, one thread a row: token s + t of its request sits in page (s + t) / 16,
+// at slot (s + t) % 16; the row that starts a page enters it.  Nothing here reads what the call may
+// overwrite in place (the lengths and the list's head come from the plan), and a table entry that
+// is read (a page begun earlier) is never one that is written.
+constexpr int kRowsThreads = 256;
+__global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const TablesParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int32_t* plan = p.plan;
+    const int32_t* seq = plan + plan_array(CA_SEQ, p.n);
+    const int32_t* add = plan + plan_array(CA_NEW, p.n);
+    const int32_t* base = plan + plan_array(CA_ROW, p.n);
+    const int32_t* take = plan + plan_array(CA_TAKE, p.n);
+    const int32_t* start = plan + plan_array(CA_START, p.n);
+    const int32_t rows = plan[C_ROWS], head = plan[C_HEAD];
+    const int32_t i = blockIdx.x * kRowsThreads + threadIdx.x;
+    const int32_t step = gridDim.x * kRowsThreads;
+    for (int32_t b = i; b <= p.n; b += step) {
+        p.row_base[b] = base[b];
+        if (b < p.n) p.seq_out[b] = seq[b] + add[b];
+        else p.head_out[0] = head + plan[C_TAKEN];
+    }
+    for (int32_t r = i; r < p.max_rows; r += step) {
+        int32_t slot = -1, pos = -1;
+        if (r < rows) {
+            const int b = row_request(base, p.n, r);
+            const int32_t t = r - base[b], s = seq[b] + t, pg = s / kPage, first = pages_of(seq[b]);
+            const int64_t e = (int64_t)b * p.max_pages + pg;
+            pos = start[b] + t;
+            int32_t ph;
+            if (pg >= first) {
+                ph = p.free_pages[head + take[b] + pg - first];
+                if (s % kPage == 0) {
+                    p.block_table[e] = ph;
+                    p.page_pos[e] = pos;
+                }
+            } else {
+                ph = p.block_table[e];
+                if (ph < 0 || ph >= p.n_phys) {
+                    set_dev_error(kDevErrBounds);
+                    ph = -1;
+                }
+            }
+            if (ph >= 0) slot = ph * kPage + s % kPage;
+        }
+        p.slot_map[r] = slot;
+        p.row_pos[r] = pos;
+    }
+}
+
+// ------------------------------------------------------------------ append
+// Row i's key and value into slot slot_map[i] of the pools, every kv head.  A slot's position is
+// fixed by its page (page_pos + r), and attention rotates a key by it; a row whose own position
+// `at` differs (a recomputed token, kept behind its request's shared pages) is stored turned by the
+// difference, R_{at - slot} k, so that R_slot of the stored key is R_at k.  Where the two agree the
+// key is copied bit for bit.  A thread takes the 16-byte chunks c and c + d/16 of one head's key
+// (the pairs i, i + d/2 that turn together) and of its value: 64 bytes in flight a thread.
+struct AppendParams {
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    __nv_bfloat16* k_pool;
+    __nv_bfloat16* v_pool;
+    const int32_t* slot_map;
+    const int32_t* slot_pos;   // the slots' positions (row_pos of the tables)
+    const int32_t* at;         // the rows' own positions, or null
+    const float* rope;         // with `at`
+    int64_t k_stride, v_stride;   // elements between rows
+    int32_t max_rows, hkv, n_phys, max_pos;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+    constexpr int CPR = D / 16;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t total = (int64_t)p.max_rows * p.hkv * CPR;
+    for (int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x; it < total; it += (int64_t)gridDim.x * 256) {
+        const int c = (int)(it % CPR);
+        const int64_t rh = it / CPR;
+        const int h = (int)(rh % p.hkv);
+        const int32_t row = (int32_t)(rh / p.hkv);
+        const int32_t slot = p.slot_map[row];
+        if (slot < 0) continue;
+        if (slot >= p.n_phys * kPage) {
+            set_dev_error(kDevErrBounds);
+            continue;
+        }
+        const __nv_bfloat16* ks = p.k + row * p.k_stride + h * D;
+        const __nv_bfloat16* vs = p.v + row * p.v_stride + h * D;
+        const uint4 v0 = *reinterpret_cast<const uint4*>(vs + 8 * c);
+        const uint4 v1 = *reinterpret_cast<const uint4*>(vs + D / 2 + 8 * c);
+        uint4 k0 = *reinterpret_cast<const uint4*>(ks + 8 * c);
+        uint4 k1 = *reinterpret_cast<const uint4*>(ks + D / 2 + 8 * c);
+        if (p.at != nullptr) {
+            const int32_t at = p.at[row], by = at - p.slot_pos[row];
+            if (at < 0 || at >= p.max_pos || by <= -p.max_pos || by >= p.max_pos) {
+                set_dev_error(kDevErrBounds);
+                continue;
+            }
+            if (by != 0) {
+                const float sgn = by < 0 ? -1.f : 1.f;   // cos(-a) = cos a, sin(-a) = -sin a
+                const float4* cs = reinterpret_cast<const float4*>(p.rope + (int64_t)abs(by) * D + 16 * c);
+                const uint32_t ia[4] = {k0.x, k0.y, k0.z, k0.w}, ib[4] = {k1.x, k1.y, k1.z, k1.w};
+                uint32_t oa[4], ob[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 q = cs[e];   // cos, sin of two frequencies
+                    const float s0 = sgn * q.y, s1 = sgn * q.w;
+                    const float a0 = bf16_lo(ia[e]), a1 = bf16_hi(ia[e]), b0 = bf16_lo(ib[e]), b1 = bf16_hi(ib[e]);
+                    oa[e] = pack_bf16x2(fmaf(a0, q.x, -b0 * s0), fmaf(a1, q.z, -b1 * s1));
+                    ob[e] = pack_bf16x2(fmaf(b0, q.x, a0 * s0), fmaf(b1, q.z, a1 * s1));
+                }
+                k0 = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+                k1 = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+            }
+        }
+        const int64_t dst = (((int64_t)(slot / kPage) * p.hkv + h) * kPage + slot % kPage) * D + 8 * c;
+        *reinterpret_cast<uint4*>(p.k_pool + dst) = k0;
+        *reinterpret_cast<uint4*>(p.k_pool + dst + D / 2) = k1;
+        *reinterpret_cast<uint4*>(p.v_pool + dst) = v0;
+        *reinterpret_cast<uint4*>(p.v_pool + dst + D / 2) = v1;
+    }
+}
+
+}  // namespace pcf

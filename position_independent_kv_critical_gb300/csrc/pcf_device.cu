@@ -12,7 +12,10 @@
 #include <vector>
 
 #include "../../include/pcf.h"
+#include "chunk_format.h"
 #include "kernel_attn.cuh"
+#include "kernel_chunk_attn.cuh"
+#include "kernel_chunk_tables.cuh"
 #include "kernel_imp.cuh"
 #include "kernels_simple.cuh"
 #include "layout_format.h"
@@ -958,4 +961,89 @@ extern "C" pcf_status pcf_score_noalloc(const pcf_layout* layout, const uint16_t
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return H[L_D] == 128 ? score_impl<128>(layout, q_query, k_pool, rope, importance, ws, st)
                          : score_impl<64>(layout, q_query, k_pool, rope, importance, ws, st);
+}
+
+// ------------------------------------------------------------------ continuing on the pool
+extern "C" pcf_status pcf_chunk_tables(const pcf_chunk_dims* dims, const int32_t* seq_len, const int32_t* new_len,
+                                       const int32_t* next_pos, const int32_t* free_pages, int32_t n_free,
+                                       const int32_t* free_head, int32_t* block_table, int32_t* page_pos,
+                                       int32_t* slot_map, int32_t* row_pos, int32_t* row_base, int32_t* seq_len_out,
+                                       int32_t* free_head_out, int32_t* plan, void* stream) {
+    pcf_status s = check_chunk_dims(dims);
+    if (s != PCF_OK) return s;
+    if (!seq_len || !new_len || n_free < 0 || (n_free > 0 && !free_pages) || !free_head || !block_table || !page_pos ||
+        !slot_map || !row_pos || !row_base || !seq_len_out || !free_head_out || !plan)
+        return PCF_ERR_INVALID_ARG;
+    const void* words[] = {seq_len, new_len, next_pos, free_pages, free_head, block_table, page_pos, slot_map,
+                           row_pos, row_base, seq_len_out, free_head_out, plan};
+    for (const void* w : words)
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return PCF_ERR_INVALID_ARG;
+    if ((s = check_device()) != PCF_OK) return s;
+    const TablesParams p{seq_len, new_len, next_pos, free_pages, free_head, block_table, page_pos, slot_map, row_pos,
+                         row_base, seq_len_out, free_head_out, plan, dims->n_reqs, dims->max_pages, dims->max_rows,
+                         dims->max_chunk, dims->max_total_pages, dims->n_phys_pages, dims->max_pos, n_free,
+                         dims->n_q_heads, dims->n_kv_heads, dims->head_dim};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((s = launch(chunk_plan_kernel, dim3(1), dim3(kTablesThreads), 0, st, p)) != PCF_OK) return s;
+    const int items = std::max(dims->max_rows, dims->n_reqs + 1);
+    const int blocks = std::min((items + kRowsThreads - 1) / kRowsThreads, 8 * device_sms());
+    return launch(chunk_rows_kernel, dim3(blocks), dim3(kRowsThreads), 0, st, p);
+}
+
+extern "C" pcf_status pcf_append_kv(const pcf_chunk_dims* dims, const uint16_t* k_new, int64_t k_row_stride,
+                                    const uint16_t* v_new, int64_t v_row_stride, const int32_t* slot_map,
+                                    const int32_t* slot_pos, const int32_t* row_pos, const float* rope,
+                                    uint16_t* k_pool, uint16_t* v_pool, void* stream) {
+    pcf_status s = check_chunk_dims(dims);
+    if (s != PCF_OK) return s;
+    const int64_t row = (int64_t)dims->n_kv_heads * dims->head_dim;
+    if (!k_new || !v_new || !slot_map || !k_pool || !v_pool || (row_pos && (!slot_pos || !rope)))
+        return PCF_ERR_INVALID_ARG;
+    if (k_row_stride < row || v_row_stride < row || k_row_stride % 8 != 0 || v_row_stride % 8 != 0)
+        return PCF_ERR_INVALID_ARG;
+    for (const void* q : {(const void*)k_new, (const void*)v_new, (const void*)rope, (const void*)k_pool, (const void*)v_pool})
+        if (!aligned16(q)) return PCF_ERR_INVALID_ARG;
+    for (const void* w : {(const void*)slot_map, (const void*)slot_pos, (const void*)row_pos})
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return PCF_ERR_INVALID_ARG;
+    if ((s = check_device()) != PCF_OK) return s;
+    const AppendParams p{reinterpret_cast<const __nv_bfloat16*>(k_new), reinterpret_cast<const __nv_bfloat16*>(v_new),
+                         reinterpret_cast<__nv_bfloat16*>(k_pool), reinterpret_cast<__nv_bfloat16*>(v_pool), slot_map,
+                         slot_pos, row_pos, rope, k_row_stride, v_row_stride, dims->max_rows, dims->n_kv_heads,
+                         dims->n_phys_pages, dims->max_pos};
+    const int64_t items = (int64_t)dims->max_rows * dims->n_kv_heads * (dims->head_dim / 16);
+    const unsigned blocks = (unsigned)std::min<int64_t>((items + 255) / 256, 1 << 20);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dims->head_dim == 128 ? launch(append_kernel<128>, dim3(blocks), dim3(256), 0, st, p)
+                                 : launch(append_kernel<64>, dim3(blocks), dim3(256), 0, st, p);
+}
+
+extern "C" pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, const int32_t* plan, const uint16_t* q,
+                                          int64_t q_row_stride, const uint16_t* k_pool, const uint16_t* v_pool,
+                                          const int32_t* block_table, const int32_t* page_pos, const uint16_t* excl,
+                                          const int32_t* row_pos, const float* rope, uint16_t* out, void* ws,
+                                          size_t ws_bytes, void* stream) {
+    pcf_status s = check_chunk_dims(dims);
+    if (s != PCF_OK) return s;
+    if (!plan || !q || !k_pool || !v_pool || !block_table || !page_pos || !row_pos || !rope || !out || !ws)
+        return PCF_ERR_INVALID_ARG;
+    if (q_row_stride < (int64_t)dims->n_q_heads * dims->head_dim || q_row_stride % 8 != 0) return PCF_ERR_INVALID_ARG;
+    for (const void* a : {(const void*)q, (const void*)k_pool, (const void*)v_pool, (const void*)rope,
+                          (const void*)out, (const void*)ws})
+        if (!aligned16(a)) return PCF_ERR_INVALID_ARG;
+    for (const void* w : {(const void*)plan, (const void*)block_table, (const void*)page_pos, (const void*)row_pos})
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return PCF_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(excl) & 1u) return PCF_ERR_INVALID_ARG;
+    size_t need = 0;
+    if ((s = pcf_chunk_attention_workspace_bytes(dims, &need)) != PCF_OK) return s;
+    if (ws_bytes < need) return PCF_ERR_WORKSPACE_TOO_SMALL;
+    if ((s = check_device()) != PCF_OK) return s;
+    const ChunkAttnParams p{plan, reinterpret_cast<const __nv_bfloat16*>(q),
+                            reinterpret_cast<const __nv_bfloat16*>(k_pool),
+                            reinterpret_cast<const __nv_bfloat16*>(v_pool), block_table, page_pos, excl, row_pos, rope,
+                            reinterpret_cast<__nv_bfloat16*>(out), q_row_stride, dims->n_reqs, dims->max_pages,
+                            dims->max_rows, dims->n_q_heads, dims->n_kv_heads, dims->n_phys_pages, dims->max_pos};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const dim3 grid(dims->max_rows, dims->n_q_heads);
+    return dims->head_dim == 128 ? launch(chunk_attn_simple_kernel<128>, grid, dim3(128), 0, st, p)
+                                 : launch(chunk_attn_simple_kernel<64>, grid, dim3(128), 0, st, p);
 }

@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "../../include/pcf.h"
+#include "chunk_format.h"
 #include "layout_format.h"
 
 using namespace pcf;
@@ -524,5 +525,21 @@ extern "C" pcf_status pcf_layout_query(const int32_t* blob, int32_t field, int64
     if (!blob || !value || blob[L_MAGIC] != kMagic || field < 1 || field >= L_HEADER)
         return PCF_ERR_INVALID_ARG;
     *value = blob[field];
+    return PCF_OK;
+}
+
+extern "C" pcf_status pcf_chunk_plan_words(const pcf_chunk_dims* dims, int64_t* n_words) {
+    const pcf_status s = check_chunk_dims(dims);
+    if (s != PCF_OK) return s;
+    if (!n_words) return PCF_ERR_INVALID_ARG;
+    *n_words = plan_words(dims->n_reqs);
+    return PCF_OK;
+}
+
+extern "C" pcf_status pcf_chunk_attention_workspace_bytes(const pcf_chunk_dims* dims, size_t* bytes) {
+    const pcf_status s = check_chunk_dims(dims);
+    if (s != PCF_OK) return s;
+    if (!bytes) return PCF_ERR_INVALID_ARG;
+    *bytes = 0;
     return PCF_OK;
 }
