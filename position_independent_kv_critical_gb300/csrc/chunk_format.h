@@ -25,15 +25,32 @@ enum : int {
     C_HEAD = 10,      // the free list's first page not taken before this chunk
     C_TAKEN = 11,     // pages taken for the chunk
     C_BAD = 12,       // 1: the lengths were refused and nothing was done
+    C_WORKERS = 13,   // warps the few-row requests' pages are dealt to
     C_HEADER = 16
 };
-// arrays behind the header, n_reqs + 1 words each
-enum : int { CA_SEQ = 0, CA_NEW = 1, CA_ROW = 2, CA_TAKE = 3, CA_START = 4, CA_COUNT = 5 };
+// arrays behind the header, n_reqs + 1 words each: tokens held, new tokens, first row, pages taken
+// before the request, position of its first row, and the (page, kv head) units of the requests
+// before it that have few rows; then the few-row work split, kStartWords words a worker
+enum : int { CA_SEQ = 0, CA_NEW = 1, CA_ROW = 2, CA_TAKE = 3, CA_START = 4, CA_FEW = 5, CA_COUNT = 6 };
+constexpr int kStartWords = 4;   // {request, kv head, page, units}
 
 PCF_HOST_DEVICE inline int64_t plan_array(int which, int32_t n_reqs) {
     return C_HEADER + (int64_t)which * (n_reqs + 1);
 }
-PCF_HOST_DEVICE inline int64_t plan_words(int32_t n_reqs) { return plan_array(CA_COUNT, n_reqs); }
+PCF_HOST_DEVICE inline int64_t plan_starts(int32_t n_reqs) {
+    return (plan_array(CA_COUNT, n_reqs) + 3) / 4 * 4;
+}
+PCF_HOST_DEVICE inline int64_t plan_words(int32_t n_reqs, int32_t workers) {
+    return plan_starts(n_reqs) + (int64_t)workers * kStartWords;
+}
+
+// A request has few rows when its new tokens times the query heads of a kv head are at most this:
+// two 16-row tiles of mma.sync a warp.  Below, reading the pages bounds the attention (a key and
+// value of 4 d bytes meet 4 d flops a row, 32 flops a byte at most).
+constexpr int kFewRows = 32;
+constexpr int kFewWarps = 8;   // warps of a block of the few-row kernel, each a worker
+
+PCF_HOST_DEVICE inline int32_t chunk_sms(int32_t n_sms) { return n_sms > 0 ? n_sms : kDefaultSms; }
 
 inline pcf_status check_chunk_dims(const pcf_chunk_dims* c) {
     if (!c) return PCF_ERR_INVALID_ARG;
@@ -48,6 +65,26 @@ inline pcf_status check_chunk_dims(const pcf_chunk_dims* c) {
     if (c->head_dim != 64 && c->head_dim != 128) return PCF_ERR_UNSUPPORTED;
     if (kTileRows % (c->n_q_heads / c->n_kv_heads) != 0) return PCF_ERR_UNSUPPORTED;
     return PCF_OK;
+}
+
+// Workspace of pcf_chunk_attention (byte offsets).  Few-row partial results: a worker's first run,
+// when the block has more of it to come, and per block the two runs it shares with its neighbours.
+struct ChunkWs {
+    size_t worker_o, block_o, block_ml, block_desc, total;
+};
+inline size_t chunk_align(size_t x) { return (x + 255) / 256 * 256; }
+inline int few_tiles(const pcf_chunk_dims* c) {   // 16-row tiles a warp: 1 when no request can have more
+    return (int64_t)c->max_chunk * (c->n_q_heads / c->n_kv_heads) <= 16 ? 1 : 2;
+}
+inline ChunkWs chunk_ws(const pcf_chunk_dims* c) {
+    ChunkWs w;
+    const size_t rows = 16 * (size_t)few_tiles(c), blocks = chunk_sms(c->n_sms), d = c->head_dim;
+    w.worker_o = 0;
+    w.block_o = chunk_align(w.worker_o + blocks * kFewWarps * rows * d * 4);
+    w.block_ml = chunk_align(w.block_o + blocks * 2 * rows * d * 4);
+    w.block_desc = chunk_align(w.block_ml + blocks * 2 * rows * 8);
+    w.total = chunk_align(w.block_desc + blocks * 16);
+    return w;
 }
 
 }  // namespace pcf

@@ -23,7 +23,7 @@ struct ChunkAttnParams {
     const float* rope;
     __nv_bfloat16* out;
     int64_t q_stride;
-    int32_t n, max_pages, max_rows, hq, hkv, n_phys, max_pos;
+    int32_t n, max_pages, max_rows, hq, hkv, n_phys, max_pos, workers;
 };
 
 // One block per (row, query head), a warp a page at a time: lane l holds the frequencies l (and
@@ -38,10 +38,11 @@ __global__ void __launch_bounds__(128) chunk_attn_simple_kernel(const ChunkAttnP
     grid_dep_wait();
     grid_dep_launch();
     const int32_t row = blockIdx.x;
-    if (!plan_fits(p.plan, p.n, p.max_pages, p.max_rows, p.hkv)) return;
+    if (!plan_fits(p.plan, p.n, p.max_pages, p.max_rows, p.hq, p.hkv, p.workers)) return;
     if (row >= p.plan[C_ROWS]) return;
     const int32_t* base = p.plan + plan_array(CA_ROW, p.n);
     const int b = row_request(base, p.n, row);
+    if (p.plan[plan_array(CA_NEW, p.n) + b] * (p.hq / p.hkv) <= kFewRows) return;
     const int32_t last = p.plan[plan_array(CA_SEQ, p.n) + b] + row - base[b];
     const int h = blockIdx.y, kvh = h / (p.hq / p.hkv);
     const __nv_bfloat16* q = p.q + row * p.q_stride + h * D;

@@ -21,7 +21,7 @@ struct TablesParams {
     int32_t* seq_out;          // [n], may be seq
     int32_t* head_out;         // [1], may be free_head
     int32_t* plan;
-    int32_t n, max_pages, max_rows, max_chunk, max_total_pages, n_phys, max_pos, n_free, hq, hkv, d;
+    int32_t n, max_pages, max_rows, max_chunk, max_total_pages, n_phys, max_pos, n_free, hq, hkv, d, workers;
 };
 
 constexpr int kTablesThreads = 1024;
@@ -32,11 +32,18 @@ constexpr int kTablesThreads = 1024;
 // a prefix sum of n gives its first row.  Thread t takes a run of consecutive requests, so one
 // block scan of per-thread sums is enough for any batch size.
 // (Sums of refused lengths may be as large as 4096 x 2^22: they stop at 2^29, above every limit.)
+constexpr int kSumLimit = 1 << 29;
+constexpr int kSums = 4;   // rows, pages taken, pages held afterwards, few-row units
 __device__ __forceinline__ int32_t pages_of(int32_t tokens) { return (tokens + kPage - 1) / kPage; }
-__device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) { return min(a + b, 1 << 29); }
+__device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) { return min(a + b, kSumLimit); }
+
+// (page, kv head) units of a request with few rows, 0 for any other
+__device__ __forceinline__ int32_t few_units(const TablesParams& p, int32_t s, int32_t n) {
+    return n > 0 && (int64_t)n * (p.hq / p.hkv) <= kFewRows ? pages_of(s + n) * p.hkv : 0;
+}
 
 __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const TablesParams p) {
-    __shared__ int s_warp[3][kTablesThreads / 32];
+    __shared__ int s_warp[kSums][kTablesThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dep_wait();
     grid_dep_launch();
@@ -48,9 +55,10 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
     int32_t* o_row = plan + plan_array(CA_ROW, p.n);
     int32_t* o_take = plan + plan_array(CA_TAKE, p.n);
     int32_t* o_start = plan + plan_array(CA_START, p.n);
+    int32_t* o_few = plan + plan_array(CA_FEW, p.n);
     const int32_t head = p.free_head[0];
     bool bad = head < 0 || head > p.n_free;
-    int sum[3] = {0, 0, 0};   // rows, pages taken, pages held afterwards
+    int sum[kSums] = {};
     for (int b = b0; b < b1; ++b) {
         const int32_t s = p.seq[b], n = p.add[b];
         if (s < 0 || s > p.max_pages * kPage || n < 0 || n > p.max_chunk || s + n > p.max_pages * kPage) {
@@ -74,14 +82,15 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         sum[0] = sat_add(sum[0], n);
         sum[1] = sat_add(sum[1], after - before);
         sum[2] = sat_add(sum[2], after);
+        sum[3] = sat_add(sum[3], few_units(p, s, n));
         o_seq[b] = s;
         o_new[b] = n;
         o_start[b] = start;
     }
     const bool any_bad = __syncthreads_or(bad);
-    int pre[3], tot[3];
+    int pre[kSums], tot[kSums];
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < kSums; ++i) {
         int x = any_bad ? 0 : sum[i];
         sum[i] = x;
 #pragma unroll
@@ -93,7 +102,7 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         if (lane == 31) s_warp[i][warp] = x;
     }
     __syncthreads();
-    if (warp < 3) {
+    if (warp < kSums) {
         int x = s_warp[warp][lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -104,11 +113,11 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < kSums; ++i) {
         tot[i] = s_warp[i][31];
         pre[i] += (warp ? s_warp[i][warp - 1] : 0) - sum[i];
     }
-    bad = any_bad || tot[0] > p.max_rows || tot[2] > p.max_total_pages || tot[1] > p.n_free - head;
+    bad = any_bad || tot[0] > p.max_rows || tot[2] > p.max_total_pages || tot[1] > p.n_free - head || tot[3] >= kSumLimit;
     if (!bad) {   // the pages about to be taken exist
         bool out = false;
         for (int i = tid; i < tot[1]; i += kTablesThreads) {
@@ -118,7 +127,7 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         bad = out;
     }
     bad = __syncthreads_or(bad);
-    int32_t row = pre[0], take = pre[1];
+    int32_t row = pre[0], take = pre[1], few = pre[3];
     for (int b = b0; b < b1; ++b) {
         if (bad) {
             o_seq[b] = p.seq[b];
@@ -127,7 +136,9 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         }
         o_row[b] = bad ? 0 : row;
         o_take[b] = bad ? 0 : take;
+        o_few[b] = bad ? 0 : few;
         if (!bad) {
+            few += few_units(p, o_seq[b], o_new[b]);
             row += o_new[b];
             take += pages_of(o_seq[b] + o_new[b]) - pages_of(o_seq[b]);
         }
@@ -148,15 +159,18 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         plan[C_BAD] = bad ? 1 : 0;
         o_row[p.n] = bad ? 0 : tot[0];
         o_take[p.n] = bad ? 0 : tot[1];
+        o_few[p.n] = bad ? 0 : tot[3];
+        plan[C_WORKERS] = p.workers;
         if (bad) set_dev_error(kDevErrBounds);
     }
 }
 
 // The plan of another batch's dims, or of no pcf_chunk_tables call at all, is refused.
 __device__ __forceinline__ bool plan_fits(const int32_t* plan, int32_t n, int32_t max_pages, int32_t max_rows,
-                                          int32_t hkv) {
-    const bool ok = plan[C_MAGIC] == kPlanMagic && plan[C_N_REQS] == n && plan[C_MAX_PAGES] == max_pages &&
-                    plan[C_MAX_ROWS] == max_rows && plan[C_HKV] == hkv;
+                                          int32_t hq, int32_t hkv, int32_t workers) {
+    const int4 a = reinterpret_cast<const int4*>(plan)[0], b = reinterpret_cast<const int4*>(plan)[1];
+    const bool ok = a.x == kPlanMagic && a.y == n && a.z == max_pages && a.w == max_rows && b.x == hq && b.y == hkv &&
+                    plan[C_WORKERS] == workers;
     if (!ok) set_dev_error(kDevErrBounds);
     return ok;
 }
@@ -192,6 +206,21 @@ __global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const TablesPa
         p.row_base[b] = base[b];
         if (b < p.n) p.seq_out[b] = seq[b] + add[b];
         else p.head_out[0] = head + plan[C_TAKEN];
+    }
+    // the few-row requests' units, dealt to the workers in equal runs
+    const int32_t* few = plan + plan_array(CA_FEW, p.n);
+    const int64_t units = few[p.n];
+    for (int32_t w = i; w < p.workers; w += step) {
+        const int64_t u0 = w * units / p.workers, u1 = (w + 1) * units / p.workers;
+        int4 e = make_int4(0, 0, 0, (int)(u1 - u0));
+        if (e.w > 0) {
+            const int b = row_request(few, p.n, (int32_t)u0);
+            const int32_t local = (int32_t)u0 - few[b], pages = pages_of(seq[b] + add[b]);
+            e.x = b;
+            e.y = local / pages;
+            e.z = local % pages;
+        }
+        reinterpret_cast<int4*>(p.plan + plan_starts(p.n))[w] = e;
     }
     for (int32_t r = i; r < p.max_rows; r += step) {
         int32_t slot = -1, pos = -1;

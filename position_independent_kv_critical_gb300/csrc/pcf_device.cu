@@ -16,6 +16,7 @@
 #include "kernel_attn.cuh"
 #include "kernel_chunk_attn.cuh"
 #include "kernel_chunk_tables.cuh"
+#include "kernel_few_rows.cuh"
 #include "kernel_imp.cuh"
 #include "kernels_simple.cuh"
 #include "layout_format.h"
@@ -978,11 +979,12 @@ extern "C" pcf_status pcf_chunk_tables(const pcf_chunk_dims* dims, const int32_t
                            row_pos, row_base, seq_len_out, free_head_out, plan};
     for (const void* w : words)
         if (reinterpret_cast<uintptr_t>(w) & 3u) return PCF_ERR_INVALID_ARG;
+    if (!aligned16(plan)) return PCF_ERR_INVALID_ARG;
     if ((s = check_device()) != PCF_OK) return s;
     const TablesParams p{seq_len, new_len, next_pos, free_pages, free_head, block_table, page_pos, slot_map, row_pos,
                          row_base, seq_len_out, free_head_out, plan, dims->n_reqs, dims->max_pages, dims->max_rows,
                          dims->max_chunk, dims->max_total_pages, dims->n_phys_pages, dims->max_pos, n_free,
-                         dims->n_q_heads, dims->n_kv_heads, dims->head_dim};
+                         dims->n_q_heads, dims->n_kv_heads, dims->head_dim, kFewWarps * chunk_sms(dims->n_sms)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((s = launch(chunk_plan_kernel, dim3(1), dim3(kTablesThreads), 0, st, p)) != PCF_OK) return s;
     const int items = std::max(dims->max_rows, dims->n_reqs + 1);
@@ -1017,6 +1019,64 @@ extern "C" pcf_status pcf_append_kv(const pcf_chunk_dims* dims, const uint16_t* 
                                  : launch(append_kernel<64>, dim3(blocks), dim3(256), 0, st, p);
 }
 
+namespace {
+struct ChunkCall {
+    const pcf_chunk_dims* dims;
+    const int32_t* plan;
+    const uint16_t* q;
+    int64_t q_stride;
+    const uint16_t *k_pool, *v_pool;
+    const int32_t *block_table, *page_pos;
+    const uint16_t* excl;
+    const int32_t* row_pos;
+    const float* rope;
+    uint16_t* out;
+    uint8_t* ws;
+};
+
+// requests with few rows: the kernel over their pages, then the runs that blocks share
+template <int D, int MT>
+pcf_status few_rows_impl(const ChunkCall& c, cudaStream_t st) {
+    const pcf_chunk_dims& d = *c.dims;
+    const ChunkWs w = chunk_ws(&d);
+    const int blocks = chunk_sms(d.n_sms);
+    CUtensorMap tk, tv;
+    pcf_status s;
+    const uint64_t rows = (uint64_t)d.n_phys_pages * d.n_kv_heads * kPage;
+    if ((s = make_map_2d(&tk, c.k_pool, D, rows, D * 2, kPage)) != PCF_OK) return s;
+    if ((s = make_map_2d(&tv, c.v_pool, D, rows, D * 2, kPage)) != PCF_OK) return s;
+    const FewParams p{c.plan, reinterpret_cast<const __nv_bfloat16*>(c.q), c.block_table, c.page_pos, c.excl, c.row_pos,
+                      c.rope, reinterpret_cast<__nv_bfloat16*>(c.out), reinterpret_cast<float*>(c.ws + w.worker_o),
+                      reinterpret_cast<float*>(c.ws + w.block_o), reinterpret_cast<float2*>(c.ws + w.block_ml),
+                      reinterpret_cast<int4*>(c.ws + w.block_desc), c.q_stride, d.n_reqs, d.max_pages, d.max_rows,
+                      d.n_q_heads, d.n_kv_heads, d.n_phys_pages, d.max_pos, blocks};
+    using SM = FewSmem<D, MT>;
+    auto kern = few_rows_kernel<D, MT>;
+    if ((s = set_smem(kern, SM::kAlloc)) != PCF_OK) return s;
+    if ((s = launch(kern, dim3(blocks), dim3(kFewThreads), SM::kAlloc, st, tk, tv, p)) != PCF_OK) return s;
+    return launch(few_join_kernel<D, MT>, dim3(blocks), dim3(256), 0, st, p);
+}
+
+template <int D>
+pcf_status chunk_attention_impl(const ChunkCall& c, cudaStream_t st) {
+    const pcf_chunk_dims& d = *c.dims;
+    const int g = d.n_q_heads / d.n_kv_heads;
+    pcf_status s;
+    if (g <= kFewRows) {
+        s = few_tiles(&d) == 1 ? few_rows_impl<D, 1>(c, st) : few_rows_impl<D, 2>(c, st);
+        if (s != PCF_OK) return s;
+    }
+    if ((int64_t)d.max_chunk * g <= kFewRows) return PCF_OK;
+    const ChunkAttnParams p{c.plan, reinterpret_cast<const __nv_bfloat16*>(c.q),
+                            reinterpret_cast<const __nv_bfloat16*>(c.k_pool),
+                            reinterpret_cast<const __nv_bfloat16*>(c.v_pool), c.block_table, c.page_pos, c.excl,
+                            c.row_pos, c.rope, reinterpret_cast<__nv_bfloat16*>(c.out), c.q_stride, d.n_reqs,
+                            d.max_pages, d.max_rows, d.n_q_heads, d.n_kv_heads, d.n_phys_pages, d.max_pos,
+                            kFewWarps * chunk_sms(d.n_sms)};
+    return launch(chunk_attn_simple_kernel<D>, dim3(d.max_rows, d.n_q_heads), dim3(128), 0, st, p);
+}
+}  // namespace
+
 extern "C" pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, const int32_t* plan, const uint16_t* q,
                                           int64_t q_row_stride, const uint16_t* k_pool, const uint16_t* v_pool,
                                           const int32_t* block_table, const int32_t* page_pos, const uint16_t* excl,
@@ -1027,23 +1087,18 @@ extern "C" pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, const int3
     if (!plan || !q || !k_pool || !v_pool || !block_table || !page_pos || !row_pos || !rope || !out || !ws)
         return PCF_ERR_INVALID_ARG;
     if (q_row_stride < (int64_t)dims->n_q_heads * dims->head_dim || q_row_stride % 8 != 0) return PCF_ERR_INVALID_ARG;
-    for (const void* a : {(const void*)q, (const void*)k_pool, (const void*)v_pool, (const void*)rope,
-                          (const void*)out, (const void*)ws})
+    for (const void* a : {(const void*)plan, (const void*)q, (const void*)k_pool, (const void*)v_pool,
+                          (const void*)rope, (const void*)out, (const void*)ws})
         if (!aligned16(a)) return PCF_ERR_INVALID_ARG;
-    for (const void* w : {(const void*)plan, (const void*)block_table, (const void*)page_pos, (const void*)row_pos})
+    for (const void* w : {(const void*)block_table, (const void*)page_pos, (const void*)row_pos})
         if (reinterpret_cast<uintptr_t>(w) & 3u) return PCF_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(excl) & 1u) return PCF_ERR_INVALID_ARG;
     size_t need = 0;
     if ((s = pcf_chunk_attention_workspace_bytes(dims, &need)) != PCF_OK) return s;
     if (ws_bytes < need) return PCF_ERR_WORKSPACE_TOO_SMALL;
     if ((s = check_device()) != PCF_OK) return s;
-    const ChunkAttnParams p{plan, reinterpret_cast<const __nv_bfloat16*>(q),
-                            reinterpret_cast<const __nv_bfloat16*>(k_pool),
-                            reinterpret_cast<const __nv_bfloat16*>(v_pool), block_table, page_pos, excl, row_pos, rope,
-                            reinterpret_cast<__nv_bfloat16*>(out), q_row_stride, dims->n_reqs, dims->max_pages,
-                            dims->max_rows, dims->n_q_heads, dims->n_kv_heads, dims->n_phys_pages, dims->max_pos};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const dim3 grid(dims->max_rows, dims->n_q_heads);
-    return dims->head_dim == 128 ? launch(chunk_attn_simple_kernel<128>, grid, dim3(128), 0, st, p)
-                                 : launch(chunk_attn_simple_kernel<64>, grid, dim3(128), 0, st, p);
+    const ChunkCall c{dims, plan, q, q_row_stride, k_pool, v_pool, block_table, page_pos, excl, row_pos, rope, out,
+                      static_cast<uint8_t*>(ws)};
+    return dims->head_dim == 128 ? chunk_attention_impl<128>(c, st) : chunk_attention_impl<64>(c, st);
 }
