@@ -298,8 +298,10 @@ class ChunkLayout:
         total = n_reqs * max_pages if max_total_pages is None else max_total_pages
         self.dims = _lib.ChunkDims(n_reqs, max_pages, max_rows, max_chunk, total, hq, hkv, d, n_phys_pages, max_pos,
                                    n_sms)
+        self.dims_ref = ctypes.byref(self.dims)
+        self.pool_elems = n_phys_pages * hkv * 16 * d
         n = ctypes.c_int64(0)
-        _lib.check("pcf_chunk_plan_words", lib.pcf_chunk_plan_words(ctypes.byref(self.dims), ctypes.byref(n)))
+        _lib.check("pcf_chunk_plan_words", lib.pcf_chunk_plan_words(self.dims_ref, ctypes.byref(n)))
         ints = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)
         self.block_table, self.page_pos = ints(n_reqs, max_pages), ints(n_reqs, max_pages)
         self.slot_map, self.row_pos, self.row_base = ints(max_rows), ints(max_rows), ints(n_reqs + 1)
@@ -337,55 +339,75 @@ class ChunkLayout:
     def attention_workspace_bytes(self) -> int:
         v = ctypes.c_size_t(0)
         _lib.check("pcf_chunk_attention_workspace_bytes", _lib.load().pcf_chunk_attention_workspace_bytes(
-            ctypes.byref(self.dims), ctypes.byref(v)))
+            self.dims_ref, ctypes.byref(v)))
         return int(v.value)
 
 
-def _chunk_ints(L: ChunkLayout, t: Optional[torch.Tensor], name: str, n: Optional[int] = None, dtype=torch.int32):
-    if t is None:
-        return
+# The checks of the chunk calls are written as one condition a tensor with the explanation apart: a
+# decoding step makes three of these calls a layer, so their host time counts.
+def _bad_ints(L: ChunkLayout, t, name: str, n: Optional[int], dtype=torch.int32):
     _need(t, dtype, name)
     if t.device != L.device:
         raise ValueError(f"{name}: on {t.device}, the layout is on {L.device}")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+    raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+
+
+def _chunk_ints(L: ChunkLayout, t: Optional[torch.Tensor], name: str, n: Optional[int] = None, dtype=torch.int32):
+    """Address of an integer tensor of n elements, None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_contiguous() or t.device != L.device or (n is not None and t.numel() != n):
+        _bad_ints(L, t, name, n, dtype)
+    return t.data_ptr() or None
 
 
 def _chunk_rows(L: ChunkLayout, t: torch.Tensor, heads: int, name: str) -> int:
     """Checks a [max_rows, heads, d] bf16 tensor whose rows may be columns of wider ones; elements
     from row to row."""
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (L.max_rows, heads, L.d):
+    if t.dtype != torch.bfloat16 or t.shape != (L.max_rows, heads, L.d):
         raise ValueError(f"{name}: expected bfloat16 [{L.max_rows}, {heads}, {L.d}], got {t.dtype} {tuple(t.shape)}")
     if t.device != L.device:
         raise ValueError(f"{name}: on {t.device}, the layout is on {L.device}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != L.d):
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != L.d):
         raise ValueError(f"{name}: a row's heads must be contiguous")
     if L.max_rows == 1:
         return heads * L.d
-    if t.stride(0) < heads * L.d:
-        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)})")
-    return t.stride(0)
+    if row < heads * L.d:
+        raise ValueError(f"{name}: rows overlap (stride {row})")
+    return row
 
 
 def _chunk_pool(L: ChunkLayout, t: torch.Tensor, name: str):
-    _need(t, torch.bfloat16, name)
+    if t.dtype != torch.bfloat16 or not t.is_contiguous():
+        _need(t, torch.bfloat16, name)
     if t.device != L.device:
         raise ValueError(f"{name}: on {t.device}, the layout is on {L.device}")
-    if t.numel() < L.dims.n_phys_pages * L.hkv * 16 * L.d:
+    if t.numel() < L.pool_elems:
         raise ValueError(f"{name}: smaller than the {L.dims.n_phys_pages} pages of the layout")
+    return t.data_ptr()
 
 
 def _chunk_rope(L: ChunkLayout, t: Optional[torch.Tensor]):
-    if t is not None:
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or not t.is_contiguous():
         _need(t, torch.float32, "rope")
-        if t.device != L.device or t.numel() < L.dims.max_pos * L.d:
-            raise ValueError(f"rope: expected {L.dims.max_pos} rows on {L.device}")
+    if t.device != L.device or t.numel() < L.dims.max_pos * L.d:
+        raise ValueError(f"rope: expected {L.dims.max_pos} rows on {L.device}")
+    return t.data_ptr()
 
 
 def _chunk_call(L: ChunkLayout, fn: str, stream, *args):
-    """The call on the layout's device, on its current stream unless one is named."""
-    with torch.cuda.device(L.device):
-        _lib.check(fn, getattr(_lib.load(), fn)(ctypes.byref(L.dims), *args, _stream(stream)))
+    """The call on the layout's device, on that device's current stream unless one is named."""
+    call = getattr(_lib.load(), fn)
+    if L.device.type == "cuda" and torch.cuda.current_device() != L.device.index:
+        with torch.cuda.device(L.device):
+            status = call(L.dims_ref, *args, (stream or torch.cuda.current_stream()).cuda_stream)
+    else:
+        status = call(L.dims_ref, *args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    if status:
+        _lib.check(fn, status)
 
 
 def chunk_tables(layout: ChunkLayout, seq_len, new_len, free_pages, free_head, seq_len_out, free_head_out,
@@ -394,13 +416,13 @@ def chunk_tables(layout: ChunkLayout, seq_len, new_len, free_pages, free_head, s
     ``free_pages[free_head:]``) in the layout's tables and fills its slot map, row positions and plan.
     ``seq_len_out`` / ``free_head_out`` may be ``seq_len`` / ``free_head`` themselves."""
     L = layout
-    for t, n, k in ((seq_len, "seq_len", L.n_reqs), (new_len, "new_len", L.n_reqs), (next_pos, "next_pos", L.n_reqs),
-                    (seq_len_out, "seq_len_out", L.n_reqs), (free_head, "free_head", 1),
-                    (free_head_out, "free_head_out", 1), (free_pages, "free_pages", None)):
-        _chunk_ints(L, t, n, k)
-    _chunk_call(L, "pcf_chunk_tables", stream, _p(seq_len), _p(new_len), _p(next_pos), _p(free_pages),
-                free_pages.numel(), _p(free_head), _p(L.block_table), _p(L.page_pos), _p(L.slot_map), _p(L.row_pos),
-                _p(L.row_base), _p(seq_len_out), _p(free_head_out), _p(L.plan))
+    n = L.n_reqs
+    _chunk_call(L, "pcf_chunk_tables", stream, _chunk_ints(L, seq_len, "seq_len", n),
+                _chunk_ints(L, new_len, "new_len", n), _chunk_ints(L, next_pos, "next_pos", n),
+                _chunk_ints(L, free_pages, "free_pages"), free_pages.numel(), _chunk_ints(L, free_head, "free_head", 1),
+                L.block_table.data_ptr(), L.page_pos.data_ptr(), L.slot_map.data_ptr(), L.row_pos.data_ptr(),
+                L.row_base.data_ptr(), _chunk_ints(L, seq_len_out, "seq_len_out", n),
+                _chunk_ints(L, free_head_out, "free_head_out", 1), L.plan.data_ptr())
 
 
 def append_kv(layout: ChunkLayout, k_new, v_new, k_pool, v_pool, rope=None, row_pos=None, stream=None):
@@ -409,12 +431,9 @@ def append_kv(layout: ChunkLayout, k_new, v_new, k_pool, v_pool, rope=None, row_
     slots', whose keys are stored turned by the difference."""
     L = layout
     ks, vs = _chunk_rows(L, k_new, L.hkv, "k_new"), _chunk_rows(L, v_new, L.hkv, "v_new")
-    _chunk_pool(L, k_pool, "k_pool")
-    _chunk_pool(L, v_pool, "v_pool")
-    _chunk_ints(L, row_pos, "row_pos", L.max_rows)
-    _chunk_rope(L, rope)
-    _chunk_call(L, "pcf_append_kv", stream, _p(k_new), ks, _p(v_new), vs, _p(L.slot_map), _p(L.row_pos), _p(row_pos),
-                _p(rope), _p(k_pool), _p(v_pool))
+    _chunk_call(L, "pcf_append_kv", stream, k_new.data_ptr(), ks, v_new.data_ptr(), vs, L.slot_map.data_ptr(),
+                L.row_pos.data_ptr(), _chunk_ints(L, row_pos, "row_pos", L.max_rows), _chunk_rope(L, rope),
+                _chunk_pool(L, k_pool, "k_pool"), _chunk_pool(L, v_pool, "v_pool"))
 
 
 def chunk_attention(layout: ChunkLayout, q, k_pool, v_pool, rope, out, ws, excl=None, stream=None):
@@ -423,17 +442,16 @@ def chunk_attention(layout: ChunkLayout, q, k_pool, v_pool, rope, out, ws, excl=
     no part.  ``ws`` sized by ``ChunkLayout.attention_workspace_bytes``."""
     L = layout
     qs = _chunk_rows(L, q, L.hq, "q")
-    _chunk_pool(L, k_pool, "k_pool")
-    _chunk_pool(L, v_pool, "v_pool")
-    _chunk_ints(L, excl, "excl", L.n_reqs * L.max_pages, torch.int16)
-    _chunk_rope(L, rope)
+    if out.dtype != torch.bfloat16 or not out.is_contiguous():
+        _need(out, torch.bfloat16, "out")
     if out.shape != (L.max_rows, L.hq, L.d) or out.device != L.device:
         raise ValueError(f"out: expected [{L.max_rows}, {L.hq}, {L.d}] on {L.device}")
-    _need(out, torch.bfloat16, "out")
     if ws.device != L.device or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on {L.device}")
-    _chunk_call(L, "pcf_chunk_attention", stream, _p(L.plan), _p(q), qs, _p(k_pool), _p(v_pool), _p(L.block_table),
-                _p(L.page_pos), _p(excl), _p(L.row_pos), _p(rope), _p(out), _p(ws), ws.numel() * ws.element_size())
+    _chunk_call(L, "pcf_chunk_attention", stream, L.plan.data_ptr(), q.data_ptr(), qs, _chunk_pool(L, k_pool, "k_pool"),
+                _chunk_pool(L, v_pool, "v_pool"), L.block_table.data_ptr(), L.page_pos.data_ptr(),
+                _chunk_ints(L, excl, "excl", L.n_reqs * L.max_pages, torch.int16), L.row_pos.data_ptr(),
+                _chunk_rope(L, rope), out.data_ptr(), ws.data_ptr(), ws.nbytes)
 
 
 def wait_limit_check(limit_cycles: int, flag, stream=None):

@@ -32,7 +32,7 @@ enum : int {
 // before the request, position of its first row, and the (page, kv head) units of the requests
 // before it that have few rows; then the few-row work split, kStartWords words a worker
 enum : int { CA_SEQ = 0, CA_NEW = 1, CA_ROW = 2, CA_TAKE = 3, CA_START = 4, CA_FEW = 5, CA_COUNT = 6 };
-constexpr int kStartWords = 4;   // {request, kv head, page, units}
+constexpr int kStartWords = 8;   // {request, kv head, page, units; its pages, tokens held, new tokens, first row}
 
 PCF_HOST_DEVICE inline int64_t plan_array(int which, int32_t n_reqs) {
     return C_HEADER + (int64_t)which * (n_reqs + 1);
@@ -49,6 +49,10 @@ PCF_HOST_DEVICE inline int64_t plan_words(int32_t n_reqs, int32_t workers) {
 // value of 4 d bytes meet 4 d flops a row, 32 flops a byte at most).
 constexpr int kFewRows = 32;
 constexpr int kFewWarps = 8;   // warps of a block of the few-row kernel, each a worker
+
+// Units go to the workers in equal runs, worker w from the w-th of `active` equal parts on; with
+// fewer units than workers the first ones take one each, so that a run's parts sit in few blocks.
+PCF_HOST_DEVICE inline int64_t few_active(int64_t units, int32_t workers) { return units < workers ? units : workers; }
 
 PCF_HOST_DEVICE inline int32_t chunk_sms(int32_t n_sms) { return n_sms > 0 ? n_sms : kDefaultSms; }
 

@@ -209,18 +209,21 @@ __global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const TablesPa
     }
     // the few-row requests' units, dealt to the workers in equal runs
     const int32_t* few = plan + plan_array(CA_FEW, p.n);
-    const int64_t units = few[p.n];
+    const int64_t units = few[p.n], active = few_active(units, p.workers);
     for (int32_t w = i; w < p.workers; w += step) {
-        const int64_t u0 = w * units / p.workers, u1 = (w + 1) * units / p.workers;
-        int4 e = make_int4(0, 0, 0, (int)(u1 - u0));
+        const int64_t u0 = w < active ? w * units / active : 0, u1 = w < active ? (w + 1) * units / active : 0;
+        int4 e = make_int4(0, 0, 0, (int)(u1 - u0)), f = make_int4(1, 0, 0, 0);
         if (e.w > 0) {
             const int b = row_request(few, p.n, (int32_t)u0);
-            const int32_t local = (int32_t)u0 - few[b], pages = pages_of(seq[b] + add[b]);
+            f = make_int4(pages_of(seq[b] + add[b]), seq[b], add[b], base[b]);
+            const int32_t local = (int32_t)u0 - few[b];
             e.x = b;
-            e.y = local / pages;
-            e.z = local % pages;
+            e.y = local / f.x;
+            e.z = local % f.x;
         }
-        reinterpret_cast<int4*>(p.plan + plan_starts(p.n))[w] = e;
+        int4* dst = reinterpret_cast<int4*>(p.plan + plan_starts(p.n)) + 2 * w;
+        dst[0] = e;
+        dst[1] = f;
     }
     for (int32_t r = i; r < p.max_rows; r += step) {
         int32_t slot = -1, pos = -1;

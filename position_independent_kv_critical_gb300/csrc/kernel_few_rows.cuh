@@ -48,7 +48,7 @@ struct FewParams {
     float* worker_o;            // [workers][16 MT][D]
     float* block_o;             // [blocks][2][16 MT][D]
     float2* block_ml;           // [blocks][2][16 MT]
-    int4* block_desc;           // [blocks]: {run starts here and goes on, request, kv head, its last unit}
+    int4* block_desc;           // [blocks]: a run that starts here and goes on: {last block << 8 | 255, rows, kv head, first row}
     int64_t q_stride;
     int32_t n, max_pages, max_rows, hq, hkv, n_phys, max_pos, blocks;
 };
@@ -156,15 +156,15 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const int g = p.hq / p.hkv, gs = __ffs(g) - 1;   // g divides 128
     const bool fits = plan_fits(plan, p.n, p.max_pages, p.max_rows, p.hq, p.hkv, p.blocks * kFewWarps);
     const int worker = blockIdx.x * kFewWarps + warp;
-    const int4 start = fits ? reinterpret_cast<const int4*>(plan + plan_starts(p.n))[worker] : make_int4(0, 0, 0, 0);
-    const int n_units = start.w;
+    const int4 start = reinterpret_cast<const int4*>(plan + plan_starts(p.n))[2 * worker];
+    const int4 first = reinterpret_cast<const int4*>(plan + plan_starts(p.n))[2 * worker + 1];
+    const int n_units = fits ? start.w : 0;
 
     // ---------------- the copies: unit i of the worker into slot i % NS
-    FewCursor is{start.x, start.y, start.z, 0};
+    FewCursor is{start.x, start.y, start.z, first.x};
     int32_t win_req = -1, win_page = 0;            // the 32 table entries the lanes hold
     int32_t e_ph = 0, e_pos = 0;
     uint32_t e_ex = 0;
-    if (n_units > 0) is.open(seq, add);
     auto issue = [&](int i) {
         if (is.req != win_req || is.page < win_page || is.page >= win_page + 32) {
             win_req = is.req;
@@ -214,8 +214,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
     // ---------------- the units
     const float scale = 1.4426950408889634f * (D == 128 ? 0.08838834764831845f : 0.125f);   // log2(e) / sqrt(d)
-    FewCursor cu{start.x, start.y, start.z, 0};
-    if (n_units > 0) cu.open(seq, add);
+    FewCursor cu{start.x, start.y, start.z, first.x};
     float o[MT][NT][4], m_run[MT][2], l_run[MT][2];
     uint32_t qf[MT == 1 ? KS : 1][4];
     uint4* s_q = reinterpret_cast<uint4*>(smem + SM::oQ + warp * SM::kQ);   // MT == 2: [mt][ks][lane]
@@ -230,9 +229,9 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // fragments (rows behind the last one zero)
             open = true;
             seg_page = cu.page;
-            s_len = seq[cu.req];
-            t_len = add[cu.req];
-            r_base = base[cu.req];
+            s_len = i == 0 ? first.y : seq[cu.req];
+            t_len = i == 0 ? first.z : add[cu.req];
+            r_base = i == 0 ? first.w : base[cu.req];
             n_rows = t_len * g;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -462,6 +461,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 d[0] = 1 | (ended ? 2 : 0) | (last ? 4 : 0);
                 d[1] = cu.req;
                 d[2] = cu.kvh;
+                d[3] = r_base << 8 | n_rows;         // (rows of a chunk: below 2^22)
             }
             open = false;
         }
@@ -470,114 +470,145 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     if (!(big < kF16Limit)) set_dev_error(kDevErrRange);
     if (!ok && lane == 0)        // an abort: the copies in flight land before the block exits
         for (int i = done; i < issued; ++i) mbar_drain(&bars[i % NS], (i / NS) & 1);
-    const bool any = __syncthreads_or(n_units > 0);
-    // a block without units stands between two parts of a run as an empty one
-    if (!any && tid < ROWS) p.block_ml[blockIdx.x * 2 * ROWS + tid] = make_float2(-INFINITY, 0.f);
+    __syncthreads();
     // ---------------- join the warps' partial results, run by run
     const bool aborted = *abort_flag != 0;
     int4 desc = make_int4(0, 0, 0, 0);
-    if (!aborted) {
-#pragma unroll 1
-        for (int k = 0; k <= kFewWarps; ++k) {
-            // k = 0: the run the block before began; k > 0: the one warp k - 1 began and left open
-            int w = k == 0 ? 0 : k - 1, kind = k == 0 ? 0 : 1;
-            if (k == 0)      // warps without units are passed over
-                while (w < kFewWarps && !(s_desc[w * 8] & 1) && !(s_desc[w * 8 + 4] & 1)) ++w;
-            if (w >= kFewWarps) continue;
-            if (!(s_desc[(w * 2 + kind) * 4] & 1)) continue;
-            const int32_t req = s_desc[(w * 2 + kind) * 4 + 1], kvh = s_desc[(w * 2 + kind) * 4 + 2];
-            int parts[kFewWarps], np = 0;
-            bool ended = (s_desc[(w * 2 + kind) * 4] & 2) != 0;
-            parts[np++] = w * 2 + kind;
-            for (int x = w + 1; x < kFewWarps && !ended; ++x)
-                if (s_desc[(x * 2) * 4] & 1) {
-                    parts[np++] = x * 2;
-                    ended = (s_desc[(x * 2) * 4] & 2) != 0;
-                }
-            const int rows_run = add[req] * g, rb = base[req];
-            const bool final_run = k > 0 && ended;
-            const int slot = blockIdx.x * 2 + (k == 0 ? 0 : 1);
-            for (int idx = tid; idx < rows_run * (D / 4); idx += kFewThreads) {
-                const int r = idx / (D / 4), f = idx % (D / 4);
-                float top = -INFINITY;
-                for (int x = 0; x < np; ++x) top = fmaxf(top, s_ml[parts[x] * ROWS + r].x);
-                const float ref = top == -INFINITY ? 0.f : top;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                float l = 0.f;
-                for (int x = 0; x < np; ++x) {
-                    const float2 ml = s_ml[parts[x] * ROWS + r];
-                    const float a = ex2(ml.x - ref);
-                    const int pw = parts[x] >> 1;
-                    const float* src = (s_desc[parts[x] * 4] & 4)
-                                           ? reinterpret_cast<const float*>(smem + pw * NS * SM::kSlot)
-                                           : p.worker_o + (int64_t)(blockIdx.x * kFewWarps + pw) * ROWS * D;
-                    const float4 v = *reinterpret_cast<const float4*>(src + r * D + 4 * f);
-                    acc.x += a * v.x;
-                    acc.y += a * v.y;
-                    acc.z += a * v.z;
-                    acc.w += a * v.w;
-                    l += a * ml.y;
-                }
-                if (final_run) {
-                    const float inv = l > 0.f ? 1.0f / l : 0.f;
-                    *reinterpret_cast<uint2*>(p.out + ((int64_t)(rb + (r >> gs)) * p.hq + kvh * g + (r & (g - 1))) * D + 4 * f) =
-                        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                } else {
-                    *reinterpret_cast<float4*>(p.block_o + ((int64_t)slot * ROWS + r) * D + 4 * f) = acc;
-                    if (f == 0) p.block_ml[slot * ROWS + r] = make_float2(top, l);
-                }
-            }
-            if (k > 0 && !ended) {
-                const int32_t pages = pages_of(seq[req] + add[req]);
-                desc = make_int4(1, req, kvh, few[req] + (kvh + 1) * pages - 1);
-            }
+    // bit 2 w: what warp w ends of a run begun before it; bit 2 w + 1: what it leaves open
+    const int32_t state = lane < 2 * kFewWarps ? s_desc[lane * 4] : 0;
+    const uint32_t present = __ballot_sync(0xffffffffu, state & 1), closing = __ballot_sync(0xffffffffu, state & 2);
+    const uint32_t in_ring = __ballot_sync(0xffffffffu, state & 4);
+    // a run's first part here: one left open, or the block's very first part where that is an end
+    const uint32_t lowest = present & (0u - present);
+    const uint32_t before = lowest & 0x5555u;
+    for (uint32_t todo = aborted ? 0u : (present & 0xAAAAu) | before; todo != 0u; todo &= todo - 1u) {
+        const int sb = __ffs(todo) - 1;
+        const bool from_before = (before >> sb & 1u) != 0u;
+        uint32_t parts = 1u << sb;
+        bool ended = (closing >> sb & 1u) != 0u;
+        for (uint32_t rest = present & 0x5555u & ~((2u << sb) - 1u); rest != 0u && !ended; rest &= rest - 1u) {
+            parts |= rest & (0u - rest);
+            ended = (closing & rest & (0u - rest)) != 0u;
         }
-    }
-    if (tid == 0) p.block_desc[blockIdx.x] = desc;
-}
-
-// Block j adds up the run that block j of few_rows_kernel began and left open: its part, then those
-// of the blocks behind up to the one that holds the run's last unit.
-template <int D, int MT>
-__global__ void __launch_bounds__(256) few_join_kernel(const FewParams p) {
-    constexpr int ROWS = 16 * MT;
-    grid_dep_wait();
-    grid_dep_launch();
-    const int j = blockIdx.x;
-    const int4 d = p.block_desc[j];
-    if (d.x == 0) return;
-    const int32_t* plan = p.plan;
-    const int64_t units = plan[plan_array(CA_FEW, p.n) + p.n];
-    const int64_t workers = (int64_t)p.blocks * kFewWarps;
-    // block b holds the units [8 b U / W, 8 (b + 1) U / W): the owner of unit u is the last worker
-    // whose first unit is not behind it
-    const int last = (int)((((int64_t)d.w + 1) * workers - 1) / units) / kFewWarps;
-    const int g = p.hq / p.hkv, gs = __ffs(g) - 1, rows = plan[plan_array(CA_NEW, p.n) + d.y] * g;
-    const int32_t rb = plan[plan_array(CA_ROW, p.n) + d.y];
-    for (int idx = threadIdx.x; idx < rows * (D / 4); idx += 256) {
-        const int r = idx / (D / 4), f = idx % (D / 4);
-        float top = -INFINITY;
-        for (int b = j; b <= last; ++b) top = fmaxf(top, p.block_ml[(b * 2 + (b == j)) * ROWS + r].x);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-#pragma unroll 4
-        for (int b = j; b <= last; ++b) {
-            const int slot = b * 2 + (b == j);
-            const float2 ml = p.block_ml[slot * ROWS + r];
-            const float4 v = *reinterpret_cast<const float4*>(p.block_o + ((int64_t)slot * ROWS + r) * D + 4 * f);
-            if (ml.x != -INFINITY) {
+        const int32_t req = s_desc[sb * 4 + 1], kvh = s_desc[sb * 4 + 2];
+        const int rows_run = s_desc[sb * 4 + 3] & 0xFF, rb = s_desc[sb * 4 + 3] >> 8;
+        const int slot = blockIdx.x * 2 + (from_before ? 0 : 1);
+        for (int idx = tid; idx < rows_run * (D / 4); idx += kFewThreads) {
+            const int r = idx / (D / 4), f = idx % (D / 4);
+            float top = -INFINITY;
+            for (uint32_t m = parts; m != 0u; m &= m - 1u) top = fmaxf(top, s_ml[(__ffs(m) - 1) * ROWS + r].x);
+            const float ref = top == -INFINITY ? 0.f : top;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f;
+            for (uint32_t m = parts; m != 0u; m &= m - 1u) {
+                const int x = __ffs(m) - 1;
+                const float2 ml = s_ml[x * ROWS + r];
                 const float a = ex2(ml.x - ref);
+                const float* src = (in_ring >> x & 1u)
+                                       ? reinterpret_cast<const float*>(smem + (x >> 1) * NS * SM::kSlot)
+                                       : p.worker_o + (int64_t)(blockIdx.x * kFewWarps + (x >> 1)) * ROWS * D;
+                const float4 v = *reinterpret_cast<const float4*>(src + r * D + 4 * f);
                 acc.x += a * v.x;
                 acc.y += a * v.y;
                 acc.z += a * v.z;
                 acc.w += a * v.w;
                 l += a * ml.y;
             }
+            if (!from_before && ended) {
+                const float inv = l > 0.f ? 1.0f / l : 0.f;
+                *reinterpret_cast<uint2*>(p.out + ((int64_t)(rb + (r >> gs)) * p.hq + kvh * g + (r & (g - 1))) * D + 4 * f) =
+                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+            } else {
+                *reinterpret_cast<float4*>(p.block_o + ((int64_t)slot * ROWS + r) * D + 4 * f) = acc;
+                if (f == 0) p.block_ml[slot * ROWS + r] = make_float2(top, l);
+            }
         }
-        const float inv = l > 0.f ? 1.0f / l : 0.f;
-        *reinterpret_cast<uint2*>(p.out + ((int64_t)(rb + (r >> gs)) * p.hq + d.z * g + (r & (g - 1))) * D + 4 * f) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (!from_before && !ended) {
+            // the block that holds the run's last unit u: u's owner is the last worker whose first unit
+            // is not behind it
+            const int64_t units = few[p.n], active = few_active(units, p.blocks * kFewWarps);
+            const int64_t u = few[req] + (int64_t)(kvh + 1) * pages_of(seq[req] + add[req]) - 1;
+            desc = make_int4(((int)(((u + 1) * active - 1) / units) / kFewWarps) << 8 | 0xFF, rows_run, kvh, rb);
+        }
+    }
+    if (tid == 0) p.block_desc[blockIdx.x] = desc;
+}
+
+// Block j adds up the run that block j of few_rows_kernel began and left open: its part, then those of
+// the blocks behind up to the one that holds the run's last unit.  A run of a single long request has
+// a part in every eighth block or so and few rows, so the parts are taken by groups of threads side by
+// side, four loads in flight a thread, and the groups joined in shared memory in their order.
+constexpr int kJoinThreads = 512;
+template <int D, int MT>
+__global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const FewParams p) {
+    constexpr int ROWS = 16 * MT;
+    __shared__ float4 s_acc[kJoinThreads];
+    __shared__ float2 s_w[kJoinThreads];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int j = blockIdx.x;
+    const int4 d = p.block_desc[j];
+    if (d.x == 0) return;
+    const int last = d.x >> 8, rows = d.y, kvh = d.z, rb = d.w;
+    const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
+    const int cols = rows * (D / 4);
+    const int groups = max(1, min(kJoinThreads / cols, last - j + 1));
+    for (int c0 = 0; c0 < cols; c0 += kJoinThreads) {
+        const int grp = threadIdx.x / min(cols, kJoinThreads), idx = c0 + threadIdx.x - grp * min(cols, kJoinThreads);
+        const int r = idx / (D / 4), f = idx % (D / 4);
+        const bool mine = grp < groups && idx < cols;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float top = -INFINITY, l = 0.f;
+        if (mine)
+            for (int b0 = j + grp; b0 <= last; b0 += 4 * groups) {
+                float2 ml[4];
+                float4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int b = b0 + i * groups, slot = min(b, last) * 2 + (b == j ? 1 : 0);
+                    ml[i] = p.block_ml[slot * ROWS + r];
+                    v[i] = *reinterpret_cast<const float4*>(p.block_o + ((int64_t)slot * ROWS + r) * D + 4 * f);
+                    if (b > last) ml[i].x = -INFINITY;
+                }
+                const float now = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), top);
+                const float ref = now == -INFINITY ? 0.f : now, old = ex2(top - ref);
+                top = now;
+                l *= old;
+                acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a = ex2(ml[i].x - ref);
+                    acc.x += a * v[i].x;
+                    acc.y += a * v[i].y;
+                    acc.z += a * v[i].z;
+                    acc.w += a * v[i].w;
+                    l += a * ml[i].y;
+                }
+            }
+        s_acc[threadIdx.x] = acc;
+        s_w[threadIdx.x] = make_float2(top, l);
+        __syncthreads();
+        if (mine && grp == 0) {
+            float all = top;
+            for (int q = 1; q < groups; ++q) all = fmaxf(all, s_w[q * cols + threadIdx.x].x);
+            const float ref = all == -INFINITY ? 0.f : all, a0 = ex2(top - ref);
+            acc = make_float4(acc.x * a0, acc.y * a0, acc.z * a0, acc.w * a0);
+            l *= a0;
+            for (int q = 1; q < groups; ++q) {
+                const float2 w = s_w[q * cols + threadIdx.x];
+                const float4 v = s_acc[q * cols + threadIdx.x];
+                const float a = ex2(w.x - ref);
+                acc.x += a * v.x;
+                acc.y += a * v.y;
+                acc.z += a * v.z;
+                acc.w += a * v.w;
+                l += a * w.y;
+            }
+            const float inv = l > 0.f ? 1.0f / l : 0.f;
+            *reinterpret_cast<uint2*>(p.out + ((int64_t)(rb + (r >> gs)) * p.hq + kvh * g + (r & (g - 1))) * D + 4 * f) =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        }
+        __syncthreads();
     }
 }
 

@@ -987,7 +987,7 @@ extern "C" pcf_status pcf_chunk_tables(const pcf_chunk_dims* dims, const int32_t
                          dims->n_q_heads, dims->n_kv_heads, dims->head_dim, kFewWarps * chunk_sms(dims->n_sms)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((s = launch(chunk_plan_kernel, dim3(1), dim3(kTablesThreads), 0, st, p)) != PCF_OK) return s;
-    const int items = std::max(dims->max_rows, dims->n_reqs + 1);
+    const int items = std::max({dims->max_rows, dims->n_reqs + 1, p.workers});
     const int blocks = std::min((items + kRowsThreads - 1) / kRowsThreads, 8 * device_sms());
     return launch(chunk_rows_kernel, dim3(blocks), dim3(kRowsThreads), 0, st, p);
 }
@@ -1054,7 +1054,7 @@ pcf_status few_rows_impl(const ChunkCall& c, cudaStream_t st) {
     auto kern = few_rows_kernel<D, MT>;
     if ((s = set_smem(kern, SM::kAlloc)) != PCF_OK) return s;
     if ((s = launch(kern, dim3(blocks), dim3(kFewThreads), SM::kAlloc, st, tk, tv, p)) != PCF_OK) return s;
-    return launch(few_join_kernel<D, MT>, dim3(blocks), dim3(256), 0, st, p);
+    return launch(few_join_kernel<D, MT>, dim3(blocks), dim3(kJoinThreads), 0, st, p);
 }
 
 template <int D>
