@@ -26,12 +26,15 @@ enum : int {
     C_TAKEN = 11,     // pages taken for the chunk
     C_BAD = 12,       // 1: the lengths were refused and nothing was done
     C_WORKERS = 13,   // warps the few-row requests' pages are dealt to
+    C_BLOCKS = 14,    // blocks the other requests' key tiles are dealt to
     C_HEADER = 16
 };
 // arrays behind the header, n_reqs + 1 words each: tokens held, new tokens, first row, pages taken
 // before the request, position of its first row, and the (page, kv head) units of the requests
-// before it that have few rows; then the few-row work split, kStartWords words a worker
-enum : int { CA_SEQ = 0, CA_NEW = 1, CA_ROW = 2, CA_TAKE = 3, CA_START = 4, CA_FEW = 5, CA_COUNT = 6 };
+// before it that have few rows,
+// and, for the requests with more, the key tiles their row pairs visit and the pages they hold.
+// Behind them the work split of both kinds: kStartWords words a worker, then kManyWords a block.
+enum : int { CA_SEQ = 0, CA_NEW = 1, CA_ROW = 2, CA_TAKE = 3, CA_START = 4, CA_FEW = 5, CA_MANY = 6, CA_KPAGE = 7, CA_COUNT = 8 };
 constexpr int kStartWords = 8;   // {request, kv head, page, units; its pages, tokens held, new tokens, first row}
 
 PCF_HOST_DEVICE inline int64_t plan_array(int which, int32_t n_reqs) {
@@ -40,8 +43,31 @@ PCF_HOST_DEVICE inline int64_t plan_array(int which, int32_t n_reqs) {
 PCF_HOST_DEVICE inline int64_t plan_starts(int32_t n_reqs) {
     return (plan_array(CA_COUNT, n_reqs) + 3) / 4 * 4;
 }
-PCF_HOST_DEVICE inline int64_t plan_words(int32_t n_reqs, int32_t workers) {
+constexpr int kManyWords = 8;    // {request, kv head, row pair, key tile; units}
+PCF_HOST_DEVICE inline int64_t plan_many(int32_t n_reqs, int32_t workers) {
     return plan_starts(n_reqs) + (int64_t)workers * kStartWords;
+}
+PCF_HOST_DEVICE inline int64_t plan_words(int32_t n_reqs, int32_t workers, int32_t blocks) {
+    return plan_many(n_reqs, workers) + (int64_t)blocks * kManyWords;
+}
+
+// A request with more rows: row pair p holds the tokens [p tpp, (p + 1) tpp) of the chunk, tpp = 256 / g
+// of them (two tiles of 128 rows, token by token, the g query heads of a kv head together), which see
+// the slots up to seq + min(T, (p + 1) tpp) - 1.
+PCF_HOST_DEVICE inline int32_t many_pairs(int32_t add, int32_t tpp) { return (add + tpp - 1) / tpp; }
+PCF_HOST_DEVICE inline int32_t many_tiles(int32_t seq, int32_t add, int32_t tpp, int32_t pair) {
+    const int32_t end = (pair + 1) * tpp < add ? (pair + 1) * tpp : add;
+    return (seq + end + kTileKeys - 1) / kTileKeys;
+}
+// key tiles of the pairs before `pair` (not behind the last one): sum of floor((a + i tpp) / 128),
+// a = seq + tpp + 127.  With m = 128 / tpp pairs to a tile (tpp divides 128, or is 256), i = m u + v
+// adds u whole tiles and one more from v = v0 on, the first whose tokens cross a tile.
+PCF_HOST_DEVICE inline int64_t many_before(int32_t seq, int32_t tpp, int32_t pair) {
+    const int64_t a = (seq + tpp + kTileKeys - 1) / kTileKeys, p = pair;
+    if (tpp == 2 * kTileKeys) return p * a + p * (p - 1);
+    const int64_t r = (seq + tpp + kTileKeys - 1) % kTileKeys, m = kTileKeys / tpp, u = p / m, w = p % m;
+    const int64_t v0 = (kTileKeys - r + tpp - 1) / tpp;
+    return p * a + m * (u * (u - 1) / 2) + u * w + u * (m - v0) + (w > v0 ? w - v0 : 0);
 }
 
 // A request has few rows when its new tokens times the query heads of a kv head are at most this:
@@ -66,6 +92,11 @@ inline pcf_status check_chunk_dims(const pcf_chunk_dims* c) {
         return PCF_ERR_INVALID_ARG;
     // slots and the rows of the pool's tensor maps are 32-bit numbers
     if ((int64_t)c->n_phys_pages * c->n_kv_heads * kPage > INT32_MAX) return PCF_ERR_INVALID_ARG;
+    // and so are the rows of the rotated copies that longer chunks use
+    if ((int64_t)c->max_chunk * (c->n_q_heads / c->n_kv_heads) > kFewRows &&
+        ((int64_t)c->max_rows * c->n_q_heads > INT32_MAX ||
+         (int64_t)c->max_total_pages * c->n_kv_heads * kPage > INT32_MAX))
+        return PCF_ERR_INVALID_ARG;
     if (c->head_dim != 64 && c->head_dim != 128) return PCF_ERR_UNSUPPORTED;
     if (kTileRows % (c->n_q_heads / c->n_kv_heads) != 0) return PCF_ERR_UNSUPPORTED;
     return PCF_OK;
@@ -74,11 +105,16 @@ inline pcf_status check_chunk_dims(const pcf_chunk_dims* c) {
 // Workspace of pcf_chunk_attention (byte offsets).  Few-row partial results: a worker's first run,
 // when the block has more of it to come, and per block the two runs it shares with its neighbours.
 struct ChunkWs {
-    size_t worker_o, block_o, block_ml, block_desc, total;
+    size_t worker_o, block_o, block_ml, block_desc;
+    // requests with more rows: rotated queries and keys, the two runs a block shares with its neighbours
+    size_t q_rot, k_rot, many_o, many_ml, many_desc, total;
 };
 inline size_t chunk_align(size_t x) { return (x + 255) / 256 * 256; }
 inline int few_tiles(const pcf_chunk_dims* c) {   // 16-row tiles a warp: 1 when no request can have more
     return (int64_t)c->max_chunk * (c->n_q_heads / c->n_kv_heads) <= 16 ? 1 : 2;
+}
+inline bool any_many(const pcf_chunk_dims* c) {   // a request may have more than few rows
+    return (int64_t)c->max_chunk * (c->n_q_heads / c->n_kv_heads) > kFewRows;
 }
 inline ChunkWs chunk_ws(const pcf_chunk_dims* c) {
     ChunkWs w;
@@ -87,7 +123,14 @@ inline ChunkWs chunk_ws(const pcf_chunk_dims* c) {
     w.block_o = chunk_align(w.worker_o + blocks * kFewWarps * rows * d * 4);
     w.block_ml = chunk_align(w.block_o + blocks * 2 * rows * d * 4);
     w.block_desc = chunk_align(w.block_ml + blocks * 2 * rows * 8);
-    w.total = chunk_align(w.block_desc + blocks * 16);
+    w.q_rot = chunk_align(w.block_desc + blocks * 16);
+    w.total = w.k_rot = w.many_o = w.many_ml = w.many_desc = w.q_rot;
+    if (!any_many(c)) return w;
+    w.k_rot = chunk_align(w.q_rot + (size_t)c->max_rows * c->n_q_heads * d * 2);
+    w.many_o = chunk_align(w.k_rot + (size_t)c->max_total_pages * kPage * c->n_kv_heads * d * 2);
+    w.many_ml = chunk_align(w.many_o + blocks * 2 * 256 * d * 4);
+    w.many_desc = chunk_align(w.many_ml + blocks * 2 * 256 * 8);
+    w.total = chunk_align(w.many_desc + blocks * 16);
     return w;
 }
 

@@ -21,7 +21,7 @@ struct TablesParams {
     int32_t* seq_out;          // [n], may be seq
     int32_t* head_out;         // [1], may be free_head
     int32_t* plan;
-    int32_t n, max_pages, max_rows, max_chunk, max_total_pages, n_phys, max_pos, n_free, hq, hkv, d, workers;
+    int32_t n, max_pages, max_rows, max_chunk, max_total_pages, n_phys, max_pos, n_free, hq, hkv, d, workers, blocks;
 };
 
 constexpr int kTablesThreads = 1024;
@@ -33,13 +33,23 @@ constexpr int kTablesThreads = 1024;
 // block scan of per-thread sums is enough for any batch size.
 // (Sums of refused lengths may be as large as 4096 x 2^22: they stop at 2^29, above every limit.)
 constexpr int kSumLimit = 1 << 29;
-constexpr int kSums = 4;   // rows, pages taken, pages held afterwards, few-row units
+constexpr int kSums = 6;   // rows, pages taken, pages held afterwards, few-row units, key tiles and pages of the others
 __device__ __forceinline__ int32_t pages_of(int32_t tokens) { return (tokens + kPage - 1) / kPage; }
 __device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) { return min(a + b, kSumLimit); }
 
-// (page, kv head) units of a request with few rows, 0 for any other
-__device__ __forceinline__ int32_t few_units(const TablesParams& p, int32_t s, int32_t n) {
-    return n > 0 && (int64_t)n * (p.hq / p.hkv) <= kFewRows ? pages_of(s + n) * p.hkv : 0;
+// A request's work in the attention: (page, kv head) units with few rows, else the key tiles all its
+// row pairs visit (every kv head) and its pages.
+struct ChunkWork {
+    int32_t few, many, pages;
+};
+__device__ __forceinline__ ChunkWork chunk_work(const TablesParams& p, int32_t s, int32_t n) {
+    const int g = p.hq / p.hkv;
+    const int32_t pages = pages_of(s + n);
+    if (n == 0) return {0, 0, 0};
+    if ((int64_t)n * g <= kFewRows) return {pages * p.hkv, 0, 0};
+    const int tpp = 2 * kTileRows / g, last = many_pairs(n, tpp) - 1;
+    const int64_t tiles = (many_before(s, tpp, last) + many_tiles(s, n, tpp, last)) * p.hkv;
+    return {0, (int32_t)min(tiles, (int64_t)kSumLimit), pages};
 }
 
 __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const TablesParams p) {
@@ -56,6 +66,8 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
     int32_t* o_take = plan + plan_array(CA_TAKE, p.n);
     int32_t* o_start = plan + plan_array(CA_START, p.n);
     int32_t* o_few = plan + plan_array(CA_FEW, p.n);
+    int32_t* o_many = plan + plan_array(CA_MANY, p.n);
+    int32_t* o_kpage = plan + plan_array(CA_KPAGE, p.n);
     const int32_t head = p.free_head[0];
     bool bad = head < 0 || head > p.n_free;
     int sum[kSums] = {};
@@ -82,7 +94,10 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         sum[0] = sat_add(sum[0], n);
         sum[1] = sat_add(sum[1], after - before);
         sum[2] = sat_add(sum[2], after);
-        sum[3] = sat_add(sum[3], few_units(p, s, n));
+        const ChunkWork work = chunk_work(p, s, n);
+        sum[3] = sat_add(sum[3], work.few);
+        sum[4] = sat_add(sum[4], work.many);
+        sum[5] = sat_add(sum[5], work.pages);
         o_seq[b] = s;
         o_new[b] = n;
         o_start[b] = start;
@@ -117,7 +132,8 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         tot[i] = s_warp[i][31];
         pre[i] += (warp ? s_warp[i][warp - 1] : 0) - sum[i];
     }
-    bad = any_bad || tot[0] > p.max_rows || tot[2] > p.max_total_pages || tot[1] > p.n_free - head || tot[3] >= kSumLimit;
+    bad = any_bad || tot[0] > p.max_rows || tot[2] > p.max_total_pages || tot[1] > p.n_free - head || tot[3] >= kSumLimit ||
+          tot[4] >= kSumLimit;
     if (!bad) {   // the pages about to be taken exist
         bool out = false;
         for (int i = tid; i < tot[1]; i += kTablesThreads) {
@@ -127,7 +143,7 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         bad = out;
     }
     bad = __syncthreads_or(bad);
-    int32_t row = pre[0], take = pre[1], few = pre[3];
+    int32_t row = pre[0], take = pre[1], few = pre[3], many = pre[4], kpage = pre[5];
     for (int b = b0; b < b1; ++b) {
         if (bad) {
             o_seq[b] = p.seq[b];
@@ -137,8 +153,13 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         o_row[b] = bad ? 0 : row;
         o_take[b] = bad ? 0 : take;
         o_few[b] = bad ? 0 : few;
+        o_many[b] = bad ? 0 : many;
+        o_kpage[b] = bad ? 0 : kpage;
         if (!bad) {
-            few += few_units(p, o_seq[b], o_new[b]);
+            const ChunkWork work = chunk_work(p, o_seq[b], o_new[b]);
+            few += work.few;
+            many += work.many;
+            kpage += work.pages;
             row += o_new[b];
             take += pages_of(o_seq[b] + o_new[b]) - pages_of(o_seq[b]);
         }
@@ -160,6 +181,9 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         o_row[p.n] = bad ? 0 : tot[0];
         o_take[p.n] = bad ? 0 : tot[1];
         o_few[p.n] = bad ? 0 : tot[3];
+        o_many[p.n] = bad ? 0 : tot[4];
+        o_kpage[p.n] = bad ? 0 : tot[5];
+        plan[C_BLOCKS] = p.blocks;
         plan[C_WORKERS] = p.workers;
         if (bad) set_dev_error(kDevErrBounds);
     }
@@ -222,6 +246,32 @@ __global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const TablesPa
             e.z = local % f.x;
         }
         int4* dst = reinterpret_cast<int4*>(p.plan + plan_starts(p.n)) + 2 * w;
+        dst[0] = e;
+        dst[1] = f;
+    }
+    // the others' key tiles, in (request, kv head, row pair, tile) order, dealt to the blocks
+    const int32_t* many = plan + plan_array(CA_MANY, p.n);
+    const int64_t tiles = many[p.n], on = few_active(tiles, p.blocks);
+    const int g = p.hq / p.hkv, tpp = 2 * kTileRows / g;
+    for (int32_t w = i; w < p.blocks; w += step) {
+        const int64_t u0 = w < on ? w * tiles / on : 0, u1 = w < on ? (w + 1) * tiles / on : 0;
+        int4 e = make_int4(0, 0, 0, 0), f = make_int4((int)(u1 - u0), 0, 0, 0);
+        if (f.x > 0) {
+            const int b = row_request(many, p.n, (int32_t)u0);
+            const int32_t per = (many[b + 1] - many[b]) / p.hkv;
+            int32_t local = (int32_t)u0 - many[b];
+            e.x = b;
+            e.y = local / per;
+            local %= per;
+            int lo = 0, hi = many_pairs(add[b], tpp) - 1;   // the pair the tile falls into
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (many_before(seq[b], tpp, mid) <= local) lo = mid; else hi = mid - 1;
+            }
+            e.z = lo;
+            e.w = local - (int32_t)many_before(seq[b], tpp, lo);
+        }
+        int4* dst = reinterpret_cast<int4*>(p.plan + plan_many(p.n, p.workers)) + 2 * w;
         dst[0] = e;
         dst[1] = f;
     }

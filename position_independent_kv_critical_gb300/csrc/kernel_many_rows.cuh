@@ -1,0 +1,719 @@
+// Attention of requests with more than a few new rows (prompt chunks) over their pages.
+//
+// The same sums as kernel_few_rows.cuh; here a key meets up to thousands of rows, so the tensor cores
+// bound it.  Two launches: chunk_rotate_kernel rotates the chunk's queries and, once, the keys of the
+// requests' pages into the workspace (fp16, slot order, slots that take no part zeroed); a key tile is
+// visited by every pair of row tiles of its request, and rotating it at each visit costs more than
+// writing and re-reading it once (the page-reading fused attention of this library, which does rotate
+// in the kernel, takes twice as long).  The values stay in the pool: many_rows_kernel copies a key
+// tile's eight pages straight from it.
+//
+// many_rows_kernel: one block an SM; a run is two 128-row tiles A and B of one (request, kv head) --
+// row m of a tile is token m / g, query head m % g of the kv head -- against the 128-key tiles its last
+// row sees.  All runs' key tiles, in (request, kv head, row pair, tile) order, are dealt to the blocks
+// in equal contiguous parts by pcf_chunk_tables, whatever the lengths; a block passes on what it has of
+// the runs it shares with its neighbours (two at most) and many_join_kernel adds those up in a fixed
+// order.
+//   warps 0-3   softmax of tile A, warps 4-7 of tile B: S row from TMEM, causal cut and exclusion bits,
+//               online softmax (lazy rescale), P -> TMEM over the S columns, O epilogue
+//   warps 8/11  Q K^T issue for tile A / B (warp 8 also owns the TMEM allocation)
+//   warps 12/13 P V issue for tile A / B
+//   warp  9     runs in order, Q and K tiles (TMA), exclusion bits of a tile
+//   warp  10    V tiles: a page and half per TMA copy; rows of slots that hold nothing are zeroed
+// A key tile is worked in two 64-key halves, S double-buffered per row tile: P(q) V runs, then Q K(q+2)
+// goes into the buffer P(q) came from, while the softmax works on S(q+1).  TMEM: tile t's S halves at
+// columns t*128 + {0, 64}, O_A at 256, O_B at 384; P (bf16 pairs) overwrites the S half it came from and
+// is the A operand of O += P V (M = 128, N = d, K = 64 keys).
+#pragma once
+#include "chunk_format.h"
+#include "kernel_attn.cuh"
+#include "kernel_chunk_tables.cuh"
+#include "ptx.cuh"
+
+namespace pcf {
+
+// ------------------------------------------------------------------ rotation
+// A block takes 16 rows at a time: a page of a request (every kv head) or 16 rows of the chunk (every
+// query head).  Thread (r, c) turns the 16-byte chunks c and c + d/16 of row r, at one angle for all
+// heads, so the table is read once a row; four heads' loads are in flight a thread.  Bound by HBM (reads
+// the keys, writes them once).
+struct RotateParams {
+    const int32_t* plan;
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* k_pool;
+    const int32_t* block_table;
+    const int32_t* page_pos;
+    const uint16_t* excl;
+    const int32_t* row_pos;
+    const float* rope;
+    __half* q_rot;              // [Hkv][max_rows][g][D], scaled by log2(e) / sqrt(d)
+    __half* k_rot;              // [Hkv][pages][16][D]
+    int64_t q_stride;
+    int32_t n, max_pages, max_rows, hq, hkv, n_phys, max_pos, workers, total_pages;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) chunk_rotate_kernel(const RotateParams p) {
+    constexpr int CPR = D / 16;
+    constexpr int LANES = 256 / (kPage * CPR);   // heads side by side
+    grid_dep_wait();
+    grid_dep_launch();
+    if (!plan_fits(p.plan, p.n, p.max_pages, p.max_rows, p.hq, p.hkv, p.workers)) return;
+    const int32_t* seq = p.plan + plan_array(CA_SEQ, p.n);
+    const int32_t* add = p.plan + plan_array(CA_NEW, p.n);
+    const int32_t* kpage = p.plan + plan_array(CA_KPAGE, p.n);
+    const int32_t rows = p.plan[C_ROWS], pages = kpage[p.n];
+    if (pages == 0) return;      // no request with many rows
+    const int c = threadIdx.x % CPR, r = threadIdx.x / CPR % kPage, h0 = threadIdx.x / (CPR * kPage);
+    const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
+    const int q_blocks = (rows + kPage - 1) / kPage;
+    float big = 0.f;
+    for (int t = blockIdx.x; t < pages + q_blocks; t += gridDim.x) {
+        const bool is_k = t < pages;
+        const __nv_bfloat16* src = nullptr;      // row of head 0
+        int64_t src_head, dst_head = 0;
+        __half* dst = nullptr;
+        int32_t pos = 0;
+        bool have = true;                        // else zeros
+        int heads;
+        float scale = 1.f;
+        if (is_k) {
+            const int b = row_request(kpage, p.n, t);
+            const int pg = t - kpage[b];
+            const int64_t e = (int64_t)b * p.max_pages + pg;
+            const int32_t ph = p.block_table[e], pp = p.page_pos[e];
+            const uint32_t ex = p.excl ? p.excl[e] : 0u;
+            have = !(ex >> r & 1u) && pg * kPage + r < seq[b] + add[b];
+            if (ph < 0 || ph >= p.n_phys || pp < 0 || pp > p.max_pos - kPage) {
+                set_dev_error(kDevErrBounds);
+                have = false;
+            }
+            pos = pp + r;
+            heads = p.hkv;
+            src = p.k_pool + ((int64_t)ph * p.hkv * kPage + r) * D;
+            src_head = kPage * D;
+            dst = p.k_rot + ((int64_t)t * kPage + r) * D;
+            dst_head = (int64_t)p.total_pages * kPage * D;
+        } else {
+            const int32_t row = (t - pages) * kPage + r;
+            if (row >= rows) continue;
+            pos = p.row_pos[row];
+            if (pos < 0 || pos >= p.max_pos) {
+                set_dev_error(kDevErrBounds);
+                have = false;
+            }
+            heads = p.hq;
+            src = p.q + row * p.q_stride;
+            src_head = D;
+            dst = p.q_rot + (int64_t)row * g * D;
+            scale = 1.4426950408889634f * (D == 128 ? 0.08838834764831845f : 0.125f);   // log2(e) / sqrt(d)
+        }
+        float4 cs[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            cs[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (have) cs[e] = reinterpret_cast<const float4*>(p.rope + (int64_t)pos * D + 16 * c)[e];
+            cs[e].x *= scale;
+            cs[e].y *= scale;
+            cs[e].z *= scale;
+            cs[e].w *= scale;
+        }
+        for (int h = h0; h < heads; h += 4 * LANES) {
+            uint4 lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+                if (have && h + i * LANES < heads) {
+                    const __nv_bfloat16* x = src + (h + i * LANES) * src_head;
+                    lo[i] = *reinterpret_cast<const uint4*>(x + 8 * c);
+                    hi[i] = *reinterpret_cast<const uint4*>(x + D / 2 + 8 * c);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int hh = h + i * LANES;
+                if (hh >= heads) break;
+                const uint32_t ia[4] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w}, ib[4] = {hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+                uint32_t oa[4], ob[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a0 = bf16_lo(ia[e]), a1 = bf16_hi(ia[e]), b0 = bf16_lo(ib[e]), b1 = bf16_hi(ib[e]);
+                    oa[e] = pack_f16x2_track(fmaf(a0, cs[e].x, -b0 * cs[e].y), fmaf(a1, cs[e].z, -b1 * cs[e].w), big);
+                    ob[e] = pack_f16x2_track(fmaf(b0, cs[e].x, a0 * cs[e].y), fmaf(b1, cs[e].z, a1 * cs[e].w), big);
+                }
+                __half* o = is_k ? dst + hh * dst_head
+                                 : dst + (int64_t)(hh >> gs) * p.max_rows * g * D + (hh & (g - 1)) * D;
+                *reinterpret_cast<uint4*>(o + 8 * c) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+                *reinterpret_cast<uint4*>(o + D / 2 + 8 * c) = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+            }
+        }
+    }
+    if (!(big < kF16Limit)) set_dev_error(kDevErrRange);
+}
+
+// ------------------------------------------------------------------ attention
+struct ManyParams {
+    const int32_t* plan;
+    const int32_t* block_table;
+    const uint16_t* excl;       // or null
+    __nv_bfloat16* out;
+    float* part_o;              // [blocks][2][256][D]
+    float2* part_ml;            // [blocks][2][256]
+    int4* desc;                 // [blocks]: a run begun here that goes on: {last block << 8 | 255, request, kv head, pair}
+    int32_t n, max_pages, max_rows, hq, hkv, n_phys, workers, blocks, total_pages;
+};
+
+constexpr int kManyThreads = 448;
+constexpr int kPairRows = 2 * kTileRows;
+
+// One run, or the part of one this block has, as warp 9 hands it to the others.
+struct ManyItem {
+    int32_t req;                // < 0: no more
+    int32_t kvh, pair;
+    int32_t jb, n_loc;          // its key tiles
+    int32_t seq, add, row_base, kpage;
+    int32_t slot;               // partial result, or -1: the whole run
+    int32_t pad[2];
+};
+
+template <int D>
+struct ManySmem {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kQ = kTileRows * D * 2;
+    static constexpr int kK = kTileKeys * D * 2;
+    static constexpr int oK = 2 * kQ;
+    static constexpr int oV = oK + 2 * kK;
+    static constexpr int oMask = oV + 2 * kK;          // [2 stages] 128 exclusion bits
+    static constexpr int oBar = oMask + 2 * 16;
+    static constexpr int kNumBars = 48;
+    static constexpr int oMisc = oBar + kNumBars * 8;
+    static constexpr int oItem = oMisc + 64;
+    static constexpr int kBytes = oItem + 2 * (int)sizeof(ManyItem);
+    static constexpr int kAlloc = kBytes + 1024;
+    static_assert(kAlloc <= 232448, "more dynamic shared memory than a GB300 block can have");
+};
+
+enum : int {
+    MB_Q_FULL = 0, MB_Q_EMPTY = 1,
+    MB_K_FULL = 2,      // [2]
+    MB_K_EMPTY = 4,     // [2] both Q K^T that read the stage are done
+    MB_V_FULL = 6,      // [2] the V tile is ready to be read
+    MB_V_RAW = 8,       // [2] the copy of a V tile with rows to be zeroed landed
+    MB_V_EMPTY = 10,    // [2]
+    MB_M_FULL = 12,     // [2] the tile's exclusion bits (only where the call has them)
+    MB_M_EMPTY = 14,    // [2] both softmax groups have read them
+    MB_S_FULL = 16,     // [4] per (row tile, S half)
+    MB_P_FULL = 20,     // [4]
+    MB_PV_DONE = 24,    // [4]
+    MB_O_DONE = 28,     // [2]
+    MB_O_FREE = 30,     // [2]
+    MB_DRAIN = 32,      // [4]
+    MB_ITEM_FULL = 36,  // [2]
+    MB_ITEM_EMPTY = 38  // [2]
+};
+
+template <int D>
+__global__ void __launch_bounds__(kManyThreads)
+many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const ManyParams prm) {
+    using SM = ManySmem<D>;
+    constexpr int H = SM::kHalves;
+    constexpr int kReaders = 13;   // softmax warps, issuers, V producer
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    auto sQ = [&](int t) { return smem + t * SM::kQ; };
+    auto sK = [&](int st) { return smem + SM::oK + st * SM::kK; };
+    auto sV = [&](int st) { return smem + SM::oV + st * SM::kK; };
+    uint16_t* s_mask = reinterpret_cast<uint16_t*>(smem + SM::oMask);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::oBar);
+    int32_t* misc = reinterpret_cast<int32_t*>(smem + SM::oMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
+    ManyItem* slots = reinterpret_cast<ManyItem*>(smem + SM::oItem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        mbar_init(&bars[MB_Q_FULL], 1);
+        mbar_init(&bars[MB_Q_EMPTY], 2);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars[MB_K_FULL + s], 1);
+            mbar_init(&bars[MB_K_EMPTY + s], 2);
+            mbar_init(&bars[MB_V_FULL + s], 1);
+            mbar_init(&bars[MB_V_RAW + s], 1);
+            mbar_init(&bars[MB_V_EMPTY + s], 2);
+            mbar_init(&bars[MB_M_FULL + s], 1);
+            mbar_init(&bars[MB_M_EMPTY + s], 8);
+            mbar_init(&bars[MB_O_DONE + s], 1);
+            mbar_init(&bars[MB_O_FREE + s], 128);
+            mbar_init(&bars[MB_ITEM_FULL + s], 1);
+            mbar_init(&bars[MB_ITEM_EMPTY + s], kReaders);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bars[MB_S_FULL + i], 1);
+            mbar_init(&bars[MB_P_FULL + i], 128);
+            mbar_init(&bars[MB_PV_DONE + i], 1);
+            mbar_init(&bars[MB_DRAIN + i], 1);
+        }
+        fence_mbar_init();
+        misc[4] = 0;
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    grid_dep_wait();
+    grid_dep_launch();
+    if (warp == kWarpMma) {
+        tmem_alloc(reinterpret_cast<uint32_t*>(misc), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+
+    const int32_t* plan = prm.plan;
+    const int g = prm.hq / prm.hkv, gs = __ffs(g) - 1;
+    const int tpt = kTileRows >> gs, tpp = 2 * tpt;      // tokens of a row tile, of a pair
+    const bool masked = prm.excl != nullptr;
+
+    auto take_item = [&](int it, ManyItem& w) -> bool {
+        if (!mbar_wait(&bars[MB_ITEM_FULL + (it & 1)], (it >> 1) & 1, abort_flag)) return false;
+        w = slots[it & 1];
+        return true;
+    };
+
+    if (warp == kWarpTma) {
+        // ------------------------------------------------------------ runs, Q and K tiles
+        const int32_t* seq = plan + plan_array(CA_SEQ, prm.n);
+        const int32_t* add = plan + plan_array(CA_NEW, prm.n);
+        const int32_t* row = plan + plan_array(CA_ROW, prm.n);
+        const int32_t* many = plan + plan_array(CA_MANY, prm.n);
+        const int32_t* kpage = plan + plan_array(CA_KPAGE, prm.n);
+        const bool fits = plan_fits(plan, prm.n, prm.max_pages, prm.max_rows, prm.hq, prm.hkv, prm.workers) &&
+                          plan[C_BLOCKS] == prm.blocks;
+        const int4* st = reinterpret_cast<const int4*>(plan + plan_many(prm.n, prm.workers)) + 2 * blockIdx.x;
+        const int4 start = st[0];
+        int left = fits ? st[1].x : 0;
+        int32_t req = start.x, kvh = start.y, pair = start.z, tile = start.w;
+        int kc = 0, last_k[2] = {-1, -1}, last_q = -1;
+        bool ok = true;
+        int4 desc = make_int4(0, 0, 0, 0);
+        for (int it = 0; ok; ++it) {
+            ManyItem w;
+            w.req = left > 0 ? req : -1;
+            w.kvh = kvh;
+            w.pair = pair;
+            w.jb = tile;
+            w.n_loc = w.seq = w.add = w.row_base = w.kpage = 0;
+            w.slot = -1;
+            w.pad[0] = w.pad[1] = 0;
+            if (left > 0) {
+                w.seq = seq[req];
+                w.add = add[req];
+                w.row_base = row[req];
+                w.kpage = kpage[req];
+                const int all = many_tiles(w.seq, w.add, tpp, pair);
+                w.n_loc = min(all - tile, left);
+                left -= w.n_loc;
+                if (w.n_loc < all) w.slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);
+                if (tile == 0 && w.n_loc < all) {
+                    // the block that holds the run's last tile (block b's part begins at b * U / B)
+                    const int64_t units = many[prm.n], on = few_active(units, prm.blocks);
+                    const int64_t u = many[req] + (int64_t)kvh * ((many[req + 1] - many[req]) / prm.hkv) +
+                                      many_before(w.seq, tpp, pair) + all - 1;
+                    desc = make_int4((int)(((u + 1) * on - 1) / units) << 8 | 0xFF, req, kvh, pair);
+                }
+            }
+            if (lane == 0) {
+                ok = it < 2 || mbar_wait(&bars[MB_ITEM_EMPTY + (it & 1)], ((it >> 1) - 1) & 1, abort_flag);
+                if (ok) {
+                    slots[it & 1] = w;
+                    mbar_arrive(&bars[MB_ITEM_FULL + (it & 1)]);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok || w.req < 0) break;
+            if (lane == 0) {
+                const int32_t qy = (w.kvh * prm.max_rows + w.row_base + w.pair * tpp) * g;
+                if (it > 0) ok = mbar_wait(&bars[MB_Q_EMPTY], (it - 1) & 1, abort_flag);
+                if (ok) {
+                    mbar_arrive_expect_tx(&bars[MB_Q_FULL], 2 * SM::kQ);
+                    for (int t = 0; t < 2; ++t)
+                        for (int hb = 0; hb < H; ++hb)
+                            tma_load_2d(sQ(t) + hb * 16384, &tm_q, &bars[MB_Q_FULL], hb * 64, qy + t * kTileRows);
+                    last_q = it;
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            const uint16_t* ex = masked ? prm.excl + (int64_t)w.req * prm.max_pages : nullptr;
+            for (int jj = 0; jj < w.n_loc; ++jj, ++kc) {
+                const int j = w.jb + jj, ks = kc & 1;
+                uint32_t bits = 0;
+                if (masked && lane < kPagesPerTile) {
+                    const int pg = j * kPagesPerTile + lane;
+                    if (pg < prm.max_pages) bits = ex[pg];
+                }
+                if (lane == 0) {
+                    ok = kc < 2 || mbar_wait(&bars[MB_K_EMPTY + ks], ((kc >> 1) - 1) & 1, abort_flag);
+                    if (ok) {
+                        mbar_arrive_expect_tx(&bars[MB_K_FULL + ks], H * 16384);
+                        const int32_t y = w.kvh * prm.total_pages * kPage + w.kpage * kPage + j * kTileKeys;
+                        for (int hb = 0; hb < H; ++hb)
+                            tma_load_2d(sK(ks) + hb * 16384, &tm_k, &bars[MB_K_FULL + ks], hb * 64, y);
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                last_k[ks] = kc;
+                if (masked) {
+                    ok = kc < 2 || mbar_wait(&bars[MB_M_EMPTY + ks], ((kc >> 1) - 1) & 1, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    if (lane < kPagesPerTile) s_mask[ks * 8 + lane] = (uint16_t)bits;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[MB_M_FULL + ks]);
+                }
+            }
+            // the next run
+            tile = 0;
+            if (w.jb + w.n_loc == many_tiles(w.seq, w.add, tpp, pair) && ++pair == many_pairs(w.add, tpp)) {
+                pair = 0;
+                if (++kvh == prm.hkv) {
+                    kvh = 0;
+                    do { ++req; } while (req < prm.n && many[req + 1] == many[req]);
+                }
+            }
+        }
+        if (lane == 0) {
+            prm.desc[blockIdx.x] = ok ? desc : make_int4(0, 0, 0, 0);
+            if (last_q >= 0) mbar_drain(&bars[MB_Q_FULL], last_q & 1);
+            for (int s = 0; s < 2; ++s)
+                if (last_k[s] >= 0) mbar_drain(&bars[MB_K_FULL + s], (last_k[s] >> 1) & 1);
+        }
+    } else if (warp == kWarpTmaV) {
+        // ------------------------------------------------------------ V tiles
+        // Lane 8 hb + m copies half hb of page m of the tile (a page behind the last one repeats it).
+        // A tile with slots that take no part for any row -- excluded, or behind the last token --
+        // lands on a barrier of this warp, which zeroes their rows (they may hold anything, and a
+        // weight of zero does not silence a NaN) before it hands the tile on.
+        int vc = 0, raw_n[2] = {0, 0};
+        int last_v[2] = {-1, -1};        // last copy that landed on V_FULL itself
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            ManyItem w;
+            ok = take_item(it, w);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[MB_ITEM_EMPTY + (it & 1)]);
+            if (w.req < 0) break;
+            const int n_slots = w.seq + w.add, n_pages = pages_of(n_slots);
+            const int32_t* table = prm.block_table + (int64_t)w.req * prm.max_pages;
+            const uint16_t* ex = masked ? prm.excl + (int64_t)w.req * prm.max_pages : nullptr;
+            const int m = lane % kPagesPerTile, hb = lane / kPagesPerTile;
+            int32_t ph_n = 0;
+            uint32_t gone_n = 0;
+            auto meta = [&](int j) {     // page m of tile j: its physical page, its slots without a part
+                const int pg = j * kPagesPerTile + m;
+                ph_n = table[min(pg, n_pages - 1)];
+                const int have = min(max(n_slots - pg * kPage, 0), kPage);
+                gone_n = 0xFFFFu & ~((1u << have) - 1u);
+                if (ph_n < 0 || ph_n >= prm.n_phys) {    // (reported by the rotation; finite data instead)
+                    ph_n = 0;
+                    gone_n = 0xFFFFu;
+                }
+                if (masked && pg < n_pages) gone_n |= ex[pg];
+            };
+            meta(w.jb);
+            for (int jj = 0; jj < w.n_loc; ++jj, ++vc) {
+                const int vs = vc & 1;
+                const int32_t ph = ph_n;
+                const uint32_t gone = gone_n;
+                const bool dirty = __any_sync(0xffffffffu, gone != 0u);
+                uint64_t* bar = &bars[(dirty ? MB_V_RAW : MB_V_FULL) + vs];
+                if (lane == 0) {
+                    ok = vc < 2 || mbar_wait(&bars[MB_V_EMPTY + vs], ((vc >> 1) - 1) & 1, abort_flag);
+                    if (ok) mbar_arrive_expect_tx(bar, H * 16384);
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                if (lane < kPagesPerTile * H)
+                    tma_load_2d(sV(vs) + hb * 16384 + m * (kPage * 128), &tm_v, bar, hb * 64,
+                                (ph * prm.hkv + w.kvh) * kPage);
+                if (jj + 1 < w.n_loc) meta(w.jb + jj + 1);
+                if (!dirty) {
+                    last_v[vs] = vc;
+                } else {
+                    ok = mbar_wait(bar, raw_n[vs] & 1, abort_flag);
+                    ++raw_n[vs];
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    // lanes m, m + 8, m + 16, m + 24 share page m's rows
+                    for (uint32_t rest = gone; rest != 0u; rest &= rest - 1u) {
+                        const int r = m * kPage + __ffs(rest) - 1;
+                        for (int ch = lane / kPagesPerTile; ch < D / 8; ch += 32 / kPagesPerTile)
+                            *reinterpret_cast<uint4*>(sV(vs) + (ch >> 3) * 16384 + sw128_off(r, ch & 7)) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[MB_V_FULL + vs]);
+                }
+            }
+        }
+        if (lane == 0) {
+            for (int s = 0; s < 2; ++s) {
+                if (last_v[s] >= 0 && last_v[s] >= vc - 2) mbar_drain(&bars[MB_V_FULL + s], (last_v[s] >> 1) & 1);
+                if (!ok && raw_n[s] > 0) mbar_drain(&bars[MB_V_RAW + s], (raw_n[s] - 1) & 1);
+            }
+        }
+    } else if (warp >= kWarpMma) {
+        // ------------------------------------------------------------ MMA issuers (8, 11: Q K^T; 12, 13: P V)
+        const bool qk_role = warp == kWarpMma || warp == kWarpMmaB;
+        const int t = (warp == kWarpMma || warp == kWarpPvA) ? 0 : 1;
+        const uint32_t leader = lane == 0 ? 1u : 0u;
+        int hq = 0, kc = 0;
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            ManyItem w;
+            ok = __all_sync(0xffffffffu, take_item(it, w));
+            if (!ok) break;
+            __syncwarp();
+            if (leader) mbar_arrive(&bars[MB_ITEM_EMPTY + (it & 1)]);
+            if (w.req < 0) break;
+            const int nq = 2 * w.n_loc;
+            if (qk_role) {
+                constexpr uint32_t idesc_qk = idesc_f16(128, 64);
+                const uint32_t aQ = desc_sw128_lo(smem_u32(sQ(t)), 16);
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars[MB_Q_FULL], it & 1, abort_flag));
+                for (int q = 0; ok && q < nq; ++q) {
+                    const int hg = hq + q, kt = kc + (q >> 1), h = q & 1;
+                    ok = __all_sync(0xffffffffu,
+                                    (h == 1 || mbar_wait(&bars[MB_K_FULL + (kt & 1)], (kt >> 1) & 1, abort_flag)) &&
+                                        (hg < 2 || mbar_wait(&bars[MB_PV_DONE + 2 * t + (hg & 1)],
+                                                             ((hg - 2) >> 1) & 1, abort_flag)));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t aK = desc_sw128_lo(smem_u32(sK(kt & 1)) + h * 64 * 128, 16);
+                    const uint32_t tS = tmem + t * 128 + (hg & 1) * 64;
+#pragma unroll
+                    for (int k4 = 0; k4 < D / 64; ++k4)
+                        mma_ss_k4(leader, tS, aQ + k4 * 1024, aK + k4 * 1024, kDescSw128Hi, idesc_qk, k4 > 0 ? 1u : 0u);
+                    mma_commit_by(leader, &bars[MB_S_FULL + 2 * t + (hg & 1)]);
+                    if (h == 1) mma_commit_by(leader, &bars[MB_K_EMPTY + (kt & 1)]);
+                }
+                if (ok) mma_commit_by(leader, &bars[MB_Q_EMPTY]);
+            } else {
+                constexpr uint32_t idesc_pv = idesc_bf16(128, D, true);
+                const uint32_t tO = tmem + kTmemO + t * 128;
+                for (int q = 0; ok && q < nq; ++q) {
+                    const int hg = hq + q, kt = kc + (q >> 1), h = q & 1;
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&bars[MB_P_FULL + 2 * t + (hg & 1)], (hg >> 1) & 1, abort_flag) &&
+                                        (h == 1 || mbar_wait(&bars[MB_V_FULL + (kt & 1)], (kt >> 1) & 1, abort_flag)) &&
+                                        (q > 0 || it == 0 ||
+                                         mbar_wait(&bars[MB_O_FREE + t], (it - 1) & 1, abort_flag)));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t aV = desc_sw128_lo(smem_u32(sV(kt & 1)) + h * 64 * 128, 16384);
+                    const uint32_t tP = tmem + t * 128 + (hg & 1) * 64;
+                    mma_ts_k4(leader, tO, tP, aV, kDescSw128Hi, idesc_pv, q > 0 ? 1u : 0u);
+                    mma_commit_by(leader, &bars[MB_PV_DONE + 2 * t + (hg & 1)]);
+                    if (h == 1) mma_commit_by(leader, &bars[MB_V_EMPTY + (kt & 1)]);
+                }
+                if (ok) mma_commit_by(leader, &bars[MB_O_DONE + t]);
+            }
+            hq += nq;
+            kc += w.n_loc;
+        }
+        const int di = (qk_role ? 0 : 2) + t;
+        mma_commit_by(leader, &bars[MB_DRAIN + di]);
+        if (leader) mbar_drain(&bars[MB_DRAIN + di], 0);
+    } else {
+        // ------------------------------------------------------------ softmax (warps 0-7)
+        const int t = warp >> 2;
+        const int m = tid - t * 128;                       // row of the tile = TMEM lane
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tO = tmem + lane_addr + kTmemO + t * 128;
+        int hq = 0, kc = 0;
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            ManyItem w;
+            ok = take_item(it, w);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[MB_ITEM_EMPTY + (it & 1)]);
+            if (w.req < 0) break;
+            const int tok = w.pair * tpp + t * tpt + (m >> gs);
+            const bool valid = tok < w.add;
+            const int limit = w.seq + min(tok, w.add - 1) + 1;   // slots the row sees
+            float m_run = -INFINITY, l_run = 0.f;
+            const int nq = 2 * w.n_loc;
+            uint4 mask = make_uint4(0, 0, 0, 0);
+            for (int q = 0; q < nq; ++q) {
+                const int hg = hq + q, h = q & 1, ks = (kc + (q >> 1)) & 1;
+                const uint32_t tS = tmem + lane_addr + t * 128 + (hg & 1) * 64;
+                ok = mbar_wait(&bars[MB_S_FULL + 2 * t + (hg & 1)], (hg >> 1) & 1, abort_flag);
+                if (masked && h == 0) ok = ok && mbar_wait(&bars[MB_M_FULL + ks], ((kc + (q >> 1)) >> 1) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                tc_fence_after();
+                if (masked && h == 0) {
+                    mask = *reinterpret_cast<const uint4*>(s_mask + ks * 8);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[MB_M_EMPTY + ks]);
+                }
+                const int cut = limit - (w.jb + (q >> 1)) * kTileKeys - 64 * h;   // the half's keys [0, cut) are seen
+                const uint32_t m0 = h ? mask.z : mask.x, m1 = h ? mask.w : mask.y;
+                const bool full = __all_sync(0xffffffffu, cut >= 64 && (m0 | m1) == 0u);
+                uint32_t sv[64];
+                tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+                tmem_ld_wait();
+                if (!full) {
+                    // keys behind the row's own token and excluded ones: score -inf
+                    const uint32_t hide0 = m0 | (cut >= 32 ? 0u : cut <= 0 ? ~0u : ~0u << cut);
+                    const uint32_t hide1 = m1 | (cut >= 64 ? 0u : cut <= 32 ? ~0u : ~0u << (cut - 32));
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        if (hide0 >> e & 1u) sv[e] = __float_as_uint(-INFINITY);
+                        if (hide1 >> e & 1u) sv[32 + e] = __float_as_uint(-INFINITY);
+                    }
+                }
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < 64; e += 8) {
+                    m4[0] = max3f(m4[0], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                    m4[1] = max3f(m4[1], __uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]));
+                    m4[2] = max3f(m4[2], __uint_as_float(sv[e + 4]), __uint_as_float(sv[e + 5]));
+                    m4[3] = max3f(m4[3], __uint_as_float(sv[e + 6]), __uint_as_float(sv[e + 7]));
+                }
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                const float m_new = fmaxf(m_run, mx);
+                const bool need = m_new > m_run + 8.0f;     // lazy rescale: keep P <= 2^8
+                const float alpha = need ? ex2(m_run - m_new) : 1.0f;
+                if (need) { l_run *= alpha; m_run = m_new; }
+                const float msub = m_run == -INFINITY ? 0.f : m_run;
+                const uint64_t negm2 = f2_pack(-msub, -msub);
+                uint64_t acc2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                uint32_t pk[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    float d0, d1;
+                    f2_unpack(f2_add(f2_pack(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), negm2), d0, d1);
+                    const float p0 = ex2(d0), p1 = ex2(d1);
+                    acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(p0, p1));
+                    pk[e] = pack_bf16x2(p0, p1);   // bf16 like the values they meet (an MMA's operands share a type)
+                }
+                tmem_st32(tS, pk);
+                float a0, a1, b0, b1;
+                f2_unpack(acc2[0], a0, a1);
+                f2_unpack(acc2[1], b0, b1);
+                l_run += (a0 + b0) + (a1 + b1);
+                if (q > 0 && __any_sync(0xffffffffu, need)) {
+                    // every earlier P V of this tile must be done before O is rescaled
+                    ok = mbar_wait(&bars[MB_PV_DONE + 2 * t + ((hg - 1) & 1)], ((hg - 1) >> 1) & 1, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + cc * 32, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st32(tO + cc * 32, o);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&bars[MB_P_FULL + 2 * t + (hg & 1)]);
+            }
+            if (!ok) break;
+            // epilogue: O / l, or the part's sums as they are
+            ok = mbar_wait(&bars[MB_O_DONE + t], it & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            tc_fence_after();
+            if (w.slot >= 0) {
+                const int64_t prow = (int64_t)w.slot * kPairRows + t * kTileRows + m;
+                if (valid) prm.part_ml[prow] = make_float2(m_run, l_run);
+#pragma unroll 1
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + cc * 32, o);
+                    tmem_ld_wait();
+                    if (valid) {
+                        float* dst = prm.part_o + prow * D + cc * 32;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4*>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+            } else {
+                const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
+#pragma unroll 1
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + cc * 32, o);
+                    tmem_ld_wait();
+                    if (valid) {
+                        __nv_bfloat16* dst = prm.out + ((int64_t)(w.row_base + tok) * prm.hq + w.kvh * g + (m & (g - 1))) * D + cc * 32;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint4 v;
+                            v.x = pack_bf16x2(__uint_as_float(o[8 * e + 0]) * inv, __uint_as_float(o[8 * e + 1]) * inv);
+                            v.y = pack_bf16x2(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv);
+                            v.z = pack_bf16x2(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv);
+                            v.w = pack_bf16x2(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv);
+                            *reinterpret_cast<uint4*>(dst + 8 * e) = v;
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&bars[MB_O_FREE + t]);
+            hq += nq;
+            kc += w.n_loc;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Blocks (j, y) add up the run that block j of many_rows_kernel began and left open, 8 rows of it each:
+// its part, then those of the blocks behind up to the run's last.
+template <int D>
+__global__ void __launch_bounds__(256) many_join_kernel(const ManyParams p) {
+    constexpr int ROWS = 256 / (D / 4);
+    grid_dep_wait();
+    grid_dep_launch();
+    const int j = blockIdx.x;
+    const int4 d = p.desc[j];
+    if (d.x == 0) return;
+    const int last = d.x >> 8;
+    const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
+    const int r = blockIdx.y * ROWS + threadIdx.x / (D / 4), f = threadIdx.x % (D / 4);
+    const int tok = d.w * (kPairRows >> gs) + (r >> gs);
+    if (tok >= p.plan[plan_array(CA_NEW, p.n) + d.y]) return;
+    float top = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = j; b <= last; ++b) {
+        const int64_t row = ((int64_t)b * 2 + (b == j ? 1 : 0)) * kPairRows + r;
+        const float2 ml = p.part_ml[row];
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + row * D + 4 * f);
+        const float now = fmaxf(top, ml.x), ref = now == -INFINITY ? 0.f : now;
+        const float old = ex2(top - ref), a = ex2(ml.x - ref);
+        top = now;
+        l = l * old + a * ml.y;
+        acc.x = acc.x * old + a * v.x;
+        acc.y = acc.y * old + a * v.y;
+        acc.z = acc.z * old + a * v.z;
+        acc.w = acc.w * old + a * v.w;
+    }
+    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const int64_t row = (int64_t)(p.plan[plan_array(CA_ROW, p.n) + d.y] + tok) * p.hq + d.z * g + (r & (g - 1));
+    *reinterpret_cast<uint2*>(p.out + row * D + 4 * f) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
+}  // namespace pcf
