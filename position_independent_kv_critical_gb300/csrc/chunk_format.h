@@ -13,21 +13,16 @@
 
 namespace pcf {
 
-constexpr int32_t kPlanMagic = 0x504B4843;   // "CHKP"
 constexpr int kMaxReqs = 4096;               // requests of one chunk batch (one block scans them)
 constexpr int32_t kMaxChunkRows = 1 << 22;   // rows of one chunk batch
 constexpr int32_t kMaxTotalPages = 1 << 26;  // pages of all requests together, repeats counted
 
 enum : int {
-    C_MAGIC = 0, C_N_REQS = 1, C_MAX_PAGES = 2, C_MAX_ROWS = 3, C_HQ = 4, C_HKV = 5, C_D = 6, C_N_PHYS = 7,
-    C_MAX_POS = 8,
-    C_ROWS = 9,       // rows of the chunk; 0 also where the lengths were refused
-    C_HEAD = 10,      // the free list's first page not taken before this chunk
-    C_TAKEN = 11,     // pages taken for the chunk
-    C_BAD = 12,       // 1: the lengths were refused and nothing was done
-    C_WORKERS = 13,   // warps the few-row requests' pages are dealt to
-    C_BLOCKS = 14,    // blocks the other requests' key tiles are dealt to
-    C_HEADER = 16
+    C_TAG = 0,        // of the dims the plan was made for (plan_tag)
+    C_ROWS = 1,       // rows of the chunk; 0 also where the lengths were refused
+    C_HEAD = 2,       // the free list's first page not taken before this chunk
+    C_TAKEN = 3,      // pages taken for the chunk
+    C_HEADER = 4
 };
 // arrays behind the header, n_reqs + 1 words each: tokens held, new tokens, first row, pages taken
 // before the request, position of its first row, and the (page, kv head) units of the requests
@@ -35,7 +30,8 @@ enum : int {
 // and, for the requests with more, the key tiles their row pairs visit and the pages they hold.
 // Behind them the work split of both kinds: kStartWords words a worker, then kManyWords a block.
 enum : int { CA_SEQ = 0, CA_NEW = 1, CA_ROW = 2, CA_TAKE = 3, CA_START = 4, CA_FEW = 5, CA_MANY = 6, CA_KPAGE = 7, CA_COUNT = 8 };
-constexpr int kStartWords = 8;   // {request, kv head, page, units; its pages, tokens held, new tokens, first row}
+// {request, kv head, page, units; its pages, tokens held, new tokens, first row; tag, 0, 0, 0}
+constexpr int kStartWords = 12;
 
 PCF_HOST_DEVICE inline int64_t plan_array(int which, int32_t n_reqs) {
     return C_HEADER + (int64_t)which * (n_reqs + 1);
@@ -43,7 +39,7 @@ PCF_HOST_DEVICE inline int64_t plan_array(int which, int32_t n_reqs) {
 PCF_HOST_DEVICE inline int64_t plan_starts(int32_t n_reqs) {
     return (plan_array(CA_COUNT, n_reqs) + 3) / 4 * 4;
 }
-constexpr int kManyWords = 8;    // {request, kv head, row pair, key tile; units}
+constexpr int kManyWords = 8;    // {request, kv head, row pair, key tile; units, tag, 0, 0}
 PCF_HOST_DEVICE inline int64_t plan_many(int32_t n_reqs, int32_t workers) {
     return plan_starts(n_reqs) + (int64_t)workers * kStartWords;
 }
@@ -70,12 +66,14 @@ PCF_HOST_DEVICE inline int64_t many_before(int32_t seq, int32_t tpp, int32_t pai
     return p * a + m * (u * (u - 1) / 2) + u * w + u * (m - v0) + (w > v0 ? w - v0 : 0);
 }
 
-// A request has few rows when its new tokens times the query heads of a kv head are at most this:
-// two 16-row tiles of mma.sync a warp.  Below, reading the pages bounds the attention (a key and
-// value of 4 d bytes meet 4 d flops a row, 32 flops a byte at most).
+// A request has few rows when its new tokens times the query heads of a kv head are at most this.
+// Reading the pages then bounds the attention (a key and value of 4 d bytes meet 4 d flops a row, 32
+// flops a byte at most).
 constexpr int kFewRows = 32;
-constexpr int kFewWarps = 8;   // warps of a block of the few-row kernel, each a worker
-
+// warps of a block of the few-row kernel, each a worker, with 1, 2 or 4 tiles of 8 rows: as many as
+// their accumulators leave registers for (twelve of 168, three a sub-partition; eight of 255, as two
+// tiles already spill with 168)
+PCF_HOST_DEVICE constexpr int few_warps(int tiles) { return tiles == 1 ? 12 : 8; }
 // Units go to the workers in equal runs, worker w from the w-th of `active` equal parts on; with
 // fewer units than workers the first ones take one each, so that a run's parts sit in few blocks.
 PCF_HOST_DEVICE inline int64_t few_active(int64_t units, int32_t workers) { return units < workers ? units : workers; }
@@ -110,17 +108,33 @@ struct ChunkWs {
     size_t q_rot, k_rot, many_o, many_ml, many_desc, total;
 };
 inline size_t chunk_align(size_t x) { return (x + 255) / 256 * 256; }
-inline int few_tiles(const pcf_chunk_dims* c) {   // 16-row tiles a warp: 1 when no request can have more
-    return (int64_t)c->max_chunk * (c->n_q_heads / c->n_kv_heads) <= 16 ? 1 : 2;
+// Most rows of a request the few-row kernel takes: 8, 16 or 32, what the dims allow.  Where some request
+// may have more than 32, so that the other kernels run anyway, only what a single token needs: more row
+// tiles a warp cost every request of the batch (twelve warps against eight).
+inline int few_limit(const pcf_chunk_dims* c) {
+    const int64_t g = c->n_q_heads / c->n_kv_heads, rows = c->max_chunk * g > kFewRows ? g : c->max_chunk * g;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : kFewRows;
 }
+inline int few_tiles(const pcf_chunk_dims* c) { return few_limit(c) / 8; }   // tiles of 8 rows a warp
+inline int few_workers(const pcf_chunk_dims* c) { return few_warps(few_tiles(c)) * chunk_sms(c->n_sms); }
+// A word the kernels compare with the plan's, so that a plan made for other dims (or by no
+// pcf_chunk_tables call at all) is refused instead of read.
+inline int32_t plan_tag(const pcf_chunk_dims* c) {
+    uint32_t h = 2166136261u;
+    for (int32_t v : {c->n_reqs, c->max_pages, c->max_rows, c->max_chunk, c->max_total_pages, c->n_q_heads, c->n_kv_heads,
+                      c->head_dim, c->n_phys_pages, c->max_pos, chunk_sms(c->n_sms)})
+        h = (h ^ (uint32_t)v) * 16777619u;
+    return (int32_t)(h | 1u);   // never 0
+}
+
 inline bool any_many(const pcf_chunk_dims* c) {   // a request may have more than few rows
     return (int64_t)c->max_chunk * (c->n_q_heads / c->n_kv_heads) > kFewRows;
 }
 inline ChunkWs chunk_ws(const pcf_chunk_dims* c) {
     ChunkWs w;
-    const size_t rows = 16 * (size_t)few_tiles(c), blocks = chunk_sms(c->n_sms), d = c->head_dim;
+    const size_t rows = 8 * (size_t)few_tiles(c), blocks = chunk_sms(c->n_sms), d = c->head_dim;
     w.worker_o = 0;
-    w.block_o = chunk_align(w.worker_o + blocks * kFewWarps * rows * d * 4);
+    w.block_o = chunk_align(w.worker_o + (size_t)few_workers(c) * rows * d * 4);
     w.block_ml = chunk_align(w.block_o + blocks * 2 * rows * d * 4);
     w.block_desc = chunk_align(w.block_ml + blocks * 2 * rows * 8);
     w.q_rot = chunk_align(w.block_desc + blocks * 16);

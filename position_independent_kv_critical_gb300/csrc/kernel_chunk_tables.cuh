@@ -21,7 +21,7 @@ struct TablesParams {
     int32_t* seq_out;          // [n], may be seq
     int32_t* head_out;         // [1], may be free_head
     int32_t* plan;
-    int32_t n, max_pages, max_rows, max_chunk, max_total_pages, n_phys, max_pos, n_free, hq, hkv, d, workers, blocks;
+    int32_t n, max_pages, max_rows, max_chunk, max_total_pages, n_phys, max_pos, n_free, hq, hkv, few_rows, workers, blocks, tag;
 };
 
 constexpr int kTablesThreads = 1024;
@@ -46,7 +46,7 @@ __device__ __forceinline__ ChunkWork chunk_work(const TablesParams& p, int32_t s
     const int g = p.hq / p.hkv;
     const int32_t pages = pages_of(s + n);
     if (n == 0) return {0, 0, 0};
-    if ((int64_t)n * g <= kFewRows) return {pages * p.hkv, 0, 0};
+    if ((int64_t)n * g <= p.few_rows) return {pages * p.hkv, 0, 0};
     const int tpp = 2 * kTileRows / g, last = many_pairs(n, tpp) - 1;
     const int64_t tiles = (many_before(s, tpp, last) + many_tiles(s, n, tpp, last)) * p.hkv;
     return {0, (int32_t)min(tiles, (int64_t)kSumLimit), pages};
@@ -165,36 +165,21 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         }
     }
     if (tid == 0) {
-        plan[C_MAGIC] = kPlanMagic;
-        plan[C_N_REQS] = p.n;
-        plan[C_MAX_PAGES] = p.max_pages;
-        plan[C_MAX_ROWS] = p.max_rows;
-        plan[C_HQ] = p.hq;
-        plan[C_HKV] = p.hkv;
-        plan[C_D] = p.d;
-        plan[C_N_PHYS] = p.n_phys;
-        plan[C_MAX_POS] = p.max_pos;
+        plan[C_TAG] = p.tag;
         plan[C_ROWS] = bad ? 0 : tot[0];
         plan[C_HEAD] = head;
         plan[C_TAKEN] = bad ? 0 : tot[1];
-        plan[C_BAD] = bad ? 1 : 0;
         o_row[p.n] = bad ? 0 : tot[0];
         o_take[p.n] = bad ? 0 : tot[1];
         o_few[p.n] = bad ? 0 : tot[3];
         o_many[p.n] = bad ? 0 : tot[4];
         o_kpage[p.n] = bad ? 0 : tot[5];
-        plan[C_BLOCKS] = p.blocks;
-        plan[C_WORKERS] = p.workers;
         if (bad) set_dev_error(kDevErrBounds);
     }
 }
 
-// The plan of another batch's dims, or of no pcf_chunk_tables call at all, is refused.
-__device__ __forceinline__ bool plan_fits(const int32_t* plan, int32_t n, int32_t max_pages, int32_t max_rows,
-                                          int32_t hq, int32_t hkv, int32_t workers) {
-    const int4 a = reinterpret_cast<const int4*>(plan)[0], b = reinterpret_cast<const int4*>(plan)[1];
-    const bool ok = a.x == kPlanMagic && a.y == n && a.z == max_pages && a.w == max_rows && b.x == hq && b.y == hkv &&
-                    plan[C_WORKERS] == workers;
+__device__ __forceinline__ bool plan_fits(const int32_t* plan, int32_t tag) {
+    const bool ok = plan[C_TAG] == tag;
     if (!ok) set_dev_error(kDevErrBounds);
     return ok;
 }
@@ -245,9 +230,10 @@ __global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const TablesPa
             e.y = local / f.x;
             e.z = local % f.x;
         }
-        int4* dst = reinterpret_cast<int4*>(p.plan + plan_starts(p.n)) + 2 * w;
+        int4* dst = reinterpret_cast<int4*>(p.plan + plan_starts(p.n)) + 3 * w;
         dst[0] = e;
         dst[1] = f;
+        dst[2] = make_int4(p.tag, 0, 0, 0);
     }
     // the others' key tiles, in (request, kv head, row pair, tile) order, dealt to the blocks
     const int32_t* many = plan + plan_array(CA_MANY, p.n);
@@ -255,7 +241,7 @@ __global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const TablesPa
     const int g = p.hq / p.hkv, tpp = 2 * kTileRows / g;
     for (int32_t w = i; w < p.blocks; w += step) {
         const int64_t u0 = w < on ? w * tiles / on : 0, u1 = w < on ? (w + 1) * tiles / on : 0;
-        int4 e = make_int4(0, 0, 0, 0), f = make_int4((int)(u1 - u0), 0, 0, 0);
+        int4 e = make_int4(0, 0, 0, 0), f = make_int4((int)(u1 - u0), p.tag, 0, 0);
         if (f.x > 0) {
             const int b = row_request(many, p.n, (int32_t)u0);
             const int32_t per = (many[b + 1] - many[b]) / p.hkv;

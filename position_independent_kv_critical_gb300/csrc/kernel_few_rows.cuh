@@ -13,17 +13,16 @@
 // TMA, 128-byte swizzled, and the cos/sin row of the page's first position), so no warp waits for
 // another and an SM has 8 x (stages - 1) units, 130 KB, on the way.
 //
-// The keys are rotated in registers: the fragment of mma.m16n8k16's B operand (k = d, n = keys)
-// that ldmatrix gives a thread holds dimensions i and i + d/2 of the same key, so a pair turns inside
-// one thread.  The angle of slot r is that of the page's first position plus r steps:
+// The keys are rotated in registers: the fragments of mma.m16n8k16's A operand (m = the page's 16 keys,
+// k = d) that ldmatrix gives a thread hold dimensions i and i + d/2 of the same key, so a pair turns
+// inside one thread.  The angle of slot r is that of the page's first position plus r steps:
 // (C + iS)(c_r + i s_r) with the table row copied beside the page and rows 0..15 kept in shared
 // memory -- four more multiply-adds a pair instead of sixteen table rows (8 KB at d = 128, as much as
-// the unit itself) a page.  S = Q K^T (fp16), the running maximum and sum of the softmax in registers
-// (rescaled only when the maximum grows by more than 2^8), P in bf16 as the A operand of O += P V:
-// the accumulator layout of S is the A layout of the next product, nothing goes through memory.  The
-// sum takes the rounded weights, so a row with one dominant key is exact.  With 16 or 32 rows a tile
-// mma.sync is the right size (64 tensor-pipe cycles of the some 350 an SM has per unit at full HBM
-// rate); a tcgen05 tile of 128 rows would be nine tenths padding.
+// the unit itself) a page.  S^T = K Q^T (fp16) takes the rows as its 8-wide side, so 8, 16 or 32 rows
+// cost one, two or four products a step; the running maximum and sum of the softmax stay in registers
+// (rescaled only when the maximum grows by more than 2^8), P^T in bf16 becomes the B operand of O^T +=
+// V^T P^T by an 8 x 8 transpose in registers (movmatrix).  The sum takes the rounded weights, so a row
+// with one dominant key is exact.  A tcgen05 tile of 128 rows would be nine tenths padding here.
 //
 // A run of a (request, kv head) that lies within one worker is written out directly.  Otherwise the
 // block joins its warps' partial results through shared memory and passes on at most two (the run
@@ -45,39 +44,40 @@ struct FewParams {
     const int32_t* row_pos;
     const float* rope;
     __nv_bfloat16* out;
-    float* worker_o;            // [workers][16 MT][D]
-    float* block_o;             // [blocks][2][16 MT][D]
-    float2* block_ml;           // [blocks][2][16 MT]
+    float* worker_o;            // [workers][8 NQ][D]
+    float* block_o;             // [blocks][2][8 NQ][D]
+    float2* block_ml;           // [blocks][2][8 NQ]
     int4* block_desc;           // [blocks]: a run that starts here and goes on: {last block << 8 | 255, rows, kv head, first row}
     int64_t q_stride;
-    int32_t n, max_pages, max_rows, hq, hkv, n_phys, max_pos, blocks;
+    int32_t n, max_pages, max_rows, hq, hkv, n_phys, max_pos, blocks, tag;
 };
 
-constexpr int kFewThreads = kFewWarps * 32;
 
-template <int D, int MT>
+template <int D, int NQ>
 struct FewSmem {
+    static constexpr int kWarps = few_warps(NQ);
+    static constexpr int kThreads = kWarps * 32;
     static constexpr int kHalf = kPage * 128;                       // 16 rows of 64 elements
     static constexpr int kK = kPage * D * 2;
     static constexpr int kSlot = 2 * kK;
     static constexpr int kCs = D * 4;                               // cos/sin row
-    static constexpr int kQ = MT == 2 ? MT * (D / 16) * 512 : 0;    // A fragments of a warp's rows
+    static constexpr int kQ = NQ == 4 ? NQ * (D / 32) * 512 : 0;    // B fragments of a warp's rows
     static constexpr int kTabRow = D * 4 + 64;                      // rows 64 bytes apart modulo 128
-    static constexpr int kMl = 2 * 16 * MT * 8;
-    static constexpr int kFixed = kPage * kTabRow + kFewWarps * (kQ + kMl + 2 * 16) + 1024 + 64;
-    static constexpr int kPerStage = kFewWarps * (kSlot + kCs + 16);
+    static constexpr int kMl = 2 * 8 * NQ * 8;
+    static constexpr int kFixed = kPage * kTabRow + kWarps * (kQ + kMl + 2 * 16) + 1024 + 64;
+    static constexpr int kPerStage = kWarps * (kSlot + kCs + 24);
     static constexpr int kFit = (232448 - kFixed) / kPerStage;
     static constexpr int kStages = kFit < 6 ? kFit : 6;
     static_assert(kStages >= 2, "the ring needs two stages");
-    static_assert(kStages * kSlot >= 16 * MT * D * 4, "a worker's partial result fits its ring");
-    static constexpr int oCs = kFewWarps * kStages * kSlot;
-    static constexpr int oTab = oCs + kFewWarps * kStages * kCs;
+    static_assert(kStages * kSlot >= 8 * NQ * D * 4, "a worker's partial result fits its ring");
+    static constexpr int oCs = kWarps * kStages * kSlot;
+    static constexpr int oTab = oCs + kWarps * kStages * kCs;
     static constexpr int oQ = oTab + kPage * kTabRow;
-    static constexpr int oMl = oQ + kFewWarps * kQ;
-    static constexpr int oDesc = oMl + kFewWarps * kMl;
-    static constexpr int oBar = oDesc + kFewWarps * 2 * 16;
-    static constexpr int oMeta = oBar + kFewWarps * kStages * 8;
-    static constexpr int oAbort = oMeta + kFewWarps * kStages * 4;
+    static constexpr int oMl = oQ + kWarps * kQ;
+    static constexpr int oDesc = oMl + kWarps * kMl;
+    static constexpr int oBar = oDesc + kWarps * 2 * 16;
+    static constexpr int oMeta = oBar + kWarps * 2 * kStages * 8;
+    static constexpr int oAbort = oMeta + kWarps * kStages * 4;
     static constexpr int kBytes = oAbort + 16;
     static constexpr int kAlloc = kBytes + 1024;
     static_assert(kAlloc <= 232448, "more dynamic shared memory than a GB300 block can have");
@@ -90,6 +90,27 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t& a, uint32_t& b, u
 __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+// two packed fp32 pairs, 16 bytes
+__device__ __forceinline__ void lds_pair(uint32_t addr, uint64_t& a, uint64_t& b) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint64_t f2_neg(uint64_t v) {
+    float a, b;
+    f2_unpack(v, a, b);
+    return f2_pack(-a, -b);
+}
+// to fp16 with infinities kept (a key beyond the range shows in its scores)
+__device__ __forceinline__ uint32_t pack_f16x2_inf(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// 8 x 8 matrix of 16-bit elements, a fragment's row lane / 4 and columns 2 (lane % 4), + 1: transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -117,20 +138,21 @@ struct FewCursor {
     }
 };
 
-template <int D, int MT>
-__global__ void __launch_bounds__(kFewThreads, 1)
+template <int D, int NQ>
+__global__ void __launch_bounds__(FewSmem<D, NQ>::kThreads, 1)
 few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const FewParams p) {
-    using SM = FewSmem<D, MT>;
-    constexpr int NS = SM::kStages;
-    constexpr int KS = D / 16;       // k steps of Q K^T
-    constexpr int NT = D / 8;        // 8-column tiles of O
+    using SM = FewSmem<D, NQ>;
+    constexpr int NS = SM::kStages, WARPS = SM::kWarps, THREADS = SM::kThreads;
+    constexpr int KS = D / 16;       // k steps of K Q^T
+    constexpr int MT = D / 16;       // 16-dimension tiles of O^T
     constexpr int J = D / 16;        // 8-frequency chunks: chunk j turns with chunk j + J
-    constexpr int ROWS = 16 * MT;
+    constexpr int ROWS = 8 * NQ;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = lane >> 2, c = lane & 3;     // fragment coordinates
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::oBar) + warp * NS;
+    uint64_t* bar_k = reinterpret_cast<uint64_t*>(smem + SM::oBar) + warp * 2 * NS;
+    uint64_t* bar_v = bar_k + NS;
     volatile uint32_t* meta = reinterpret_cast<volatile uint32_t*>(smem + SM::oMeta) + warp * NS;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::oAbort);
     uint8_t* ring = smem + warp * NS * SM::kSlot;
@@ -138,7 +160,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     float2* s_ml = reinterpret_cast<float2*>(smem + SM::oMl);       // [warp][first, last][row]
     volatile int32_t* s_desc = reinterpret_cast<volatile int32_t*>(smem + SM::oDesc);   // [warp][2][4]
     if (lane == 0) {
-        for (int s = 0; s < NS; ++s) mbar_init(&bars[s], 1);
+        for (int s = 0; s < 2 * NS; ++s) mbar_init(&bar_k[s], 1);
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
         for (int i = 0; i < 8; ++i) s_desc[warp * 8 + i] = 0;
@@ -154,18 +176,27 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const int32_t* base = plan + plan_array(CA_ROW, p.n);
     const int32_t* few = plan + plan_array(CA_FEW, p.n);
     const int g = p.hq / p.hkv, gs = __ffs(g) - 1;   // g divides 128
-    const bool fits = plan_fits(plan, p.n, p.max_pages, p.max_rows, p.hq, p.hkv, p.blocks * kFewWarps);
-    const int worker = blockIdx.x * kFewWarps + warp;
-    const int4 start = reinterpret_cast<const int4*>(plan + plan_starts(p.n))[2 * worker];
-    const int4 first = reinterpret_cast<const int4*>(plan + plan_starts(p.n))[2 * worker + 1];
-    const int n_units = fits ? start.w : 0;
+    const int worker = blockIdx.x * WARPS + warp;
+    const int4* entry = reinterpret_cast<const int4*>(plan + plan_starts(p.n)) + 3 * worker;
+    const int4 start = entry[0], first = entry[1];
+    const int32_t tag = entry[2].x;
+    if (tag != p.tag) set_dev_error(kDevErrBounds);
+    const int n_units = tag == p.tag ? start.w : 0;
+    // cos/sin of 0..15 steps, for everyone, as pairs: (cos, cos', sin, sin') of two frequencies
+    for (int i = tid; i < kPage * D / 4; i += THREADS) {
+        const int r = i / (D / 4), f = i % (D / 4);
+        const float4 v = reinterpret_cast<const float4*>(p.rope)[i];
+        *reinterpret_cast<float4*>(smem + SM::oTab + r * SM::kTabRow + f * 16) = make_float4(v.x, v.z, v.y, v.w);
+    }
 
-    // ---------------- the copies: unit i of the worker into slot i % NS
+    // ---------------- the copies: unit i of the worker into slot i % NS, its value once its key's
+    // slot is under way (K is free again a whole softmax and P V earlier)
     FewCursor is{start.x, start.y, start.z, first.x};
     int32_t win_req = -1, win_page = 0;            // the 32 table entries the lanes hold
     int32_t e_ph = 0, e_pos = 0;
     uint32_t e_ex = 0;
-    auto issue = [&](int i) {
+    int32_t y_v = 0;                               // pool row of the value that follows the last key
+    auto look_up = [&]() {
         if (is.req != win_req || is.page < win_page || is.page >= win_page + 32) {
             win_req = is.req;
             win_page = is.page;
@@ -184,116 +215,147 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 }
             }
         }
+    };
+    auto issue_k = [&](int i) {
+        look_up();
         const int src = is.page - win_page, s = i % NS;
         const int32_t ph = __shfl_sync(0xffffffffu, e_ph, src), pos = __shfl_sync(0xffffffffu, e_pos, src);
         const uint32_t ex = __shfl_sync(0xffffffffu, e_ex, src);
+        y_v = (ph * p.hkv + is.kvh) * kPage;
         if (lane == 0) {
             meta[s] = ex;
-            mbar_arrive_expect_tx(&bars[s], SM::kSlot + SM::kCs);
-            const int32_t y = (ph * p.hkv + is.kvh) * kPage;
+            mbar_arrive_expect_tx(&bar_k[s], SM::kK + SM::kCs);
 #pragma unroll
             for (int hb = 0; hb < D / 64; ++hb)
-                tma_load_2d(ring + s * SM::kSlot + hb * SM::kHalf, &tm_k, &bars[s], hb * 64, y);
-            bulk_load(ring_cs + s * SM::kCs, p.rope + (int64_t)pos * D, SM::kCs, &bars[s]);
-#pragma unroll
-            for (int hb = 0; hb < D / 64; ++hb)
-                tma_load_2d(ring + s * SM::kSlot + SM::kK + hb * SM::kHalf, &tm_v, &bars[s], hb * 64, y);
+                tma_load_2d(ring + s * SM::kSlot + hb * SM::kHalf, &tm_k, &bar_k[s], hb * 64, y_v);
+            bulk_load(ring_cs + s * SM::kCs, p.rope + (int64_t)pos * D, SM::kCs, &bar_k[s]);
         }
         is.step(few, seq, add, p.hkv, p.n);
     };
-    int issued = 0;
-    for (; issued < NS && issued < n_units; ++issued) issue(issued);
-
-    // cos/sin of 0..15 steps, for everyone
-    for (int i = tid; i < kPage * D / 4; i += kFewThreads) {
-        const int r = i / (D / 4), f = i % (D / 4);
-        *reinterpret_cast<float4*>(smem + SM::oTab + r * SM::kTabRow + f * 16) =
-            reinterpret_cast<const float4*>(p.rope)[i];
-    }
+    auto issue_v = [&](int i) {
+        const int s = i % NS;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bar_v[s], SM::kK);
+#pragma unroll
+            for (int hb = 0; hb < D / 64; ++hb)
+                tma_load_2d(ring + s * SM::kSlot + SM::kK + hb * SM::kHalf, &tm_v, &bar_v[s], hb * 64, y_v);
+        }
+    };
+    int issued_k = 0, issued_v = 0;
+    if (n_units > 0) look_up();
+    // positions of the rows of a run (row 8 q + lane / 4); a row behind the last one, or one whose
+    // position is out of range, has none and scores 0 everywhere
+    int32_t s_len = first.y, t_len = first.z, r_base = first.w, n_rows = t_len * g;
+    int32_t row_at[NQ];
+    auto load_positions = [&]() {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            const int r = q * 8 + row;
+            row_at[q] = r < n_rows ? p.row_pos[r_base + (r >> gs)] : -1;
+            if (r < n_rows && (row_at[q] < 0 || row_at[q] >= p.max_pos)) {
+                set_dev_error(kDevErrBounds);
+                row_at[q] = -1;
+            }
+        }
+    };
+    if (n_units > 0) load_positions();
     __syncthreads();
 
     // ---------------- the units
     const float scale = 1.4426950408889634f * (D == 128 ? 0.08838834764831845f : 0.125f);   // log2(e) / sqrt(d)
     FewCursor cu{start.x, start.y, start.z, first.x};
-    float o[MT][NT][4], m_run[MT][2], l_run[MT][2];
-    uint32_t qf[MT == 1 ? KS : 1][4];
-    uint4* s_q = reinterpret_cast<uint4*>(smem + SM::oQ + warp * SM::kQ);   // MT == 2: [mt][ks][lane]
-    float big = 0.f;
-    int32_t seg_page = 0, s_len = 0, t_len = 0, r_base = 0, n_rows = 0;
+    // O^T, columns 2 c and 2 c + 1 of every row tile; the softmax of those two rows over this lane's keys
+    float o[NQ][MT][4], m_run[NQ][2], l_run[NQ][2];
+    uint32_t qf[NQ == 4 ? 1 : NQ][2 * J];                                   // chunks of row 8 q + lane / 4
+    uint4* s_q = reinterpret_cast<uint4*>(smem + SM::oQ + warp * SM::kQ);   // NQ == 4: [q][chunk / 4][lane]
+    // where ldmatrix finds a lane's row: K matrices (low chunk, its neighbour, their partners) of keys
+    // 0-7, V matrices (keys 0-7, 8-15 of two neighbouring chunks); 16-byte chunk x of a row sits at
+    // x ^ (row & 7), so the chunk of a step is one exclusive or away
+    const uint32_t k_off = (D == 128 ? (uint32_t)(lane >> 4) * SM::kHalf : 0u) + (lane & 7) * 128u +
+                           ((((lane >> 3) & 1u) ^ (D == 128 ? 0u : (uint32_t)(lane >> 4) * 4u) ^ (lane & 7u)) << 4);
+    const uint32_t v_off = (lane & 15) * 128u + (((uint32_t)(lane >> 4) ^ (lane & 7u)) << 4);
+    float big = 0.f;                 // largest rotated query
+    uint64_t seen = 0;               // sum of all scores: not finite where a key left fp16's range
+    int32_t seg_page = 0;
     bool open = false, ok = true;
-    int done = 0;
+    int done_k = 0, done_v = 0;
 
     for (int i = 0; i < n_units; ++i) {
         if (!open) {
-            // a run of one (request, kv head) begins: its rows' queries, rotated and scaled, as A
+            // a run of one (request, kv head) begins: its rows' queries, rotated and scaled, as B
             // fragments (rows behind the last one zero)
             open = true;
             seg_page = cu.page;
-            s_len = i == 0 ? first.y : seq[cu.req];
-            t_len = i == 0 ? first.z : add[cu.req];
-            r_base = i == 0 ? first.w : base[cu.req];
-            n_rows = t_len * g;
+            if (i > 0) {
+                s_len = seq[cu.req];
+                t_len = add[cu.req];
+                r_base = base[cu.req];
+                n_rows = t_len * g;
+                load_positions();
+            }
+            uint32_t x[NQ][2 * J];
+            float4 w[NQ][J];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                uint32_t lo[2][J], hi[2][J];
+            for (int q = 0; q < NQ; ++q) {
+                const int r = q * 8 + row;
+                const __nv_bfloat16* src = p.q + (r_base + (r >> gs)) * p.q_stride + (cu.kvh * g + (r & (g - 1))) * D + 2 * c;
+                const float* cs = p.rope + (int64_t)row_at[q] * D + 4 * c;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = mt * 16 + e * 8 + row;
-#pragma unroll
-                    for (int j = 0; j < J; ++j) lo[e][j] = hi[e][j] = 0;
-                    if (r < n_rows) {
-                        const int t = r >> gs, h = cu.kvh * g + (r & (g - 1));
-                        const int32_t pos = p.row_pos[r_base + t];
-                        if (pos < 0 || pos >= p.max_pos) {
-                            set_dev_error(kDevErrBounds);
-                        } else {
-                            const __nv_bfloat16* q = p.q + (r_base + t) * p.q_stride + h * D + 2 * c;
-                            const float* cs = p.rope + (int64_t)pos * D + 4 * c;
-#pragma unroll
-                            for (int j = 0; j < J; ++j) {
-                                const uint32_t a = *reinterpret_cast<const uint32_t*>(q + 8 * j);
-                                const uint32_t b = *reinterpret_cast<const uint32_t*>(q + D / 2 + 8 * j);
-                                const float4 w = *reinterpret_cast<const float4*>(cs + 16 * j);
-                                const float a0 = bf16_lo(a) * scale, a1 = bf16_hi(a) * scale;
-                                const float b0 = bf16_lo(b) * scale, b1 = bf16_hi(b) * scale;
-                                lo[e][j] = pack_f16x2_track(fmaf(a0, w.x, -b0 * w.y), fmaf(a1, w.z, -b1 * w.w), big);
-                                hi[e][j] = pack_f16x2_track(fmaf(b0, w.x, a0 * w.y), fmaf(b1, w.z, a1 * w.w), big);
-                            }
-                        }
+                for (int j = 0; j < J; ++j) {
+                    x[q][j] = x[q][j + J] = 0;
+                    w[q][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (row_at[q] >= 0) {
+                        x[q][j] = *reinterpret_cast<const uint32_t*>(src + 8 * j);
+                        x[q][j + J] = *reinterpret_cast<const uint32_t*>(src + D / 2 + 8 * j);
+                        w[q][j] = *reinterpret_cast<const float4*>(cs + 16 * j);
                     }
                 }
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    // dimensions 16 ks ..: chunks 2 ks and 2 ks + 1, from the lower or the upper half
-                    const int j0 = (2 * ks) % J, j1 = (2 * ks + 1) % J;
-                    const bool up = 2 * ks >= J;
-                    const uint32_t f0 = up ? hi[0][j0] : lo[0][j0], f1 = up ? hi[1][j0] : lo[1][j0];
-                    const uint32_t f2 = up ? hi[0][j1] : lo[0][j1], f3 = up ? hi[1][j1] : lo[1][j1];
-                    if constexpr (MT == 1) {
-                        qf[ks][0] = f0;
-                        qf[ks][1] = f1;
-                        qf[ks][2] = f2;
-                        qf[ks][3] = f3;
-                    } else {
-                        s_q[(mt * KS + ks) * 32 + lane] = make_uint4(f0, f1, f2, f3);
-                    }
+            }
+            // the first copies go out behind the first rows' loads, not before: 30 MB of them over the
+            // whole device would make those wait
+            if (i == 0)
+                for (; issued_k < NS && issued_k < n_units; ++issued_k, ++issued_v) {
+                    issue_k(issued_k);
+                    issue_v(issued_v);
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int q = 0; q < NQ; ++q) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
-                m_run[mt][0] = m_run[mt][1] = -INFINITY;
-                l_run[mt][0] = l_run[mt][1] = 0.f;
+                for (int j = 0; j < J; ++j) {
+                    const float a0 = bf16_lo(x[q][j]) * scale, a1 = bf16_hi(x[q][j]) * scale;
+                    const float b0 = bf16_lo(x[q][j + J]) * scale, b1 = bf16_hi(x[q][j + J]) * scale;
+                    const float4 v = w[q][j];
+                    x[q][j] = pack_f16x2_track(fmaf(a0, v.x, -b0 * v.y), fmaf(a1, v.z, -b1 * v.w), big);
+                    x[q][j + J] = pack_f16x2_track(fmaf(b0, v.x, a0 * v.y), fmaf(b1, v.z, a1 * v.w), big);
+                }
+                if constexpr (NQ == 4) {
+#pragma unroll
+                    for (int j = 0; j < 2 * J; j += 4)
+                        s_q[(q * (J / 2) + j / 4) * 32 + lane] = make_uint4(x[q][j], x[q][j + 1], x[q][j + 2], x[q][j + 3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2 * J; ++j) qf[q][j] = x[q][j];
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[q][mt][e] = 0.f;
+                m_run[q][0] = m_run[q][1] = -INFINITY;
+                l_run[q][0] = l_run[q][1] = 0.f;
             }
         }
         const int s = i % NS;
-        ok = mbar_wait(&bars[s], (i / NS) & 1, abort_flag);
+        ok = mbar_wait(&bar_k[s], (i / NS) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        ++done;
+        ++done_k;
+        uint8_t* sv = ring + s * SM::kSlot + SM::kK;
+        float4* cs0 = reinterpret_cast<float4*>(ring_cs + s * SM::kCs);
+        if (lane < D / 4) {          // the page's cos/sin row, as pairs
+            const float4 v = cs0[lane];
+            cs0[lane] = make_float4(v.x, v.z, v.y, v.w);
+        }
         const uint32_t ex = meta[s];
         const int32_t j0 = cu.page * kPage;                        // the page's first slot
-        uint8_t* sk = ring + s * SM::kSlot;
-        uint8_t* sv = sk + SM::kK;
         // every row sees every key of the page: nothing excluded and the page ends at or before the
         // first row's own slot
         const bool clean = ex == 0u && j0 + kPage - 1 <= s_len;
@@ -302,129 +364,143 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (!clean) {
             const int left = s_len + t_len - j0;                   // slots of the page that hold tokens
             if (left < kPage) gone |= 0xFFFFu & ~((1u << left) - 1u);
-            // their values must not meet a weight of zero
+        }
+        if (gone != 0u) {
+            // keys that take no part score 0 (whatever they hold) until the softmax drops them
+            uint8_t* sk = ring + s * SM::kSlot;
+            for (int q = lane; q < kPage * (D / 8); q += 32) {
+                const int r = q / (D / 8), ch = q % (D / 8);
+                if (gone >> r & 1u)
+                    *reinterpret_cast<uint4*>(sk + (ch >> 3) * SM::kHalf + sw128_off(r, ch & 7)) = make_uint4(0, 0, 0, 0);
+            }
+        }
+        __syncwarp();
+        // S^T = K Q^T, keys 0-7 and 8-15 of the page: a k step of the lower half and its partner at a
+        // time, in two chains of products
+        float sc[NQ][2][4];
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[q][0][e] = sc[q][1][e] = 0.f;
+        const uint32_t sk_u = smem_u32(ring) + s * SM::kSlot + k_off;
+        const uint32_t tab = smem_u32(smem + SM::oTab) + row * SM::kTabRow + c * 16, cs_u = smem_u32(cs0) + c * 16;
+#pragma unroll
+        for (int jj = 0; jj < J / 2; ++jj) {
+            uint32_t kf[2][4];                                     // chunks 2 jj, 2 jj + 1, and theirs + J
+            ldsm4(sk_u ^ (jj * 32), kf[0][0], kf[0][1], kf[0][2], kf[0][3]);
+            ldsm4((sk_u + 1024) ^ (jj * 32), kf[1][0], kf[1][1], kf[1][2], kf[1][3]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint64_t C0, S0;
+                lds_pair(cs_u + (2 * jj + q) * 64, C0, S0);
+                const uint64_t NS0 = f2_neg(S0);
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    uint64_t Cr, Sr;
+                    lds_pair(tab + nt * 8 * SM::kTabRow + (2 * jj + q) * 64, Cr, Sr);
+                    const uint64_t C = f2_fma(NS0, Sr, f2_mul(C0, Cr)), S = f2_fma(C0, Sr, f2_mul(S0, Cr));
+                    const uint64_t A = bf16x2_to_f2(kf[nt][q]), B = bf16x2_to_f2(kf[nt][q + 2]);
+                    float y0, y1, z0, z1;
+                    f2_unpack(f2_fma(A, C, f2_neg(f2_mul(B, S))), y0, y1);   // a cos - b sin
+                    f2_unpack(f2_fma(A, S, f2_mul(B, C)), z0, z1);           // a sin + b cos
+                    kf[nt][q] = pack_f16x2_inf(y0, y1);
+                    kf[nt][q + 2] = pack_f16x2_inf(z0, z1);
+                }
+            }
+#pragma unroll
+            for (int up = 0; up < 2; ++up) {
+                const uint32_t a[4] = {kf[0][2 * up], kf[1][2 * up], kf[0][2 * up + 1], kf[1][2 * up + 1]};
+                const int j = 2 * jj + up * J;                     // first chunk of the k step
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    if (NQ == 4 && q == 2 && n_rows <= 16) break;   // (a branch a tile would cost more than the tile)
+                    if constexpr (NQ == 4) {
+                        const uint2 b = reinterpret_cast<const uint2*>(s_q + (q * (J / 2) + j / 4) * 32 + lane)[j / 2 % 2];
+                        mma_f16_16816(sc[q][up], a, b.x, b.y);
+                    } else {
+                        mma_f16_16816(sc[q][up], a, qf[q][j], qf[q][j + 1]);
+                    }
+                }
+            }
+        }
+        // K has been read (and the cos/sin row rewritten in place): the next key but NS into its slot
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (issued_k < n_units) issue_k(issued_k++);
+        // softmax of the unit's 16 keys: this lane has keys lane / 4 and + 8 of rows 2 c and 2 c + 1
+        uint32_t pf[NQ][2];
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            if (NQ == 4 && q == 2 && n_rows <= 16) break;
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = sc[q][0][e] + sc[q][1][e];
+            seen = f2_add(seen, f2_add(f2_pack(x[0], x[1]), f2_pack(x[2], x[3])));
+            if (!clean) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = row + 8 * (e >> 1);
+                    const int last = s_len + ((q * 8 + 2 * c + (e & 1)) >> gs) - j0;   // last slot of the page the row sees
+                    if (key > last || (gone >> key & 1u)) x[e] = -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(x[e], x[2 + e]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const bool need = mx > m_run[q][e] + 8.0f;
+                if (__any_sync(0xffffffffu, need)) {
+                    const float al = need ? ex2(m_run[q][e] - mx) : 1.0f;
+                    if (need) m_run[q][e] = mx;
+                    l_run[q][e] *= al;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        o[q][mt][e] *= al;
+                        o[q][mt][2 + e] *= al;
+                    }
+                }
+                const float ms = m_run[q][e] == -INFINITY ? 0.f : m_run[q][e];
+                x[e] = ex2(x[e] - ms);
+                x[2 + e] = ex2(x[2 + e] - ms);
+            }
+            // bf16 like the values they meet (an MMA's operands share a type); summed as rounded
+            const uint32_t w0 = pack_bf16x2(x[0], x[1]), w1 = pack_bf16x2(x[2], x[3]);
+            l_run[q][0] += bf16_lo(w0) + bf16_lo(w1);
+            l_run[q][1] += bf16_hi(w0) + bf16_hi(w1);
+            pf[q][0] = transpose8(w0);
+            pf[q][1] = transpose8(w1);
+        }
+        ok = mbar_wait(&bar_v[s], (i / NS) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        ++done_v;
+        if (!clean && gone != 0u) {
+            // values of keys that take no part must not meet a weight of zero
             for (int q = lane; q < kPage * (D / 8); q += 32) {
                 const int r = q / (D / 8), ch = q % (D / 8);
                 if (gone >> r & 1u)
                     *reinterpret_cast<uint4*>(sv + (ch >> 3) * SM::kHalf + sw128_off(r, ch & 7)) = make_uint4(0, 0, 0, 0);
             }
+            fence_proxy_async_smem();              // before the slot's next copy
             __syncwarp();
         }
-        // S = Q K^T, keys 0-7 and 8-15: a thread turns pairs of key row (+ 8)
-        float sc[MT][2][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
-        const uint32_t sk_u = smem_u32(sk), sv_u = smem_u32(sv);
-        const float4* cs0 = reinterpret_cast<const float4*>(ring_cs + s * SM::kCs) + c;
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            uint32_t kf[2 * J];                                    // chunk j: dimensions 8 j + 2 c, + 1
-            {
-                const int kr = nt * 8 + (lane & 7), ch = lane >> 3;
-#pragma unroll
-                for (int q = 0; q < 2 * J; q += 4) {
-                    const int cc = q + ch;
-                    ldsm4(sk_u + (cc >> 3) * SM::kHalf + sw128_off(kr, cc & 7), kf[q], kf[q + 1], kf[q + 2], kf[q + 3]);
-                }
-            }
-            if (!clean && (gone >> (nt * 8 + row) & 1u)) {
-#pragma unroll
-                for (int q = 0; q < 2 * J; ++q) kf[q] = 0;
-            }
-            const float4* csr = reinterpret_cast<const float4*>(smem + SM::oTab + (nt * 8 + row) * SM::kTabRow) + c;
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const float4 u = cs0[4 * j], w = csr[4 * j];
-                const float c0 = fmaf(u.x, w.x, -u.y * w.y), s0 = fmaf(u.y, w.x, u.x * w.y);
-                const float c1 = fmaf(u.z, w.z, -u.w * w.w), s1 = fmaf(u.w, w.z, u.z * w.w);
-                const float a0 = bf16_lo(kf[j]), a1 = bf16_hi(kf[j]);
-                const float b0 = bf16_lo(kf[j + J]), b1 = bf16_hi(kf[j + J]);
-                kf[j] = pack_f16x2_track(fmaf(a0, c0, -b0 * s0), fmaf(a1, c1, -b1 * s1), big);
-                kf[j + J] = pack_f16x2_track(fmaf(b0, c0, a0 * s0), fmaf(b1, c1, a1 * s1), big);
-            }
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                if constexpr (MT == 1) {
-                    mma_f16_16816(sc[0][nt], qf[ks], kf[2 * ks], kf[2 * ks + 1]);
-                } else {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        if (mt > 0 && n_rows <= 16) continue;
-                        const uint4 a = s_q[(mt * KS + ks) * 32 + lane];
-                        const uint32_t af[4] = {a.x, a.y, a.z, a.w};
-                        mma_f16_16816(sc[mt][nt], af, kf[2 * ks], kf[2 * ks + 1]);
-                    }
-                }
-            }
-        }
-        // softmax of the unit's 16 keys
-        uint32_t pf[MT][4];
+        // O^T += V^T P^T
+        const uint32_t sv_u = smem_u32(ring) + s * SM::kSlot + SM::kK + v_off;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            if (mt > 0 && n_rows <= 16) continue;
-            if (!clean) {
+            uint32_t a[4];                                         // (dims, keys): low/high dims, then high keys
+            ldsm4_t((sv_u ^ ((2 * mt & 7) * 16)) + (mt >> 2) * SM::kHalf, a[0], a[2], a[1], a[3]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int last = s_len + ((mt * 16 + e * 8 + row) >> gs) - j0;   // last slot of the page the row sees
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int key = nt * 8 + 2 * c + x;
-                            if (key > last || (gone >> key & 1u)) sc[mt][nt][2 * e + x] = -INFINITY;
-                        }
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = fmaxf(fmaxf(sc[mt][0][2 * e], sc[mt][0][2 * e + 1]), fmaxf(sc[mt][1][2 * e], sc[mt][1][2 * e + 1]));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const bool need = mx > m_run[mt][e] + 8.0f;
-                if (__any_sync(0xffffffffu, need)) {
-                    const float al = need ? ex2(m_run[mt][e] - mx) : 1.0f;
-                    if (need) m_run[mt][e] = mx;
-                    l_run[mt][e] *= al;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        o[mt][nt][2 * e] *= al;
-                        o[mt][nt][2 * e + 1] *= al;
-                    }
-                }
-                const float ms = m_run[mt][e] == -INFINITY ? 0.f : m_run[mt][e];
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const uint32_t w = pack_bf16x2(ex2(sc[mt][nt][2 * e] - ms), ex2(sc[mt][nt][2 * e + 1] - ms));
-                    l_run[mt][e] += bf16_lo(w) + bf16_hi(w);
-                    pf[mt][2 * nt + e] = w;
-                }
+            for (int q = 0; q < NQ; ++q) {
+                if (NQ == 4 && q == 2 && n_rows <= 16) break;
+                mma_bf16_16816(o[q][mt], a, pf[q][0], pf[q][1]);
             }
         }
-        // O += P V: column tiles two at a time
-        {
-            const int kr = lane & 15, up = lane >> 4;
-#pragma unroll
-            for (int nt = 0; nt < NT; nt += 2) {
-                const int ch = nt + up;
-                uint32_t v0, v1, v2, v3;
-                ldsm4_t(sv_u + (ch >> 3) * SM::kHalf + sw128_off(kr, ch & 7), v0, v1, v2, v3);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    if (mt > 0 && n_rows <= 16) continue;
-                    mma_bf16_16816(o[mt][nt], pf[mt], v0, v1);
-                    mma_bf16_16816(o[mt][nt + 1], pf[mt], v2, v3);
-                }
-            }
-        }
-        if (!clean) fence_proxy_async_smem();      // zeros written above, before the slot's next copy
         __syncwarp();
-        if (issued < n_units) issue(issued++);
+        if (issued_v < issued_k) issue_v(issued_v++);
 
-        // ---------------- the end of a run, or of the worker
+    // ---------------- the end of a run, or of the worker
         const bool last = i + 1 == n_units, ended = cu.page + 1 == cu.pages;
         if (ended || last) {
             const bool whole = ended && seg_page == 0;
@@ -432,30 +508,45 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // a worker's last partial result takes its ring, an earlier one (its first run) the workspace
             float* part = last ? reinterpret_cast<float*>(ring) : p.worker_o + (int64_t)worker * ROWS * D;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int q = 0; q < NQ; ++q) {
+                if (NQ == 4 && q == 2 && n_rows <= 16) break;
+                float l[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float l = l_run[mt][e];
-                    l += __shfl_xor_sync(0xffffffffu, l, 1);
-                    l += __shfl_xor_sync(0xffffffffu, l, 2);
-                    const int r = mt * 16 + e * 8 + row;
-                    if (r < n_rows) {
-                        if (whole) {
-                            const float inv = l > 0.f ? 1.0f / l : 0.f;
-                            uint32_t* dst = reinterpret_cast<uint32_t*>(
-                                p.out + ((int64_t)(r_base + (r >> gs)) * p.hq + cu.kvh * g + (r & (g - 1))) * D + 2 * c);
+                    l[e] = l_run[q][e];
+                    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+                    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+                    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
+                }
+                if (whole) {
+                    const float i0 = l[0] > 0.f ? 1.0f / l[0] : 0.f, i1 = l[1] > 0.f ? 1.0f / l[1] : 0.f;
+                    const int r = q * 8 + row;                     // after the transpose: row, dimensions 2 c, + 1
+                    uint32_t* dst = reinterpret_cast<uint32_t*>(
+                        p.out + ((int64_t)(r_base + (r >> gs)) * p.hq + cu.kvh * g + (r & (g - 1))) * D + 2 * c);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                dst[4 * nt] = pack_bf16x2(o[mt][nt][2 * e] * inv, o[mt][nt][2 * e + 1] * inv);
-                        } else {
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint32_t w0 = transpose8(pack_bf16x2(o[q][mt][0] * i0, o[q][mt][1] * i1));
+                        const uint32_t w1 = transpose8(pack_bf16x2(o[q][mt][2] * i0, o[q][mt][3] * i1));
+                        if (r < n_rows) {
+                            dst[8 * mt] = w0;
+                            dst[8 * mt + 4] = w1;
+                        }
+                    }
+                } else {
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                *reinterpret_cast<float2*>(part + r * D + nt * 8 + 2 * c) =
-                                    make_float2(o[mt][nt][2 * e], o[mt][nt][2 * e + 1]);
-                            if (c == 0) s_ml[(warp * 2 + kind) * ROWS + r] = make_float2(m_run[mt][e], l);
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = q * 8 + 2 * c + e;
+                        if (r < n_rows) {
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                part[r * D + 16 * mt + row] = o[q][mt][e];
+                                part[r * D + 16 * mt + 8 + row] = o[q][mt][2 + e];
+                            }
+                            if (row == 0) s_ml[(warp * 2 + kind) * ROWS + r] = make_float2(m_run[q][e], l[e]);
                         }
                     }
                 }
+            }
             if (!whole && lane == 0) {
                 volatile int32_t* d = s_desc + (warp * 2 + kind) * 4;
                 d[0] = 1 | (ended ? 2 : 0) | (last ? 4 : 0);
@@ -467,33 +558,40 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
         cu.step(few, seq, add, p.hkv, p.n);
     }
-    if (!(big < kF16Limit)) set_dev_error(kDevErrRange);
+    {
+        float a, b;
+        f2_unpack(seen, a, b);
+        if (!(big < kF16Limit) || !(fabsf(a) + fabsf(b) < INFINITY)) set_dev_error(kDevErrRange);
+    }
     if (!ok && lane == 0)        // an abort: the copies in flight land before the block exits
-        for (int i = done; i < issued; ++i) mbar_drain(&bars[i % NS], (i / NS) & 1);
+    {
+        for (int i = done_k; i < issued_k; ++i) mbar_drain(&bar_k[i % NS], (i / NS) & 1);
+        for (int i = done_v; i < issued_v; ++i) mbar_drain(&bar_v[i % NS], (i / NS) & 1);
+    }
     __syncthreads();
     // ---------------- join the warps' partial results, run by run
     const bool aborted = *abort_flag != 0;
     int4 desc = make_int4(0, 0, 0, 0);
     // bit 2 w: what warp w ends of a run begun before it; bit 2 w + 1: what it leaves open
-    const int32_t state = lane < 2 * kFewWarps ? s_desc[lane * 4] : 0;
+    const int32_t state = lane < 2 * WARPS ? s_desc[lane * 4] : 0;
     const uint32_t present = __ballot_sync(0xffffffffu, state & 1), closing = __ballot_sync(0xffffffffu, state & 2);
     const uint32_t in_ring = __ballot_sync(0xffffffffu, state & 4);
     // a run's first part here: one left open, or the block's very first part where that is an end
     const uint32_t lowest = present & (0u - present);
-    const uint32_t before = lowest & 0x5555u;
-    for (uint32_t todo = aborted ? 0u : (present & 0xAAAAu) | before; todo != 0u; todo &= todo - 1u) {
+    const uint32_t before = lowest & 0x55555555u;
+    for (uint32_t todo = aborted ? 0u : (present & 0xAAAAAAAAu) | before; todo != 0u; todo &= todo - 1u) {
         const int sb = __ffs(todo) - 1;
         const bool from_before = (before >> sb & 1u) != 0u;
         uint32_t parts = 1u << sb;
         bool ended = (closing >> sb & 1u) != 0u;
-        for (uint32_t rest = present & 0x5555u & ~((2u << sb) - 1u); rest != 0u && !ended; rest &= rest - 1u) {
+        for (uint32_t rest = present & 0x55555555u & ~((2u << sb) - 1u); rest != 0u && !ended; rest &= rest - 1u) {
             parts |= rest & (0u - rest);
             ended = (closing & rest & (0u - rest)) != 0u;
         }
         const int32_t req = s_desc[sb * 4 + 1], kvh = s_desc[sb * 4 + 2];
         const int rows_run = s_desc[sb * 4 + 3] & 0xFF, rb = s_desc[sb * 4 + 3] >> 8;
         const int slot = blockIdx.x * 2 + (from_before ? 0 : 1);
-        for (int idx = tid; idx < rows_run * (D / 4); idx += kFewThreads) {
+        for (int idx = tid; idx < rows_run * (D / 4); idx += THREADS) {
             const int r = idx / (D / 4), f = idx % (D / 4);
             float top = -INFINITY;
             for (uint32_t m = parts; m != 0u; m &= m - 1u) top = fmaxf(top, s_ml[(__ffs(m) - 1) * ROWS + r].x);
@@ -506,7 +604,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 const float a = ex2(ml.x - ref);
                 const float* src = (in_ring >> x & 1u)
                                        ? reinterpret_cast<const float*>(smem + (x >> 1) * NS * SM::kSlot)
-                                       : p.worker_o + (int64_t)(blockIdx.x * kFewWarps + (x >> 1)) * ROWS * D;
+                                       : p.worker_o + (int64_t)(blockIdx.x * WARPS + (x >> 1)) * ROWS * D;
                 const float4 v = *reinterpret_cast<const float4*>(src + r * D + 4 * f);
                 acc.x += a * v.x;
                 acc.y += a * v.y;
@@ -526,9 +624,9 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (!from_before && !ended) {
             // the block that holds the run's last unit u: u's owner is the last worker whose first unit
             // is not behind it
-            const int64_t units = few[p.n], active = few_active(units, p.blocks * kFewWarps);
+            const int64_t units = few[p.n], active = few_active(units, p.blocks * WARPS);
             const int64_t u = few[req] + (int64_t)(kvh + 1) * pages_of(seq[req] + add[req]) - 1;
-            desc = make_int4(((int)(((u + 1) * active - 1) / units) / kFewWarps) << 8 | 0xFF, rows_run, kvh, rb);
+            desc = make_int4(((int)(((u + 1) * active - 1) / units) / WARPS) << 8 | 0xFF, rows_run, kvh, rb);
         }
     }
     if (tid == 0) p.block_desc[blockIdx.x] = desc;
@@ -539,9 +637,9 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 // a part in every eighth block or so and few rows, so the parts are taken by groups of threads side by
 // side, four loads in flight a thread, and the groups joined in shared memory in their order.
 constexpr int kJoinThreads = 512;
-template <int D, int MT>
+template <int D, int NQ>
 __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const FewParams p) {
-    constexpr int ROWS = 16 * MT;
+    constexpr int ROWS = 8 * NQ;
     __shared__ float4 s_acc[kJoinThreads];
     __shared__ float2 s_w[kJoinThreads];
     grid_dep_wait();

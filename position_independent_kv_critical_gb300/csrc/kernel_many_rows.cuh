@@ -49,7 +49,7 @@ struct RotateParams {
     __half* q_rot;              // [Hkv][max_rows][g][D], scaled by log2(e) / sqrt(d)
     __half* k_rot;              // [Hkv][pages][16][D]
     int64_t q_stride;
-    int32_t n, max_pages, max_rows, hq, hkv, n_phys, max_pos, workers, total_pages;
+    int32_t n, max_pages, max_rows, hq, hkv, n_phys, max_pos, tag, total_pages;
 };
 
 template <int D>
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const RotateParams p)
     constexpr int LANES = 256 / (kPage * CPR);   // heads side by side
     grid_dep_wait();
     grid_dep_launch();
-    if (!plan_fits(p.plan, p.n, p.max_pages, p.max_rows, p.hq, p.hkv, p.workers)) return;
+    if (!plan_fits(p.plan, p.tag)) return;
     const int32_t* seq = p.plan + plan_array(CA_SEQ, p.n);
     const int32_t* add = p.plan + plan_array(CA_NEW, p.n);
     const int32_t* kpage = p.plan + plan_array(CA_KPAGE, p.n);
@@ -160,7 +160,7 @@ struct ManyParams {
     float* part_o;              // [blocks][2][256][D]
     float2* part_ml;            // [blocks][2][256]
     int4* desc;                 // [blocks]: a run begun here that goes on: {last block << 8 | 255, request, kv head, pair}
-    int32_t n, max_pages, max_rows, hq, hkv, n_phys, workers, blocks, total_pages;
+    int32_t n, max_pages, max_rows, hq, hkv, n_phys, workers, blocks, tag, total_pages;
 };
 
 constexpr int kManyThreads = 448;
@@ -288,11 +288,9 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int32_t* row = plan + plan_array(CA_ROW, prm.n);
         const int32_t* many = plan + plan_array(CA_MANY, prm.n);
         const int32_t* kpage = plan + plan_array(CA_KPAGE, prm.n);
-        const bool fits = plan_fits(plan, prm.n, prm.max_pages, prm.max_rows, prm.hq, prm.hkv, prm.workers) &&
-                          plan[C_BLOCKS] == prm.blocks;
         const int4* st = reinterpret_cast<const int4*>(plan + plan_many(prm.n, prm.workers)) + 2 * blockIdx.x;
-        const int4 start = st[0];
-        int left = fits ? st[1].x : 0;
+        const int4 start = st[0], part = st[1];
+        int left = part.y == prm.tag ? part.x : 0;
         int32_t req = start.x, kvh = start.y, pair = start.z, tile = start.w;
         int kc = 0, last_k[2] = {-1, -1}, last_q = -1;
         bool ok = true;

@@ -984,8 +984,8 @@ extern "C" pcf_status pcf_chunk_tables(const pcf_chunk_dims* dims, const int32_t
     const TablesParams p{seq_len, new_len, next_pos, free_pages, free_head, block_table, page_pos, slot_map, row_pos,
                          row_base, seq_len_out, free_head_out, plan, dims->n_reqs, dims->max_pages, dims->max_rows,
                          dims->max_chunk, dims->max_total_pages, dims->n_phys_pages, dims->max_pos, n_free,
-                         dims->n_q_heads, dims->n_kv_heads, dims->head_dim, kFewWarps * chunk_sms(dims->n_sms),
-                         chunk_sms(dims->n_sms)};
+                         dims->n_q_heads, dims->n_kv_heads, few_limit(dims), few_workers(dims),
+                         chunk_sms(dims->n_sms), plan_tag(dims)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((s = launch(chunk_plan_kernel, dim3(1), dim3(kTablesThreads), 0, st, p)) != PCF_OK) return s;
     const int items = std::max({dims->max_rows, dims->n_reqs + 1, p.workers});
@@ -1036,7 +1036,7 @@ struct ChunkCall {
 };
 
 // requests with few rows: the kernel over their pages, then the runs that blocks share
-template <int D, int MT>
+template <int D, int NQ>
 pcf_status few_rows_impl(const ChunkCall& c, cudaStream_t st) {
     const pcf_chunk_dims& d = *c.dims;
     const ChunkWs w = chunk_ws(&d);
@@ -1050,12 +1050,12 @@ pcf_status few_rows_impl(const ChunkCall& c, cudaStream_t st) {
                       c.rope, reinterpret_cast<__nv_bfloat16*>(c.out), reinterpret_cast<float*>(c.ws + w.worker_o),
                       reinterpret_cast<float*>(c.ws + w.block_o), reinterpret_cast<float2*>(c.ws + w.block_ml),
                       reinterpret_cast<int4*>(c.ws + w.block_desc), c.q_stride, d.n_reqs, d.max_pages, d.max_rows,
-                      d.n_q_heads, d.n_kv_heads, d.n_phys_pages, d.max_pos, blocks};
-    using SM = FewSmem<D, MT>;
-    auto kern = few_rows_kernel<D, MT>;
+                      d.n_q_heads, d.n_kv_heads, d.n_phys_pages, d.max_pos, blocks, plan_tag(&d)};
+    using SM = FewSmem<D, NQ>;
+    auto kern = few_rows_kernel<D, NQ>;
     if ((s = set_smem(kern, SM::kAlloc)) != PCF_OK) return s;
-    if ((s = launch(kern, dim3(blocks), dim3(kFewThreads), SM::kAlloc, st, tk, tv, p)) != PCF_OK) return s;
-    return launch(few_join_kernel<D, MT>, dim3(blocks), dim3(kJoinThreads), 0, st, p);
+    if ((s = launch(kern, dim3(blocks), dim3(SM::kThreads), SM::kAlloc, st, tk, tv, p)) != PCF_OK) return s;
+    return launch(few_join_kernel<D, NQ>, dim3(blocks), dim3(kJoinThreads), 0, st, p);
 }
 
 // requests with more rows: queries and keys rotated into the workspace, the tensor-core kernel, then
@@ -1064,7 +1064,7 @@ template <int D>
 pcf_status many_rows_impl(const ChunkCall& c, cudaStream_t st) {
     const pcf_chunk_dims& d = *c.dims;
     const ChunkWs w = chunk_ws(&d);
-    const int blocks = chunk_sms(d.n_sms), workers = kFewWarps * blocks;
+    const int blocks = chunk_sms(d.n_sms), workers = few_workers(&d);
     __half* q_rot = reinterpret_cast<__half*>(c.ws + w.q_rot);
     __half* k_rot = reinterpret_cast<__half*>(c.ws + w.k_rot);
     CUtensorMap tq, tk, tv;
@@ -1078,12 +1078,12 @@ pcf_status many_rows_impl(const ChunkCall& c, cudaStream_t st) {
     const RotateParams r{c.plan, reinterpret_cast<const __nv_bfloat16*>(c.q),
                          reinterpret_cast<const __nv_bfloat16*>(c.k_pool), c.block_table, c.page_pos, c.excl, c.row_pos,
                          c.rope, q_rot, k_rot, c.q_stride, d.n_reqs, d.max_pages, d.max_rows, d.n_q_heads,
-                         d.n_kv_heads, d.n_phys_pages, d.max_pos, workers, d.max_total_pages};
+                         d.n_kv_heads, d.n_phys_pages, d.max_pos, plan_tag(&d), d.max_total_pages};
     if ((s = launch(chunk_rotate_kernel<D>, dim3(8 * blocks), dim3(256), 0, st, r)) != PCF_OK) return s;
     const ManyParams p{c.plan, c.block_table, c.excl, reinterpret_cast<__nv_bfloat16*>(c.out),
                        reinterpret_cast<float*>(c.ws + w.many_o), reinterpret_cast<float2*>(c.ws + w.many_ml),
                        reinterpret_cast<int4*>(c.ws + w.many_desc), d.n_reqs, d.max_pages, d.max_rows, d.n_q_heads,
-                       d.n_kv_heads, d.n_phys_pages, workers, blocks, d.max_total_pages};
+                       d.n_kv_heads, d.n_phys_pages, workers, blocks, plan_tag(&d), d.max_total_pages};
     using SM = ManySmem<D>;
     auto kern = many_rows_kernel<D>;
     if ((s = set_smem(kern, SM::kAlloc)) != PCF_OK) return s;
@@ -1096,8 +1096,10 @@ template <int D>
 pcf_status chunk_attention_impl(const ChunkCall& c, cudaStream_t st) {
     pcf_status s;
     if (any_many(c.dims) && (s = many_rows_impl<D>(c, st)) != PCF_OK) return s;
-    if (c.dims->n_q_heads / c.dims->n_kv_heads > kFewRows) return PCF_OK;
-    return few_tiles(c.dims) == 1 ? few_rows_impl<D, 1>(c, st) : few_rows_impl<D, 2>(c, st);
+    if (c.dims->n_q_heads / c.dims->n_kv_heads > few_limit(c.dims)) return PCF_OK;
+    const int tiles = few_tiles(c.dims);
+    return tiles == 1 ? few_rows_impl<D, 1>(c, st)
+                      : tiles == 2 ? few_rows_impl<D, 2>(c, st) : few_rows_impl<D, 4>(c, st);
 }
 }  // namespace
 

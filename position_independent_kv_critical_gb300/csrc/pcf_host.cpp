@@ -532,7 +532,7 @@ extern "C" pcf_status pcf_chunk_plan_words(const pcf_chunk_dims* dims, int64_t* 
     const pcf_status s = check_chunk_dims(dims);
     if (s != PCF_OK) return s;
     if (!n_words) return PCF_ERR_INVALID_ARG;
-    *n_words = plan_words(dims->n_reqs, kFewWarps * chunk_sms(dims->n_sms), chunk_sms(dims->n_sms));
+    *n_words = plan_words(dims->n_reqs, few_workers(dims), chunk_sms(dims->n_sms));
     return PCF_OK;
 }
 
