@@ -70,10 +70,9 @@ PCF_HOST_DEVICE inline int64_t many_before(int32_t seq, int32_t tpp, int32_t pai
 // Reading the pages then bounds the attention (a key and value of 4 d bytes meet 4 d flops a row, 32
 // flops a byte at most).
 constexpr int kFewRows = 32;
-// warps of a block of the few-row kernel, each a worker, with 1, 2 or 4 tiles of 8 rows: as many as
-// their accumulators leave registers for (twelve of 168, three a sub-partition; eight of 255, as two
-// tiles already spill with 168)
-PCF_HOST_DEVICE constexpr int few_warps(int tiles) { return tiles == 1 ? 12 : 8; }
+// Warps of a block of the few-row kernel, each a worker, with 1, 2 or 4 tiles of 8 rows: twelve of 168
+// registers, three a sub-partition, while the accumulators leave room; eight of 255 with four tiles.
+PCF_HOST_DEVICE constexpr int few_warps(int tiles) { return tiles <= 2 ? 12 : 8; }
 // Units go to the workers in equal runs, worker w from the w-th of `active` equal parts on; with
 // fewer units than workers the first ones take one each, so that a run's parts sit in few blocks.
 PCF_HOST_DEVICE inline int64_t few_active(int64_t units, int32_t workers) { return units < workers ? units : workers; }

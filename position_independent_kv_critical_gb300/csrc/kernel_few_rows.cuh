@@ -11,7 +11,7 @@
 // head, page) order, are dealt to the workers in equal contiguous runs by pcf_chunk_tables, whatever
 // the lengths.  A worker keeps a ring of units in flight (its lane 0 copies K and V of a page by
 // TMA, 128-byte swizzled, and the cos/sin row of the page's first position), so no warp waits for
-// another and an SM has 8 x (stages - 1) units, 130 KB, on the way.
+// another and an SM has more than 100 KB on the way.
 //
 // The keys are rotated in registers: the fragments of mma.m16n8k16's A operand (m = the page's 16 keys,
 // k = d) that ldmatrix gives a thread hold dimensions i and i + d/2 of the same key, so a pair turns
@@ -59,25 +59,29 @@ struct FewSmem {
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kHalf = kPage * 128;                       // 16 rows of 64 elements
     static constexpr int kK = kPage * D * 2;
-    static constexpr int kSlot = 2 * kK;
     static constexpr int kCs = D * 4;                               // cos/sin row
-    static constexpr int kQ = NQ == 4 ? NQ * (D / 32) * 512 : 0;    // B fragments of a warp's rows
+    // B fragments of a warp's rows: in registers with one tile of 8 rows, here with more
+    static constexpr int kQ = NQ > 1 ? NQ * (D / 32) * 512 : 0;
     static constexpr int kTabRow = D * 4 + 64;                      // rows 64 bytes apart modulo 128
     static constexpr int kMl = 2 * 8 * NQ * 8;
     static constexpr int kFixed = kPage * kTabRow + kWarps * (kQ + kMl + 2 * 16) + 1024 + 64;
-    static constexpr int kPerStage = kWarps * (kSlot + kCs + 24);
-    static constexpr int kFit = (232448 - kFixed) / kPerStage;
-    static constexpr int kStages = kFit < 6 ? kFit : 6;
-    static_assert(kStages >= 2, "the ring needs two stages");
-    static_assert(kStages * kSlot >= 8 * NQ * D * 4, "a worker's partial result fits its ring");
-    static constexpr int oCs = kWarps * kStages * kSlot;
-    static constexpr int oTab = oCs + kWarps * kStages * kCs;
+    // stages of the ring: whole units while they fit, then one more key than values
+    static constexpr int kKeyStage = kK + kCs + 16, kValueStage = kK + 8;
+    static constexpr int kRoom = (232448 - kFixed) / kWarps;
+    static constexpr int kUnits = kRoom / (kKeyStage + kValueStage) < 6 ? kRoom / (kKeyStage + kValueStage) : 6;
+    static constexpr int kStagesK = kUnits >= 2 ? kUnits : (kRoom - kUnits * kValueStage) / kKeyStage;
+    static constexpr int kStagesV = kUnits;
+    static_assert(kStagesK >= 2 && kStagesK <= 6 && kStagesV >= 1, "the ring needs two keys and a value");
+    static constexpr int kRing = (kStagesK + kStagesV) * kK;        // a warp's keys, then its values
+    static_assert(kRing >= 8 * NQ * D * 4, "a worker's partial result fits its ring");
+    static constexpr int oCs = kWarps * kRing;
+    static constexpr int oTab = oCs + kWarps * kStagesK * kCs;
     static constexpr int oQ = oTab + kPage * kTabRow;
     static constexpr int oMl = oQ + kWarps * kQ;
     static constexpr int oDesc = oMl + kWarps * kMl;
     static constexpr int oBar = oDesc + kWarps * 2 * 16;
-    static constexpr int oMeta = oBar + kWarps * 2 * kStages * 8;
-    static constexpr int oAbort = oMeta + kWarps * kStages * 4;
+    static constexpr int oMeta = oBar + kWarps * (kStagesK + kStagesV) * 8;
+    static constexpr int oAbort = oMeta + kWarps * kStagesK * 8;
     static constexpr int kBytes = oAbort + 16;
     static constexpr int kAlloc = kBytes + 1024;
     static_assert(kAlloc <= 232448, "more dynamic shared memory than a GB300 block can have");
@@ -142,7 +146,7 @@ template <int D, int NQ>
 __global__ void __launch_bounds__(FewSmem<D, NQ>::kThreads, 1)
 few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const FewParams p) {
     using SM = FewSmem<D, NQ>;
-    constexpr int NS = SM::kStages, WARPS = SM::kWarps, THREADS = SM::kThreads;
+    constexpr int NK = SM::kStagesK, NV = SM::kStagesV, WARPS = SM::kWarps, THREADS = SM::kThreads;
     constexpr int KS = D / 16;       // k steps of K Q^T
     constexpr int MT = D / 16;       // 16-dimension tiles of O^T
     constexpr int J = D / 16;        // 8-frequency chunks: chunk j turns with chunk j + J
@@ -151,16 +155,18 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = lane >> 2, c = lane & 3;     // fragment coordinates
-    uint64_t* bar_k = reinterpret_cast<uint64_t*>(smem + SM::oBar) + warp * 2 * NS;
-    uint64_t* bar_v = bar_k + NS;
-    volatile uint32_t* meta = reinterpret_cast<volatile uint32_t*>(smem + SM::oMeta) + warp * NS;
+    uint64_t* bar_k = reinterpret_cast<uint64_t*>(smem + SM::oBar) + warp * (NK + NV);
+    uint64_t* bar_v = bar_k + NK;
+    // per key slot: exclusion bits, and the pool row its value will be copied from
+    volatile uint32_t* meta = reinterpret_cast<volatile uint32_t*>(smem + SM::oMeta) + warp * NK * 2;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::oAbort);
-    uint8_t* ring = smem + warp * NS * SM::kSlot;
-    uint8_t* ring_cs = smem + SM::oCs + warp * NS * SM::kCs;
+    uint8_t* ring = smem + warp * SM::kRing;
+    uint8_t* ring_v = ring + NK * SM::kK;
+    uint8_t* ring_cs = smem + SM::oCs + warp * NK * SM::kCs;
     float2* s_ml = reinterpret_cast<float2*>(smem + SM::oMl);       // [warp][first, last][row]
     volatile int32_t* s_desc = reinterpret_cast<volatile int32_t*>(smem + SM::oDesc);   // [warp][2][4]
     if (lane == 0) {
-        for (int s = 0; s < 2 * NS; ++s) mbar_init(&bar_k[s], 1);
+        for (int s = 0; s < NK + NV; ++s) mbar_init(&bar_k[s], 1);
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
         for (int i = 0; i < 8; ++i) s_desc[warp * 8 + i] = 0;
@@ -189,13 +195,12 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         *reinterpret_cast<float4*>(smem + SM::oTab + r * SM::kTabRow + f * 16) = make_float4(v.x, v.z, v.y, v.w);
     }
 
-    // ---------------- the copies: unit i of the worker into slot i % NS, its value once its key's
-    // slot is under way (K is free again a whole softmax and P V earlier)
+    // ---------------- the copies: unit i's key into slot i % NK, its value into slot i % NV (a key's slot
+    // is free again a whole softmax and P V earlier)
     FewCursor is{start.x, start.y, start.z, first.x};
     int32_t win_req = -1, win_page = 0;            // the 32 table entries the lanes hold
     int32_t e_ph = 0, e_pos = 0;
     uint32_t e_ex = 0;
-    int32_t y_v = 0;                               // pool row of the value that follows the last key
     auto look_up = [&]() {
         if (is.req != win_req || is.page < win_page || is.page >= win_page + 32) {
             win_req = is.req;
@@ -218,27 +223,29 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     };
     auto issue_k = [&](int i) {
         look_up();
-        const int src = is.page - win_page, s = i % NS;
+        const int src = is.page - win_page, s = i % NK;
         const int32_t ph = __shfl_sync(0xffffffffu, e_ph, src), pos = __shfl_sync(0xffffffffu, e_pos, src);
         const uint32_t ex = __shfl_sync(0xffffffffu, e_ex, src);
-        y_v = (ph * p.hkv + is.kvh) * kPage;
         if (lane == 0) {
-            meta[s] = ex;
+            const int32_t y = (ph * p.hkv + is.kvh) * kPage;
+            meta[2 * s] = ex;
+            meta[2 * s + 1] = (uint32_t)y;
             mbar_arrive_expect_tx(&bar_k[s], SM::kK + SM::kCs);
 #pragma unroll
             for (int hb = 0; hb < D / 64; ++hb)
-                tma_load_2d(ring + s * SM::kSlot + hb * SM::kHalf, &tm_k, &bar_k[s], hb * 64, y_v);
+                tma_load_2d(ring + s * SM::kK + hb * SM::kHalf, &tm_k, &bar_k[s], hb * 64, y);
             bulk_load(ring_cs + s * SM::kCs, p.rope + (int64_t)pos * D, SM::kCs, &bar_k[s]);
         }
         is.step(few, seq, add, p.hkv, p.n);
     };
     auto issue_v = [&](int i) {
-        const int s = i % NS;
+        const int s = i % NV;
         if (lane == 0) {
+            const int32_t y = (int32_t)meta[2 * (i % NK) + 1];
             mbar_arrive_expect_tx(&bar_v[s], SM::kK);
 #pragma unroll
             for (int hb = 0; hb < D / 64; ++hb)
-                tma_load_2d(ring + s * SM::kSlot + SM::kK + hb * SM::kHalf, &tm_v, &bar_v[s], hb * 64, y_v);
+                tma_load_2d(ring_v + s * SM::kK + hb * SM::kHalf, &tm_v, &bar_v[s], hb * 64, y);
         }
     };
     int issued_k = 0, issued_v = 0;
@@ -266,8 +273,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     FewCursor cu{start.x, start.y, start.z, first.x};
     // O^T, columns 2 c and 2 c + 1 of every row tile; the softmax of those two rows over this lane's keys
     float o[NQ][MT][4], m_run[NQ][2], l_run[NQ][2];
-    uint32_t qf[NQ == 4 ? 1 : NQ][2 * J];                                   // chunks of row 8 q + lane / 4
-    uint4* s_q = reinterpret_cast<uint4*>(smem + SM::oQ + warp * SM::kQ);   // NQ == 4: [q][chunk / 4][lane]
+    uint32_t qf[2 * J];                                                     // NQ == 1: chunks of row lane / 4
+    uint4* s_q = reinterpret_cast<uint4*>(smem + SM::oQ + warp * SM::kQ);   // NQ > 1: [q][chunk / 4][lane]
     // where ldmatrix finds a lane's row: K matrices (low chunk, its neighbour, their partners) of keys
     // 0-7, V matrices (keys 0-7, 8-15 of two neighbouring chunks); 16-byte chunk x of a row sits at
     // x ^ (row & 7), so the chunk of a step is one exclusive or away
@@ -314,9 +321,9 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // the first copies go out behind the first rows' loads, not before: 30 MB of them over the
             // whole device would make those wait
             if (i == 0)
-                for (; issued_k < NS && issued_k < n_units; ++issued_k, ++issued_v) {
+                for (; issued_k < NK && issued_k < n_units; ++issued_k) {
                     issue_k(issued_k);
-                    issue_v(issued_v);
+                    if (issued_v < NV) issue_v(issued_v++);
                 }
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
@@ -328,13 +335,13 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     x[q][j] = pack_f16x2_track(fmaf(a0, v.x, -b0 * v.y), fmaf(a1, v.z, -b1 * v.w), big);
                     x[q][j + J] = pack_f16x2_track(fmaf(b0, v.x, a0 * v.y), fmaf(b1, v.z, a1 * v.w), big);
                 }
-                if constexpr (NQ == 4) {
+                if constexpr (NQ > 1) {
 #pragma unroll
                     for (int j = 0; j < 2 * J; j += 4)
                         s_q[(q * (J / 2) + j / 4) * 32 + lane] = make_uint4(x[q][j], x[q][j + 1], x[q][j + 2], x[q][j + 3]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 2 * J; ++j) qf[q][j] = x[q][j];
+                    for (int j = 0; j < 2 * J; ++j) qf[j] = x[q][j];
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
@@ -344,17 +351,18 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 l_run[q][0] = l_run[q][1] = 0.f;
             }
         }
-        const int s = i % NS;
-        ok = mbar_wait(&bar_k[s], (i / NS) & 1, abort_flag);
+        const int s = i % NK, s_v = i % NV;
+        ok = mbar_wait(&bar_k[s], (i / NK) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         ++done_k;
-        uint8_t* sv = ring + s * SM::kSlot + SM::kK;
+        uint8_t* sk = ring + s * SM::kK;
+        uint8_t* sv = ring_v + s_v * SM::kK;
         float4* cs0 = reinterpret_cast<float4*>(ring_cs + s * SM::kCs);
         if (lane < D / 4) {          // the page's cos/sin row, as pairs
             const float4 v = cs0[lane];
             cs0[lane] = make_float4(v.x, v.z, v.y, v.w);
         }
-        const uint32_t ex = meta[s];
+        const uint32_t ex = meta[2 * s];
         const int32_t j0 = cu.page * kPage;                        // the page's first slot
         // every row sees every key of the page: nothing excluded and the page ends at or before the
         // first row's own slot
@@ -367,7 +375,6 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
         if (gone != 0u) {
             // keys that take no part score 0 (whatever they hold) until the softmax drops them
-            uint8_t* sk = ring + s * SM::kSlot;
             for (int q = lane; q < kPage * (D / 8); q += 32) {
                 const int r = q / (D / 8), ch = q % (D / 8);
                 if (gone >> r & 1u)
@@ -382,7 +389,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         for (int q = 0; q < NQ; ++q)
 #pragma unroll
             for (int e = 0; e < 4; ++e) sc[q][0][e] = sc[q][1][e] = 0.f;
-        const uint32_t sk_u = smem_u32(ring) + s * SM::kSlot + k_off;
+        const uint32_t sk_u = smem_u32(sk) + k_off;
         const uint32_t tab = smem_u32(smem + SM::oTab) + row * SM::kTabRow + c * 16, cs_u = smem_u32(cs0) + c * 16;
 #pragma unroll
         for (int jj = 0; jj < J / 2; ++jj) {
@@ -414,16 +421,16 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
                     if (NQ == 4 && q == 2 && n_rows <= 16) break;   // (a branch a tile would cost more than the tile)
-                    if constexpr (NQ == 4) {
+                    if constexpr (NQ > 1) {
                         const uint2 b = reinterpret_cast<const uint2*>(s_q + (q * (J / 2) + j / 4) * 32 + lane)[j / 2 % 2];
                         mma_f16_16816(sc[q][up], a, b.x, b.y);
                     } else {
-                        mma_f16_16816(sc[q][up], a, qf[q][j], qf[q][j + 1]);
+                        mma_f16_16816(sc[q][up], a, qf[j], qf[j + 1]);
                     }
                 }
             }
         }
-        // K has been read (and the cos/sin row rewritten in place): the next key but NS into its slot
+        // K has been read (and the cos/sin row rewritten in place): the next key for its slot
         fence_proxy_async_smem();
         __syncwarp();
         if (issued_k < n_units) issue_k(issued_k++);
@@ -472,7 +479,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             pf[q][0] = transpose8(w0);
             pf[q][1] = transpose8(w1);
         }
-        ok = mbar_wait(&bar_v[s], (i / NS) & 1, abort_flag);
+        ok = mbar_wait(&bar_v[s_v], (i / NV) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         ++done_v;
         if (!clean && gone != 0u) {
@@ -486,7 +493,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             __syncwarp();
         }
         // O^T += V^T P^T
-        const uint32_t sv_u = smem_u32(ring) + s * SM::kSlot + SM::kK + v_off;
+        const uint32_t sv_u = smem_u32(sv) + v_off;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             uint32_t a[4];                                         // (dims, keys): low/high dims, then high keys
@@ -565,8 +572,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     if (!ok && lane == 0)        // an abort: the copies in flight land before the block exits
     {
-        for (int i = done_k; i < issued_k; ++i) mbar_drain(&bar_k[i % NS], (i / NS) & 1);
-        for (int i = done_v; i < issued_v; ++i) mbar_drain(&bar_v[i % NS], (i / NS) & 1);
+        for (int i = done_k; i < issued_k; ++i) mbar_drain(&bar_k[i % NK], (i / NK) & 1);
+        for (int i = done_v; i < issued_v; ++i) mbar_drain(&bar_v[i % NV], (i / NV) & 1);
     }
     __syncthreads();
     // ---------------- join the warps' partial results, run by run
@@ -603,7 +610,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 const float2 ml = s_ml[x * ROWS + r];
                 const float a = ex2(ml.x - ref);
                 const float* src = (in_ring >> x & 1u)
-                                       ? reinterpret_cast<const float*>(smem + (x >> 1) * NS * SM::kSlot)
+                                       ? reinterpret_cast<const float*>(smem + (x >> 1) * SM::kRing)
                                        : p.worker_o + (int64_t)(blockIdx.x * WARPS + (x >> 1)) * ROWS * D;
                 const float4 v = *reinterpret_cast<const float4*>(src + r * D + 4 * f);
                 acc.x += a * v.x;
