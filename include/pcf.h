@@ -395,11 +395,12 @@ pcf_status pcf_chunk_attention_workspace_bytes(const pcf_chunk_dims* dims, size_
  * request's last token and excluded slots may hold anything, infinities and NaN included.
  * q: [max_rows][Hq][d] bf16, q_row_stride elements from row to row (a multiple of 8); out
  * [max_rows][Hq][d] bf16, rows behind the last one left as they are.  ws: device workspace of >=
- * pcf_chunk_attention_workspace_bytes, contents need not be initialised; two calls that may overlap
- * need one each.  Deterministic.  A page outside the pool or a position outside the rope table raises
+ * pcf_chunk_attention_workspace_bytes, contents need not be initialised.  Any number of calls may use
+ * one plan, one behind the other (a model's layers); two calls that may overlap need a plan (a
+ * pcf_chunk_tables call) and a workspace each, as the plan holds counters that a call moves on.  Deterministic.  A page outside the pool or a position outside the rope table raises
  * PCF_ERR_DEVICE_BOUNDS, a rotated query or key beyond fp16 PCF_ERR_DEVICE_RANGE; the call's results
  * must then be discarded. */
-pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, const int32_t* plan, const uint16_t* q, int64_t q_row_stride,
+pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, int32_t* plan, const uint16_t* q, int64_t q_row_stride,
                                const uint16_t* k_pool, const uint16_t* v_pool, const int32_t* block_table,
                                const int32_t* page_pos, const uint16_t* excl, const int32_t* row_pos,
                                const float* rope, uint16_t* out, void* ws, size_t ws_bytes, void* stream);

@@ -14,6 +14,7 @@
 namespace pcf {
 
 constexpr int kMaxReqs = 4096;               // requests of one chunk batch (one block scans them)
+constexpr int kTablesAlone = 4096;           // rows up to which one block writes the tables by itself
 constexpr int32_t kMaxChunkRows = 1 << 22;   // rows of one chunk batch
 constexpr int32_t kMaxTotalPages = 1 << 26;  // pages of all requests together, repeats counted
 
@@ -30,7 +31,8 @@ enum : int {
 // and, for the requests with more, the key tiles their row pairs visit and the pages they hold.
 // Behind them the work split of both kinds: kStartWords words a worker, then kManyWords a block.
 enum : int { CA_SEQ = 0, CA_NEW = 1, CA_ROW = 2, CA_TAKE = 3, CA_START = 4, CA_FEW = 5, CA_MANY = 6, CA_KPAGE = 7, CA_COUNT = 8 };
-// {request, kv head, page, units; its pages, tokens held, new tokens, first row; tag, 0, 0, 0}
+// {request, kv head, page, units; its pages, tokens held, new tokens, first row; tag, and for a block's
+// first worker the blocks its first and last run reach: first, last; last}
 constexpr int kStartWords = 12;
 
 PCF_HOST_DEVICE inline int64_t plan_array(int which, int32_t n_reqs) {
@@ -43,8 +45,12 @@ constexpr int kManyWords = 8;    // {request, kv head, row pair, key tile; units
 PCF_HOST_DEVICE inline int64_t plan_many(int32_t n_reqs, int32_t workers) {
     return plan_starts(n_reqs) + (int64_t)workers * kStartWords;
 }
-PCF_HOST_DEVICE inline int64_t plan_words(int32_t n_reqs, int32_t workers, int32_t blocks) {
+// parts brought of runs that blocks share, one counter a block
+PCF_HOST_DEVICE inline int64_t plan_count(int32_t n_reqs, int32_t workers, int32_t blocks) {
     return plan_many(n_reqs, workers) + (int64_t)blocks * kManyWords;
+}
+PCF_HOST_DEVICE inline int64_t plan_words(int32_t n_reqs, int32_t workers, int32_t blocks) {
+    return plan_count(n_reqs, workers, blocks) + blocks;
 }
 
 // A request with more rows: row pair p holds the tokens [p tpp, (p + 1) tpp) of the chunk, tpp = 256 / g
@@ -102,7 +108,7 @@ inline pcf_status check_chunk_dims(const pcf_chunk_dims* c) {
 // Workspace of pcf_chunk_attention (byte offsets).  Few-row partial results: a worker's first run,
 // when the block has more of it to come, and per block the two runs it shares with its neighbours.
 struct ChunkWs {
-    size_t worker_o, block_o, block_ml, block_desc;
+    size_t worker_o, block_o, block_ml;
     // requests with more rows: rotated queries and keys, the two runs a block shares with its neighbours
     size_t q_rot, k_rot, many_o, many_ml, many_desc, total;
 };
@@ -135,8 +141,7 @@ inline ChunkWs chunk_ws(const pcf_chunk_dims* c) {
     w.worker_o = 0;
     w.block_o = chunk_align(w.worker_o + (size_t)few_workers(c) * rows * d * 4);
     w.block_ml = chunk_align(w.block_o + blocks * 2 * rows * d * 4);
-    w.block_desc = chunk_align(w.block_ml + blocks * 2 * rows * 8);
-    w.q_rot = chunk_align(w.block_desc + blocks * 16);
+    w.q_rot = chunk_align(w.block_ml + blocks * 2 * rows * 8);
     w.total = w.k_rot = w.many_o = w.many_ml = w.many_desc = w.q_rot;
     if (!any_many(c)) return w;
     w.k_rot = chunk_align(w.q_rot + (size_t)c->max_rows * c->n_q_heads * d * 2);

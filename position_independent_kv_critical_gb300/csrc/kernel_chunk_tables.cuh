@@ -30,7 +30,10 @@ constexpr int kTablesThreads = 1024;
 // ceil(s / 16) pages and grows by n: the pages behind are taken from the free list in request
 // order, so a prefix sum of ceil((s + n) / 16) - ceil(s / 16) gives every request its first one;
 // a prefix sum of n gives its first row.  Thread t takes a run of consecutive requests, so one
-// block scan of per-thread sums is enough for any batch size.
+// block scan of per-thread sums is enough for any batch size.  Everything that is looked up by
+// bisection (rows, units, tiles) is kept in shared memory: a probe costs some 30 cycles there and
+// several hundred in L2.  What bounds the call is the chain of dependent loads and barriers; with
+// few rows the same block goes on to write them (one launch, `alone`), else a second launch does.
 // (Sums of refused lengths may be as large as 4096 x 2^22: they stop at 2^29, above every limit.)
 constexpr int kSumLimit = 1 << 29;
 constexpr int kSums = 6;   // rows, pages taken, pages held afterwards, few-row units, key tiles and pages of the others
@@ -52,138 +55,6 @@ __device__ __forceinline__ ChunkWork chunk_work(const TablesParams& p, int32_t s
     return {0, (int32_t)min(tiles, (int64_t)kSumLimit), pages};
 }
 
-__global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const TablesParams p) {
-    __shared__ int s_warp[kSums][kTablesThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    grid_dep_wait();
-    grid_dep_launch();
-    const int per = (p.n + kTablesThreads - 1) / kTablesThreads;
-    const int b0 = min(p.n, tid * per), b1 = min(p.n, b0 + per);
-    int32_t* plan = p.plan;
-    int32_t* o_seq = plan + plan_array(CA_SEQ, p.n);
-    int32_t* o_new = plan + plan_array(CA_NEW, p.n);
-    int32_t* o_row = plan + plan_array(CA_ROW, p.n);
-    int32_t* o_take = plan + plan_array(CA_TAKE, p.n);
-    int32_t* o_start = plan + plan_array(CA_START, p.n);
-    int32_t* o_few = plan + plan_array(CA_FEW, p.n);
-    int32_t* o_many = plan + plan_array(CA_MANY, p.n);
-    int32_t* o_kpage = plan + plan_array(CA_KPAGE, p.n);
-    const int32_t head = p.free_head[0];
-    bool bad = head < 0 || head > p.n_free;
-    int sum[kSums] = {};
-    for (int b = b0; b < b1; ++b) {
-        const int32_t s = p.seq[b], n = p.add[b];
-        if (s < 0 || s > p.max_pages * kPage || n < 0 || n > p.max_chunk || s + n > p.max_pages * kPage) {
-            bad = true;
-            continue;
-        }
-        const int32_t before = pages_of(s), after = pages_of(s + n);
-        int32_t start = 0;
-        if (n > 0) {
-            // a page's slots sit at consecutive positions, so a started page fixes the next one
-            const int32_t last = s > 0 ? p.page_pos[(int64_t)b * p.max_pages + before - 1] : -kPage;
-            start = last < -kPage || last > p.max_pos ? -1 : last + (s % kPage ? s % kPage : kPage);
-            if (p.next_pos) {
-                const int32_t want = p.next_pos[b];
-                if (s % kPage && want != start) bad = true;
-                start = want;
-            }
-            // every slot of the last page has a row in the cos/sin table
-            if (start < 0 || start > p.max_pos || start + (after * kPage - s) > p.max_pos) bad = true;
-        }
-        sum[0] = sat_add(sum[0], n);
-        sum[1] = sat_add(sum[1], after - before);
-        sum[2] = sat_add(sum[2], after);
-        const ChunkWork work = chunk_work(p, s, n);
-        sum[3] = sat_add(sum[3], work.few);
-        sum[4] = sat_add(sum[4], work.many);
-        sum[5] = sat_add(sum[5], work.pages);
-        o_seq[b] = s;
-        o_new[b] = n;
-        o_start[b] = start;
-    }
-    const bool any_bad = __syncthreads_or(bad);
-    int pre[kSums], tot[kSums];
-#pragma unroll
-    for (int i = 0; i < kSums; ++i) {
-        int x = any_bad ? 0 : sum[i];
-        sum[i] = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x = sat_add(x, y);
-        }
-        pre[i] = x;
-        if (lane == 31) s_warp[i][warp] = x;
-    }
-    __syncthreads();
-    if (warp < kSums) {
-        int x = s_warp[warp][lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x = sat_add(x, y);
-        }
-        s_warp[warp][lane] = x;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kSums; ++i) {
-        tot[i] = s_warp[i][31];
-        pre[i] += (warp ? s_warp[i][warp - 1] : 0) - sum[i];
-    }
-    bad = any_bad || tot[0] > p.max_rows || tot[2] > p.max_total_pages || tot[1] > p.n_free - head || tot[3] >= kSumLimit ||
-          tot[4] >= kSumLimit;
-    if (!bad) {   // the pages about to be taken exist
-        bool out = false;
-        for (int i = tid; i < tot[1]; i += kTablesThreads) {
-            const int32_t ph = p.free_pages[head + i];
-            out |= ph < 0 || ph >= p.n_phys;
-        }
-        bad = out;
-    }
-    bad = __syncthreads_or(bad);
-    int32_t row = pre[0], take = pre[1], few = pre[3], many = pre[4], kpage = pre[5];
-    for (int b = b0; b < b1; ++b) {
-        if (bad) {
-            o_seq[b] = p.seq[b];
-            o_new[b] = 0;
-            o_start[b] = 0;
-        }
-        o_row[b] = bad ? 0 : row;
-        o_take[b] = bad ? 0 : take;
-        o_few[b] = bad ? 0 : few;
-        o_many[b] = bad ? 0 : many;
-        o_kpage[b] = bad ? 0 : kpage;
-        if (!bad) {
-            const ChunkWork work = chunk_work(p, o_seq[b], o_new[b]);
-            few += work.few;
-            many += work.many;
-            kpage += work.pages;
-            row += o_new[b];
-            take += pages_of(o_seq[b] + o_new[b]) - pages_of(o_seq[b]);
-        }
-    }
-    if (tid == 0) {
-        plan[C_TAG] = p.tag;
-        plan[C_ROWS] = bad ? 0 : tot[0];
-        plan[C_HEAD] = head;
-        plan[C_TAKEN] = bad ? 0 : tot[1];
-        o_row[p.n] = bad ? 0 : tot[0];
-        o_take[p.n] = bad ? 0 : tot[1];
-        o_few[p.n] = bad ? 0 : tot[3];
-        o_many[p.n] = bad ? 0 : tot[4];
-        o_kpage[p.n] = bad ? 0 : tot[5];
-        if (bad) set_dev_error(kDevErrBounds);
-    }
-}
-
-__device__ __forceinline__ bool plan_fits(const int32_t* plan, int32_t tag) {
-    const bool ok = plan[C_TAG] == tag;
-    if (!ok) set_dev_error(kDevErrBounds);
-    return ok;
-}
-
 // Request of row i: the last b with base[b] <= i (requests without rows are passed over).
 __device__ __forceinline__ int row_request(const int32_t* __restrict__ base, int n, int32_t i) {
     int lo = 0, hi = n - 1;
@@ -194,73 +65,25 @@ __device__ __forceinline__ int row_request(const int32_t* __restrict__ base, int
     return lo;
 }
 
-// The tables from the plan, one thread a row: token s + t of its request sits in page (s + t) / 16,
-// at slot (s + t) % 16; the row that starts a page enters it.  Nothing here reads what the call may
-// overwrite in place (the lengths and the list's head come from the plan), and a table entry that
-// is read (a page begun earlier) is never one that is written.
-constexpr int kRowsThreads = 256;
-__global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const TablesParams p) {
-    grid_dep_wait();
-    grid_dep_launch();
-    const int32_t* plan = p.plan;
-    const int32_t* seq = plan + plan_array(CA_SEQ, p.n);
-    const int32_t* add = plan + plan_array(CA_NEW, p.n);
-    const int32_t* base = plan + plan_array(CA_ROW, p.n);
-    const int32_t* take = plan + plan_array(CA_TAKE, p.n);
-    const int32_t* start = plan + plan_array(CA_START, p.n);
-    const int32_t rows = plan[C_ROWS], head = plan[C_HEAD];
-    const int32_t i = blockIdx.x * kRowsThreads + threadIdx.x;
-    const int32_t step = gridDim.x * kRowsThreads;
-    for (int32_t b = i; b <= p.n; b += step) {
-        p.row_base[b] = base[b];
-        if (b < p.n) p.seq_out[b] = seq[b] + add[b];
-        else p.head_out[0] = head + plan[C_TAKEN];
-    }
-    // the few-row requests' units, dealt to the workers in equal runs
-    const int32_t* few = plan + plan_array(CA_FEW, p.n);
-    const int64_t units = few[p.n], active = few_active(units, p.workers);
-    for (int32_t w = i; w < p.workers; w += step) {
-        const int64_t u0 = w < active ? w * units / active : 0, u1 = w < active ? (w + 1) * units / active : 0;
-        int4 e = make_int4(0, 0, 0, (int)(u1 - u0)), f = make_int4(1, 0, 0, 0);
-        if (e.w > 0) {
-            const int b = row_request(few, p.n, (int32_t)u0);
-            f = make_int4(pages_of(seq[b] + add[b]), seq[b], add[b], base[b]);
-            const int32_t local = (int32_t)u0 - few[b];
-            e.x = b;
-            e.y = local / f.x;
-            e.z = local % f.x;
-        }
-        int4* dst = reinterpret_cast<int4*>(p.plan + plan_starts(p.n)) + 3 * w;
-        dst[0] = e;
-        dst[1] = f;
-        dst[2] = make_int4(p.tag, 0, 0, 0);
-    }
-    // the others' key tiles, in (request, kv head, row pair, tile) order, dealt to the blocks
-    const int32_t* many = plan + plan_array(CA_MANY, p.n);
-    const int64_t tiles = many[p.n], on = few_active(tiles, p.blocks);
-    const int g = p.hq / p.hkv, tpp = 2 * kTileRows / g;
-    for (int32_t w = i; w < p.blocks; w += step) {
-        const int64_t u0 = w < on ? w * tiles / on : 0, u1 = w < on ? (w + 1) * tiles / on : 0;
-        int4 e = make_int4(0, 0, 0, 0), f = make_int4((int)(u1 - u0), p.tag, 0, 0);
-        if (f.x > 0) {
-            const int b = row_request(many, p.n, (int32_t)u0);
-            const int32_t per = (many[b + 1] - many[b]) / p.hkv;
-            int32_t local = (int32_t)u0 - many[b];
-            e.x = b;
-            e.y = local / per;
-            local %= per;
-            int lo = 0, hi = many_pairs(add[b], tpp) - 1;   // the pair the tile falls into
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (many_before(seq[b], tpp, mid) <= local) lo = mid; else hi = mid - 1;
-            }
-            e.z = lo;
-            e.w = local - (int32_t)many_before(seq[b], tpp, lo);
-        }
-        int4* dst = reinterpret_cast<int4*>(p.plan + plan_many(p.n, p.workers)) + 2 * w;
-        dst[0] = e;
-        dst[1] = f;
-    }
+// The plan's per-request arrays, n + 1 words each, in shared memory (order of the CA_ enumeration).
+__device__ __forceinline__ int32_t* plan_words_of(int32_t* arrays, int which, int32_t n) {
+    return arrays + (int64_t)which * (n + 1);
+}
+
+// Everything that follows from the plan, thread i of `step`: the tables' rows -- token s + t of a
+// request sits in page (s + t) / 16, at slot (s + t) % 16; the row that starts a page enters it -- and
+// the attention's work split.  Nothing here reads what the call may overwrite in place (lengths and
+// list head come from the plan), and a table entry that is read (a page begun earlier) is never one
+// that is written.
+__device__ __forceinline__ void write_rows(const TablesParams& p, int32_t* arrays, int32_t rows, int32_t head,
+                                           int32_t taken, int32_t i, int32_t step) {
+    const int32_t* seq = plan_words_of(arrays, CA_SEQ, p.n);
+    const int32_t* add = plan_words_of(arrays, CA_NEW, p.n);
+    const int32_t* base = plan_words_of(arrays, CA_ROW, p.n);
+    const int32_t* take = plan_words_of(arrays, CA_TAKE, p.n);
+    const int32_t* start = plan_words_of(arrays, CA_START, p.n);
+    const int32_t* few = plan_words_of(arrays, CA_FEW, p.n);
+    const int32_t* many = plan_words_of(arrays, CA_MANY, p.n);
     for (int32_t r = i; r < p.max_rows; r += step) {
         int32_t slot = -1, pos = -1;
         if (r < rows) {
@@ -287,6 +110,210 @@ __global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const TablesPa
         p.slot_map[r] = slot;
         p.row_pos[r] = pos;
     }
+    for (int32_t b = i; b <= p.n; b += step) {
+        p.row_base[b] = base[b];
+        if (b < p.n) p.seq_out[b] = seq[b] + add[b];
+        else p.head_out[0] = head + taken;
+    }
+    // the few-row requests' units, dealt to the workers in equal runs
+    const int64_t units = few[p.n], active = few_active(units, p.workers);
+    const int per = p.workers / p.blocks;
+    for (int32_t w = i; w < p.workers; w += step) {
+        const int64_t u0 = w < active ? w * units / active : 0, u1 = w < active ? (w + 1) * units / active : 0;
+        int4 e = make_int4(0, 0, 0, (int)(u1 - u0)), f = make_int4(1, 0, 0, 0), share = make_int4(p.tag, 0, 0, 0);
+        if (e.w > 0) {
+            const int b = row_request(few, p.n, (int32_t)u0);
+            f = make_int4(pages_of(seq[b] + add[b]), seq[b], add[b], base[b]);
+            const int32_t local = (int32_t)u0 - few[b];
+            e.x = b;
+            e.y = local / f.x;
+            e.z = local % f.x;
+            if (w % per == 0) {
+                // the block holds the units [u0, end): the owner of a unit is the last worker whose first
+                // unit is not behind it
+                auto owner = [&](int64_t u) { return (int)((((u + 1) * active - 1) / units) / per); };
+                const int64_t a = few[b] + e.y * f.x, end = w + per < active ? (w + per) * units / active : units;
+                share.y = owner(a);
+                share.z = owner(a + f.x - 1);
+                const int bl = row_request(few, p.n, (int32_t)end - 1);
+                const int64_t pages = pages_of(seq[bl] + add[bl]);
+                share.w = owner(few[bl] + (end - 1 - few[bl]) / pages * pages + pages - 1);
+            }
+        }
+        int4* dst = reinterpret_cast<int4*>(p.plan + plan_starts(p.n)) + 3 * w;
+        dst[0] = e;
+        dst[1] = f;
+        dst[2] = share;
+    }
+    // the others' key tiles, in (request, kv head, row pair, tile) order, dealt to the blocks
+    const int64_t tiles = many[p.n], on = few_active(tiles, p.blocks);
+    const int g = p.hq / p.hkv, tpp = 2 * kTileRows / g;
+    for (int32_t w = i; w < p.blocks; w += step) {
+        p.plan[plan_count(p.n, p.workers, p.blocks) + w] = 0;
+        const int64_t u0 = w < on ? w * tiles / on : 0, u1 = w < on ? (w + 1) * tiles / on : 0;
+        int4 e = make_int4(0, 0, 0, 0), f = make_int4((int)(u1 - u0), p.tag, 0, 0);
+        if (f.x > 0) {
+            const int b = row_request(many, p.n, (int32_t)u0);
+            const int32_t per_head = (many[b + 1] - many[b]) / p.hkv;
+            int32_t local = (int32_t)u0 - many[b];
+            e.x = b;
+            e.y = local / per_head;
+            local %= per_head;
+            int lo = 0, hi = many_pairs(add[b], tpp) - 1;   // the pair the tile falls into
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (many_before(seq[b], tpp, mid) <= local) lo = mid; else hi = mid - 1;
+            }
+            e.z = lo;
+            e.w = local - (int32_t)many_before(seq[b], tpp, lo);
+        }
+        int4* dst = reinterpret_cast<int4*>(p.plan + plan_many(p.n, p.workers)) + 2 * w;
+        dst[0] = e;
+        dst[1] = f;
+    }
+}
+
+__global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const TablesParams p, int alone) {
+    extern __shared__ int32_t s_arrays[];
+    __shared__ int s_warp[kSums][kTablesThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int per = (p.n + kTablesThreads - 1) / kTablesThreads;
+    const int b0 = min(p.n, tid * per), b1 = min(p.n, b0 + per);
+    int32_t* plan = p.plan;
+    int32_t* o_seq = plan_words_of(s_arrays, CA_SEQ, p.n);
+    int32_t* o_new = plan_words_of(s_arrays, CA_NEW, p.n);
+    int32_t* o_row = plan_words_of(s_arrays, CA_ROW, p.n);
+    int32_t* o_take = plan_words_of(s_arrays, CA_TAKE, p.n);
+    int32_t* o_start = plan_words_of(s_arrays, CA_START, p.n);
+    int32_t* o_few = plan_words_of(s_arrays, CA_FEW, p.n);
+    int32_t* o_many = plan_words_of(s_arrays, CA_MANY, p.n);
+    int32_t* o_kpage = plan_words_of(s_arrays, CA_KPAGE, p.n);
+    const int32_t head = p.free_head[0];
+    bool bad = head < 0 || head > p.n_free;
+    int sum[kSums] = {};
+    for (int b = b0; b < b1; ++b) {
+        const int32_t s = p.seq[b], n = p.add[b];
+        const int32_t want = p.next_pos ? p.next_pos[b] : 0;
+        o_seq[b] = s;
+        o_new[b] = 0;
+        o_start[b] = 0;
+        if (s < 0 || s > p.max_pages * kPage || n < 0 || n > p.max_chunk || s + n > p.max_pages * kPage) {
+            bad = true;
+            continue;
+        }
+        const int32_t before = pages_of(s), after = pages_of(s + n);
+        int32_t start = 0;
+        if (n > 0) {
+            // a page's slots sit at consecutive positions, so a started page fixes the next one
+            const int32_t last = s > 0 ? p.page_pos[(int64_t)b * p.max_pages + before - 1] : -kPage;
+            start = last < -kPage || last > p.max_pos ? -1 : last + (s % kPage ? s % kPage : kPage);
+            if (p.next_pos) {
+                if (s % kPage && want != start) bad = true;
+                start = want;
+            }
+            // every slot of the last page has a row in the cos/sin table
+            if (start < 0 || start > p.max_pos || start + (after * kPage - s) > p.max_pos) bad = true;
+        }
+        sum[0] = sat_add(sum[0], n);
+        sum[1] = sat_add(sum[1], after - before);
+        sum[2] = sat_add(sum[2], after);
+        const ChunkWork work = chunk_work(p, s, n);
+        sum[3] = sat_add(sum[3], work.few);
+        sum[4] = sat_add(sum[4], work.many);
+        sum[5] = sat_add(sum[5], work.pages);
+        o_new[b] = n;
+        o_start[b] = start;
+    }
+    int pre[kSums], tot[kSums];
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) {
+        int x = sum[i];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x = sat_add(x, y);
+        }
+        pre[i] = x;
+        if (lane == 31) s_warp[i][warp] = x;
+    }
+    bad = __syncthreads_or(bad);
+    if (warp < kSums) {
+        int x = s_warp[warp][lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x = sat_add(x, y);
+        }
+        s_warp[warp][lane] = x;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) {
+        tot[i] = s_warp[i][31];
+        pre[i] += (warp ? s_warp[i][warp - 1] : 0) - sum[i];
+    }
+    bad = bad || tot[0] > p.max_rows || tot[2] > p.max_total_pages || tot[1] > p.n_free - head || tot[3] >= kSumLimit ||
+          tot[4] >= kSumLimit;
+    if (!bad) {   // the pages about to be taken exist
+        for (int i = tid; i < tot[1]; i += kTablesThreads) {
+            const int32_t ph = p.free_pages[head + i];
+            bad |= ph < 0 || ph >= p.n_phys;
+        }
+    }
+    bad = __syncthreads_or(bad);
+    if (bad) {    // nothing is done: no rows, no work
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) pre[i] = tot[i] = 0;
+        if (tid == 0) set_dev_error(kDevErrBounds);
+    }
+    for (int b = b0; b < b1; ++b) {
+        if (bad) o_new[b] = 0;
+        o_row[b] = pre[0];
+        o_take[b] = pre[1];
+        o_few[b] = pre[3];
+        o_many[b] = pre[4];
+        o_kpage[b] = pre[5];
+        if (!bad) {
+            const ChunkWork work = chunk_work(p, o_seq[b], o_new[b]);
+            pre[0] += o_new[b];
+            pre[1] += pages_of(o_seq[b] + o_new[b]) - pages_of(o_seq[b]);
+            pre[3] += work.few;
+            pre[4] += work.many;
+            pre[5] += work.pages;
+        }
+    }
+    if (tid == 0) {
+        o_seq[p.n] = o_new[p.n] = o_start[p.n] = 0;
+        o_row[p.n] = tot[0];
+        o_take[p.n] = tot[1];
+        o_few[p.n] = tot[3];
+        o_many[p.n] = tot[4];
+        o_kpage[p.n] = tot[5];
+        *reinterpret_cast<int4*>(plan) = make_int4(p.tag, tot[0], head, tot[1]);   // C_TAG, C_ROWS, C_HEAD, C_TAKEN
+    }
+    __syncthreads();
+    for (int i = tid; i < CA_COUNT * (p.n + 1); i += kTablesThreads) plan[C_HEADER + i] = s_arrays[i];
+    if (alone) write_rows(p, s_arrays, tot[0], head, tot[1], tid, kTablesThreads);
+}
+
+// A plan made for other dims (or by no pcf_chunk_tables call at all) is refused.
+__device__ __forceinline__ bool plan_fits(const int32_t* plan, int32_t tag) {
+    const bool ok = plan[C_TAG] == tag;
+    if (!ok) set_dev_error(kDevErrBounds);
+    return ok;
+}
+
+constexpr int kRowsThreads = 256;
+__global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const TablesParams p) {
+    extern __shared__ int32_t s_arrays[];
+    grid_dep_wait();
+    grid_dep_launch();
+    for (int i = threadIdx.x; i < CA_COUNT * (p.n + 1); i += kRowsThreads) s_arrays[i] = p.plan[C_HEADER + i];
+    const int4 h = *reinterpret_cast<const int4*>(p.plan);
+    __syncthreads();
+    write_rows(p, s_arrays, h.y, h.z, h.w, blockIdx.x * kRowsThreads + threadIdx.x, gridDim.x * kRowsThreads);
 }
 
 // ------------------------------------------------------------------ append

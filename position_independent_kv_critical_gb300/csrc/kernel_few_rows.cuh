@@ -26,8 +26,8 @@
 //
 // A run of a (request, kv head) that lies within one worker is written out directly.  Otherwise the
 // block joins its warps' partial results through shared memory and passes on at most two (the run
-// it shares with the block before and with the block behind), which few_join_kernel adds up: every
-// sum in a fixed order, so results do not depend on timing.
+// it shares with the block before and with the block behind); the block that brings a run's last part
+// adds them up.  Every sum has a fixed order, so results do not depend on timing.
 #pragma once
 #include "chunk_format.h"
 #include "kernel_chunk_tables.cuh"
@@ -47,7 +47,7 @@ struct FewParams {
     float* worker_o;            // [workers][8 NQ][D]
     float* block_o;             // [blocks][2][8 NQ][D]
     float2* block_ml;           // [blocks][2][8 NQ]
-    int4* block_desc;           // [blocks]: a run that starts here and goes on: {last block << 8 | 255, rows, kv head, first row}
+    int32_t* count;             // [blocks] parts brought of the run that begins in a block and goes on
     int64_t q_stride;
     int32_t n, max_pages, max_rows, hq, hkv, n_phys, max_pos, blocks, tag;
 };
@@ -82,9 +82,10 @@ struct FewSmem {
     static constexpr int oBar = oDesc + kWarps * 2 * 16;
     static constexpr int oMeta = oBar + kWarps * (kStagesK + kStagesV) * 8;
     static constexpr int oAbort = oMeta + kWarps * kStagesK * 8;
-    static constexpr int kBytes = oAbort + 16;
+    static constexpr int kBytes = oAbort + 16;                      // the abort flag, two flags of the join
     static constexpr int kAlloc = kBytes + 1024;
     static_assert(kAlloc <= 232448, "more dynamic shared memory than a GB300 block can have");
+    static_assert(kThreads * 24 <= kWarps * kRing, "the join's shared memory is the ring's");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
@@ -125,6 +126,25 @@ __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], const uint32_t (&a
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four partial results of a row (maximum and sum; weighted values) joined onto a running one; a part
+// without a maximum adds nothing.
+__device__ __forceinline__ void add_parts(const float2 (&ml)[4], const float4 (&v)[4], float& top, float& l, float4& acc) {
+    const float now = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), top);
+    const float ref = now == -INFINITY ? 0.f : now, old = ex2(top - ref);
+    top = now;
+    l *= old;
+    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = ex2(ml[i].x - ref);
+        acc.x += a * v[i].x;
+        acc.y += a * v[i].y;
+        acc.z += a * v[i].z;
+        acc.w += a * v[i].w;
+        l += a * ml[i].y;
+    }
 }
 
 // Where a worker stands in the units: page `page` of `pages` of kv head `kvh` of request `req`.
@@ -185,7 +205,9 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const int worker = blockIdx.x * WARPS + warp;
     const int4* entry = reinterpret_cast<const int4*>(plan + plan_starts(p.n)) + 3 * worker;
     const int4 start = entry[0], first = entry[1];
+    // {tag; first and last block of the run this block's first unit belongs to, last of its last unit's}
     const int32_t tag = entry[2].x;
+    const int4 share = reinterpret_cast<const int4*>(plan + plan_starts(p.n))[3 * blockIdx.x * WARPS + 2];
     if (tag != p.tag) set_dev_error(kDevErrBounds);
     const int n_units = tag == p.tag ? start.w : 0;
     // cos/sin of 0..15 steps, for everyone, as pairs: (cos, cos', sin, sin') of two frequencies
@@ -274,7 +296,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     // O^T, columns 2 c and 2 c + 1 of every row tile; the softmax of those two rows over this lane's keys
     float o[NQ][MT][4], m_run[NQ][2], l_run[NQ][2];
     uint32_t qf[2 * J];                                                     // NQ == 1: chunks of row lane / 4
-    uint4* s_q = reinterpret_cast<uint4*>(smem + SM::oQ + warp * SM::kQ);   // NQ > 1: [q][chunk / 4][lane]
+    uint4* s_q = reinterpret_cast<uint4*>(smem + SM::oQ + warp * SM::kQ);   // NQ > 1, see below
     // where ldmatrix finds a lane's row: K matrices (low chunk, its neighbour, their partners) of keys
     // 0-7, V matrices (keys 0-7, 8-15 of two neighbouring chunks); 16-byte chunk x of a row sits at
     // x ^ (row & 7), so the chunk of a step is one exclusive or away
@@ -336,9 +358,11 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     x[q][j + J] = pack_f16x2_track(fmaf(b0, v.x, a0 * v.y), fmaf(b1, v.z, a1 * v.w), big);
                 }
                 if constexpr (NQ > 1) {
+                    // [pair of tiles][k step][lane]: both chunks of the k step, both tiles
 #pragma unroll
-                    for (int j = 0; j < 2 * J; j += 4)
-                        s_q[(q * (J / 2) + j / 4) * 32 + lane] = make_uint4(x[q][j], x[q][j + 1], x[q][j + 2], x[q][j + 3]);
+                    for (int ks = 0; ks < KS; ++ks)
+                        reinterpret_cast<uint2*>(s_q + ((q >> 1) * KS + ks) * 32 + lane)[q & 1] =
+                            make_uint2(x[q][2 * ks], x[q][2 * ks + 1]);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 2 * J; ++j) qf[j] = x[q][j];
@@ -417,15 +441,16 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
             for (int up = 0; up < 2; ++up) {
                 const uint32_t a[4] = {kf[0][2 * up], kf[1][2 * up], kf[0][2 * up + 1], kf[1][2 * up + 1]};
-                const int j = 2 * jj + up * J;                     // first chunk of the k step
+                const int ks = jj + up * (KS / 2);
+                if constexpr (NQ == 1) {
+                    mma_f16_16816(sc[0][up], a, qf[2 * ks], qf[2 * ks + 1]);
+                } else {
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    if (NQ == 4 && q == 2 && n_rows <= 16) break;   // (a branch a tile would cost more than the tile)
-                    if constexpr (NQ > 1) {
-                        const uint2 b = reinterpret_cast<const uint2*>(s_q + (q * (J / 2) + j / 4) * 32 + lane)[j / 2 % 2];
+                    for (int q = 0; q < NQ; q += 2) {
+                        if (NQ == 4 && q == 2 && n_rows <= 16) break;   // (a branch a tile would cost more than the tile)
+                        const uint4 b = s_q[((q >> 1) * KS + ks) * 32 + lane];
                         mma_f16_16816(sc[q][up], a, b.x, b.y);
-                    } else {
-                        mma_f16_16816(sc[q][up], a, qf[j], qf[j + 1]);
+                        mma_f16_16816(sc[q + 1][up], a, b.z, b.w);
                     }
                 }
             }
@@ -578,7 +603,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     __syncthreads();
     // ---------------- join the warps' partial results, run by run
     const bool aborted = *abort_flag != 0;
-    int4 desc = make_int4(0, 0, 0, 0);
+    int rows_of[2] = {0, 0}, kvh_of[2] = {0, 0}, base_of[2] = {0, 0};   // of the runs other blocks hold parts of
     // bit 2 w: what warp w ends of a run begun before it; bit 2 w + 1: what it leaves open
     const int32_t state = lane < 2 * WARPS ? s_desc[lane * 4] : 0;
     const uint32_t present = __ballot_sync(0xffffffffu, state & 1), closing = __ballot_sync(0xffffffffu, state & 2);
@@ -586,38 +611,35 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     // a run's first part here: one left open, or the block's very first part where that is an end
     const uint32_t lowest = present & (0u - present);
     const uint32_t before = lowest & 0x55555555u;
-    for (uint32_t todo = aborted ? 0u : (present & 0xAAAAAAAAu) | before; todo != 0u; todo &= todo - 1u) {
+    for (uint32_t todo = (present & 0xAAAAAAAAu) | before; todo != 0u; todo &= todo - 1u) {
         const int sb = __ffs(todo) - 1;
         const bool from_before = (before >> sb & 1u) != 0u;
-        uint32_t parts = 1u << sb;
+        // its parts: this one, then what the warps behind (each has units, up to the last that does) end
+        int np = 1;
         bool ended = (closing >> sb & 1u) != 0u;
-        for (uint32_t rest = present & 0x55555555u & ~((2u << sb) - 1u); rest != 0u && !ended; rest &= rest - 1u) {
-            parts |= rest & (0u - rest);
-            ended = (closing & rest & (0u - rest)) != 0u;
-        }
+        for (int w = (sb >> 1) + 1; w < WARPS && !ended && (present >> 2 * w & 1u); ++w, ++np)
+            ended = (closing >> 2 * w & 1u) != 0u;
         const int32_t req = s_desc[sb * 4 + 1], kvh = s_desc[sb * 4 + 2];
         const int rows_run = s_desc[sb * 4 + 3] & 0xFF, rb = s_desc[sb * 4 + 3] >> 8;
         const int slot = blockIdx.x * 2 + (from_before ? 0 : 1);
         for (int idx = tid; idx < rows_run * (D / 4); idx += THREADS) {
             const int r = idx / (D / 4), f = idx % (D / 4);
-            float top = -INFINITY;
-            for (uint32_t m = parts; m != 0u; m &= m - 1u) top = fmaxf(top, s_ml[(__ffs(m) - 1) * ROWS + r].x);
-            const float ref = top == -INFINITY ? 0.f : top;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float l = 0.f;
-            for (uint32_t m = parts; m != 0u; m &= m - 1u) {
-                const int x = __ffs(m) - 1;
-                const float2 ml = s_ml[x * ROWS + r];
-                const float a = ex2(ml.x - ref);
-                const float* src = (in_ring >> x & 1u)
-                                       ? reinterpret_cast<const float*>(smem + (x >> 1) * SM::kRing)
-                                       : p.worker_o + (int64_t)(blockIdx.x * WARPS + (x >> 1)) * ROWS * D;
-                const float4 v = *reinterpret_cast<const float4*>(src + r * D + 4 * f);
-                acc.x += a * v.x;
-                acc.y += a * v.y;
-                acc.z += a * v.z;
-                acc.w += a * v.w;
-                l += a * ml.y;
+            float top = -INFINITY, l = 0.f;
+            for (int x0 = 0; x0 < np; x0 += 4) {           // four parts' loads in flight
+                float2 ml[4];
+                float4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // (behind the last part: that part again, without weight -- other memory may hold NaN)
+                    const int at = min(x0 + i, np - 1), w = (sb >> 1) + at, x = at == 0 ? sb : 2 * w;
+                    const float* src = (in_ring >> x & 1u) ? reinterpret_cast<const float*>(smem + w * SM::kRing)
+                                                           : p.worker_o + (int64_t)(blockIdx.x * WARPS + w) * ROWS * D;
+                    ml[i] = s_ml[x * ROWS + r];
+                    v[i] = *reinterpret_cast<const float4*>(src + r * D + 4 * f);
+                    if (x0 + i >= np) ml[i].x = -INFINITY;
+                }
+                add_parts(ml, v, top, l, acc);
             }
             if (!from_before && ended) {
                 const float inv = l > 0.f ? 1.0f / l : 0.f;
@@ -628,92 +650,81 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 if (f == 0) p.block_ml[slot * ROWS + r] = make_float2(top, l);
             }
         }
-        if (!from_before && !ended) {
-            // the block that holds the run's last unit u: u's owner is the last worker whose first unit
-            // is not behind it
-            const int64_t units = few[p.n], active = few_active(units, p.blocks * WARPS);
-            const int64_t u = few[req] + (int64_t)(kvh + 1) * pages_of(seq[req] + add[req]) - 1;
-            desc = make_int4(((int)(((u + 1) * active - 1) / units) / WARPS) << 8 | 0xFF, rows_run, kvh, rb);
+        if (from_before || !ended) {
+            const int which = from_before ? 0 : 1;
+            rows_of[which] = rows_run;
+            kvh_of[which] = kvh;
+            base_of[which] = rb;
         }
     }
-    if (tid == 0) p.block_desc[blockIdx.x] = desc;
-}
-
-// Block j adds up the run that block j of few_rows_kernel began and left open: its part, then those of
-// the blocks behind up to the one that holds the run's last unit.  A run of a single long request has
-// a part in every eighth block or so and few rows, so the parts are taken by groups of threads side by
-// side, four loads in flight a thread, and the groups joined in shared memory in their order.
-constexpr int kJoinThreads = 512;
-template <int D, int NQ>
-__global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const FewParams p) {
-    constexpr int ROWS = 8 * NQ;
-    __shared__ float4 s_acc[kJoinThreads];
-    __shared__ float2 s_w[kJoinThreads];
-    grid_dep_wait();
-    grid_dep_launch();
-    const int j = blockIdx.x;
-    const int4 d = p.block_desc[j];
-    if (d.x == 0) return;
-    const int last = d.x >> 8, rows = d.y, kvh = d.z, rb = d.w;
-    const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
-    const int cols = rows * (D / 4);
-    const int groups = max(1, min(kJoinThreads / cols, last - j + 1));
-    for (int c0 = 0; c0 < cols; c0 += kJoinThreads) {
-        const int grp = threadIdx.x / min(cols, kJoinThreads), idx = c0 + threadIdx.x - grp * min(cols, kJoinThreads);
-        const int r = idx / (D / 4), f = idx % (D / 4);
-        const bool mine = grp < groups && idx < cols;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float top = -INFINITY, l = 0.f;
-        if (mine)
-            for (int b0 = j + grp; b0 <= last; b0 += 4 * groups) {
-                float2 ml[4];
-                float4 v[4];
+    // ---------------- runs that several blocks share: whoever brings the last part adds them up.  The
+    // parts lie in the order of the blocks whoever adds them, so the sum does not depend on timing.
+    // The counters are the plan's: cleared with it, and a multiple of the parts behind every call.
+    int* s_last = reinterpret_cast<int*>(smem + SM::oAbort) + 1;
+    if (rows_of[0] + rows_of[1] == 0) return;         // (uniform over the block)
+    __syncthreads();
+    if (tid < 2 && rows_of[tid] > 0) {
+        const int from = tid == 0 ? share.y : (int)blockIdx.x, n = (tid == 0 ? share.z : share.w) - from + 1;
+        s_last[tid] = atomic_add_acq_rel_gpu(p.count + from, 1) % n == n - 1 ? 1 : 0;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const int rows = which ? rows_of[1] : rows_of[0];
+        if (rows == 0 || s_last[which] == 0 || aborted) continue;
+        const int from = which ? (int)blockIdx.x : share.y, to = which ? share.w : share.z;
+        const int kvh = which ? kvh_of[1] : kvh_of[0], rb = which ? base_of[1] : base_of[0];
+        // groups of threads take the parts side by side, four loads in flight a thread, and are joined in
+        // shared memory in their order
+        float4* s_acc = reinterpret_cast<float4*>(smem);
+        float2* s_w = reinterpret_cast<float2*>(smem + THREADS * 16);
+        const int cols = rows * (D / 4), width = min(cols, THREADS);
+        const int groups = max(1, min(THREADS / cols, to - from + 1));
+        for (int c0 = 0; c0 < cols; c0 += THREADS) {
+            const int grp = tid / width, idx = c0 + tid - grp * width;
+            const int r = idx / (D / 4), f = idx % (D / 4);
+            const bool mine = grp < groups && idx < cols;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float top = -INFINITY, l = 0.f;
+            if (mine)
+                for (int b0 = from + grp; b0 <= to; b0 += 4 * groups) {
+                    float2 ml[4];
+                    float4 v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int b = b0 + i * groups, slot = min(b, last) * 2 + (b == j ? 1 : 0);
-                    ml[i] = p.block_ml[slot * ROWS + r];
-                    v[i] = *reinterpret_cast<const float4*>(p.block_o + ((int64_t)slot * ROWS + r) * D + 4 * f);
-                    if (b > last) ml[i].x = -INFINITY;
+                    for (int i = 0; i < 4; ++i) {
+                        const int b = b0 + i * groups;
+                        const int64_t at = (int64_t)(min(b, to) * 2 + (b == from ? 1 : 0)) * ROWS + r;
+                        ml[i] = __ldcg(p.block_ml + at);
+                        v[i] = __ldcg(reinterpret_cast<const float4*>(p.block_o + at * D) + f);
+                        if (b > to) ml[i].x = -INFINITY;
+                    }
+                    add_parts(ml, v, top, l, acc);
                 }
-                const float now = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), top);
-                const float ref = now == -INFINITY ? 0.f : now, old = ex2(top - ref);
-                top = now;
-                l *= old;
-                acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = ex2(ml[i].x - ref);
-                    acc.x += a * v[i].x;
-                    acc.y += a * v[i].y;
-                    acc.z += a * v[i].z;
-                    acc.w += a * v[i].w;
-                    l += a * ml[i].y;
+            s_acc[tid] = acc;
+            s_w[tid] = make_float2(top, l);
+            __syncthreads();
+            if (mine && grp == 0) {
+                float all = top;
+                for (int q = 1; q < groups; ++q) all = fmaxf(all, s_w[q * cols + tid].x);
+                const float ref = all == -INFINITY ? 0.f : all, a0 = ex2(top - ref);
+                acc = make_float4(acc.x * a0, acc.y * a0, acc.z * a0, acc.w * a0);
+                l *= a0;
+                for (int q = 1; q < groups; ++q) {
+                    const float2 w = s_w[q * cols + tid];
+                    const float4 v = s_acc[q * cols + tid];
+                    const float a = ex2(w.x - ref);
+                    acc.x += a * v.x;
+                    acc.y += a * v.y;
+                    acc.z += a * v.z;
+                    acc.w += a * v.w;
+                    l += a * w.y;
                 }
+                const float inv = l > 0.f ? 1.0f / l : 0.f;
+                *reinterpret_cast<uint2*>(p.out + ((int64_t)(rb + (r >> gs)) * p.hq + kvh * g + (r & (g - 1))) * D + 4 * f) =
+                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
             }
-        s_acc[threadIdx.x] = acc;
-        s_w[threadIdx.x] = make_float2(top, l);
-        __syncthreads();
-        if (mine && grp == 0) {
-            float all = top;
-            for (int q = 1; q < groups; ++q) all = fmaxf(all, s_w[q * cols + threadIdx.x].x);
-            const float ref = all == -INFINITY ? 0.f : all, a0 = ex2(top - ref);
-            acc = make_float4(acc.x * a0, acc.y * a0, acc.z * a0, acc.w * a0);
-            l *= a0;
-            for (int q = 1; q < groups; ++q) {
-                const float2 w = s_w[q * cols + threadIdx.x];
-                const float4 v = s_acc[q * cols + threadIdx.x];
-                const float a = ex2(w.x - ref);
-                acc.x += a * v.x;
-                acc.y += a * v.y;
-                acc.z += a * v.z;
-                acc.w += a * v.w;
-                l += a * w.y;
-            }
-            const float inv = l > 0.f ? 1.0f / l : 0.f;
-            *reinterpret_cast<uint2*>(p.out + ((int64_t)(rb + (r >> gs)) * p.hq + kvh * g + (r & (g - 1))) * D + 4 * f) =
-                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 

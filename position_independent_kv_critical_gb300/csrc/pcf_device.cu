@@ -987,10 +987,16 @@ extern "C" pcf_status pcf_chunk_tables(const pcf_chunk_dims* dims, const int32_t
                          dims->n_q_heads, dims->n_kv_heads, few_limit(dims), few_workers(dims),
                          chunk_sms(dims->n_sms), plan_tag(dims)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((s = launch(chunk_plan_kernel, dim3(1), dim3(kTablesThreads), 0, st, p)) != PCF_OK) return s;
+    // One launch while a single block writes the rows about as fast as a second launch would start
+    // (measured in the design doc's table); more blocks from there on.
+    const int arrays = (int)(plan_array(CA_COUNT, dims->n_reqs) - C_HEADER) * (int)sizeof(int32_t);
+    const int alone = dims->max_rows <= kTablesAlone ? 1 : 0;
+    if ((s = set_smem(chunk_plan_kernel, arrays)) != PCF_OK) return s;
+    if ((s = launch(chunk_plan_kernel, dim3(1), dim3(kTablesThreads), arrays, st, p, alone)) != PCF_OK || alone) return s;
+    if ((s = set_smem(chunk_rows_kernel, arrays)) != PCF_OK) return s;
     const int items = std::max({dims->max_rows, dims->n_reqs + 1, p.workers});
-    const int blocks = std::min((items + kRowsThreads - 1) / kRowsThreads, 8 * device_sms());
-    return launch(chunk_rows_kernel, dim3(blocks), dim3(kRowsThreads), 0, st, p);
+    const int blocks = std::min((items + kRowsThreads - 1) / kRowsThreads, device_sms());
+    return launch(chunk_rows_kernel, dim3(blocks), dim3(kRowsThreads), arrays, st, p);
 }
 
 extern "C" pcf_status pcf_append_kv(const pcf_chunk_dims* dims, const uint16_t* k_new, int64_t k_row_stride,
@@ -1023,7 +1029,7 @@ extern "C" pcf_status pcf_append_kv(const pcf_chunk_dims* dims, const uint16_t* 
 namespace {
 struct ChunkCall {
     const pcf_chunk_dims* dims;
-    const int32_t* plan;
+    int32_t* plan;
     const uint16_t* q;
     int64_t q_stride;
     const uint16_t *k_pool, *v_pool;
@@ -1035,7 +1041,7 @@ struct ChunkCall {
     uint8_t* ws;
 };
 
-// requests with few rows: the kernel over their pages, then the runs that blocks share
+// requests with few rows: one kernel over their pages
 template <int D, int NQ>
 pcf_status few_rows_impl(const ChunkCall& c, cudaStream_t st) {
     const pcf_chunk_dims& d = *c.dims;
@@ -1049,13 +1055,12 @@ pcf_status few_rows_impl(const ChunkCall& c, cudaStream_t st) {
     const FewParams p{c.plan, reinterpret_cast<const __nv_bfloat16*>(c.q), c.block_table, c.page_pos, c.excl, c.row_pos,
                       c.rope, reinterpret_cast<__nv_bfloat16*>(c.out), reinterpret_cast<float*>(c.ws + w.worker_o),
                       reinterpret_cast<float*>(c.ws + w.block_o), reinterpret_cast<float2*>(c.ws + w.block_ml),
-                      reinterpret_cast<int4*>(c.ws + w.block_desc), c.q_stride, d.n_reqs, d.max_pages, d.max_rows,
+                      c.plan + plan_count(d.n_reqs, few_workers(&d), blocks), c.q_stride, d.n_reqs, d.max_pages, d.max_rows,
                       d.n_q_heads, d.n_kv_heads, d.n_phys_pages, d.max_pos, blocks, plan_tag(&d)};
     using SM = FewSmem<D, NQ>;
     auto kern = few_rows_kernel<D, NQ>;
     if ((s = set_smem(kern, SM::kAlloc)) != PCF_OK) return s;
-    if ((s = launch(kern, dim3(blocks), dim3(SM::kThreads), SM::kAlloc, st, tk, tv, p)) != PCF_OK) return s;
-    return launch(few_join_kernel<D, NQ>, dim3(blocks), dim3(kJoinThreads), 0, st, p);
+    return launch(kern, dim3(blocks), dim3(SM::kThreads), SM::kAlloc, st, tk, tv, p);
 }
 
 // requests with more rows: queries and keys rotated into the workspace, the tensor-core kernel, then
@@ -1103,7 +1108,7 @@ pcf_status chunk_attention_impl(const ChunkCall& c, cudaStream_t st) {
 }
 }  // namespace
 
-extern "C" pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, const int32_t* plan, const uint16_t* q,
+extern "C" pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, int32_t* plan, const uint16_t* q,
                                           int64_t q_row_stride, const uint16_t* k_pool, const uint16_t* v_pool,
                                           const int32_t* block_table, const int32_t* page_pos, const uint16_t* excl,
                                           const int32_t* row_pos, const float* rope, uint16_t* out, void* ws,

@@ -585,3 +585,15 @@ def test_two_captured_graphs_share_a_workspace_in_order():
     pcf.check_device_error()
     for c in (a, b):
         c.check(c.out.float().cpu().double().numpy(), rows=6)
+
+
+@pytest.mark.parametrize("seq,new", [([300], [1]), ([40, 3], [1, 1]), ([2000], [2]), ([30, 900], [70, 1])])
+def test_a_workspace_full_of_nan_does_not_matter(seq, new):
+    """Partial results that a call has not written must not be read, not even with weight zero."""
+    c = ChunkCase(seq, new, hq=32, hkv=8, d=128).to_device()
+    c.tables()
+    c.append()
+    c.ws.fill_(255)
+    c.attend()
+    pcf.check_device_error()
+    c.check(c.out.float().cpu().double().numpy(), rows=6)
