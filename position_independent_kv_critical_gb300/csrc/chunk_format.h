@@ -79,9 +79,19 @@ constexpr int kFewRows = 32;
 // Warps of a block of the few-row kernel, each a worker, with 1, 2 or 4 tiles of 8 rows: twelve of 168
 // registers, three a sub-partition, while the accumulators leave room; eight of 255 with four tiles.
 PCF_HOST_DEVICE constexpr int few_warps(int tiles) { return tiles <= 2 ? 12 : 8; }
-// Units go to the workers in equal runs, worker w from the w-th of `active` equal parts on; with
-// fewer units than workers the first ones take one each, so that a run's parts sit in few blocks.
-PCF_HOST_DEVICE inline int64_t few_active(int64_t units, int32_t workers) { return units < workers ? units : workers; }
+// Units go to the workers in contiguous runs as equal as can be: with fewer units than workers the
+// first ones take one each (so that a run's parts sit in few blocks), else each takes units / workers
+// and the first units % workers one more.  No 64-bit division: one costs more than a lookup.
+struct Deal {
+    int32_t units, active, each, more;
+    PCF_HOST_DEVICE Deal(int32_t n, int32_t workers)
+        : units(n), active(n < workers ? n : workers), each(n > 0 ? n / active : 0), more(n > 0 ? n % active : 0) {}
+    PCF_HOST_DEVICE int32_t first(int32_t w) const { return w < active ? w * each + (w < more ? w : more) : units; }
+    PCF_HOST_DEVICE int32_t owner(int32_t u) const {   // (0 <= u < units)
+        const int32_t big = more * (each + 1);
+        return u < big ? u / (each + 1) : more + (u - big) / each;
+    }
+};
 
 PCF_HOST_DEVICE inline int32_t chunk_sms(int32_t n_sms) { return n_sms > 0 ? n_sms : kDefaultSms; }
 

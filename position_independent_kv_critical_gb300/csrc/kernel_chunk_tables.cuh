@@ -116,28 +116,25 @@ __device__ __forceinline__ void write_rows(const TablesParams& p, int32_t* array
         else p.head_out[0] = head + taken;
     }
     // the few-row requests' units, dealt to the workers in equal runs
-    const int64_t units = few[p.n], active = few_active(units, p.workers);
+    const Deal deal(few[p.n], p.workers);
     const int per = p.workers / p.blocks;
     for (int32_t w = i; w < p.workers; w += step) {
-        const int64_t u0 = w < active ? w * units / active : 0, u1 = w < active ? (w + 1) * units / active : 0;
-        int4 e = make_int4(0, 0, 0, (int)(u1 - u0)), f = make_int4(1, 0, 0, 0), share = make_int4(p.tag, 0, 0, 0);
-        if (e.w > 0) {
-            const int b = row_request(few, p.n, (int32_t)u0);
+        const int32_t u0 = deal.first(w), n_units = deal.first(w + 1) - u0;
+        int4 e = make_int4(0, 0, 0, n_units), f = make_int4(1, 0, 0, 0), share = make_int4(p.tag, 0, 0, 0);
+        if (n_units > 0) {
+            const int b = row_request(few, p.n, u0);
             f = make_int4(pages_of(seq[b] + add[b]), seq[b], add[b], base[b]);
-            const int32_t local = (int32_t)u0 - few[b];
+            const int32_t local = u0 - few[b];
             e.x = b;
             e.y = local / f.x;
-            e.z = local % f.x;
-            if (w % per == 0) {
-                // the block holds the units [u0, end): the owner of a unit is the last worker whose first
-                // unit is not behind it
-                auto owner = [&](int64_t u) { return (int)((((u + 1) * active - 1) / units) / per); };
-                const int64_t a = few[b] + e.y * f.x, end = w + per < active ? (w + per) * units / active : units;
-                share.y = owner(a);
-                share.z = owner(a + f.x - 1);
-                const int bl = row_request(few, p.n, (int32_t)end - 1);
-                const int64_t pages = pages_of(seq[bl] + add[bl]);
-                share.w = owner(few[bl] + (end - 1 - few[bl]) / pages * pages + pages - 1);
+            e.z = local - e.y * f.x;
+            if (w % per == 0) {   // the blocks that the runs of the block's first and last unit reach
+                const int32_t a = u0 - e.z, end = deal.first(w + per) - 1;
+                share.y = deal.owner(a) / per;
+                share.z = deal.owner(a + f.x - 1) / per;
+                const int bl = row_request(few, p.n, end);
+                const int32_t pages = pages_of(seq[bl] + add[bl]);
+                share.w = deal.owner(few[bl] + (end - few[bl]) / pages * pages + pages - 1) / per;
             }
         }
         int4* dst = reinterpret_cast<int4*>(p.plan + plan_starts(p.n)) + 3 * w;
@@ -146,16 +143,16 @@ __device__ __forceinline__ void write_rows(const TablesParams& p, int32_t* array
         dst[2] = share;
     }
     // the others' key tiles, in (request, kv head, row pair, tile) order, dealt to the blocks
-    const int64_t tiles = many[p.n], on = few_active(tiles, p.blocks);
+    const Deal tiles(many[p.n], p.blocks);
     const int g = p.hq / p.hkv, tpp = 2 * kTileRows / g;
     for (int32_t w = i; w < p.blocks; w += step) {
         p.plan[plan_count(p.n, p.workers, p.blocks) + w] = 0;
-        const int64_t u0 = w < on ? w * tiles / on : 0, u1 = w < on ? (w + 1) * tiles / on : 0;
-        int4 e = make_int4(0, 0, 0, 0), f = make_int4((int)(u1 - u0), p.tag, 0, 0);
+        const int32_t u0 = tiles.first(w);
+        int4 e = make_int4(0, 0, 0, 0), f = make_int4(tiles.first(w + 1) - u0, p.tag, 0, 0);
         if (f.x > 0) {
-            const int b = row_request(many, p.n, (int32_t)u0);
+            const int b = row_request(many, p.n, u0);
             const int32_t per_head = (many[b + 1] - many[b]) / p.hkv;
-            int32_t local = (int32_t)u0 - many[b];
+            int32_t local = u0 - many[b];
             e.x = b;
             e.y = local / per_head;
             local %= per_head;

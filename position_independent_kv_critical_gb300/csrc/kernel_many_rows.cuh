@@ -314,11 +314,10 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 left -= w.n_loc;
                 if (w.n_loc < all) w.slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);
                 if (tile == 0 && w.n_loc < all) {
-                    // the block that holds the run's last tile (block b's part begins at b * U / B)
-                    const int64_t units = many[prm.n], on = few_active(units, prm.blocks);
-                    const int64_t u = many[req] + (int64_t)kvh * ((many[req + 1] - many[req]) / prm.hkv) +
-                                      many_before(w.seq, tpp, pair) + all - 1;
-                    desc = make_int4((int)(((u + 1) * on - 1) / units) << 8 | 0xFF, req, kvh, pair);
+                    // the block that holds the run's last tile
+                    const int32_t u = many[req] + kvh * ((many[req + 1] - many[req]) / prm.hkv) +
+                                      (int32_t)many_before(w.seq, tpp, pair) + all - 1;
+                    desc = make_int4(Deal(many[prm.n], prm.blocks).owner(u) << 8 | 0xFF, req, kvh, pair);
                 }
             }
             if (lane == 0) {
