@@ -350,6 +350,7 @@ pcf_status pcf_chunk_plan_words(const pcf_chunk_dims* dims, int64_t* n_words);
  *             from free_pages[free_head[0]] on, request after request
  *   in/out  block_table, page_pos [n_reqs][max_pages] int32: the entries of pages already held are
  *             read, those of the pages a chunk starts are written, the others are left alone
+ *           (apart from the pairs named below, outputs overlap no other buffer of the call)
  *   out     slot_map [max_rows] int32: page * 16 + slot of every row; -1 behind the last row
  *           row_pos [max_rows] int32: logical position of every row; -1 behind the last row
  *           row_base [n_reqs + 1] int32: first row of every request, then the number of rows
@@ -361,7 +362,7 @@ pcf_status pcf_chunk_plan_words(const pcf_chunk_dims* dims, int64_t* n_words);
  * writes to), a next_pos that breaks a started page, a free list that runs out or names a page
  * outside the pool.  Then no table entry is written, the lengths and the list's head stay, slot_map
  * and row_pos are all -1, and calls that use the plan do nothing.
- * One block scans the lengths; a second launch writes the rows. */
+ * One launch, or two where lengths or list head are updated in place. */
 pcf_status pcf_chunk_tables(const pcf_chunk_dims* dims, const int32_t* seq_len, const int32_t* new_len,
                             const int32_t* next_pos, const int32_t* free_pages, int32_t n_free,
                             const int32_t* free_head, int32_t* block_table, int32_t* page_pos, int32_t* slot_map,

@@ -295,6 +295,7 @@ class ChunkLayout:
                 dev = torch.device("cuda", torch.cuda.current_device())
             n_sms = torch.cuda.get_device_properties(dev).multi_processor_count
         self.device = dev
+        self.index = -1 if dev.index is None else dev.index
         total = n_reqs * max_pages if max_total_pages is None else max_total_pages
         self.dims = _lib.ChunkDims(n_reqs, max_pages, max_rows, max_chunk, total, hq, hkv, d, n_phys_pages, max_pos,
                                    n_sms)
@@ -356,7 +357,7 @@ def _chunk_ints(L: ChunkLayout, t: Optional[torch.Tensor], name: str, n: Optiona
     """Address of an integer tensor of n elements, None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or not t.is_contiguous() or t.device != L.device or (n is not None and t.numel() != n):
+    if t.dtype != dtype or not t.is_contiguous() or t.get_device() != L.index or (n is not None and t.numel() != n):
         _bad_ints(L, t, name, n, dtype)
     return t.data_ptr() or None
 
@@ -366,7 +367,7 @@ def _chunk_rows(L: ChunkLayout, t: torch.Tensor, heads: int, name: str) -> int:
     from row to row."""
     if t.dtype != torch.bfloat16 or t.shape != (L.max_rows, heads, L.d):
         raise ValueError(f"{name}: expected bfloat16 [{L.max_rows}, {heads}, {L.d}], got {t.dtype} {tuple(t.shape)}")
-    if t.device != L.device:
+    if t.get_device() != L.index:
         raise ValueError(f"{name}: on {t.device}, the layout is on {L.device}")
     row, head, one = t.stride()
     if one != 1 or (heads > 1 and head != L.d):
@@ -381,7 +382,7 @@ def _chunk_rows(L: ChunkLayout, t: torch.Tensor, heads: int, name: str) -> int:
 def _chunk_pool(L: ChunkLayout, t: torch.Tensor, name: str):
     if t.dtype != torch.bfloat16 or not t.is_contiguous():
         _need(t, torch.bfloat16, name)
-    if t.device != L.device:
+    if t.get_device() != L.index:
         raise ValueError(f"{name}: on {t.device}, the layout is on {L.device}")
     if t.numel() < L.pool_elems:
         raise ValueError(f"{name}: smaller than the {L.dims.n_phys_pages} pages of the layout")
@@ -393,7 +394,7 @@ def _chunk_rope(L: ChunkLayout, t: Optional[torch.Tensor]):
         return None
     if t.dtype != torch.float32 or not t.is_contiguous():
         _need(t, torch.float32, "rope")
-    if t.device != L.device or t.numel() < L.dims.max_pos * L.d:
+    if t.get_device() != L.index or t.numel() < L.dims.max_pos * L.d:
         raise ValueError(f"rope: expected {L.dims.max_pos} rows on {L.device}")
     return t.data_ptr()
 
@@ -401,13 +402,18 @@ def _chunk_rope(L: ChunkLayout, t: Optional[torch.Tensor]):
 def _chunk_call(L: ChunkLayout, fn: str, stream, *args):
     """The call on the layout's device, on that device's current stream unless one is named."""
     call = getattr(_lib.load(), fn)
-    if L.device.type == "cuda" and torch.cuda.current_device() != L.device.index:
-        with torch.cuda.device(L.device):
-            status = call(L.dims_ref, *args, (stream or torch.cuda.current_stream()).cuda_stream)
+    if L.index < 0 or torch.cuda.current_device() == L.index:
+        status = call(L.dims_ref, *args, _raw_stream(L.index) if stream is None else stream.cuda_stream)
     else:
-        status = call(L.dims_ref, *args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+        with torch.cuda.device(L.device):
+            status = call(L.dims_ref, *args, _raw_stream(L.index) if stream is None else stream.cuda_stream)
     if status:
         _lib.check(fn, status)
+
+
+def _raw_stream(index: int) -> int:
+    """The current stream's handle on device ``index`` (without building a torch.cuda.Stream)."""
+    return torch._C._cuda_getCurrentRawStream(index) if index >= 0 else torch.cuda.current_stream().cuda_stream
 
 
 def chunk_tables(layout: ChunkLayout, seq_len, new_len, free_pages, free_head, seq_len_out, free_head_out,
@@ -444,9 +450,9 @@ def chunk_attention(layout: ChunkLayout, q, k_pool, v_pool, rope, out, ws, excl=
     qs = _chunk_rows(L, q, L.hq, "q")
     if out.dtype != torch.bfloat16 or not out.is_contiguous():
         _need(out, torch.bfloat16, "out")
-    if out.shape != (L.max_rows, L.hq, L.d) or out.device != L.device:
+    if out.shape != (L.max_rows, L.hq, L.d) or out.get_device() != L.index:
         raise ValueError(f"out: expected [{L.max_rows}, {L.hq}, {L.d}] on {L.device}")
-    if ws.device != L.device or not ws.is_contiguous():
+    if ws.get_device() != L.index or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on {L.device}")
     _chunk_call(L, "pcf_chunk_attention", stream, L.plan.data_ptr(), q.data_ptr(), qs, _chunk_pool(L, k_pool, "k_pool"),
                 _chunk_pool(L, v_pool, "v_pool"), L.block_table.data_ptr(), L.page_pos.data_ptr(),

@@ -14,7 +14,6 @@
 namespace pcf {
 
 constexpr int kMaxReqs = 4096;               // requests of one chunk batch (one block scans them)
-constexpr int kTablesAlone = 4096;           // rows up to which one block writes the tables by itself
 constexpr int32_t kMaxChunkRows = 1 << 22;   // rows of one chunk batch
 constexpr int32_t kMaxTotalPages = 1 << 26;  // pages of all requests together, repeats counted
 

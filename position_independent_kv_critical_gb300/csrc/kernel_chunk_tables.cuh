@@ -24,7 +24,7 @@ struct TablesParams {
     int32_t n, max_pages, max_rows, max_chunk, max_total_pages, n_phys, max_pos, n_free, hq, hkv, few_rows, workers, blocks, tag;
 };
 
-constexpr int kTablesThreads = 1024;
+constexpr int kTablesThreads = 512;
 
 // One block reads the lengths, checks them and leaves the plan.  Request b holds s tokens on
 // ceil(s / 16) pages and grows by n: the pages behind are taken from the free list in request
@@ -32,8 +32,11 @@ constexpr int kTablesThreads = 1024;
 // a prefix sum of n gives its first row.  Thread t takes a run of consecutive requests, so one
 // block scan of per-thread sums is enough for any batch size.  Everything that is looked up by
 // bisection (rows, units, tiles) is kept in shared memory: a probe costs some 30 cycles there and
-// several hundred in L2.  What bounds the call is the chain of dependent loads and barriers; with
-// few rows the same block goes on to write them (one launch, `alone`), else a second launch does.
+// several hundred in L2.  What bounds the call is the chain of dependent loads and barriers: where the
+// outputs are buffers of their own, every block of one launch reads the lengths and scans them for
+// itself and then writes its share of the rows (`alone`); where lengths or list head are updated in
+// place, a block must not write them while another still reads, so one block leaves the plan and a
+// second launch writes the rows (64 requests of one token: 5 and 7 us).
 // (Sums of refused lengths may be as large as 4096 x 2^22: they stop at 2^29, above every limit.)
 constexpr int kSumLimit = 1 << 29;
 constexpr int kSums = 6;   // rows, pages taken, pages held afterwards, few-row units, key tiles and pages of the others
@@ -172,7 +175,8 @@ __device__ __forceinline__ void write_rows(const TablesParams& p, int32_t* array
 
 __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const TablesParams p, int alone) {
     extern __shared__ int32_t s_arrays[];
-    __shared__ int s_warp[kSums][kTablesThreads / 32];
+    constexpr int kWarps = kTablesThreads / 32;
+    __shared__ int s_warp[kSums][kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dep_wait();
     grid_dep_launch();
@@ -237,18 +241,18 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
     }
     bad = __syncthreads_or(bad);
     if (warp < kSums) {
-        int x = s_warp[warp][lane];
+        int x = lane < kWarps ? s_warp[warp][lane] : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
+        for (int o = 1; o < kWarps; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x = sat_add(x, y);
         }
-        s_warp[warp][lane] = x;
+        if (lane < kWarps) s_warp[warp][lane] = x;
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSums; ++i) {
-        tot[i] = s_warp[i][31];
+        tot[i] = s_warp[i][kWarps - 1];
         pre[i] += (warp ? s_warp[i][warp - 1] : 0) - sum[i];
     }
     bad = bad || tot[0] > p.max_rows || tot[2] > p.max_total_pages || tot[1] > p.n_free - head || tot[3] >= kSumLimit ||
@@ -288,11 +292,14 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         o_few[p.n] = tot[3];
         o_many[p.n] = tot[4];
         o_kpage[p.n] = tot[5];
-        *reinterpret_cast<int4*>(plan) = make_int4(p.tag, tot[0], head, tot[1]);   // C_TAG, C_ROWS, C_HEAD, C_TAKEN
+        if (blockIdx.x == 0)
+            *reinterpret_cast<int4*>(plan) = make_int4(p.tag, tot[0], head, tot[1]);   // C_TAG, C_ROWS, C_HEAD, C_TAKEN
     }
     __syncthreads();
-    for (int i = tid; i < CA_COUNT * (p.n + 1); i += kTablesThreads) plan[C_HEADER + i] = s_arrays[i];
-    if (alone) write_rows(p, s_arrays, tot[0], head, tot[1], tid, kTablesThreads);
+    if (blockIdx.x == 0)
+        for (int i = tid; i < CA_COUNT * (p.n + 1); i += kTablesThreads) plan[C_HEADER + i] = s_arrays[i];
+    if (alone)
+        write_rows(p, s_arrays, tot[0], head, tot[1], blockIdx.x * kTablesThreads + tid, gridDim.x * kTablesThreads);
 }
 
 // A plan made for other dims (or by no pcf_chunk_tables call at all) is refused.

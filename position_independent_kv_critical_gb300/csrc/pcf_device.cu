@@ -987,16 +987,16 @@ extern "C" pcf_status pcf_chunk_tables(const pcf_chunk_dims* dims, const int32_t
                          dims->n_q_heads, dims->n_kv_heads, few_limit(dims), few_workers(dims),
                          chunk_sms(dims->n_sms), plan_tag(dims)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // One launch while a single block writes the rows about as fast as a second launch would start
-    // (measured in the design doc's table); more blocks from there on.
+    // one launch where the outputs are buffers of their own, else two (see chunk_plan_kernel)
     const int arrays = (int)(plan_array(CA_COUNT, dims->n_reqs) - C_HEADER) * (int)sizeof(int32_t);
-    const int alone = dims->max_rows <= kTablesAlone ? 1 : 0;
-    if ((s = set_smem(chunk_plan_kernel, arrays)) != PCF_OK) return s;
-    if ((s = launch(chunk_plan_kernel, dim3(1), dim3(kTablesThreads), arrays, st, p, alone)) != PCF_OK || alone) return s;
-    if ((s = set_smem(chunk_rows_kernel, arrays)) != PCF_OK) return s;
     const int items = std::max({dims->max_rows, dims->n_reqs + 1, p.workers});
-    const int blocks = std::min((items + kRowsThreads - 1) / kRowsThreads, device_sms());
-    return launch(chunk_rows_kernel, dim3(blocks), dim3(kRowsThreads), arrays, st, p);
+    auto blocks = [&](int threads) { return dim3(std::min((items + threads - 1) / threads, device_sms())); };
+    const int alone = seq_len_out != seq_len && free_head_out != free_head ? 1 : 0;
+    if ((s = set_smem(chunk_plan_kernel, arrays)) != PCF_OK) return s;
+    s = launch(chunk_plan_kernel, alone ? blocks(kTablesThreads) : dim3(1), dim3(kTablesThreads), arrays, st, p, alone);
+    if (s != PCF_OK || alone) return s;
+    if ((s = set_smem(chunk_rows_kernel, arrays)) != PCF_OK) return s;
+    return launch(chunk_rows_kernel, blocks(kRowsThreads), dim3(kRowsThreads), arrays, st, p);
 }
 
 extern "C" pcf_status pcf_append_kv(const pcf_chunk_dims* dims, const uint16_t* k_new, int64_t k_row_stride,
