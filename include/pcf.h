@@ -398,9 +398,10 @@ pcf_status pcf_chunk_attention_workspace_bytes(const pcf_chunk_dims* dims, size_
  * [max_rows][Hq][d] bf16, rows behind the last one left as they are.  ws: device workspace of >=
  * pcf_chunk_attention_workspace_bytes, contents need not be initialised.  Any number of calls may use
  * one plan, one behind the other (a model's layers); two calls that may overlap need a plan (a
- * pcf_chunk_tables call) and a workspace each, as the plan holds counters that a call moves on.  Deterministic.  A page outside the pool or a position outside the rope table raises
- * PCF_ERR_DEVICE_BOUNDS, a rotated query or key beyond fp16 PCF_ERR_DEVICE_RANGE; the call's results
- * must then be discarded. */
+ * pcf_chunk_tables call) and a workspace each, as the plan holds counters that a call moves on.
+ * Deterministic.  A page outside the pool, a position outside the rope table or a plan of other dims
+ * raises PCF_ERR_DEVICE_BOUNDS; a rotated query or key that takes part and is not finite in fp16 (beyond
+ * 65504, or NaN) PCF_ERR_DEVICE_RANGE.  The call's results must then be discarded. */
 pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, int32_t* plan, const uint16_t* q, int64_t q_row_stride,
                                const uint16_t* k_pool, const uint16_t* v_pool, const int32_t* block_table,
                                const int32_t* page_pos, const uint16_t* excl, const int32_t* row_pos,

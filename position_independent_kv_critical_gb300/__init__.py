@@ -281,7 +281,8 @@ class ChunkLayout:
     what is cached (or starts from ``from_layout``), ``chunk_tables`` adds the pages new tokens start.
     ``slot_map``, ``row_pos`` [max_rows] and ``row_base`` [n_reqs + 1] describe the rows of the last
     ``chunk_tables``, ``plan`` is what the calls after it read.  All are int32 tensors on ``device``
-    with fixed addresses, so that a captured step can be replayed."""
+    that stay where they are, so that a captured step can be replayed.  Calls that may overlap need a
+    ChunkLayout and a workspace each."""
 
     def __init__(self, n_reqs: int, hq: int, hkv: int, d: int, n_phys_pages: int, max_pos: int, max_pages: int,
                  max_rows: int, max_chunk: int, max_total_pages: Optional[int] = None, device: str = "cuda"):
@@ -304,9 +305,23 @@ class ChunkLayout:
         n = ctypes.c_int64(0)
         _lib.check("pcf_chunk_plan_words", lib.pcf_chunk_plan_words(self.dims_ref, ctypes.byref(n)))
         ints = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)
-        self.block_table, self.page_pos = ints(n_reqs, max_pages), ints(n_reqs, max_pages)
-        self.slot_map, self.row_pos, self.row_base = ints(max_rows), ints(max_rows), ints(n_reqs + 1)
-        self.plan = ints(n.value)
+        self._tables = {"block_table": ints(n_reqs, max_pages), "page_pos": ints(n_reqs, max_pages),
+                        "slot_map": ints(max_rows), "row_pos": ints(max_rows), "row_base": ints(n_reqs + 1),
+                        "plan": ints(n.value)}
+
+    def _table(name):
+        def put(self, t):
+            old = self._tables[name]
+            if t.dtype != old.dtype or t.shape != old.shape or t.device != old.device or not t.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous {old.dtype} {tuple(old.shape)} on {old.device}, got "
+                                 f"{t.dtype} {tuple(t.shape)} on {t.device}")
+            self._tables[name] = t
+        return property(lambda self: self._tables[name], put)
+
+    # (may be replaced by tensors of the same kind, e.g. one batch's tables under two sizes of chunk)
+    block_table, page_pos = _table("block_table"), _table("page_pos")
+    slot_map, row_pos, row_base, plan = _table("slot_map"), _table("row_pos"), _table("row_base"), _table("plan")
+    del _table
 
     @classmethod
     def from_layout(cls, layout: Layout, max_pages: int, max_rows: int, max_chunk: int, max_pos: int,

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const RotateParams p)
     const int c = threadIdx.x % CPR, r = threadIdx.x / CPR % kPage, h0 = threadIdx.x / (CPR * kPage);
     const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
     const int q_blocks = (rows + kPage - 1) / kPage;
-    float big = 0.f;
+    float big = 0.f, nan = 0.f;   // largest magnitude; NaN where a value is
     for (int t = blockIdx.x; t < pages + q_blocks; t += gridDim.x) {
         const bool is_k = t < pages;
         const __nv_bfloat16* src = nullptr;      // row of head 0
@@ -138,7 +138,9 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const RotateParams p)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float a0 = bf16_lo(ia[e]), a1 = bf16_hi(ia[e]), b0 = bf16_lo(ib[e]), b1 = bf16_hi(ib[e]);
-                    oa[e] = pack_f16x2_track(fmaf(a0, cs[e].x, -b0 * cs[e].y), fmaf(a1, cs[e].z, -b1 * cs[e].w), big);
+                    const float y0 = fmaf(a0, cs[e].x, -b0 * cs[e].y), y1 = fmaf(a1, cs[e].z, -b1 * cs[e].w);
+                    nan = fmaf(y0 + y1, 0.f, nan);    // (a NaN in b shows in a's rotation too)
+                    oa[e] = pack_f16x2_track(y0, y1, big);
                     ob[e] = pack_f16x2_track(fmaf(b0, cs[e].x, a0 * cs[e].y), fmaf(b1, cs[e].z, a1 * cs[e].w), big);
                 }
                 __half* o = is_k ? dst + hh * dst_head
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const RotateParams p)
             }
         }
     }
-    if (!(big < kF16Limit)) set_dev_error(kDevErrRange);
+    if (!(big < kF16Limit) || nan != nan) set_dev_error(kDevErrRange);
 }
 
 // ------------------------------------------------------------------ attention

@@ -141,6 +141,18 @@ def test_binding_refuses_tensors_of_other_shapes_types_and_strides():
         pcf.chunk_attention(L, q, pool, pool, rope, q[:19], ws)
 
 
+def test_tables_are_replaced_only_by_tables_of_the_same_kind():
+    L = pcf.ChunkLayout(3, 8, 2, 64, 40, 512, max_pages=8, max_rows=20, max_chunk=9, device="cpu")
+    other = torch.zeros((3, 8), dtype=torch.int32)
+    L.block_table = other
+    assert L.block_table is other
+    for bad in (other[:2], other.long(), torch.zeros((8, 3), dtype=torch.int32).t(), torch.zeros(24, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="block_table"):
+            L.block_table = bad
+    with pytest.raises(ValueError, match="plan"):
+        L.plan = L.plan[:-1]
+
+
 def test_layout_from_a_fused_batch_lists_its_spans():
     from workload import small_custom_batch
     b = small_custom_batch([(0, 3, 7, 5), (20, 2, 60, 1)], 2, hq=8, hkv=2, d=64, n_phys_pages=40,

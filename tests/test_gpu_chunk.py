@@ -409,6 +409,41 @@ def test_values_beyond_fp16_are_reported(new, which):
     assert e.value.status == RANGE
 
 
+@pytest.mark.parametrize("new", [1, 3, 60])
+@pytest.mark.parametrize("which", ["k", "q"])
+def test_nan_that_takes_part_is_reported(new, which):
+    c = ChunkCase([40], [new], hq=32, hkv=8, d=128, stale="normal")
+    if which == "k":
+        c.k_pool[c.table[0, 1], 3, 5, 7] = float("nan")
+    else:
+        c.q[0, 9, 99] = float("nan")
+    c.to_device()
+    c.tables()
+    c.append()
+    c.attend()
+    with pytest.raises(pcf.PcfError) as e:
+        pcf.check_device_error()
+    assert e.value.status == RANGE
+
+
+def test_plan_of_other_dims_is_refused():
+    for new in ([1], [60]):
+        c = ChunkCase([40], new, hq=32, hkv=8, d=128, stale="normal", spare_rows=70).to_device()
+        c.tables()
+        c.append()
+        plan = c.L.plan.clone()
+        other = pcf.ChunkLayout(1, 32, 8, 128, c.n_phys, c.max_pos, max_pages=c.max_pages, max_rows=c.max_rows,
+                                max_chunk=new[0] + 1)
+        other.block_table, other.page_pos = c.L.block_table, c.L.page_pos
+        other.row_pos = c.L.row_pos
+        other.plan[: plan.numel()] = plan[: other.plan.numel()]
+        ws = torch.empty(other.attention_workspace_bytes() + 16, dtype=torch.uint8, device="cuda")
+        pcf.chunk_attention(other, c.dq, c.dk, c.dv, c.rope, c.out, ws)
+        with pytest.raises(pcf.PcfError) as e:
+            pcf.check_device_error()
+        assert e.value.status == BOUNDS and bool((c.out == 3.0).all())
+
+
 def test_idle_batch_writes_nothing():
     c = ChunkCase([40, 0], [0, 0], spare_rows=4).to_device()
     c.step()
