@@ -245,19 +245,18 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     };
     auto issue_k = [&](int i) {
         look_up();
-        const int src = is.page - win_page, s = i % NK;
-        const int32_t ph = __shfl_sync(0xffffffffu, e_ph, src), pos = __shfl_sync(0xffffffffu, e_pos, src);
-        const uint32_t ex = __shfl_sync(0xffffffffu, e_ex, src);
-        if (lane == 0) {
-            const int32_t y = (ph * p.hkv + is.kvh) * kPage;
-            meta[2 * s] = ex;
+        const int s = i % NK;
+        if (lane == is.page - win_page) {          // the lane that holds the page's entry
+            const int32_t y = (e_ph * p.hkv + is.kvh) * kPage;
+            meta[2 * s] = e_ex;
             meta[2 * s + 1] = (uint32_t)y;
             mbar_arrive_expect_tx(&bar_k[s], SM::kK + SM::kCs);
 #pragma unroll
             for (int hb = 0; hb < D / 64; ++hb)
                 tma_load_2d(ring + s * SM::kK + hb * SM::kHalf, &tm_k, &bar_k[s], hb * 64, y);
-            bulk_load(ring_cs + s * SM::kCs, p.rope + (int64_t)pos * D, SM::kCs, &bar_k[s]);
+            bulk_load(ring_cs + s * SM::kCs, p.rope + (int64_t)e_pos * D, SM::kCs, &bar_k[s]);
         }
+        __syncwarp();
         is.step(few, seq, add, p.hkv, p.n);
     };
     auto issue_v = [&](int i) {
@@ -460,45 +459,62 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         __syncwarp();
         if (issued_k < n_units) issue_k(issued_k++);
         // softmax of the unit's 16 keys: this lane has keys lane / 4 and + 8 of rows 2 c and 2 c + 1
+        // The reference of a row's exponentials is any number near its running maximum: it moves only
+        // when some score passes it by more than 2^8, so most units need no maximum over the lanes.
         uint32_t pf[NQ][2];
+        float x[NQ][4];
+        bool over = false;
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
             if (NQ == 4 && q == 2 && n_rows <= 16) break;
-            float x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = sc[q][0][e] + sc[q][1][e];
-            seen = f2_add(seen, f2_add(f2_pack(x[0], x[1]), f2_pack(x[2], x[3])));
+            for (int e = 0; e < 4; ++e) x[q][e] = sc[q][0][e] + sc[q][1][e];
+            seen = f2_add(seen, f2_add(f2_pack(x[q][0], x[q][1]), f2_pack(x[q][2], x[q][3])));
             if (!clean) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int key = row + 8 * (e >> 1);
                     const int last = s_len + ((q * 8 + 2 * c + (e & 1)) >> gs) - j0;   // last slot of the page the row sees
-                    if (key > last || (gone >> key & 1u)) x[e] = -INFINITY;
+                    if (key > last || (gone >> key & 1u)) x[q][e] = -INFINITY;
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = fmaxf(x[e], x[2 + e]);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                const bool need = mx > m_run[q][e] + 8.0f;
-                if (__any_sync(0xffffffffu, need)) {
-                    const float al = need ? ex2(m_run[q][e] - mx) : 1.0f;
-                    if (need) m_run[q][e] = mx;
-                    l_run[q][e] *= al;
+            for (int e = 0; e < 4; ++e) over |= x[q][e] > m_run[q][e & 1] + 8.0f;
+        }
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        o[q][mt][e] *= al;
-                        o[q][mt][2 + e] *= al;
+            for (int q = 0; q < NQ; ++q) {
+                if (NQ == 4 && q == 2 && n_rows <= 16) break;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(x[q][e], x[q][2 + e]);
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    if (mx > m_run[q][e] + 8.0f) {     // (the same for all lanes of a row)
+                        const float al = ex2(m_run[q][e] - mx);
+                        m_run[q][e] = mx;
+                        l_run[q][e] *= al;
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            o[q][mt][e] *= al;
+                            o[q][mt][2 + e] *= al;
+                        }
                     }
                 }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            if (NQ == 4 && q == 2 && n_rows <= 16) break;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
                 const float ms = m_run[q][e] == -INFINITY ? 0.f : m_run[q][e];
-                x[e] = ex2(x[e] - ms);
-                x[2 + e] = ex2(x[2 + e] - ms);
+                x[q][e] = ex2(x[q][e] - ms);
+                x[q][2 + e] = ex2(x[q][2 + e] - ms);
             }
             // bf16 like the values they meet (an MMA's operands share a type); summed as rounded
-            const uint32_t w0 = pack_bf16x2(x[0], x[1]), w1 = pack_bf16x2(x[2], x[3]);
+            const uint32_t w0 = pack_bf16x2(x[q][0], x[q][1]), w1 = pack_bf16x2(x[q][2], x[q][3]);
             l_run[q][0] += bf16_lo(w0) + bf16_lo(w1);
             l_run[q][1] += bf16_hi(w0) + bf16_hi(w1);
             pf[q][0] = transpose8(w0);
