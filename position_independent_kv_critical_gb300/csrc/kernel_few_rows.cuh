@@ -68,10 +68,10 @@ struct FewSmem {
     // stages of the ring: whole units while they fit, then one more key than values
     static constexpr int kKeyStage = kK + kCs + 16, kValueStage = kK + 8;
     static constexpr int kRoom = (232448 - kFixed) / kWarps;
-    static constexpr int kUnits = kRoom / (kKeyStage + kValueStage) < 6 ? kRoom / (kKeyStage + kValueStage) : 6;
-    static constexpr int kStagesK = kUnits >= 2 ? kUnits : (kRoom - kUnits * kValueStage) / kKeyStage;
-    static constexpr int kStagesV = kUnits;
-    static_assert(kStagesK >= 2 && kStagesK <= 6 && kStagesV >= 1, "the ring needs two keys and a value");
+    static constexpr int kUnits = kRoom / (kKeyStage + kValueStage);
+    static constexpr int kStagesV = kUnits >= 4 ? 4 : kUnits >= 2 ? 2 : 1;    // powers of two: slots are masks
+    static constexpr int kStagesK = kStagesV > 1 ? kStagesV : 2;
+    static_assert(kStagesK * kKeyStage + kStagesV * kValueStage <= kRoom, "the ring needs two keys and a value");
     static constexpr int kRing = (kStagesK + kStagesV) * kK;        // a warp's keys, then its values
     static_assert(kRing >= 8 * NQ * D * 4, "a worker's partial result fits its ring");
     static constexpr int oCs = kWarps * kRing;
@@ -147,18 +147,70 @@ __device__ __forceinline__ void add_parts(const float2 (&ml)[4], const float4 (&
     }
 }
 
+// The ring's barriers and copies by shared-memory address: the loop keeps those in registers, where a
+// generic pointer would take two and a conversion at every use.
+__device__ __forceinline__ void ring_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void ring_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void ring_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar) : "memory");
+}
+__device__ __forceinline__ bool ring_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Bounded like mbar_wait (which says what happens when the limit runs out); the same answer in every lane.
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (__all_sync(0xffffffffu, ring_try(bar, parity))) return true;
+    const long long t0 = clock64();
+    while (!__all_sync(0xffffffffu, ring_try(bar, parity))) {
+        const bool late = clock64() - t0 > kWaitLimitCycles;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+            if (late) {
+                *abort_flag = 1;
+                set_dev_error(kDevErrTimeout);
+            }
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void sts_2(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_1(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// (cos, sin, cos', sin') of two frequencies rewritten as (cos, cos', sin, sin')
+__device__ __forceinline__ void pair_cs(uint32_t addr) {
+    asm volatile("{\n\t.reg .b32 a, b, c, d;\n\tld.shared.v4.b32 {a, b, c, d}, [%0];\n\t"
+                 "st.shared.v4.b32 [%0], {a, c, b, d};\n\t}\n" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void sts_zero4(uint32_t addr) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
+}
+
 // Where a worker stands in the units: page `page` of `pages` of kv head `kvh` of request `req`.
 struct FewCursor {
     int32_t req, kvh, page, pages;
-    __device__ __forceinline__ void open(const int32_t* seq, const int32_t* add) { pages = pages_of(seq[req] + add[req]); }
-    // one unit on; the next request is the next one with few rows (units left guarantee there is one)
-    __device__ __forceinline__ void step(const int32_t* few, const int32_t* seq, const int32_t* add, int32_t hkv, int32_t n) {
-        if (++page < pages) return;
+    // the run behind this one; the next request is the next one with few rows (units left say there is one)
+    __device__ __forceinline__ void next_run(const int32_t* few, const int32_t* seq, const int32_t* add, int32_t hkv, int32_t n) {
         page = 0;
         if (++kvh < hkv) return;
         kvh = 0;
         do { ++req; } while (req < n && few[req + 1] == few[req]);
-        if (req < n) open(seq, add);
+        if (req < n) pages = pages_of(seq[req] + add[req]);
     }
 };
 
@@ -177,12 +229,13 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const int row = lane >> 2, c = lane & 3;     // fragment coordinates
     uint64_t* bar_k = reinterpret_cast<uint64_t*>(smem + SM::oBar) + warp * (NK + NV);
     uint64_t* bar_v = bar_k + NK;
-    // per key slot: exclusion bits, and the pool row its value will be copied from
-    volatile uint32_t* meta = reinterpret_cast<volatile uint32_t*>(smem + SM::oMeta) + warp * NK * 2;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::oAbort);
     uint8_t* ring = smem + warp * SM::kRing;
-    uint8_t* ring_v = ring + NK * SM::kK;
-    uint8_t* ring_cs = smem + SM::oCs + warp * NK * SM::kCs;
+    const uint32_t a_bar_k = smem_u32(bar_k), a_bar_v = smem_u32(bar_v);
+    const uint32_t a_ring = smem_u32(ring), a_ring_v = a_ring + NK * SM::kK;
+    const uint32_t a_cs = smem_u32(smem + SM::oCs + warp * NK * SM::kCs);
+    // per key slot: exclusion bits, and the pool row its value will be copied from
+    const uint32_t a_meta = smem_u32(smem + SM::oMeta + warp * NK * 8);
     float2* s_ml = reinterpret_cast<float2*>(smem + SM::oMl);       // [warp][first, last][row]
     volatile int32_t* s_desc = reinterpret_cast<volatile int32_t*>(smem + SM::oDesc);   // [warp][2][4]
     if (lane == 0) {
@@ -220,56 +273,55 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     // ---------------- the copies: unit i's key into slot i % NK, its value into slot i % NV (a key's slot
     // is free again a whole softmax and P V earlier)
     FewCursor is{start.x, start.y, start.z, first.x};
-    int32_t win_req = -1, win_page = 0;            // the 32 table entries the lanes hold
-    int32_t e_ph = 0, e_pos = 0;
+    // lane l holds the table entry of page is.page + l of the run: pool row of its head, cos/sin row, bits
+    int32_t win_n = 0, win_at = 0;
+    int32_t e_y = 0;
+    const float* e_cs = p.rope;
     uint32_t e_ex = 0;
     auto look_up = [&]() {
-        if (is.req != win_req || is.page < win_page || is.page >= win_page + 32) {
-            win_req = is.req;
-            win_page = is.page;
-            const int32_t pg = is.page + lane;
-            e_ph = e_pos = 0;
-            e_ex = 0;
-            if (pg < is.pages) {
-                const int64_t e = (int64_t)is.req * p.max_pages + pg;
-                e_ph = p.block_table[e];
-                e_pos = p.page_pos[e];
-                if (p.excl) e_ex = p.excl[e];
-                if (e_ph < 0 || e_ph >= p.n_phys || e_pos < 0 || e_pos > p.max_pos - kPage) {
-                    set_dev_error(kDevErrBounds);
-                    e_ph = e_pos = 0;
-                    e_ex = 0xFFFFu;                // nothing of it takes part
-                }
+        win_n = min(32, is.pages - is.page);
+        win_at = 0;
+        if (lane < win_n) {
+            const int64_t e = (int64_t)is.req * p.max_pages + is.page + lane;
+            int32_t ph = p.block_table[e], pos = p.page_pos[e];
+            e_ex = p.excl ? p.excl[e] : 0u;
+            if (ph < 0 || ph >= p.n_phys || pos < 0 || pos > p.max_pos - kPage) {
+                set_dev_error(kDevErrBounds);
+                ph = pos = 0;
+                e_ex = 0xFFFFu;                    // nothing of it takes part
             }
-        }
-    };
-    auto issue_k = [&](int i) {
-        look_up();
-        const int s = i % NK;
-        if (lane == is.page - win_page) {          // the lane that holds the page's entry
-            const int32_t y = (e_ph * p.hkv + is.kvh) * kPage;
-            meta[2 * s] = e_ex;
-            meta[2 * s + 1] = (uint32_t)y;
-            mbar_arrive_expect_tx(&bar_k[s], SM::kK + SM::kCs);
-#pragma unroll
-            for (int hb = 0; hb < D / 64; ++hb)
-                tma_load_2d(ring + s * SM::kK + hb * SM::kHalf, &tm_k, &bar_k[s], hb * 64, y);
-            bulk_load(ring_cs + s * SM::kCs, p.rope + (int64_t)e_pos * D, SM::kCs, &bar_k[s]);
-        }
-        __syncwarp();
-        is.step(few, seq, add, p.hkv, p.n);
-    };
-    auto issue_v = [&](int i) {
-        const int s = i % NV;
-        if (lane == 0) {
-            const int32_t y = (int32_t)meta[2 * (i % NK) + 1];
-            mbar_arrive_expect_tx(&bar_v[s], SM::kK);
-#pragma unroll
-            for (int hb = 0; hb < D / 64; ++hb)
-                tma_load_2d(ring_v + s * SM::kK + hb * SM::kHalf, &tm_v, &bar_v[s], hb * 64, y);
+            e_y = (ph * p.hkv + is.kvh) * kPage;
+            e_cs = p.rope + (int64_t)pos * D;
         }
     };
     int issued_k = 0, issued_v = 0;
+    auto issue_k = [&]() {
+        if (lane == win_at) {
+            const uint32_t s = (uint32_t)issued_k % NK, bar = a_bar_k + s * 8;
+            sts_2(a_meta + s * 8, e_ex, (uint32_t)e_y);
+            ring_expect(bar, SM::kK + SM::kCs);
+#pragma unroll
+            for (int hb = 0; hb < D / 64; ++hb) ring_load_2d(a_ring + s * SM::kK + hb * SM::kHalf, &tm_k, bar, hb * 64, e_y);
+            ring_load(a_cs + s * SM::kCs, e_cs, SM::kCs, bar);
+        }
+        __syncwarp();
+        ++issued_k;
+        if (++win_at == win_n && issued_k < n_units) {
+            is.page += win_n;
+            if (is.page == is.pages) is.next_run(few, seq, add, p.hkv, p.n);
+            look_up();
+        }
+    };
+    auto issue_v = [&]() {
+        if (lane == 0) {
+            const uint32_t s = (uint32_t)issued_v % NV, bar = a_bar_v + s * 8;
+            const int32_t y = (int32_t)lds_1(a_meta + (uint32_t)issued_v % NK * 8 + 4);
+            ring_expect(bar, SM::kK);
+#pragma unroll
+            for (int hb = 0; hb < D / 64; ++hb) ring_load_2d(a_ring_v + s * SM::kK + hb * SM::kHalf, &tm_v, bar, hb * 64, y);
+        }
+        ++issued_v;
+    };
     if (n_units > 0) look_up();
     // positions of the rows of a run (row 8 q + lane / 4); a row behind the last one, or one whose
     // position is out of range, has none and scores 0 everywhere
@@ -307,6 +359,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     int32_t seg_page = 0;
     bool open = false, ok = true;
     int done_k = 0, done_v = 0;
+    int32_t clean_pages = 0;                                 // pages of the run that every row sees whole
 
     for (int i = 0; i < n_units; ++i) {
         if (!open) {
@@ -321,6 +374,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 n_rows = t_len * g;
                 load_positions();
             }
+            clean_pages = (s_len + 1) / kPage;
             uint32_t x[NQ][2 * J];
             float4 w[NQ][J];
 #pragma unroll
@@ -342,9 +396,9 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // the first copies go out behind the first rows' loads, not before: 30 MB of them over the
             // whole device would make those wait
             if (i == 0)
-                for (; issued_k < NK && issued_k < n_units; ++issued_k) {
-                    issue_k(issued_k);
-                    if (issued_v < NV) issue_v(issued_v++);
+                while (issued_k < NK && issued_k < n_units) {
+                    issue_k();
+                    if (issued_v < NV) issue_v();
                 }
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
@@ -374,24 +428,18 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 l_run[q][0] = l_run[q][1] = 0.f;
             }
         }
-        const int s = i % NK, s_v = i % NV;
-        ok = mbar_wait(&bar_k[s], (i / NK) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        const uint32_t s_k = (uint32_t)i % NK, s_v = (uint32_t)i % NV;
+        if (!(ok = ring_wait(a_bar_k + s_k * 8, (uint32_t)i / NK & 1u, abort_flag))) break;
         ++done_k;
-        uint8_t* sk = ring + s * SM::kK;
-        uint8_t* sv = ring_v + s_v * SM::kK;
-        float4* cs0 = reinterpret_cast<float4*>(ring_cs + s * SM::kCs);
-        if (lane < D / 4) {          // the page's cos/sin row, as pairs
-            const float4 v = cs0[lane];
-            cs0[lane] = make_float4(v.x, v.z, v.y, v.w);
-        }
-        const uint32_t ex = meta[2 * s];
-        const int32_t j0 = cu.page * kPage;                        // the page's first slot
+        const uint32_t sk_a = a_ring + s_k * SM::kK, cs_a = a_cs + s_k * SM::kCs;
+        if (lane < D / 4) pair_cs(cs_a + lane * 16);               // the page's cos/sin row, as pairs
+        const uint32_t ex = lds_1(a_meta + s_k * 8);
         // every row sees every key of the page: nothing excluded and the page ends at or before the
         // first row's own slot
-        const bool clean = ex == 0u && j0 + kPage - 1 <= s_len;
+        const bool clean = ex == 0u && cu.page < clean_pages;
         // keys that no row may see: excluded, or behind the last token (the slot may hold anything)
         uint32_t gone = ex;
+        const int32_t j0 = cu.page * kPage;                        // the page's first slot
         if (!clean) {
             const int left = s_len + t_len - j0;                   // slots of the page that hold tokens
             if (left < kPage) gone |= 0xFFFFu & ~((1u << left) - 1u);
@@ -401,7 +449,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             for (int q = lane; q < kPage * (D / 8); q += 32) {
                 const int r = q / (D / 8), ch = q % (D / 8);
                 if (gone >> r & 1u)
-                    *reinterpret_cast<uint4*>(sk + (ch >> 3) * SM::kHalf + sw128_off(r, ch & 7)) = make_uint4(0, 0, 0, 0);
+                    sts_zero4(sk_a + (ch >> 3) * SM::kHalf + sw128_off(r, ch & 7));
             }
         }
         __syncwarp();
@@ -412,8 +460,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         for (int q = 0; q < NQ; ++q)
 #pragma unroll
             for (int e = 0; e < 4; ++e) sc[q][0][e] = sc[q][1][e] = 0.f;
-        const uint32_t sk_u = smem_u32(sk) + k_off;
-        const uint32_t tab = smem_u32(smem + SM::oTab) + row * SM::kTabRow + c * 16, cs_u = smem_u32(cs0) + c * 16;
+        const uint32_t sk_u = sk_a + k_off;
+        const uint32_t tab = smem_u32(smem + SM::oTab) + row * SM::kTabRow + c * 16, cs_u = cs_a + c * 16;
 #pragma unroll
         for (int jj = 0; jj < J / 2; ++jj) {
             uint32_t kf[2][4];                                     // chunks 2 jj, 2 jj + 1, and theirs + J
@@ -431,7 +479,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const uint64_t C = f2_fma(NS0, Sr, f2_mul(C0, Cr)), S = f2_fma(C0, Sr, f2_mul(S0, Cr));
                     const uint64_t A = bf16x2_to_f2(kf[nt][q]), B = bf16x2_to_f2(kf[nt][q + 2]);
                     float y0, y1, z0, z1;
-                    f2_unpack(f2_fma(A, C, f2_neg(f2_mul(B, S))), y0, y1);   // a cos - b sin
+                    f2_unpack(f2_fma(f2_mul(B, S), f2_pack(-1.f, -1.f), f2_mul(A, C)), y0, y1);   // a cos - b sin
                     f2_unpack(f2_fma(A, S, f2_mul(B, C)), z0, z1);           // a sin + b cos
                     kf[nt][q] = pack_f16x2_inf(y0, y1);
                     kf[nt][q + 2] = pack_f16x2_inf(z0, z1);
@@ -457,7 +505,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // K has been read (and the cos/sin row rewritten in place): the next key for its slot
         fence_proxy_async_smem();
         __syncwarp();
-        if (issued_k < n_units) issue_k(issued_k++);
+        if (issued_k < n_units) issue_k();
         // softmax of the unit's 16 keys: this lane has keys lane / 4 and + 8 of rows 2 c and 2 c + 1
         // The reference of a row's exponentials is any number near its running maximum: it moves only
         // when some score passes it by more than 2^8, so most units need no maximum over the lanes.
@@ -520,21 +568,21 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             pf[q][0] = transpose8(w0);
             pf[q][1] = transpose8(w1);
         }
-        ok = mbar_wait(&bar_v[s_v], (i / NV) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        if (!(ok = ring_wait(a_bar_v + s_v * 8, (uint32_t)i / NV & 1u, abort_flag))) break;
         ++done_v;
-        if (!clean && gone != 0u) {
+        const uint32_t sv_a = a_ring_v + s_v * SM::kK;
+        if (gone != 0u) {
             // values of keys that take no part must not meet a weight of zero
             for (int q = lane; q < kPage * (D / 8); q += 32) {
                 const int r = q / (D / 8), ch = q % (D / 8);
                 if (gone >> r & 1u)
-                    *reinterpret_cast<uint4*>(sv + (ch >> 3) * SM::kHalf + sw128_off(r, ch & 7)) = make_uint4(0, 0, 0, 0);
+                    sts_zero4(sv_a + (ch >> 3) * SM::kHalf + sw128_off(r, ch & 7));
             }
             fence_proxy_async_smem();              // before the slot's next copy
             __syncwarp();
         }
         // O^T += V^T P^T
-        const uint32_t sv_u = smem_u32(sv) + v_off;
+        const uint32_t sv_u = sv_a + v_off;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             uint32_t a[4];                                         // (dims, keys): low/high dims, then high keys
@@ -546,7 +594,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
         }
         __syncwarp();
-        if (issued_v < issued_k) issue_v(issued_v++);
+        if (issued_v < issued_k) issue_v();
 
     // ---------------- the end of a run, or of the worker
         const bool last = i + 1 == n_units, ended = cu.page + 1 == cu.pages;
@@ -604,7 +652,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
             open = false;
         }
-        cu.step(few, seq, add, p.hkv, p.n);
+        ++cu.page;
+        if (ended && !last) cu.next_run(few, seq, add, p.hkv, p.n);
     }
     {
         float a, b;
