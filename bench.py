@@ -413,9 +413,52 @@ def run_layer_prefetch(args, pcf, b, L, cf, k_pool, dev, rank, local):
         }))
 
 
+def _decode_setup(args, pcf, b, L, cf, k_pool, dev):
+    """One decoding step of one layer behind the fused prefill: the batch's recomputed and query rows
+    are moved into pages of their own, then every request decodes ``args.tokens`` tokens (tables,
+    append, attention).  Returns (call, bytes a step cannot do without)."""
+    n, rows = len(b.requests), L.total_rows
+    T = args.tokens
+    private = sum(-(-(r.n_rows + T) // PAGE) for r in b.requests)
+    grow = lambda t: torch.cat([t, torch.zeros((private,) + tuple(t.shape[1:]), dtype=t.dtype, device=dev)])
+    kp, vp = grow(k_pool), grow(b.v_pool.to(dev))
+    cf.step(b.q_query.to(dev), k_pool, vp[: b.n_phys_pages], b.q_fresh.to(dev), b.k_fresh.to(dev), b.v_fresh.to(dev))
+    max_pos = b.max_pos + T + 2 * PAGE
+    max_pages = max(r.n_cached // PAGE + -(-(r.n_rows + T) // PAGE) for r in b.requests)
+    kw = dict(max_pages=max_pages, max_pos=max_pos, n_phys_pages=b.n_phys_pages + private, device=str(dev))
+    L0, excl = pcf.ChunkLayout.from_layout(L, max_rows=rows, max_chunk=max(r.n_rows for r in b.requests), excl=cf.excl,
+                                           **kw)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+    rope = pcf.rope_table(b.d, b.theta, max_pos).to(dev)
+    free = torch.arange(b.n_phys_pages, b.n_phys_pages + private, dtype=torch.int32, device=dev)
+    head, seq = i32([0]), i32([r.n_cached for r in b.requests])
+    start = i32([r.query_pos0 - (r.n_rows - r.n_query) for r in b.requests])
+    pcf.chunk_tables(L0, seq, i32([r.n_rows for r in b.requests]), free, head, seq, head, next_pos=start)
+    pcf.append_kv(L0, b.k_fresh.to(dev), b.v_fresh.to(dev), kp, vp, rope=rope, row_pos=cf.row_pos)
+    L1 = pcf.ChunkLayout(n, b.hq, b.hkv, b.d, kw["n_phys_pages"], max_pos, max_pages=max_pages, max_rows=n * T,
+                         max_chunk=T, device=str(dev))
+    L1.block_table, L1.page_pos = L0.block_table, L0.page_pos
+    gen = torch.Generator(device=dev).manual_seed(1)
+    draw = lambda h: torch.randn((n * T, h, b.d), generator=gen, device=dev).to(torch.bfloat16)
+    q, k, v = draw(b.hq), draw(b.hkv), draw(b.hkv)
+    out = torch.empty_like(q)
+    ws = torch.empty(max(16, L1.attention_workspace_bytes()), dtype=torch.uint8, device=dev)
+    new, seq1, head1 = i32([T] * n), torch.empty_like(seq), torch.empty_like(head)
+
+    def call():
+        pcf.chunk_tables(L1, seq, new, free, head, seq1, head1)
+        pcf.append_kv(L1, k, v, kp, vp)
+        pcf.chunk_attention(L1, q, kp, vp, rope, out, ws, excl=excl)
+
+    shared = {p for r in b.requests for s in r.spans for p in range(s.phys_first_page, s.phys_first_page + s.n_pages)}
+    tokens = len(shared) * PAGE + sum(r.n_rows + T for r in b.requests)
+    return call, tokens * b.hkv * b.d * 4 + n * T * (b.hq + b.hkv) * b.d * 4
+
+
 def run_op(args, pcf, b, L, cf, k_pool, dev, world, rank, local):
-    """Time one selection variant alone: anchor key norms (HBM-bound: reads every cached key once)
-    or the global Top-N (one block per request, launch- and latency-bound)."""
+    """Time one variant alone: anchor key norms (HBM-bound: reads every cached key once), the global
+    Top-N (one block per request, launch- and latency-bound), all-layer scoring, the anchor probe, or a
+    decoding step behind the fused prefill."""
     stream = torch.cuda.current_stream()
     flush = torch.empty(512 << 20, dtype=torch.uint8, device=dev)
     if args.op == "key_norms":
@@ -444,6 +487,9 @@ def run_op(args, pcf, b, L, cf, k_pool, dev, world, rank, local):
         per_call = int(args.layers * (1 + int(hw[19] > 0) + int(hw[20] > 0)) + 1)
     elif args.op == "topn_global":
         call = lambda: pcf.select_topn_global(L, norms, cf.sel_idx, cf.excl, cf.row_pos)
+    elif args.op == "decode":
+        call, decode_bytes = _decode_setup(args, pcf, b, L, cf, k_pool, dev)
+        per_call = 3 if args.tokens * (b.hq // b.hkv) <= 32 else 6
     else:
         call, probe_flops, offline, per_call = _anchor_probe_setup(args, pcf, b, k_pool, dev)
     for _ in range(max(3, args.warmup)):
@@ -481,6 +527,11 @@ def run_op(args, pcf, b, L, cf, k_pool, dev, world, rank, local):
         roof = {"bound": "tensor", "achieved": tf, "peak": peak, "unit": "TFLOP/s", "frac": tf / peak,
                 "issued_tflops": 2 * tf, "issued_frac": 2 * tf / peak, "peak_source": src + " bf16 burst",
                 "traffic": None, "algorithmic_flops_per_launch": flops}
+    elif args.op == "decode":
+        gbs = decode_bytes / (ms / 1e3) / 1e9     # every page once, however many requests share it
+        metric, value, unit, hib = "decoding step of one layer behind the fused prefill", ms * 1e3, "us", False
+        roof = {"bound": "hbm", "achieved": gbs, "peak": hbm, "unit": "GB/s", "frac": gbs / hbm,
+                "peak_source": src + " copy", "traffic": None, "algorithmic_bytes_per_launch": decode_bytes}
     elif args.op == "key_norms":
         nbytes = L.total_tokens * (b.hkv * b.d * 2 + 4)     # every cached key read once, one fp32 out
         gbs = world * nbytes / (ms / 1e3) / 1e9
@@ -501,7 +552,8 @@ def run_op(args, pcf, b, L, cf, k_pool, dev, world, rank, local):
             "data": "synthetic",
             "config": {"workload": f"{args.config}: {DESCR[args.config]}", "tokens": L.total_tokens,
                        "l2": "flushed between timed calls (512 MB write)",
-                       **({"layers": args.layers} if args.op == "score_layers" else {})},
+                       **({"layers": args.layers} if args.op == "score_layers" else {}),
+                       **({"new_tokens_per_request": args.tokens} if args.op == "decode" else {})},
             "roofline": roof, "gpu_launches": K * per_call, "clocks": clk,
         }))
 
@@ -517,9 +569,11 @@ def main():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--op", default="step",
                     choices=["step", "key_norms", "topn_global", "anchor_probe", "layer_prefetch",
-                             "score_layers"],
+                             "score_layers", "decode"],
                     help="step: the hot path (default); key_norms / topn_global / anchor_probe / "
-                         "score_layers: one of the variants alone, on the workload's layout")
+                         "score_layers: one of the variants alone, on the workload's layout; decode: one "
+                         "decoding step of a layer behind the step")
+    ap.add_argument("--tokens", type=int, default=1, help="decode: new tokens of every request")
     ap.add_argument("--layers", type=int, default=4, help="score_layers: layers scored per call")
     ap.add_argument("--paged", action="store_true",
                     help="step: scoring and fused attention through pcf_score_paged / pcf_fused_attention_paged "
