@@ -489,7 +489,7 @@ def run_op(args, pcf, b, L, cf, k_pool, dev, world, rank, local):
         call = lambda: pcf.select_topn_global(L, norms, cf.sel_idx, cf.excl, cf.row_pos)
     elif args.op == "decode":
         call, decode_bytes = _decode_setup(args, pcf, b, L, cf, k_pool, dev)
-        per_call = 3 if args.tokens * (b.hq // b.hkv) <= 32 else 6
+        per_call = 3 if args.tokens * (b.hq // b.hkv) <= 16 else 6
     else:
         call, probe_flops, offline, per_call = _anchor_probe_setup(args, pcf, b, k_pool, dev)
     for _ in range(max(3, args.warmup)):

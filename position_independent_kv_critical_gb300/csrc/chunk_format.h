@@ -71,13 +71,15 @@ PCF_HOST_DEVICE inline int64_t many_before(int32_t seq, int32_t tpp, int32_t pai
     return p * a + m * (u * (u - 1) / 2) + u * w + u * (m - v0) + (w > v0 ? w - v0 : 0);
 }
 
-// A request has few rows when its new tokens times the query heads of a kv head are at most this.
-// Reading the pages then bounds the attention (a key and value of 4 d bytes meet 4 d flops a row, 32
-// flops a byte at most).
-constexpr int kFewRows = 32;
-// Warps of a block of the few-row kernel, each a worker, with 1, 2 or 4 tiles of 8 rows: twelve of 168
-// registers, three a sub-partition, while the accumulators leave room; eight of 255 with four tiles.
-PCF_HOST_DEVICE constexpr int few_warps(int tiles) { return tiles <= 2 ? 12 : 8; }
+// A request has few rows when its new tokens times the query heads of a kv head are at most this: two
+// 8-row tiles a warp.  Reading the pages then bounds the attention (a key and value of 4 d bytes meet 4 d
+// flops a row).  24 requests of 6 k tokens, 64/8 heads, d 128: 16 rows take 115 us in the few-row kernel
+// and 186 in the other one, 24 rows 206 with four tiles a warp (eight warps of 255 registers) and 191 in
+// the other one.
+constexpr int kFewRows = 16;
+// Warps of a block of the few-row kernel, each a worker: three a sub-partition, of 168 registers.
+constexpr int kFewWarps = 12;
+
 // Units go to the workers in contiguous runs as equal as can be: with fewer units than workers the
 // first ones take one each (so that a run's parts sit in few blocks), else each takes units / workers
 // and the first units % workers one more.  No 64-bit division: one costs more than a lookup.
@@ -122,15 +124,18 @@ struct ChunkWs {
     size_t q_rot, k_rot, many_o, many_ml, many_desc, total;
 };
 inline size_t chunk_align(size_t x) { return (x + 255) / 256 * 256; }
-// Most rows of a request the few-row kernel takes: 8, 16 or 32, what the dims allow.  Where some request
-// may have more than 32, so that the other kernels run anyway, only what a single token needs: more row
-// tiles a warp cost every request of the batch (twelve warps against eight).
+inline bool any_many(const pcf_chunk_dims* c) {   // a request may have more than few rows
+    return (int64_t)c->max_chunk * (c->n_q_heads / c->n_kv_heads) > kFewRows;
+}
+// Most rows of a request the few-row kernel takes: 8 or 16, what the dims allow.  Where some request may
+// have more, so that the other kernels run anyway, what a single token needs: a second row tile costs
+// every request of the batch.
 inline int few_limit(const pcf_chunk_dims* c) {
-    const int64_t g = c->n_q_heads / c->n_kv_heads, rows = c->max_chunk * g > kFewRows ? g : c->max_chunk * g;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : kFewRows;
+    const int64_t g = c->n_q_heads / c->n_kv_heads;
+    return (any_many(c) ? g : c->max_chunk * g) <= 8 ? 8 : kFewRows;
 }
 inline int few_tiles(const pcf_chunk_dims* c) { return few_limit(c) / 8; }   // tiles of 8 rows a warp
-inline int few_workers(const pcf_chunk_dims* c) { return few_warps(few_tiles(c)) * chunk_sms(c->n_sms); }
+inline int few_workers(const pcf_chunk_dims* c) { return kFewWarps * chunk_sms(c->n_sms); }
 // A word the kernels compare with the plan's, so that a plan made for other dims (or by no
 // pcf_chunk_tables call at all) is refused instead of read.
 inline int32_t plan_tag(const pcf_chunk_dims* c) {
@@ -141,9 +146,6 @@ inline int32_t plan_tag(const pcf_chunk_dims* c) {
     return (int32_t)(h | 1u);   // never 0
 }
 
-inline bool any_many(const pcf_chunk_dims* c) {   // a request may have more than few rows
-    return (int64_t)c->max_chunk * (c->n_q_heads / c->n_kv_heads) > kFewRows;
-}
 inline ChunkWs chunk_ws(const pcf_chunk_dims* c) {
     ChunkWs w;
     const size_t rows = 8 * (size_t)few_tiles(c), blocks = chunk_sms(c->n_sms), d = c->head_dim;
@@ -157,7 +159,7 @@ inline ChunkWs chunk_ws(const pcf_chunk_dims* c) {
     w.many_o = chunk_align(w.k_rot + (size_t)c->max_total_pages * kPage * c->n_kv_heads * d * 2);
     w.many_ml = chunk_align(w.many_o + blocks * 2 * 256 * d * 4);
     w.many_desc = chunk_align(w.many_ml + blocks * 2 * 256 * 8);
-    w.total = chunk_align(w.many_desc + blocks * 16);
+    w.total = chunk_align(w.many_desc + blocks * 32);
     return w;
 }
 

@@ -44,7 +44,7 @@ __device__ __forceinline__ int32_t pages_of(int32_t tokens) { return (tokens + k
 __device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) { return min(a + b, kSumLimit); }
 
 // A request's work in the attention: (page, kv head) units with few rows, else the key tiles all its
-// row pairs visit (every kv head) and its pages.
+// row pairs visit (every kv head) and the pages whose keys are rotated beforehand.
 struct ChunkWork {
     int32_t few, many, pages;
 };
@@ -55,7 +55,8 @@ __device__ __forceinline__ ChunkWork chunk_work(const TablesParams& p, int32_t s
     if ((int64_t)n * g <= p.few_rows) return {pages * p.hkv, 0, 0};
     const int tpp = 2 * kTileRows / g, last = many_pairs(n, tpp) - 1;
     const int64_t tiles = (many_before(s, tpp, last) + many_tiles(s, n, tpp, last)) * p.hkv;
-    return {0, (int32_t)min(tiles, (int64_t)kSumLimit), pages};
+    // (rows that fit one tile: the kernel rotates the keys itself)
+    return {0, (int32_t)min(tiles, (int64_t)kSumLimit), n * g <= kTileRows ? 0 : pages};
 }
 
 // Request of row i: the last b with base[b] <= i (requests without rows are passed over).

@@ -6,20 +6,20 @@
 // a row with no slot left giving zeros.
 //
 // What bounds it: every (page, kv head) -- 16 keys and values, 4 d bytes a token -- is read once and
-// meets at most 32 rows, so HBM bounds it and the arithmetic only has to keep out of the way.  One
-// block an SM, eight warps, each a worker of its own: the units of all requests, in (request, kv
-// head, page) order, are dealt to the workers in equal contiguous runs by pcf_chunk_tables, whatever
-// the lengths.  A worker keeps a ring of units in flight (its lane 0 copies K and V of a page by
-// TMA, 128-byte swizzled, and the cos/sin row of the page's first position), so no warp waits for
-// another and an SM has more than 100 KB on the way.
+// meets at most 16 rows, so HBM bounds it and the arithmetic only has to keep out of the way.  One block
+// an SM, twelve warps, each a worker of its own: the units of all requests, in (request, kv head, page)
+// order, are dealt to the workers in equal contiguous runs by pcf_chunk_tables, whatever the lengths.
+// Lane l of a worker holds the table entry of the l-th page ahead and copies it by TMA (128-byte
+// swizzled) with the cos/sin row of the page's first position, into a ring of the worker's own, so no
+// warp waits for another and an SM has more than 100 KB on the way.
 //
 // The keys are rotated in registers: the fragments of mma.m16n8k16's A operand (m = the page's 16 keys,
 // k = d) that ldmatrix gives a thread hold dimensions i and i + d/2 of the same key, so a pair turns
 // inside one thread.  The angle of slot r is that of the page's first position plus r steps:
 // (C + iS)(c_r + i s_r) with the table row copied beside the page and rows 0..15 kept in shared
 // memory -- four more multiply-adds a pair instead of sixteen table rows (8 KB at d = 128, as much as
-// the unit itself) a page.  S^T = K Q^T (fp16) takes the rows as its 8-wide side, so 8, 16 or 32 rows
-// cost one, two or four products a step; the running maximum and sum of the softmax stay in registers
+// the unit itself) a page.  S^T = K Q^T (fp16) takes the rows as its 8-wide side, so 8 or 16 rows cost
+// one or two products a step; the running maximum and sum of the softmax stay in registers
 // (rescaled only when the maximum grows by more than 2^8), P^T in bf16 becomes the B operand of O^T +=
 // V^T P^T by an 8 x 8 transpose in registers (movmatrix).  The sum takes the rounded weights, so a row
 // with one dominant key is exact.  A tcgen05 tile of 128 rows would be nine tenths padding here.
@@ -55,7 +55,7 @@ struct FewParams {
 
 template <int D, int NQ>
 struct FewSmem {
-    static constexpr int kWarps = few_warps(NQ);
+    static constexpr int kWarps = kFewWarps;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kHalf = kPage * 128;                       // 16 rows of 64 elements
     static constexpr int kK = kPage * D * 2;
@@ -494,7 +494,6 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 } else {
 #pragma unroll
                     for (int q = 0; q < NQ; q += 2) {
-                        if (NQ == 4 && q == 2 && n_rows <= 16) break;   // (a branch a tile would cost more than the tile)
                         const uint4 b = s_q[((q >> 1) * KS + ks) * 32 + lane];
                         mma_f16_16816(sc[q][up], a, b.x, b.y);
                         mma_f16_16816(sc[q + 1][up], a, b.z, b.w);
@@ -514,7 +513,6 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         bool over = false;
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
-            if (NQ == 4 && q == 2 && n_rows <= 16) break;
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[q][e] = sc[q][0][e] + sc[q][1][e];
             seen = f2_add(seen, f2_add(f2_pack(x[q][0], x[q][1]), f2_pack(x[q][2], x[q][3])));
@@ -532,7 +530,6 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
-                if (NQ == 4 && q == 2 && n_rows <= 16) break;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float mx = fmaxf(x[q][e], x[q][2 + e]);
@@ -554,7 +551,6 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
-            if (NQ == 4 && q == 2 && n_rows <= 16) break;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float ms = m_run[q][e] == -INFINITY ? 0.f : m_run[q][e];
@@ -589,7 +585,6 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             ldsm4_t((sv_u ^ ((2 * mt & 7) * 16)) + (mt >> 2) * SM::kHalf, a[0], a[2], a[1], a[3]);
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
-                if (NQ == 4 && q == 2 && n_rows <= 16) break;
                 mma_bf16_16816(o[q][mt], a, pf[q][0], pf[q][1]);
             }
         }
@@ -605,7 +600,6 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             float* part = last ? reinterpret_cast<float*>(ring) : p.worker_o + (int64_t)worker * ROWS * D;
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
-                if (NQ == 4 && q == 2 && n_rows <= 16) break;
                 float l[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {

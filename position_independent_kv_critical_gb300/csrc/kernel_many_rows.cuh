@@ -1,12 +1,15 @@
 // Attention of requests with more than a few new rows (prompt chunks) over their pages.
 //
 // The same sums as kernel_few_rows.cuh; here a key meets up to thousands of rows, so the tensor cores
-// bound it.  Two launches: chunk_rotate_kernel rotates the chunk's queries and, once, the keys of the
+// bound it.  Three launches: chunk_rotate_kernel rotates the chunk's queries and, once, the keys of the
 // requests' pages into the workspace (fp16, slot order, slots that take no part zeroed); a key tile is
 // visited by every pair of row tiles of its request, and rotating it at each visit costs more than
 // writing and re-reading it once (the page-reading fused attention of this library, which does rotate
 // in the kernel, takes twice as long).  The values stay in the pool: many_rows_kernel copies a key
-// tile's eight pages straight from it.
+// tile's eight pages straight from it.  A request whose rows fit one tile (128: a long draft, a short
+// chunk) visits each key once: its keys are not rotated beforehand but copied from their pages and rotated
+// in shared memory by the warps that would have tile B (24 requests of 6 k tokens with 64 rows: 262 -> 198
+// us; 152 without the rotation's arithmetic, 91 at the copy rate: two key stages hide the copies in part).
 //
 // many_rows_kernel: one block an SM; a run is two 128-row tiles A and B of one (request, kv head) --
 // row m of a tile is token m / g, query head m % g of the kv head -- against the 128-key tiles its last
@@ -14,7 +17,7 @@
 // in equal contiguous parts by pcf_chunk_tables, whatever the lengths; a block passes on what it has of
 // the runs it shares with its neighbours (two at most) and many_join_kernel adds those up in a fixed
 // order.
-//   warps 0-3   softmax of tile A, warps 4-7 of tile B: S row from TMEM, causal cut and exclusion bits,
+//   warps 0-3   softmax of tile A, warps 4-7 of tile B (or the rotation): S row from TMEM, causal cut and exclusion bits,
 //               online softmax (lazy rescale), P -> TMEM over the S columns, O epilogue
 //   warps 8/11  Q K^T issue for tile A / B (warp 8 also owns the TMEM allocation)
 //   warps 12/13 P V issue for tile A / B
@@ -63,7 +66,7 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const RotateParams p)
     const int32_t* add = p.plan + plan_array(CA_NEW, p.n);
     const int32_t* kpage = p.plan + plan_array(CA_KPAGE, p.n);
     const int32_t rows = p.plan[C_ROWS], pages = kpage[p.n];
-    if (pages == 0) return;      // no request with many rows
+    if (p.plan[plan_array(CA_MANY, p.n) + p.n] == 0) return;      // no request with many rows
     const int c = threadIdx.x % CPR, r = threadIdx.x / CPR % kPage, h0 = threadIdx.x / (CPR * kPage);
     const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
     const int q_blocks = (rows + kPage - 1) / kPage;
@@ -157,12 +160,15 @@ __global__ void __launch_bounds__(256) chunk_rotate_kernel(const RotateParams p)
 struct ManyParams {
     const int32_t* plan;
     const int32_t* block_table;
+    const int32_t* page_pos;
     const uint16_t* excl;       // or null
+    const float* rope;
     __nv_bfloat16* out;
     float* part_o;              // [blocks][2][256][D]
     float2* part_ml;            // [blocks][2][256]
-    int4* desc;                 // [blocks]: a run begun here that goes on: {last block << 8 | 255, request, kv head, pair}
-    int32_t n, max_pages, max_rows, hq, hkv, n_phys, workers, blocks, tag, total_pages;
+    int4* desc;                 // [blocks][2]: a run begun here that goes on: {last block << 8 | 255, first token, kv head, 0},
+                                //   {new tokens, first row, 0, 0}
+    int32_t n, max_pages, max_rows, hq, hkv, n_phys, max_pos, workers, blocks, tag, total_pages;
 };
 
 constexpr int kManyThreads = 448;
@@ -175,7 +181,8 @@ struct ManyItem {
     int32_t jb, n_loc;          // its key tiles
     int32_t seq, add, row_base, kpage;
     int32_t slot;               // partial result, or -1: the whole run
-    int32_t pad[2];
+    int32_t single;             // all rows fit tile A: keys straight from the pages, rotated here
+    int32_t pad;
 };
 
 template <int D>
@@ -211,13 +218,115 @@ enum : int {
     MB_O_FREE = 30,     // [2]
     MB_DRAIN = 32,      // [4]
     MB_ITEM_FULL = 36,  // [2]
-    MB_ITEM_EMPTY = 38  // [2]
+    MB_ITEM_EMPTY = 38, // [2]
+    MB_K_RAW = 40,      // [2] single: the tile's pages landed
+    MB_K_ROT = 42       // [2] single: rotated in place (every thread of warps 4-7)
 };
+
+// Warps 4-7 on a single-tile run: every key tile rotated in place, bf16 in, fp16 out.  Thread t has 16-byte
+// chunk pair c (dimensions 8 c .. and d/2 + 8 c ..) of N consecutive keys of page t / 16: their angles
+// start from the cos/sin row of the first one's position and advance by one position, a rotation by
+// table row 1, from key to key.  Slots that take no part become zeros (they may hold anything).  A tile
+// is rotated once for all its rows, beside the softmax of tile A: some 350 of the 2800 issue slots an SM
+// sub-partition has while HBM delivers a tile.
+template <int D>
+__device__ __forceinline__ bool rotate_tiles(const ManyParams& prm, const ManyItem& w, uint8_t* stages, int stage_bytes,
+                                             const uint16_t* s_mask, uint64_t* bars, int kc, int (&raw_n)[2], int t,
+                                             int lane, volatile int* abort_flag) {
+    constexpr int CP = D / 16, N = D / 16;              // chunk pairs of a row; keys a thread (16 threads a page)
+    const int page = t / 16, c = t % 16 % CP, r0 = t % 16 / CP * N;
+    const uint32_t o_hi = D == 128 ? 16384u : 0u;
+    const int c_hi = D == 128 ? c : c + 4;
+    const bool masked = prm.excl != nullptr;
+    const int n_slots = w.seq + w.add, n_pages = pages_of(n_slots);
+    const int32_t* pos_row = prm.page_pos + (int64_t)w.req * prm.max_pages;
+    auto position = [&](int j) { return pos_row[min(j * kPagesPerTile + page, n_pages - 1)]; };
+    auto in_table = [&](int32_t pos) { return pos >= 0 && pos <= prm.max_pos - kPage; };
+    auto row_of = [&](int32_t pos, float4 (&v)[4]) {
+        const float4* src = reinterpret_cast<const float4*>(prm.rope + (int64_t)(in_table(pos) ? pos + r0 : 0) * D + 16 * c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = src[e];
+    };
+    uint64_t STC[4], STS[4];
+    {
+        const float4* one = reinterpret_cast<const float4*>(prm.rope + D + 16 * c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4 v = one[e];
+            STC[e] = f2_pack(v.x, v.z);
+            STS[e] = f2_pack(v.y, v.w);
+        }
+    }
+    // the position of a tile's page is loaded two tiles ahead, its cos/sin row one
+    int32_t pos = position(w.jb), pos_n = position(w.jb + 1);
+    float4 cs[4];
+    row_of(pos, cs);
+    float big = 0.f, nan = 0.f;
+    for (int jj = 0; jj < w.n_loc; ++jj, ++kc) {
+        const int ks = kc & 1, first = (w.jb + jj) * kTileKeys + page * kPage;
+        uint32_t gone = 0;
+        if (!in_table(pos)) {
+            set_dev_error(kDevErrBounds);
+            gone = 0xFFFFu;
+        }
+        const int have = min(max(n_slots - first, 0), kPage);
+        gone |= 0xFFFFu & ~((1u << have) - 1u);
+        uint64_t C[4], S[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            C[e] = f2_pack(cs[e].x, cs[e].z);
+            S[e] = f2_pack(cs[e].y, cs[e].w);
+        }
+        pos = pos_n;
+        pos_n = position(w.jb + jj + 2);
+        row_of(pos, cs);
+        bool ok = mbar_wait(&bars[MB_K_RAW + ks], raw_n[ks]++ & 1, abort_flag);
+        if (masked) {
+            ok = ok && mbar_wait(&bars[MB_M_FULL + ks], (kc >> 1) & 1, abort_flag);
+            if (__all_sync(0xffffffffu, ok)) gone |= s_mask[ks * 8 + page];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[MB_M_EMPTY + ks]);
+        }
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        uint8_t* stage = stages + ks * stage_bytes;
+#pragma unroll 2
+        for (int r = 0; r < N; ++r) {
+            const int key = page * kPage + r0 + r;
+            uint4* plo = reinterpret_cast<uint4*>(stage + sw128_off(key, c));
+            uint4* phi = reinterpret_cast<uint4*>(stage + o_hi + sw128_off(key, c_hi));
+            uint4 a = *plo, b = *phi;
+            if (gone >> (r0 + r) & 1u) a = b = make_uint4(0, 0, 0, 0);
+            const uint32_t ia[4] = {a.x, a.y, a.z, a.w}, ib[4] = {b.x, b.y, b.z, b.w};
+            uint32_t oa[4], ob[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t A = bf16x2_to_f2(ia[e]), B = bf16x2_to_f2(ib[e]), minus = f2_pack(-1.f, -1.f);
+                float y0, y1, z0, z1;
+                f2_unpack(f2_fma(f2_mul(B, S[e]), minus, f2_mul(A, C[e])), y0, y1);   // a cos - b sin
+                f2_unpack(f2_fma(A, S[e], f2_mul(B, C[e])), z0, z1);                   // b cos + a sin
+                nan = fmaf(y0 + y1, 0.f, nan);
+                oa[e] = pack_f16x2_track(y0, y1, big);
+                ob[e] = pack_f16x2_track(z0, z1, big);
+                // one position further
+                const uint64_t cn = f2_fma(f2_mul(S[e], STS[e]), minus, f2_mul(C[e], STC[e]));
+                S[e] = f2_fma(C[e], STS[e], f2_mul(S[e], STC[e]));
+                C[e] = cn;
+            }
+            *plo = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+            *phi = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[MB_K_ROT + ks]);
+    }
+    if (!(big < kF16Limit) || nan != nan) set_dev_error(kDevErrRange);
+    return true;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kManyThreads)
 many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const ManyParams prm) {
+                 const __grid_constant__ CUtensorMap tm_kpool, const __grid_constant__ CUtensorMap tm_v,
+                 const ManyParams prm) {
     using SM = ManySmem<D>;
     constexpr int H = SM::kHalves;
     constexpr int kReaders = 13;   // softmax warps, issuers, V producer
@@ -248,6 +357,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_init(&bars[MB_O_FREE + s], 128);
             mbar_init(&bars[MB_ITEM_FULL + s], 1);
             mbar_init(&bars[MB_ITEM_EMPTY + s], kReaders);
+            mbar_init(&bars[MB_K_RAW + s], 1);
+            mbar_init(&bars[MB_K_ROT + s], 128);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars[MB_S_FULL + i], 1);
@@ -259,6 +370,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         misc[4] = 0;
         prefetch_tmap(&tm_q);
         prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_kpool);
         prefetch_tmap(&tm_v);
     }
     grid_dep_wait();
@@ -294,9 +406,9 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int4 start = st[0], part = st[1];
         int left = part.y == prm.tag ? part.x : 0;
         int32_t req = start.x, kvh = start.y, pair = start.z, tile = start.w;
-        int kc = 0, last_k[2] = {-1, -1}, last_q = -1;
+        int kc = 0, last_k[2] = {-1, -1}, last_q = -1, raw_n[2] = {0, 0}, full_n[2] = {0, 0};   // copies of either kind a stage took
         bool ok = true;
-        int4 desc = make_int4(0, 0, 0, 0);
+        int4 desc = make_int4(0, 0, 0, 0), desc_rows = desc;
         for (int it = 0; ok; ++it) {
             ManyItem w;
             w.req = left > 0 ? req : -1;
@@ -305,12 +417,13 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             w.jb = tile;
             w.n_loc = w.seq = w.add = w.row_base = w.kpage = 0;
             w.slot = -1;
-            w.pad[0] = w.pad[1] = 0;
+            w.single = w.pad = 0;
             if (left > 0) {
                 w.seq = seq[req];
                 w.add = add[req];
                 w.row_base = row[req];
                 w.kpage = kpage[req];
+                w.single = w.add << gs <= kTileRows;
                 const int all = many_tiles(w.seq, w.add, tpp, pair);
                 w.n_loc = min(all - tile, left);
                 left -= w.n_loc;
@@ -319,7 +432,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     // the block that holds the run's last tile
                     const int32_t u = many[req] + kvh * ((many[req + 1] - many[req]) / prm.hkv) +
                                       (int32_t)many_before(w.seq, tpp, pair) + all - 1;
-                    desc = make_int4(Deal(many[prm.n], prm.blocks).owner(u) << 8 | 0xFF, req, kvh, pair);
+                    desc = make_int4(Deal(many[prm.n], prm.blocks).owner(u) << 8 | 0xFF, pair * tpp, kvh, 0);
+                    desc_rows = make_int4(w.add, w.row_base, 0, 0);
                 }
             }
             if (lane == 0) {
@@ -335,8 +449,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const int32_t qy = (w.kvh * prm.max_rows + w.row_base + w.pair * tpp) * g;
                 if (it > 0) ok = mbar_wait(&bars[MB_Q_EMPTY], (it - 1) & 1, abort_flag);
                 if (ok) {
-                    mbar_arrive_expect_tx(&bars[MB_Q_FULL], 2 * SM::kQ);
-                    for (int t = 0; t < 2; ++t)
+                    mbar_arrive_expect_tx(&bars[MB_Q_FULL], (w.single ? 1 : 2) * SM::kQ);
+                    for (int t = 0; t < (w.single ? 1 : 2); ++t)
                         for (int hb = 0; hb < H; ++hb)
                             tma_load_2d(sQ(t) + hb * 16384, &tm_q, &bars[MB_Q_FULL], hb * 64, qy + t * kTileRows);
                     last_q = it;
@@ -345,8 +459,17 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             const uint16_t* ex = masked ? prm.excl + (int64_t)w.req * prm.max_pages : nullptr;
+            const int32_t* table = prm.block_table + (int64_t)w.req * prm.max_pages;
+            const int n_pages = pages_of(w.seq + w.add), m = lane % kPagesPerTile, hb_l = lane / kPagesPerTile;
+            int32_t ph_n = w.single ? table[min(w.jb * kPagesPerTile + m, n_pages - 1)] : 0;
             for (int jj = 0; jj < w.n_loc; ++jj, ++kc) {
                 const int j = w.jb + jj, ks = kc & 1;
+                int32_t ph = ph_n;
+                if (ph < 0 || ph >= prm.n_phys) {
+                    set_dev_error(kDevErrBounds);
+                    ph = 0;
+                }
+                if (w.single && jj + 1 < w.n_loc) ph_n = table[min((j + 1) * kPagesPerTile + m, n_pages - 1)];
                 uint32_t bits = 0;
                 if (masked && lane < kPagesPerTile) {
                     const int pg = j * kPagesPerTile + lane;
@@ -354,7 +477,9 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 if (lane == 0) {
                     ok = kc < 2 || mbar_wait(&bars[MB_K_EMPTY + ks], ((kc >> 1) - 1) & 1, abort_flag);
-                    if (ok) {
+                    if (ok && w.single) {
+                        mbar_arrive_expect_tx(&bars[MB_K_RAW + ks], H * 16384);
+                    } else if (ok) {
                         mbar_arrive_expect_tx(&bars[MB_K_FULL + ks], H * 16384);
                         const int32_t y = w.kvh * prm.total_pages * kPage + w.kpage * kPage + j * kTileKeys;
                         for (int hb = 0; hb < H; ++hb)
@@ -363,7 +488,14 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
-                last_k[ks] = kc;
+                if (w.single) {
+                    if (lane < kPagesPerTile * H)
+                        tma_load_2d(sK(ks) + hb_l * 16384 + m * (kPage * 128), &tm_kpool, &bars[MB_K_RAW + ks], hb_l * 64,
+                                    (ph * prm.hkv + w.kvh) * kPage);
+                    ++raw_n[ks];
+                } else {
+                    last_k[ks] = full_n[ks]++;
+                }
                 if (masked) {
                     ok = kc < 2 || mbar_wait(&bars[MB_M_EMPTY + ks], ((kc >> 1) - 1) & 1, abort_flag);
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -383,10 +515,13 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
         }
         if (lane == 0) {
-            prm.desc[blockIdx.x] = ok ? desc : make_int4(0, 0, 0, 0);
+            prm.desc[2 * blockIdx.x] = ok ? desc : make_int4(0, 0, 0, 0);
+            prm.desc[2 * blockIdx.x + 1] = desc_rows;
             if (last_q >= 0) mbar_drain(&bars[MB_Q_FULL], last_q & 1);
-            for (int s = 0; s < 2; ++s)
-                if (last_k[s] >= 0) mbar_drain(&bars[MB_K_FULL + s], (last_k[s] >> 1) & 1);
+            for (int s = 0; s < 2; ++s) {
+                if (last_k[s] >= 0) mbar_drain(&bars[MB_K_FULL + s], last_k[s] & 1);
+                if (raw_n[s] > 0) mbar_drain(&bars[MB_K_RAW + s], (raw_n[s] - 1) & 1);
+            }
         }
     } else if (warp == kWarpTmaV) {
         // ------------------------------------------------------------ V tiles
@@ -415,7 +550,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 ph_n = table[min(pg, n_pages - 1)];
                 const int have = min(max(n_slots - pg * kPage, 0), kPage);
                 gone_n = 0xFFFFu & ~((1u << have) - 1u);
-                if (ph_n < 0 || ph_n >= prm.n_phys) {    // (reported by the rotation; finite data instead)
+                if (ph_n < 0 || ph_n >= prm.n_phys) {    // (reported with its key; finite data instead)
                     ph_n = 0;
                     gone_n = 0xFFFFu;
                 }
@@ -469,6 +604,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int t = (warp == kWarpMma || warp == kWarpPvA) ? 0 : 1;
         const uint32_t leader = lane == 0 ? 1u : 0u;
         int hq = 0, kc = 0;
+        int raw_n[2] = {0, 0}, full_n[2] = {0, 0};       // K tiles of either kind a stage held before
         bool ok = true;
         for (int it = 0; ok; ++it) {
             ManyItem w;
@@ -478,6 +614,23 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (leader) mbar_arrive(&bars[MB_ITEM_EMPTY + (it & 1)]);
             if (w.req < 0) break;
             const int nq = 2 * w.n_loc;
+            auto wait_k = [&](int ks) {
+                return w.single ? mbar_wait(&bars[MB_K_ROT + ks], raw_n[ks]++ & 1, abort_flag)
+                                : mbar_wait(&bars[MB_K_FULL + ks], full_n[ks]++ & 1, abort_flag);
+            };
+            if (w.single && t == 1) {
+                // tile B is not there: its issuers only take their part in the hand-offs
+                for (int j = 0; ok && j < w.n_loc; ++j) {
+                    const int kt = kc + j;
+                    ok = __all_sync(0xffffffffu, qk_role ? wait_k(kt & 1)
+                                                         : mbar_wait(&bars[MB_V_FULL + (kt & 1)], (kt >> 1) & 1, abort_flag));
+                    if (ok && leader) mbar_arrive(&bars[(qk_role ? MB_K_EMPTY : MB_V_EMPTY) + (kt & 1)]);
+                }
+                if (ok && qk_role) ok = __all_sync(0xffffffffu, mbar_wait(&bars[MB_Q_FULL], it & 1, abort_flag));
+                if (ok && leader) mbar_arrive(&bars[qk_role ? MB_Q_EMPTY : MB_O_DONE + 1]);
+                kc += w.n_loc;
+                continue;
+            }
             if (qk_role) {
                 constexpr uint32_t idesc_qk = idesc_f16(128, 64);
                 const uint32_t aQ = desc_sw128_lo(smem_u32(sQ(t)), 16);
@@ -485,7 +638,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int q = 0; ok && q < nq; ++q) {
                     const int hg = hq + q, kt = kc + (q >> 1), h = q & 1;
                     ok = __all_sync(0xffffffffu,
-                                    (h == 1 || mbar_wait(&bars[MB_K_FULL + (kt & 1)], (kt >> 1) & 1, abort_flag)) &&
+                                    (h == 1 || wait_k(kt & 1)) &&
                                         (hg < 2 || mbar_wait(&bars[MB_PV_DONE + 2 * t + (hg & 1)],
                                                              ((hg - 2) >> 1) & 1, abort_flag)));
                     if (!ok) break;
@@ -532,6 +685,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tO = tmem + lane_addr + kTmemO + t * 128;
         int hq = 0, kc = 0;
+        int raw_n[2] = {0, 0};
         bool ok = true;
         for (int it = 0; ok; ++it) {
             ManyItem w;
@@ -540,6 +694,13 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[MB_ITEM_EMPTY + (it & 1)]);
             if (w.req < 0) break;
+            if (w.single && t == 1) {
+                ok = rotate_tiles<D>(prm, w, sK(0), SM::kK, s_mask, bars, kc, raw_n, m, lane, abort_flag);
+                if (!ok) break;
+                mbar_arrive(&bars[MB_O_FREE + 1]);
+                kc += w.n_loc;
+                continue;
+            }
             const int tok = w.pair * tpp + t * tpt + (m >> gs);
             const bool valid = tok < w.add;
             const int limit = w.seq + min(tok, w.add - 1) + 1;   // slots the row sees
@@ -687,13 +848,13 @@ __global__ void __launch_bounds__(256) many_join_kernel(const ManyParams p) {
     grid_dep_wait();
     grid_dep_launch();
     const int j = blockIdx.x;
-    const int4 d = p.desc[j];
+    const int4 d = p.desc[2 * j], rows = p.desc[2 * j + 1];
     if (d.x == 0) return;
     const int last = d.x >> 8;
     const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
     const int r = blockIdx.y * ROWS + threadIdx.x / (D / 4), f = threadIdx.x % (D / 4);
-    const int tok = d.w * (kPairRows >> gs) + (r >> gs);
-    if (tok >= p.plan[plan_array(CA_NEW, p.n) + d.y]) return;
+    const int tok = d.y + (r >> gs);
+    if (tok >= rows.x) return;
     float top = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int b = j; b <= last; ++b) {
@@ -710,7 +871,7 @@ __global__ void __launch_bounds__(256) many_join_kernel(const ManyParams p) {
         acc.w = acc.w * old + a * v.w;
     }
     const float inv = l > 0.f ? 1.0f / l : 0.f;
-    const int64_t row = (int64_t)(p.plan[plan_array(CA_ROW, p.n) + d.y] + tok) * p.hq + d.z * g + (r & (g - 1));
+    const int64_t row = (int64_t)(rows.y + tok) * p.hq + d.z * g + (r & (g - 1));
     *reinterpret_cast<uint2*>(p.out + row * D + 4 * f) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }

@@ -1072,27 +1072,28 @@ pcf_status many_rows_impl(const ChunkCall& c, cudaStream_t st) {
     const int blocks = chunk_sms(d.n_sms), workers = few_workers(&d);
     __half* q_rot = reinterpret_cast<__half*>(c.ws + w.q_rot);
     __half* k_rot = reinterpret_cast<__half*>(c.ws + w.k_rot);
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk, tkp, tv;
     pcf_status s;
     if ((s = make_map_2d(&tq, q_rot, D, (uint64_t)d.max_rows * d.n_q_heads, D * 2, kTileRows, kF16)) != PCF_OK) return s;
     if ((s = make_map_2d(&tk, k_rot, D, (uint64_t)d.max_total_pages * d.n_kv_heads * kPage, D * 2, kTileKeys, kF16)) !=
         PCF_OK)
         return s;
-    if ((s = make_map_2d(&tv, c.v_pool, D, (uint64_t)d.n_phys_pages * d.n_kv_heads * kPage, D * 2, kPage)) != PCF_OK)
-        return s;
+    const uint64_t pool_rows = (uint64_t)d.n_phys_pages * d.n_kv_heads * kPage;
+    if ((s = make_map_2d(&tkp, c.k_pool, D, pool_rows, D * 2, kPage)) != PCF_OK) return s;
+    if ((s = make_map_2d(&tv, c.v_pool, D, pool_rows, D * 2, kPage)) != PCF_OK) return s;
     const RotateParams r{c.plan, reinterpret_cast<const __nv_bfloat16*>(c.q),
                          reinterpret_cast<const __nv_bfloat16*>(c.k_pool), c.block_table, c.page_pos, c.excl, c.row_pos,
                          c.rope, q_rot, k_rot, c.q_stride, d.n_reqs, d.max_pages, d.max_rows, d.n_q_heads,
                          d.n_kv_heads, d.n_phys_pages, d.max_pos, plan_tag(&d), d.max_total_pages};
     if ((s = launch(chunk_rotate_kernel<D>, dim3(8 * blocks), dim3(256), 0, st, r)) != PCF_OK) return s;
-    const ManyParams p{c.plan, c.block_table, c.excl, reinterpret_cast<__nv_bfloat16*>(c.out),
+    const ManyParams p{c.plan, c.block_table, c.page_pos, c.excl, c.rope, reinterpret_cast<__nv_bfloat16*>(c.out),
                        reinterpret_cast<float*>(c.ws + w.many_o), reinterpret_cast<float2*>(c.ws + w.many_ml),
                        reinterpret_cast<int4*>(c.ws + w.many_desc), d.n_reqs, d.max_pages, d.max_rows, d.n_q_heads,
-                       d.n_kv_heads, d.n_phys_pages, workers, blocks, plan_tag(&d), d.max_total_pages};
+                       d.n_kv_heads, d.n_phys_pages, d.max_pos, workers, blocks, plan_tag(&d), d.max_total_pages};
     using SM = ManySmem<D>;
     auto kern = many_rows_kernel<D>;
     if ((s = set_smem(kern, SM::kAlloc)) != PCF_OK) return s;
-    if ((s = launch(kern, dim3(blocks), dim3(kManyThreads), SM::kAlloc, st, tq, tk, tv, p)) != PCF_OK) return s;
+    if ((s = launch(kern, dim3(blocks), dim3(kManyThreads), SM::kAlloc, st, tq, tk, tkp, tv, p)) != PCF_OK) return s;
     return launch(many_join_kernel<D>, dim3(blocks, kPairRows * (D / 4) / 256), dim3(256), 0, st, p);
 }
 
@@ -1102,9 +1103,7 @@ pcf_status chunk_attention_impl(const ChunkCall& c, cudaStream_t st) {
     pcf_status s;
     if (any_many(c.dims) && (s = many_rows_impl<D>(c, st)) != PCF_OK) return s;
     if (c.dims->n_q_heads / c.dims->n_kv_heads > few_limit(c.dims)) return PCF_OK;
-    const int tiles = few_tiles(c.dims);
-    return tiles == 1 ? few_rows_impl<D, 1>(c, st)
-                      : tiles == 2 ? few_rows_impl<D, 2>(c, st) : few_rows_impl<D, 4>(c, st);
+    return few_tiles(c.dims) == 1 ? few_rows_impl<D, 1>(c, st) : few_rows_impl<D, 2>(c, st);
 }
 }  // namespace
 

@@ -632,3 +632,27 @@ def test_a_workspace_full_of_nan_does_not_matter(seq, new):
     c.attend()
     pcf.check_device_error()
     c.check(c.out.float().cpu().double().numpy(), rows=6)
+
+
+@pytest.mark.parametrize("extra", [[], ["--tokens", "3"], ["--tokens", "40"]])
+def test_bench_decode_runs_behind_the_fused_prefill(extra):
+    import json
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "bench.py", "--config", "tiny", "--op", "decode", "--steps", "3", "--warmup", "3"]
+                       + extra, cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    line = json.loads(r.stdout.strip().splitlines()[-1])
+    assert line["op"] == "decode" and line["value"] > 0 and line["roofline"]["algorithmic_bytes_per_launch"] > 0
+
+
+@pytest.mark.parametrize("shape", [SHAPES[1], SHAPES[0], SHAPES[8]], ids=[IDS[1], IDS[0], IDS[8]])
+def test_requests_of_every_kind_in_one_batch(shape):
+    """Idle requests, single tokens, drafts, chunks of one row tile and of several, with exclusions."""
+    c = ChunkCase([700, 31, 0, 260, 900, 1, 145, 16], [1, 0, 33, 3, 150, 5, 20, 2], spare_rows=3, **shape)
+    random_excl(c, 0.2, 3)
+    poison_excluded(c)
+    c.to_device()
+    c.check(c.step(), rows=6)
