@@ -11,6 +11,8 @@
 #include "../../include/pcf.h"
 #include "layout_format.h"
 
+#include <initializer_list>
+
 namespace pcf {
 
 constexpr int kMaxReqs = 4096;               // requests of one chunk batch (one block scans them)
@@ -80,17 +82,30 @@ constexpr int kFewRows = 16;
 // Warps of a block of the few-row kernel, each a worker: three a sub-partition, of 168 registers.
 constexpr int kFewWarps = 12;
 
-// Units go to the workers in contiguous runs as equal as can be: with fewer units than workers the
-// first ones take one each (so that a run's parts sit in few blocks), else each takes units / workers
-// and the first units % workers one more.  No 64-bit division: one costs more than a lookup.
+// Units go to the workers in contiguous runs as equal as can be, worker w from floor(w units / active) on:
+// the longer runs are spread evenly over the blocks, and where the runs of a batch are alike (one request:
+// its kv heads) their ends fall on ends of workers, which spares a worker a second run with its queries
+// and partial results (one request of 4 k tokens: 14.3 us with the longer runs on the first workers, 11.8
+// so).  With fewer units than workers the first ones take one each (a run's parts then sit in few blocks).
+// `left` is more / active in units of 2^-32, rounded up (more units left over, active <= 12 * 4096 workers:
+// w left / 2^32 is then within 2^-16 of its value, and its floor exact); no division a worker.
 struct Deal {
-    int32_t units, active, each, more;
-    PCF_HOST_DEVICE Deal(int32_t n, int32_t workers)
-        : units(n), active(n < workers ? n : workers), each(n > 0 ? n / active : 0), more(n > 0 ? n % active : 0) {}
-    PCF_HOST_DEVICE int32_t first(int32_t w) const { return w < active ? w * each + (w < more ? w : more) : units; }
-    PCF_HOST_DEVICE int32_t owner(int32_t u) const {   // (0 <= u < units)
-        const int32_t big = more * (each + 1);
-        return u < big ? u / (each + 1) : more + (u - big) / each;
+    uint32_t units, active, each, left;
+    PCF_HOST_DEVICE Deal(int32_t n, int32_t workers) : units(n), active(n < workers ? n : workers), each(0), left(0) {
+        if (n <= 0) return;
+        each = units / active;
+        const uint32_t more = units - each * active, hi = (more << 16) / active, rest = (more << 16) - hi * active;
+        left = more ? (hi << 16 | (rest << 16) / active) + 1 : 0;
+    }
+    PCF_HOST_DEVICE int32_t first(uint32_t w) const {
+        return (int32_t)(w < active ? w * each + (uint32_t)((uint64_t)w * left >> 32) : units);
+    }
+    PCF_HOST_DEVICE int32_t owner(int32_t u) const {   // (0 <= u < units): the last worker that begins at or before u
+        int32_t w = (int32_t)((float)u * ((float)active / (float)units));
+        w = w < (int32_t)active ? w : (int32_t)active - 1;
+        while (first(w) > u) --w;
+        while (first(w + 1) <= u) ++w;
+        return w;
     }
 };
 

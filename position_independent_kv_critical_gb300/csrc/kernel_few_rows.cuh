@@ -128,16 +128,19 @@ __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], const uint32_t (&a
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Four partial results of a row (maximum and sum; weighted values) joined onto a running one; a part
-// without a maximum adds nothing.
-__device__ __forceinline__ void add_parts(const float2 (&ml)[4], const float4 (&v)[4], float& top, float& l, float4& acc) {
-    const float now = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), top);
+// Partial results of a row (maximum and sum; weighted values) joined onto a running one, in their order; a
+// part without a maximum adds nothing.
+template <int N>
+__device__ __forceinline__ void add_parts(const float2 (&ml)[N], const float4 (&v)[N], float& top, float& l, float4& acc) {
+    float now = top;
+#pragma unroll
+    for (int i = 0; i < N; ++i) now = fmaxf(now, ml[i].x);
     const float ref = now == -INFINITY ? 0.f : now, old = ex2(top - ref);
     top = now;
     l *= old;
     acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
         const float a = ex2(ml[i].x - ref);
         acc.x += a * v[i].x;
         acc.y += a * v[i].y;
