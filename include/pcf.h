@@ -57,7 +57,8 @@ typedef int32_t pcf_status;
 #define PCF_ERR_DEVICE_BOUNDS        -6  /* a kernel met an out-of-range index (reported by check) */
 #define PCF_ERR_NO_DEVICE            -7  /* no sm_103 device is current */
 #define PCF_ERR_DEVICE_RANGE         -8  /* a rotated query or key left the fp16 operand range
-                                            (infinities included; reported by check) */
+                                            (infinities included; reported by check); from
+                                            pcf_chunk_attention also a value that is not finite */
 
 /* One cached span of a request: n_pages consecutive physical pages starting at phys_first_page,
  * holding tokens at logical positions pos0 .. pos0 + 16*n_pages - 1; k of its tokens are to be
@@ -401,7 +402,8 @@ pcf_status pcf_chunk_attention_workspace_bytes(const pcf_chunk_dims* dims, size_
  * pcf_chunk_tables call) and a workspace each, as the plan holds counters that a call moves on.
  * Deterministic.  A page outside the pool, a position outside the rope table or a plan of other dims
  * raises PCF_ERR_DEVICE_BOUNDS; a rotated query or key that takes part and is not finite in fp16 (beyond
- * 65504, or NaN) PCF_ERR_DEVICE_RANGE.  The call's results must then be discarded. */
+ * 65504, or NaN), or a value that takes part and is not finite, PCF_ERR_DEVICE_RANGE (a row may share its
+ * products with keys that only later rows of its request see).  The call's results must then be discarded. */
 pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, int32_t* plan, const uint16_t* q, int64_t q_row_stride,
                                const uint16_t* k_pool, const uint16_t* v_pool, const int32_t* block_table,
                                const int32_t* page_pos, const uint16_t* excl, const int32_t* row_pos,

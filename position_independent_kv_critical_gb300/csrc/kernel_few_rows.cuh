@@ -150,6 +150,11 @@ __device__ __forceinline__ void add_parts(const float2 (&ml)[N], const float4 (&
     }
 }
 
+// `nan`, or NaN where one of the sums is not finite.
+__device__ __forceinline__ float not_finite(const float4& v, float nan) {
+    return fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, fmaf(v.w, 0.f, nan))));
+}
+
 // The ring's barriers and copies by shared-memory address: the loop keeps those in registers, where a
 // generic pointer would take two and a conversion at every use.
 __device__ __forceinline__ void ring_expect(uint32_t bar, uint32_t bytes) {
@@ -358,7 +363,9 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                            ((((lane >> 3) & 1u) ^ (D == 128 ? 0u : (uint32_t)(lane >> 4) * 4u) ^ (lane & 7u)) << 4);
     const uint32_t v_off = (lane & 15) * 128u + (((uint32_t)(lane >> 4) ^ (lane & 7u)) << 4);
     float big = 0.f;                 // largest rotated query
-    uint64_t seen = 0;               // sum of all scores: not finite where a key left fp16's range
+    // sum of all scores (not finite where a key left fp16's range), and of 0 times all results (NaN where
+    // a value that takes part is not finite)
+    uint64_t seen = 0;
     int32_t seg_page = 0;
     bool open = false, ok = true;
     int done_k = 0, done_v = 0;
@@ -620,6 +627,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     for (int mt = 0; mt < MT; ++mt) {
                         const uint32_t w0 = transpose8(pack_bf16x2(o[q][mt][0] * i0, o[q][mt][1] * i1));
                         const uint32_t w1 = transpose8(pack_bf16x2(o[q][mt][2] * i0, o[q][mt][3] * i1));
+                        seen = f2_fma(f2_pack(o[q][mt][0], o[q][mt][1]), f2_pack(0.f, 0.f), seen);
+                        seen = f2_fma(f2_pack(o[q][mt][2], o[q][mt][3]), f2_pack(0.f, 0.f), seen);
                         if (r < n_rows) {
                             dst[8 * mt] = w0;
                             dst[8 * mt + 4] = w1;
@@ -665,6 +674,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     __syncthreads();
     // ---------------- join the warps' partial results, run by run
     const bool aborted = *abort_flag != 0;
+    float nan = 0.f;                                   // NaN where a result is not finite
     int rows_of[2] = {0, 0}, kvh_of[2] = {0, 0}, base_of[2] = {0, 0};   // of the runs other blocks hold parts of
     // bit 2 w: what warp w ends of a run begun before it; bit 2 w + 1: what it leaves open
     const int32_t state = lane < 2 * WARPS ? s_desc[lane * 4] : 0;
@@ -703,6 +713,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 }
                 add_parts(ml, v, top, l, acc);
             }
+            nan = not_finite(acc, nan);
             if (!from_before && ended) {
                 const float inv = l > 0.f ? 1.0f / l : 0.f;
                 *reinterpret_cast<uint2*>(p.out + ((int64_t)(rb + (r >> gs)) * p.hq + kvh * g + (r & (g - 1))) * D + 4 * f) =
@@ -721,13 +732,14 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     // ---------------- runs that several blocks share: whoever brings the last part adds them up.  The
     // parts lie in the order of the blocks whoever adds them, so the sum does not depend on timing.
-    // The counters are the plan's: cleared with it, and a multiple of the parts behind every call.
+    // The counters are the plan's: cleared with it, and zero again behind every call.
+    if (nan != nan) set_dev_error(kDevErrRange);       // (parts of other blocks are theirs to report)
     int* s_last = reinterpret_cast<int*>(smem + SM::oAbort) + 1;
     if (rows_of[0] + rows_of[1] == 0) return;         // (uniform over the block)
     __syncthreads();
     if (tid < 2 && rows_of[tid] > 0) {
         const int from = tid == 0 ? share.y : (int)blockIdx.x, n = (tid == 0 ? share.z : share.w) - from + 1;
-        s_last[tid] = atomic_add_acq_rel_gpu(p.count + from, 1) % n == n - 1 ? 1 : 0;
+        s_last[tid] = atomic_inc_acq_rel_gpu(p.count + from, n - 1) == n - 1 ? 1 : 0;
     }
     __syncthreads();
 #pragma unroll 1

@@ -31,6 +31,7 @@
 #include "chunk_format.h"
 #include "kernel_attn.cuh"
 #include "kernel_chunk_tables.cuh"
+#include "kernel_few_rows.cuh"
 #include "ptx.cuh"
 
 namespace pcf {
@@ -686,6 +687,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t tO = tmem + lane_addr + kTmemO + t * 128;
         int hq = 0, kc = 0;
         int raw_n[2] = {0, 0};
+        float nan = 0.f;                                   // NaN where a result is not finite
         bool ok = true;
         for (int it = 0; ok; ++it) {
             ManyItem w;
@@ -813,6 +815,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     tmem_ld32(tO + cc * 32, o);
                     tmem_ld_wait();
                     if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) nan = fmaf(__uint_as_float(o[e]), 0.f, nan);
                         __nv_bfloat16* dst = prm.out + ((int64_t)(w.row_base + tok) * prm.hq + w.kvh * g + (m & (g - 1))) * D + cc * 32;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -831,6 +835,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             hq += nq;
             kc += w.n_loc;
         }
+        if (nan != nan) set_dev_error(kDevErrRange);       // (a value that takes part is not finite)
     }
     tc_fence_before();
     __syncthreads();
@@ -870,6 +875,8 @@ __global__ void __launch_bounds__(256) many_join_kernel(const ManyParams p) {
         acc.z = acc.z * old + a * v.z;
         acc.w = acc.w * old + a * v.w;
     }
+    const float odd = not_finite(acc, 0.f);
+    if (odd != odd) set_dev_error(kDevErrRange);
     const float inv = l > 0.f ? 1.0f / l : 0.f;
     const int64_t row = (int64_t)(rows.y + tok) * p.hq + d.z * g + (r & (g - 1));
     *reinterpret_cast<uint2*>(p.out + row * D + 4 * f) =

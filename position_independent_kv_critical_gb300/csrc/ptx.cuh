@@ -127,6 +127,13 @@ __device__ __forceinline__ int atomic_add_acq_rel_gpu(int* p, int v) {
     return old;
 }
 
+// The same with a counter that goes 0, 1, .. last, 0, ..: it is back at zero behind its last part.
+__device__ __forceinline__ int atomic_inc_acq_rel_gpu(int* p, int last) {
+    int old;
+    asm volatile("atom.inc.acq_rel.gpu.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(last) : "memory");
+    return old;
+}
+
 // ---------------------------------------------------------------- proxies / fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -426,6 +426,26 @@ def test_nan_that_takes_part_is_reported(new, which):
     assert e.value.status == RANGE
 
 
+@pytest.mark.parametrize("seq,new", [([40], [1]), ([40], [3]), ([40], [60]), ([40], [200]), ([3000], [1]),
+                                     ([3000], [200]), ([9, 70, 500], [2, 40, 1])])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_values_that_are_not_finite_and_take_part_are_reported(seq, new, value):
+    """In a cached page, and in the last new token's value, which earlier rows do not see."""
+    for where in ("page", "new"):
+        c = ChunkCase(seq, new, hq=32, hkv=8, d=128, stale="normal")
+        if where == "page":
+            c.v_pool[c.table[-1, 0], 5, 6, 77] = value
+        else:
+            c.v_new[c.rows - 1, 2, 9] = value
+        c.to_device()
+        c.tables()
+        c.append()
+        c.attend()
+        with pytest.raises(pcf.PcfError) as e:
+            pcf.check_device_error()
+        assert e.value.status == RANGE, where
+
+
 def test_plan_of_other_dims_is_refused():
     for new in ([1], [60]):
         c = ChunkCase([40], new, hq=32, hkv=8, d=128, stale="normal", spare_rows=70).to_device()
