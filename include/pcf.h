@@ -361,7 +361,7 @@ pcf_status pcf_chunk_plan_words(const pcf_chunk_dims* dims, int64_t* n_words);
  * Refused on the device, with PCF_ERR_DEVICE_BOUNDS from the next pcf_check_device_error: a negative
  * length, one beyond the dims, positions outside the rope table (of any slot of a page a request
  * writes to), a next_pos that breaks a started page, a free list that runs out or names a page
- * outside the pool.  Then no table entry is written, the lengths and the list's head stay, slot_map
+ * outside the pool, work of 1<<29 (page, kv head) pairs or key tiles of 128 or more.  Then no table entry is written, the lengths and the list's head stay, slot_map
  * and row_pos are all -1, and calls that use the plan do nothing.
  * One launch, or two where lengths or list head are updated in place. */
 pcf_status pcf_chunk_tables(const pcf_chunk_dims* dims, const int32_t* seq_len, const int32_t* new_len,
@@ -371,7 +371,7 @@ pcf_status pcf_chunk_tables(const pcf_chunk_dims* dims, const int32_t* seq_len, 
                             int32_t* plan, void* stream);
 
 /* Writes the rows' keys and values into the pools: row i into slot slot_map[i] (rows at -1 are
- * passed over; slots must differ).  k_new, v_new: [max_rows][Hkv][d] bf16 with k_row_stride and
+ * passed over; slots must differ, and k_new and v_new lie outside the pools).  k_new, v_new: [max_rows][Hkv][d] bf16 with k_row_stride and
  * v_row_stride elements from row to row (multiples of 8, at least Hkv * d: columns of a wider
  * product are fine).  Keys are stored unrotated.  With row_pos (NULL: none) a row sits at logical
  * position row_pos[i] although its slot's is slot_pos[i] (pcf_chunk_tables' row_pos): its key is
@@ -396,14 +396,15 @@ pcf_status pcf_chunk_attention_workspace_bytes(const pcf_chunk_dims* dims, size_
  * no slot left gives zeros.  Order is that of the slots, not of the positions.  Slots behind a
  * request's last token and excluded slots may hold anything, infinities and NaN included.
  * q: [max_rows][Hq][d] bf16, q_row_stride elements from row to row (a multiple of 8); out
- * [max_rows][Hq][d] bf16, rows behind the last one left as they are.  ws: device workspace of >=
+ * [max_rows][Hq][d] bf16, rows behind the last one left as they are; refused where it overlaps q.  ws: device workspace of >=
  * pcf_chunk_attention_workspace_bytes, contents need not be initialised.  Any number of calls may use
  * one plan, one behind the other (a model's layers); two calls that may overlap need a plan (a
  * pcf_chunk_tables call) and a workspace each, as the plan holds counters that a call moves on.
  * Deterministic.  A page outside the pool, a position outside the rope table or a plan of other dims
  * raises PCF_ERR_DEVICE_BOUNDS; a rotated query or key that takes part and is not finite in fp16 (beyond
  * 65504, or NaN), or a value that takes part and is not finite, PCF_ERR_DEVICE_RANGE (a row may share its
- * products with keys that only later rows of its request see).  The call's results must then be discarded. */
+ * products with keys that only later rows of its request see).  The call's results must then be discarded,
+ * and after PCF_ERR_DEVICE_TIMEOUT the plan as well (its counters may have stopped half way). */
 pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, int32_t* plan, const uint16_t* q, int64_t q_row_stride,
                                const uint16_t* k_pool, const uint16_t* v_pool, const int32_t* block_table,
                                const int32_t* page_pos, const uint16_t* excl, const int32_t* row_pos,

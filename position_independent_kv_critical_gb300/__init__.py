@@ -417,7 +417,9 @@ def _chunk_rope(L: ChunkLayout, t: Optional[torch.Tensor]):
 def _chunk_call(L: ChunkLayout, fn: str, stream, *args):
     """The call on the layout's device, on that device's current stream unless one is named."""
     call = getattr(_lib.load(), fn)
-    if L.index < 0 or torch.cuda.current_device() == L.index:
+    if L.index < 0:
+        raise ValueError(f"{fn}: the layout is on {L.device}, not on a GPU")
+    if torch.cuda.current_device() == L.index:
         status = call(L.dims_ref, *args, _raw_stream(L.index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(L.device):
@@ -428,7 +430,7 @@ def _chunk_call(L: ChunkLayout, fn: str, stream, *args):
 
 def _raw_stream(index: int) -> int:
     """The current stream's handle on device ``index`` (without building a torch.cuda.Stream)."""
-    return torch._C._cuda_getCurrentRawStream(index) if index >= 0 else torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def chunk_tables(layout: ChunkLayout, seq_len, new_len, free_pages, free_head, seq_len_out, free_head_out,

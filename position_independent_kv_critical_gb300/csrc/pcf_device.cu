@@ -1123,6 +1123,10 @@ extern "C" pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, int32_t* p
     for (const void* w : {(const void*)block_table, (const void*)page_pos, (const void*)row_pos})
         if (reinterpret_cast<uintptr_t>(w) & 3u) return PCF_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(excl) & 1u) return PCF_ERR_INVALID_ARG;
+    // a row is read by several blocks, some of them behind the write of its result
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out), n = (uintptr_t)dims->max_rows;
+    const uintptr_t row = (uintptr_t)dims->n_q_heads * dims->head_dim;
+    if (q0 < o0 + 2 * n * row && o0 < q0 + 2 * ((n - 1) * (uintptr_t)q_row_stride + row)) return PCF_ERR_INVALID_ARG;
     size_t need = 0;
     if ((s = pcf_chunk_attention_workspace_bytes(dims, &need)) != PCF_OK) return s;
     if (ws_bytes < need) return PCF_ERR_WORKSPACE_TOO_SMALL;

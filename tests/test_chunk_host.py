@@ -93,18 +93,23 @@ def test_attention_refuses_bad_pointers_strides_and_workspaces(lib):
     size = ctypes.c_size_t(0)
     lib.pcf_chunk_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(size))
     #       plan q  stride   k  v  table pos excl row_pos rope out ws  bytes       stream
-    args = [P, P, 512, P, P, P, P, P, P, P, P, P, size.value, None]
+    out = P + 8 * (1 << 15)
+    args = [P, P, 512, P, P, P, P, P, P, P, out, P, size.value, None]
     for i in (0, 1, 3, 4, 5, 6, 8, 9, 10, 11):
         bad = list(args)
         bad[i] = None
         assert lib.pcf_chunk_attention(ctypes.byref(d), *bad) == INVALID, i
     for i, off in ((0, 2), (1, 8), (3, 8), (4, 8), (5, 2), (6, 2), (7, 1), (8, 2), (9, 8), (10, 8), (11, 8)):
         bad = list(args)
-        bad[i] = P + off
+        bad[i] = args[i] + off
         assert lib.pcf_chunk_attention(ctypes.byref(d), *bad) == INVALID, i
     for stride in (511, 504, 516, 0):
         bad = list(args)
         bad[2] = stride
+        assert lib.pcf_chunk_attention(ctypes.byref(d), *bad) == INVALID
+    for at in (P, P + 1024, P + 20 * 1024 - 16):          # out overlaps q
+        bad = list(args)
+        bad[10] = at
         assert lib.pcf_chunk_attention(ctypes.byref(d), *bad) == INVALID
     if size.value:
         bad = list(args)
@@ -139,6 +144,13 @@ def test_binding_refuses_tensors_of_other_shapes_types_and_strides():
         pcf.chunk_attention(L, q, pool, pool, rope, q, ws, excl=torch.zeros((3, 7), dtype=torch.int16))
     with pytest.raises(ValueError, match="out"):
         pcf.chunk_attention(L, q, pool, pool, rope, q[:19], ws)
+    # host tensors of the right kinds
+    with pytest.raises(ValueError, match="not on a GPU"):
+        pcf.chunk_tables(L, **ok)
+    with pytest.raises(ValueError, match="not on a GPU"):
+        pcf.append_kv(L, kv, kv, pool, pool)
+    with pytest.raises(ValueError, match="not on a GPU"):
+        pcf.chunk_attention(L, q, pool, pool, rope, torch.zeros_like(q), ws)
 
 
 def test_tables_are_replaced_only_by_tables_of_the_same_kind():
