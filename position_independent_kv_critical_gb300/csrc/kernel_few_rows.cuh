@@ -347,7 +347,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
     };
     if (n_units > 0) load_positions();
-    __syncthreads();
+    if (!__syncthreads_or(n_units > 0)) return;        // nothing to do for the whole block
 
     // ---------------- the units
     const float scale = 1.4426950408889634f * (D == 128 ? 0.08838834764831845f : 0.125f);   // log2(e) / sqrt(d)

@@ -8,8 +8,9 @@
 // in the kernel, takes twice as long).  The values stay in the pool: many_rows_kernel copies a key
 // tile's eight pages straight from it.  A request whose rows fit one tile (128: a long draft, a short
 // chunk) visits each key once: its keys are not rotated beforehand but copied from their pages and rotated
-// in shared memory by the warps that would have tile B (24 requests of 6 k tokens with 64 rows: 262 -> 198
-// us; 152 without the rotation's arithmetic, 91 at the copy rate: two key stages hide the copies in part).
+// in shared memory by the warps that would have tile B (24 requests of 6 k tokens with 64 rows: 262 -> 194
+// us; 152 without the rotation's arithmetic, 91 at the copy rate.  One warp a sub-partition rotates and
+// one has the softmax, so latencies bind: a third stage for keys and values changed nothing).
 //
 // many_rows_kernel: one block an SM; a run is two 128-row tiles A and B of one (request, kv head) --
 // row m of a tile is token m / g, query head m % g of the kv head -- against the 128-key tiles its last
@@ -224,12 +225,20 @@ enum : int {
     MB_K_ROT = 42       // [2] single: rotated in place (every thread of warps 4-7)
 };
 
+// Larger of two fp16 and of the magnitudes of two others, NaN where one is.
+__device__ __forceinline__ uint32_t max_abs_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 t;\n\tabs.f16x2 t, %2;\n\tmax.NaN.f16x2 %0, %1, t;\n\t}\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Warps 4-7 on a single-tile run: every key tile rotated in place, bf16 in, fp16 out.  Thread t has 16-byte
 // chunk pair c (dimensions 8 c .. and d/2 + 8 c ..) of N consecutive keys of page t / 16: their angles
 // start from the cos/sin row of the first one's position and advance by one position, a rotation by
 // table row 1, from key to key.  Slots that take no part become zeros (they may hold anything).  A tile
-// is rotated once for all its rows, beside the softmax of tile A: some 350 of the 2800 issue slots an SM
-// sub-partition has while HBM delivers a tile.
+// is rotated once for all its rows, beside the softmax of tile A.  Whether every result is finite is kept
+// as the largest packed fp16 magnitudes (200 -> 194 us against a test of the fp32 values); four keys in
+// flight a thread instead of two take 300 us.
 template <int D>
 __device__ __forceinline__ bool rotate_tiles(const ManyParams& prm, const ManyItem& w, uint8_t* stages, int stage_bytes,
                                              const uint16_t* s_mask, uint64_t* bars, int kc, int (&raw_n)[2], int t,
@@ -262,7 +271,7 @@ __device__ __forceinline__ bool rotate_tiles(const ManyParams& prm, const ManyIt
     int32_t pos = position(w.jb), pos_n = position(w.jb + 1);
     float4 cs[4];
     row_of(pos, cs);
-    float big = 0.f, nan = 0.f;
+    uint32_t big = 0;                 // largest magnitudes, NaN where one was
     for (int jj = 0; jj < w.n_loc; ++jj, ++kc) {
         const int ks = kc & 1, first = (w.jb + jj) * kTileKeys + page * kPage;
         uint32_t gone = 0;
@@ -305,9 +314,9 @@ __device__ __forceinline__ bool rotate_tiles(const ManyParams& prm, const ManyIt
                 float y0, y1, z0, z1;
                 f2_unpack(f2_fma(f2_mul(B, S[e]), minus, f2_mul(A, C[e])), y0, y1);   // a cos - b sin
                 f2_unpack(f2_fma(A, S[e], f2_mul(B, C[e])), z0, z1);                   // b cos + a sin
-                nan = fmaf(y0 + y1, 0.f, nan);
-                oa[e] = pack_f16x2_track(y0, y1, big);
-                ob[e] = pack_f16x2_track(z0, z1, big);
+                oa[e] = pack_f16x2_inf(y0, y1);
+                ob[e] = pack_f16x2_inf(z0, z1);
+                big = max_abs_f16x2(max_abs_f16x2(big, oa[e]), ob[e]);
                 // one position further
                 const uint64_t cn = f2_fma(f2_mul(S[e], STS[e]), minus, f2_mul(C[e], STC[e]));
                 S[e] = f2_fma(C[e], STS[e], f2_mul(S[e], STC[e]));
@@ -319,7 +328,7 @@ __device__ __forceinline__ bool rotate_tiles(const ManyParams& prm, const ManyIt
         fence_proxy_async_smem();
         mbar_arrive(&bars[MB_K_ROT + ks]);
     }
-    if (!(big < kF16Limit) || nan != nan) set_dev_error(kDevErrRange);
+    if ((big & 0x7C00u) == 0x7C00u || (big & 0x7C000000u) == 0x7C000000u) set_dev_error(kDevErrRange);   // not finite
     return true;
 }
 
@@ -376,6 +385,9 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     grid_dep_wait();
     grid_dep_launch();
+    const int4* entry = reinterpret_cast<const int4*>(prm.plan + plan_many(prm.n, prm.workers)) + 2 * blockIdx.x;
+    const int4 share = entry[1];
+    const int n_tiles = share.y == prm.tag ? share.x : 0;
     if (warp == kWarpMma) {
         tmem_alloc(reinterpret_cast<uint32_t*>(misc), 512);
         tmem_relinquish();
@@ -396,16 +408,17 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         return true;
     };
 
-    if (warp == kWarpTma) {
+    if (n_tiles == 0) {            // nothing to do for the whole block
+        if (tid == 0) prm.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    } else if (warp == kWarpTma) {
         // ------------------------------------------------------------ runs, Q and K tiles
         const int32_t* seq = plan + plan_array(CA_SEQ, prm.n);
         const int32_t* add = plan + plan_array(CA_NEW, prm.n);
         const int32_t* row = plan + plan_array(CA_ROW, prm.n);
         const int32_t* many = plan + plan_array(CA_MANY, prm.n);
         const int32_t* kpage = plan + plan_array(CA_KPAGE, prm.n);
-        const int4* st = reinterpret_cast<const int4*>(plan + plan_many(prm.n, prm.workers)) + 2 * blockIdx.x;
-        const int4 start = st[0], part = st[1];
-        int left = part.y == prm.tag ? part.x : 0;
+        const int4 start = entry[0];
+        int left = n_tiles;
         int32_t req = start.x, kvh = start.y, pair = start.z, tile = start.w;
         int kc = 0, last_k[2] = {-1, -1}, last_q = -1, raw_n[2] = {0, 0}, full_n[2] = {0, 0};   // copies of either kind a stage took
         bool ok = true;
@@ -862,18 +875,19 @@ __global__ void __launch_bounds__(256) many_join_kernel(const ManyParams p) {
     if (tok >= rows.x) return;
     float top = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int b = j; b <= last; ++b) {
-        const int64_t row = ((int64_t)b * 2 + (b == j ? 1 : 0)) * kPairRows + r;
-        const float2 ml = p.part_ml[row];
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + row * D + 4 * f);
-        const float now = fmaxf(top, ml.x), ref = now == -INFINITY ? 0.f : now;
-        const float old = ex2(top - ref), a = ex2(ml.x - ref);
-        top = now;
-        l = l * old + a * ml.y;
-        acc.x = acc.x * old + a * v.x;
-        acc.y = acc.y * old + a * v.y;
-        acc.z = acc.z * old + a * v.z;
-        acc.w = acc.w * old + a * v.w;
+    for (int b0 = j; b0 <= last; b0 += 2) {            // two parts' loads in flight: most runs have no more
+        float2 ml[2];
+        float4 v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // (behind the last part: that part again, without weight -- other memory may hold NaN)
+            const int b = min(b0 + i, last);
+            const int64_t row = ((int64_t)b * 2 + (b == j ? 1 : 0)) * kPairRows + r;
+            ml[i] = p.part_ml[row];
+            v[i] = *reinterpret_cast<const float4*>(p.part_o + row * D + 4 * f);
+            if (b0 + i > last) ml[i].x = -INFINITY;
+        }
+        add_parts(ml, v, top, l, acc);
     }
     const float odd = not_finite(acc, 0.f);
     if (odd != odd) set_dev_error(kDevErrRange);

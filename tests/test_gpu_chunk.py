@@ -279,6 +279,29 @@ def poison_excluded(c):
                 c.v_pool[p, :, j % PAGE] = [float("nan"), float("inf"), -float("inf")][j % 3]
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("share", [0.0, 0.2])
+@pytest.mark.parametrize("kinds", [[3, 20, 16, 60, 1], [20, 3], [16, 16, 33], [5]])
+def test_runs_of_one_tile_and_of_more_take_turns(d, share, kinds):
+    """Some 480 runs over all blocks, so that a block goes from runs of one row tile to runs of two and back,
+    behind lengths that leave the rings at every stage."""
+    rng = np.random.default_rng(11)
+    n = 120
+    c = ChunkCase(rng.integers(0, 700, n).tolist(), [kinds[b % len(kinds)] for b in range(n)], hq=32, hkv=4, d=d, seed=21)
+    if share:
+        random_excl(c, share, 5)
+    got = c.to_device().step()
+    for b in range(0, n, 7):
+        _, (out, mean_abs, score_abs) = c.oracle(b)
+        lim = chunk.attention_bound(out, mean_abs, score_abs)
+        bad = ~(np.abs(got[c.base[b]: c.base[b + 1]] - out) <= lim)
+        assert not bad.any(), (b, c.seq[b], c.new[b], np.argwhere(bad)[0])
+    first = c.out.clone()
+    c.attend()
+    pcf.check_device_error()
+    assert torch.equal(c.out, first)
+
+
 @pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[1], SHAPES[5]], ids=[IDS[0], IDS[1], IDS[5]])
 @pytest.mark.parametrize("seq,new", [([40, 3, 200], [1, 1, 1]), ([300, 0, 17], [3, 1, 2]), ([150, 290], [70, 140])])
 @pytest.mark.parametrize("share", [0.1, 0.5, 1.0])
@@ -421,6 +444,25 @@ def test_nan_that_takes_part_is_reported(new, which):
     c.tables()
     c.append()
     c.attend()
+    with pytest.raises(pcf.PcfError) as e:
+        pcf.check_device_error()
+    assert e.value.status == RANGE
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf"), 1e6, -1e6, 65280.0])
+@pytest.mark.parametrize("chunk_at", [0, 7, 8, 15])
+def test_keys_of_runs_of_one_tile_are_checked(value, chunk_at):
+    """65280 is the largest bf16 that fp16 holds; the key sits at position 0, where it is not turned."""
+    c = ChunkCase([40], [20], hq=32, hkv=8, d=128, stale="normal", pos0=0)
+    c.k_pool[c.table[0, 0], 3, 0] = 0.0
+    c.k_pool[c.table[0, 0], 3, 0, 8 * chunk_at + 3] = value
+    c.to_device()
+    c.tables()
+    c.append()
+    c.attend()
+    if value == 65280.0:
+        pcf.check_device_error()
+        return
     with pytest.raises(pcf.PcfError) as e:
         pcf.check_device_error()
     assert e.value.status == RANGE
