@@ -317,7 +317,8 @@ pcf_status pcf_score_noalloc(const pcf_layout* layout, const uint16_t* q_query, 
  * A request b holds seq_len[b] tokens in the pages block_table[b][0 ..]; token 16 p + r sits in slot
  * r of page block_table[b][p] at logical position page_pos[b][p] + r.  Pages of different requests
  * may be the same physical page at different positions, as in a layout.  A chunk brings new_len[b]
- * tokens (0: the request is idle), which take the slots behind.  The rows of a chunk call are the
+ * tokens (0: the request is idle), which take the slots behind.  A page with room left that a request goes
+ * on in is held by that request alone.  The rows of a chunk call are the
  * new tokens, request after request: row row_base[b] + t is token seq_len[b] + t.
  *
  * Every buffer has the size the dims give, whatever the lengths turn out to be, so that calls can

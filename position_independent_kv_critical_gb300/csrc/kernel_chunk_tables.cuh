@@ -36,7 +36,8 @@ constexpr int kTablesThreads = 512;
 // outputs are buffers of their own, every block of one launch reads the lengths and scans them for
 // itself and then writes its share of the rows (`alone`); where lengths or list head are updated in
 // place, a block must not write them while another still reads, so one block leaves the plan and a
-// second launch writes the rows (64 requests of one token: 5 and 7 us).
+// second launch writes the rows.  Graph replay, 64 requests of one token: 6.7 us apart, 8.0 in place; 512
+// requests of four: 9.3 and 10.6.
 // (Sums of refused lengths may be as large as 4096 x 2^22: they stop at 2^29, above every limit.)
 constexpr int kSumLimit = 1 << 29;
 constexpr int kSums = 6;   // rows, pages taken, pages held afterwards, few-row units, key tiles and pages of the others
@@ -327,7 +328,9 @@ __global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const TablesPa
 // `at` differs (a recomputed token, kept behind its request's shared pages) is stored turned by the
 // difference, R_{at - slot} k, so that R_slot of the stored key is R_at k.  Where the two agree the
 // key is copied bit for bit.  A thread takes the 16-byte chunks c and c + d/16 of one head's key
-// (the pairs i, i + d/2 that turn together) and of its value: 64 bytes in flight a thread.
+// (the pairs i, i + d/2 that turn together) and of its value: 64 bytes in flight a thread.  Bound by HBM,
+// with a thread a chunk and no loop to set up: 51 k rows of 8 kv heads, d 128, most of them turned, move
+// 421 MB in 69.8 us (6.0 TB/s, 89 % of a plain copy); 64 rows take 2 us.
 struct AppendParams {
     const __nv_bfloat16* k;
     const __nv_bfloat16* v;
