@@ -64,13 +64,23 @@ PCF_HOST_DEVICE inline int32_t many_tiles(int32_t seq, int32_t add, int32_t tpp,
 }
 // key tiles of the pairs before `pair` (not behind the last one): sum of floor((a + i tpp) / 128),
 // a = seq + tpp + 127.  With m = 128 / tpp pairs to a tile (tpp divides 128, or is 256), i = m u + v
-// adds u whole tiles and one more from v = v0 on, the first whose tokens cross a tile.
+// adds u whole tiles and one more from v = v0 on, the first whose tokens cross a tile.  (tpp and m are
+// powers of two; divisions by variables would cost more than all the rest.)
+PCF_HOST_DEVICE inline int32_t log2_of(int32_t x) {
+#ifdef __CUDA_ARCH__
+    return __ffs(x) - 1;
+#else
+    return __builtin_ctz((unsigned)x);
+#endif
+}
 PCF_HOST_DEVICE inline int64_t many_before(int32_t seq, int32_t tpp, int32_t pair) {
-    const int64_t a = (seq + tpp + kTileKeys - 1) / kTileKeys, p = pair;
+    const uint32_t end = (uint32_t)(seq + tpp + kTileKeys - 1);
+    const int64_t a = end / kTileKeys, p = pair;
     if (tpp == 2 * kTileKeys) return p * a + p * (p - 1);
-    const int64_t r = (seq + tpp + kTileKeys - 1) % kTileKeys, m = kTileKeys / tpp, u = p / m, w = p % m;
-    const int64_t v0 = (kTileKeys - r + tpp - 1) / tpp;
-    return p * a + m * (u * (u - 1) / 2) + u * w + u * (m - v0) + (w > v0 ? w - v0 : 0);
+    const int32_t lt = log2_of(tpp), lm = log2_of(kTileKeys) - lt, m = 1 << lm;
+    const int32_t r = (int32_t)(end % kTileKeys), u = pair >> lm, w = pair & (m - 1);
+    const int32_t v0 = (kTileKeys - r + tpp - 1) >> lt;
+    return p * a + (((int64_t)u * (u - 1) / 2) << lm) + (int64_t)u * w + (int64_t)u * (m - v0) + (w > v0 ? w - v0 : 0);
 }
 
 // A request has few rows when its new tokens times the query heads of a kv head are at most this: two

@@ -36,8 +36,8 @@ constexpr int kTablesThreads = 512;
 // outputs are buffers of their own, every block of one launch reads the lengths and scans them for
 // itself and then writes its share of the rows (`alone`); where lengths or list head are updated in
 // place, a block must not write them while another still reads, so one block leaves the plan and a
-// second launch writes the rows.  Graph replay, 64 requests of one token: 6.7 us apart, 8.0 in place; 512
-// requests of four: 9.3 and 10.6.
+// second launch writes the rows.  Graph replay, 64 requests of one token: 5.2 us apart, 6.6 in place; 512
+// requests of four: 6.5 and 8.1.
 // (Sums of refused lengths may be as large as 4096 x 2^22: they stop at 2^29, above every limit.)
 constexpr int kSumLimit = 1 << 29;
 constexpr int kSums = 6;   // rows, pages taken, pages held afterwards, few-row units, key tiles and pages of the others
@@ -75,103 +75,144 @@ __device__ __forceinline__ int32_t* plan_words_of(int32_t* arrays, int which, in
     return arrays + (int64_t)which * (n + 1);
 }
 
-// Everything that follows from the plan, thread i of `step`: the tables' rows -- token s + t of a
-// request sits in page (s + t) / 16, at slot (s + t) % 16; the row that starts a page enters it -- and
-// the attention's work split.  Nothing here reads what the call may overwrite in place (lengths and
-// list head come from the plan), and a table entry that is read (a page begun earlier) is never one
-// that is written.
-__device__ __forceinline__ void write_rows(const TablesParams& p, int32_t* arrays, int32_t rows, int32_t head,
-                                           int32_t taken, int32_t i, int32_t step) {
+// Everything that follows from the plan, shared out to threads as one range of tasks, so that no thread has
+// the chain of one kind behind that of another: the rows, the requests' lengths, the workers' and the blocks'
+// shares of the attention's work.  Nothing here reads what the call may overwrite in place (lengths and list
+// head come from the plan), and a table entry that is read (a page begun earlier) is never one that is written.
+PCF_HOST_DEVICE inline int32_t whole_warps(int32_t n) { return (n + 31) / 32 * 32; }
+PCF_HOST_DEVICE inline int32_t rows_tasks(int32_t max_rows, int32_t n, int32_t workers, int32_t blocks) {
+    return whole_warps(max_rows) + whole_warps(n + 1) + whole_warps(workers) + 3 * whole_warps(blocks);
+}
+
+// Row r: token s + t of a request sits in page (s + t) / 16, at slot (s + t) % 16; the row that starts a page
+// enters it.
+__device__ __forceinline__ void write_row(const TablesParams& p, int32_t* arrays, int32_t rows, int32_t head, int32_t r) {
     const int32_t* seq = plan_words_of(arrays, CA_SEQ, p.n);
-    const int32_t* add = plan_words_of(arrays, CA_NEW, p.n);
     const int32_t* base = plan_words_of(arrays, CA_ROW, p.n);
     const int32_t* take = plan_words_of(arrays, CA_TAKE, p.n);
     const int32_t* start = plan_words_of(arrays, CA_START, p.n);
-    const int32_t* few = plan_words_of(arrays, CA_FEW, p.n);
-    const int32_t* many = plan_words_of(arrays, CA_MANY, p.n);
-    for (int32_t r = i; r < p.max_rows; r += step) {
-        int32_t slot = -1, pos = -1;
-        if (r < rows) {
-            const int b = row_request(base, p.n, r);
-            const int32_t t = r - base[b], s = seq[b] + t, pg = s / kPage, first = pages_of(seq[b]);
-            const int64_t e = (int64_t)b * p.max_pages + pg;
-            pos = start[b] + t;
-            int32_t ph;
-            if (pg >= first) {
-                ph = p.free_pages[head + take[b] + pg - first];
-                if (s % kPage == 0) {
-                    p.block_table[e] = ph;
-                    p.page_pos[e] = pos;
-                }
-            } else {
-                ph = p.block_table[e];
-                if (ph < 0 || ph >= p.n_phys) {
-                    set_dev_error(kDevErrBounds);
-                    ph = -1;
-                }
+    int32_t slot = -1, pos = -1;
+    if (r < rows) {
+        const int b = row_request(base, p.n, r);
+        const int32_t t = r - base[b], s = seq[b] + t, pg = s / kPage, first = pages_of(seq[b]);
+        const int64_t e = (int64_t)b * p.max_pages + pg;
+        pos = start[b] + t;
+        int32_t ph;
+        if (pg >= first) {
+            ph = p.free_pages[head + take[b] + pg - first];
+            if (s % kPage == 0) {
+                p.block_table[e] = ph;
+                p.page_pos[e] = pos;
             }
-            if (ph >= 0) slot = ph * kPage + s % kPage;
+        } else {
+            ph = p.block_table[e];
+            if (ph < 0 || ph >= p.n_phys) {
+                set_dev_error(kDevErrBounds);
+                ph = -1;
+            }
         }
-        p.slot_map[r] = slot;
-        p.row_pos[r] = pos;
+        if (ph >= 0) slot = ph * kPage + s % kPage;
     }
-    for (int32_t b = i; b <= p.n; b += step) {
-        p.row_base[b] = base[b];
-        if (b < p.n) p.seq_out[b] = seq[b] + add[b];
-        else p.head_out[0] = head + taken;
+    p.slot_map[r] = slot;
+    p.row_pos[r] = pos;
+}
+
+// Worker w's share of the few-row requests' units, dealt in equal runs.
+__device__ __forceinline__ void write_worker(const TablesParams& p, int32_t* arrays, int32_t w) {
+    const int32_t* seq = plan_words_of(arrays, CA_SEQ, p.n);
+    const int32_t* add = plan_words_of(arrays, CA_NEW, p.n);
+    const int32_t* base = plan_words_of(arrays, CA_ROW, p.n);
+    const int32_t* few = plan_words_of(arrays, CA_FEW, p.n);
+    const Deal deal(few[p.n], p.workers);
+    const int32_t u0 = deal.first(w), n_units = deal.first(w + 1) - u0;
+    int4 e = make_int4(0, 0, 0, n_units), f = make_int4(1, 0, 0, 0);
+    if (n_units > 0) {
+        const int b = row_request(few, p.n, u0);
+        f = make_int4(pages_of(seq[b] + add[b]), seq[b], add[b], base[b]);
+        const int32_t local = u0 - few[b];
+        e.x = b;
+        e.y = local / f.x;
+        e.z = local - e.y * f.x;
     }
-    // the few-row requests' units, dealt to the workers in equal runs
+    int4* dst = reinterpret_cast<int4*>(p.plan + plan_starts(p.n)) + 3 * w;
+    dst[0] = e;
+    dst[1] = f;
+    dst[2].x = p.tag;
+}
+
+// The blocks that the run of block w's first unit reaches (first, last), or that of its last unit (last).
+__device__ __forceinline__ void write_share(const TablesParams& p, int32_t* arrays, int32_t w, bool of_last) {
+    const int32_t* few = plan_words_of(arrays, CA_FEW, p.n);
     const Deal deal(few[p.n], p.workers);
     const int per = p.workers / p.blocks;
-    for (int32_t w = i; w < p.workers; w += step) {
-        const int32_t u0 = deal.first(w), n_units = deal.first(w + 1) - u0;
-        int4 e = make_int4(0, 0, 0, n_units), f = make_int4(1, 0, 0, 0), share = make_int4(p.tag, 0, 0, 0);
-        if (n_units > 0) {
-            const int b = row_request(few, p.n, u0);
-            f = make_int4(pages_of(seq[b] + add[b]), seq[b], add[b], base[b]);
-            const int32_t local = u0 - few[b];
-            e.x = b;
-            e.y = local / f.x;
-            e.z = local - e.y * f.x;
-            if (w % per == 0) {   // the blocks that the runs of the block's first and last unit reach
-                const int32_t a = u0 - e.z, end = deal.first(w + per) - 1;
-                share.y = deal.owner(a) / per;
-                share.z = deal.owner(a + f.x - 1) / per;
-                const int bl = row_request(few, p.n, end);
-                const int32_t pages = pages_of(seq[bl] + add[bl]);
-                share.w = deal.owner(few[bl] + (end - few[bl]) / pages * pages + pages - 1) / per;
-            }
-        }
-        int4* dst = reinterpret_cast<int4*>(p.plan + plan_starts(p.n)) + 3 * w;
-        dst[0] = e;
-        dst[1] = f;
-        dst[2] = share;
+    const int32_t u0 = deal.first(w * per), u1 = deal.first((w + 1) * per);
+    if (u0 == u1) return;
+    const int32_t u = of_last ? u1 - 1 : u0;
+    const int b = row_request(few, p.n, u);
+    const int32_t pages = pages_of(plan_words_of(arrays, CA_SEQ, p.n)[b] + plan_words_of(arrays, CA_NEW, p.n)[b]);
+    const int32_t first = few[b] + (u - few[b]) / pages * pages;
+    int4* dst = reinterpret_cast<int4*>(p.plan + plan_starts(p.n)) + 3 * w * per + 2;
+    if (of_last) {
+        dst->w = deal.owner(first + pages - 1) / per;
+    } else {
+        dst->y = deal.owner(first) / per;
+        dst->z = deal.owner(first + pages - 1) / per;
     }
-    // the others' key tiles, in (request, kv head, row pair, tile) order, dealt to the blocks
+}
+
+// Block w's share of the others' key tiles, in (request, kv head, row pair, tile) order.
+__device__ __forceinline__ void write_block(const TablesParams& p, int32_t* arrays, int32_t w) {
+    const int32_t* seq = plan_words_of(arrays, CA_SEQ, p.n);
+    const int32_t* add = plan_words_of(arrays, CA_NEW, p.n);
+    const int32_t* many = plan_words_of(arrays, CA_MANY, p.n);
     const Deal tiles(many[p.n], p.blocks);
     const int g = p.hq / p.hkv, tpp = 2 * kTileRows / g;
-    for (int32_t w = i; w < p.blocks; w += step) {
-        p.plan[plan_count(p.n, p.workers, p.blocks) + w] = 0;
-        const int32_t u0 = tiles.first(w);
-        int4 e = make_int4(0, 0, 0, 0), f = make_int4(tiles.first(w + 1) - u0, p.tag, 0, 0);
-        if (f.x > 0) {
-            const int b = row_request(many, p.n, u0);
-            const int32_t per_head = (many[b + 1] - many[b]) / p.hkv;
-            int32_t local = u0 - many[b];
-            e.x = b;
-            e.y = local / per_head;
-            local %= per_head;
-            int lo = 0, hi = many_pairs(add[b], tpp) - 1;   // the pair the tile falls into
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (many_before(seq[b], tpp, mid) <= local) lo = mid; else hi = mid - 1;
-            }
-            e.z = lo;
-            e.w = local - (int32_t)many_before(seq[b], tpp, lo);
+    p.plan[plan_count(p.n, p.workers, p.blocks) + w] = 0;
+    const int32_t u0 = tiles.first(w);
+    int4 e = make_int4(0, 0, 0, 0), f = make_int4(tiles.first(w + 1) - u0, p.tag, 0, 0);
+    if (f.x > 0) {
+        const int b = row_request(many, p.n, u0);
+        const int32_t per_head = (many[b + 1] - many[b]) / p.hkv;
+        int32_t local = u0 - many[b];
+        e.x = b;
+        e.y = local / per_head;
+        local %= per_head;
+        int lo = 0, hi = many_pairs(add[b], tpp) - 1;   // the pair the tile falls into
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (many_before(seq[b], tpp, mid) <= local) lo = mid; else hi = mid - 1;
         }
-        int4* dst = reinterpret_cast<int4*>(p.plan + plan_many(p.n, p.workers)) + 2 * w;
-        dst[0] = e;
-        dst[1] = f;
+        e.z = lo;
+        e.w = local - (int32_t)many_before(seq[b], tpp, lo);
+    }
+    int4* dst = reinterpret_cast<int4*>(p.plan + plan_many(p.n, p.workers)) + 2 * w;
+    dst[0] = e;
+    dst[1] = f;
+}
+
+__device__ __forceinline__ void write_rows(const TablesParams& p, int32_t* arrays, int32_t rows, int32_t head,
+                                           int32_t taken, int32_t i, int32_t step) {
+    const int32_t total = rows_tasks(p.max_rows, p.n, p.workers, p.blocks);
+    for (; i < total; i += step) {
+        int32_t k = i;
+        if (k < p.max_rows) {
+            write_row(p, arrays, rows, head, k);
+            continue;
+        }
+        k -= whole_warps(p.max_rows);
+        if (k >= 0 && k <= p.n) {
+            p.row_base[k] = plan_words_of(arrays, CA_ROW, p.n)[k];
+            if (k < p.n) p.seq_out[k] = plan_words_of(arrays, CA_SEQ, p.n)[k] + plan_words_of(arrays, CA_NEW, p.n)[k];
+            else p.head_out[0] = head + taken;
+        }
+        k -= whole_warps(p.n + 1);
+        if (k >= 0 && k < p.workers) write_worker(p, arrays, k);
+        k -= whole_warps(p.workers);
+        if (k >= 0 && k < p.blocks) write_share(p, arrays, k, false);
+        k -= whole_warps(p.blocks);
+        if (k >= 0 && k < p.blocks) write_share(p, arrays, k, true);
+        k -= whole_warps(p.blocks);
+        if (k >= 0 && k < p.blocks) write_block(p, arrays, k);
     }
 }
 

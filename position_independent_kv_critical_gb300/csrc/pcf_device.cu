@@ -989,7 +989,7 @@ extern "C" pcf_status pcf_chunk_tables(const pcf_chunk_dims* dims, const int32_t
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // one launch where the outputs are buffers of their own, else two (see chunk_plan_kernel)
     const int arrays = (int)(plan_array(CA_COUNT, dims->n_reqs) - C_HEADER) * (int)sizeof(int32_t);
-    const int items = std::max({dims->max_rows, dims->n_reqs + 1, p.workers});
+    const int items = rows_tasks(dims->max_rows, dims->n_reqs, p.workers, p.blocks);
     auto blocks = [&](int threads) { return dim3(std::min((items + threads - 1) / threads, device_sms())); };
     const int alone = seq_len_out != seq_len && free_head_out != free_head ? 1 : 0;
     if ((s = set_smem(chunk_plan_kernel, arrays)) != PCF_OK) return s;
