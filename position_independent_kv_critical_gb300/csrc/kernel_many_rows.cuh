@@ -242,9 +242,10 @@ __device__ __forceinline__ uint32_t max_abs_f16x2(uint32_t a, uint32_t b) {
 // chunk pair c (dimensions 8 c .. and d/2 + 8 c ..) of N consecutive keys of page t / 16: their angles
 // start from the cos/sin row of the first one's position and advance by one position, a rotation by
 // table row 1, from key to key.  Slots that take no part become zeros (they may hold anything).  A tile
-// is rotated once for all its rows, beside the softmax of tile A.  Whether every result is finite is kept
-// as the largest packed fp16 magnitudes (200 -> 194 us against a test of the fp32 values); four keys in
-// flight a thread instead of two take 300 us.
+// is rotated once for all its rows, beside the softmax of tile A: 3500 of the 4650 cycles a tile takes, the
+// softmax 2500 of them.  Whether every result is finite is kept as the largest packed fp16 magnitudes (200 ->
+// 194 us against a test of the fp32 values).  More code is slower, the roles' loops compete for the
+// instruction cache: the next key loaded ahead 202 us, four keys unrolled instead of two 300.
 template <int D>
 __device__ __forceinline__ bool rotate_tiles(const ManyParams& prm, const ManyItem& w, uint8_t* stages, int stage_bytes,
                                              const uint16_t* s_mask, uint64_t* bars, int kc, int (&raw_n)[2], int t,
