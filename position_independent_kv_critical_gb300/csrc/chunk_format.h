@@ -27,13 +27,13 @@ enum : int {
     C_HEADER = 4
 };
 // arrays behind the header, n_reqs + 1 words each: tokens held, new tokens, first row, pages taken
-// before the request, position of its first row, and the (page, kv head) units of the requests
-// before it that have few rows,
-// and, for the requests with more, the key tiles their row pairs visit and the pages they hold.
+// before the request, position of its first row; of the requests before it that have few rows their
+// weight (their (page, kv head) units and run_weight for each of their runs) and their number; of those with
+// more the key tiles their row pairs visit and the pages they hold.  Behind the first positions: run_weight.
 // Behind them the work split of both kinds: kStartWords words a worker, then kManyWords a block.
-enum : int { CA_SEQ = 0, CA_NEW = 1, CA_ROW = 2, CA_TAKE = 3, CA_START = 4, CA_FEW = 5, CA_MANY = 6, CA_KPAGE = 7, CA_COUNT = 8 };
-// {request, kv head, page, units; its pages, tokens held, new tokens, first row; tag, and for a block's
-// first worker the blocks its first and last run reach: first, last; last}
+enum : int { CA_SEQ = 0, CA_NEW = 1, CA_ROW = 2, CA_TAKE = 3, CA_START = 4, CA_FEW = 5, CA_MANY = 6, CA_KPAGE = 7, CA_FEWN = 8, CA_COUNT = 9 };
+// {request, kv head, page, units before; its pages, tokens held, new tokens, first row; tag, and for a block's
+// first worker the blocks its first and last run reach: first, last; last}, and one entry more with all units
 constexpr int kStartWords = 12;
 
 PCF_HOST_DEVICE inline int64_t plan_array(int which, int32_t n_reqs) {
@@ -44,7 +44,7 @@ PCF_HOST_DEVICE inline int64_t plan_starts(int32_t n_reqs) {
 }
 constexpr int kManyWords = 8;    // {request, kv head, row pair, key tile; units, tag, 0, 0}
 PCF_HOST_DEVICE inline int64_t plan_many(int32_t n_reqs, int32_t workers) {
-    return plan_starts(n_reqs) + (int64_t)workers * kStartWords;
+    return plan_starts(n_reqs) + (int64_t)(workers + 1) * kStartWords;
 }
 // parts brought of runs that blocks share, one counter a block
 PCF_HOST_DEVICE inline int64_t plan_count(int32_t n_reqs, int32_t workers, int32_t blocks) {
@@ -98,7 +98,7 @@ constexpr int kFewWarps = 12;
 // and partial results (one request of 4 k tokens: 14.3 us with the longer runs on the first workers, 11.8
 // so).  With fewer units than workers the first ones take one each (a run's parts then sit in few blocks).
 // `left` is more / active in units of 2^-32, rounded up (more units left over, active <= 12 * 4096 workers:
-// w left / 2^32 is then within 2^-16 of its value, and its floor exact); no division a worker.
+// w left / 2^32 is then within 2^-16 of its value, and its floor exact); no division a worker.  units < 2^30.
 struct Deal {
     uint32_t units, active, each, left;
     PCF_HOST_DEVICE Deal(int32_t n, int32_t workers) : units(n), active(n < workers ? n : workers), each(0), left(0) {
@@ -118,6 +118,13 @@ struct Deal {
         return w;
     }
 };
+
+// What beginning and ending a run (queries loaded and rotated, a result written) costs a worker, in units, in
+// the dealing of a batch that gives every worker four units or more (so that each has one at least, whatever
+// the runs).  48 drafts behind 100 to 9000 tokens: 146 us without it, 134 with 1, 2 or 3.  With fewer units a
+// worker latencies count, and a unit is a unit.
+constexpr int kRunWeight = 1;
+PCF_HOST_DEVICE inline int32_t run_weight(int32_t units, int32_t workers) { return units >= 4 * workers ? kRunWeight : 0; }
 
 PCF_HOST_DEVICE inline int32_t chunk_sms(int32_t n_sms) { return n_sms > 0 ? n_sms : kDefaultSms; }
 

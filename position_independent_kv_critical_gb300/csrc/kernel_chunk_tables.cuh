@@ -40,7 +40,7 @@ constexpr int kTablesThreads = 512;
 // requests of four: 6.5 and 8.1.
 // (Sums of refused lengths may be as large as 4096 x 2^22: they stop at 2^29, above every limit.)
 constexpr int kSumLimit = 1 << 29;
-constexpr int kSums = 6;   // rows, pages taken, pages held afterwards, few-row units, key tiles and pages of the others
+constexpr int kSums = 7;   // rows, pages taken, pages held afterwards, few-row units, key tiles and pages of the others, few-row requests
 __device__ __forceinline__ int32_t pages_of(int32_t tokens) { return (tokens + kPage - 1) / kPage; }
 __device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) { return min(a + b, kSumLimit); }
 
@@ -81,7 +81,7 @@ __device__ __forceinline__ int32_t* plan_words_of(int32_t* arrays, int which, in
 // head come from the plan), and a table entry that is read (a page begun earlier) is never one that is written.
 PCF_HOST_DEVICE inline int32_t whole_warps(int32_t n) { return (n + 31) / 32 * 32; }
 PCF_HOST_DEVICE inline int32_t rows_tasks(int32_t max_rows, int32_t n, int32_t workers, int32_t blocks) {
-    return whole_warps(max_rows) + whole_warps(n + 1) + whole_warps(workers) + 3 * whole_warps(blocks);
+    return whole_warps(max_rows) + whole_warps(n + 1) + whole_warps(workers + 1) + 3 * whole_warps(blocks);
 }
 
 // Row r: token s + t of a request sits in page (s + t) / 16, at slot (s + t) % 16; the row that starts a page
@@ -117,22 +117,36 @@ __device__ __forceinline__ void write_row(const TablesParams& p, int32_t* arrays
     p.row_pos[r] = pos;
 }
 
-// Worker w's share of the few-row requests' units, dealt in equal runs.
+// Where a position of the few-row requests' weights lies: request, kv head, page (the run's first one for a
+// position in the weight of its beginning), and the units before it.
+struct FewPlace {
+    int32_t req, kvh, page, pages, units;
+};
+__device__ __forceinline__ FewPlace few_place(const TablesParams& p, int32_t* arrays, int32_t u) {
+    const int32_t weight = plan_words_of(arrays, CA_START, p.n)[p.n];
+    const int32_t* few = plan_words_of(arrays, CA_FEW, p.n);
+    FewPlace at;
+    at.req = row_request(few, p.n, u);
+    at.pages = pages_of(plan_words_of(arrays, CA_SEQ, p.n)[at.req] + plan_words_of(arrays, CA_NEW, p.n)[at.req]);
+    const int32_t run = at.pages + weight, local = u - few[at.req];
+    at.kvh = local / run;
+    at.page = max(0, local - at.kvh * run - weight);
+    at.units = few[at.req] - weight * p.hkv * plan_words_of(arrays, CA_FEWN, p.n)[at.req] + at.kvh * at.pages + at.page;
+    return at;
+}
+// Where worker w's share of the few-row requests' units begins, dealt by weight in equal runs (it ends where
+// the next one's begins).
 __device__ __forceinline__ void write_worker(const TablesParams& p, int32_t* arrays, int32_t w) {
-    const int32_t* seq = plan_words_of(arrays, CA_SEQ, p.n);
-    const int32_t* add = plan_words_of(arrays, CA_NEW, p.n);
-    const int32_t* base = plan_words_of(arrays, CA_ROW, p.n);
     const int32_t* few = plan_words_of(arrays, CA_FEW, p.n);
     const Deal deal(few[p.n], p.workers);
-    const int32_t u0 = deal.first(w), n_units = deal.first(w + 1) - u0;
-    int4 e = make_int4(0, 0, 0, n_units), f = make_int4(1, 0, 0, 0);
-    if (n_units > 0) {
-        const int b = row_request(few, p.n, u0);
-        f = make_int4(pages_of(seq[b] + add[b]), seq[b], add[b], base[b]);
-        const int32_t local = u0 - few[b];
-        e.x = b;
-        e.y = local / f.x;
-        e.z = local - e.y * f.x;
+    const int32_t u0 = deal.first(w);
+    const int32_t all = few[p.n] - plan_words_of(arrays, CA_START, p.n)[p.n] * p.hkv * plan_words_of(arrays, CA_FEWN, p.n)[p.n];
+    int4 e = make_int4(0, 0, 0, all), f = make_int4(1, 0, 0, 0);
+    if (u0 < few[p.n]) {
+        const FewPlace at = few_place(p, arrays, u0);
+        e = make_int4(at.req, at.kvh, at.page, at.units);
+        f = make_int4(at.pages, plan_words_of(arrays, CA_SEQ, p.n)[at.req], plan_words_of(arrays, CA_NEW, p.n)[at.req],
+                      plan_words_of(arrays, CA_ROW, p.n)[at.req]);
     }
     int4* dst = reinterpret_cast<int4*>(p.plan + plan_starts(p.n)) + 3 * w;
     dst[0] = e;
@@ -143,20 +157,19 @@ __device__ __forceinline__ void write_worker(const TablesParams& p, int32_t* arr
 // The blocks that the run of block w's first unit reaches (first, last), or that of its last unit (last).
 __device__ __forceinline__ void write_share(const TablesParams& p, int32_t* arrays, int32_t w, bool of_last) {
     const int32_t* few = plan_words_of(arrays, CA_FEW, p.n);
+    const int32_t weight = plan_words_of(arrays, CA_START, p.n)[p.n];
     const Deal deal(few[p.n], p.workers);
     const int per = p.workers / p.blocks;
     const int32_t u0 = deal.first(w * per), u1 = deal.first((w + 1) * per);
     if (u0 == u1) return;
-    const int32_t u = of_last ? u1 - 1 : u0;
-    const int b = row_request(few, p.n, u);
-    const int32_t pages = pages_of(plan_words_of(arrays, CA_SEQ, p.n)[b] + plan_words_of(arrays, CA_NEW, p.n)[b]);
-    const int32_t first = few[b] + (u - few[b]) / pages * pages;
+    const FewPlace at = few_place(p, arrays, of_last ? u1 - 1 : u0);
+    const int32_t first = few[at.req] + at.kvh * (at.pages + weight) + weight;     // its first page
     int4* dst = reinterpret_cast<int4*>(p.plan + plan_starts(p.n)) + 3 * w * per + 2;
     if (of_last) {
-        dst->w = deal.owner(first + pages - 1) / per;
+        dst->w = deal.owner(first + at.pages - 1) / per;
     } else {
         dst->y = deal.owner(first) / per;
-        dst->z = deal.owner(first + pages - 1) / per;
+        dst->z = deal.owner(first + at.pages - 1) / per;
     }
 }
 
@@ -206,8 +219,8 @@ __device__ __forceinline__ void write_rows(const TablesParams& p, int32_t* array
             else p.head_out[0] = head + taken;
         }
         k -= whole_warps(p.n + 1);
-        if (k >= 0 && k < p.workers) write_worker(p, arrays, k);
-        k -= whole_warps(p.workers);
+        if (k >= 0 && k <= p.workers) write_worker(p, arrays, k);
+        k -= whole_warps(p.workers + 1);
         if (k >= 0 && k < p.blocks) write_share(p, arrays, k, false);
         k -= whole_warps(p.blocks);
         if (k >= 0 && k < p.blocks) write_share(p, arrays, k, true);
@@ -234,6 +247,7 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
     int32_t* o_few = plan_words_of(s_arrays, CA_FEW, p.n);
     int32_t* o_many = plan_words_of(s_arrays, CA_MANY, p.n);
     int32_t* o_kpage = plan_words_of(s_arrays, CA_KPAGE, p.n);
+    int32_t* o_fewn = plan_words_of(s_arrays, CA_FEWN, p.n);
     const int32_t head = p.free_head[0];
     bool bad = head < 0 || head > p.n_free;
     int sum[kSums] = {};
@@ -267,6 +281,7 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         sum[3] = sat_add(sum[3], work.few);
         sum[4] = sat_add(sum[4], work.many);
         sum[5] = sat_add(sum[5], work.pages);
+        sum[6] += work.few > 0;
         o_new[b] = n;
         o_start[b] = start;
     }
@@ -312,11 +327,13 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         for (int i = 0; i < kSums; ++i) pre[i] = tot[i] = 0;
         if (tid == 0) set_dev_error(kDevErrBounds);
     }
+    const int32_t run = run_weight(tot[3], p.workers), weight = run * p.hkv;      // of a run, of a request's runs
     for (int b = b0; b < b1; ++b) {
         if (bad) o_new[b] = 0;
         o_row[b] = pre[0];
         o_take[b] = pre[1];
-        o_few[b] = pre[3];
+        o_few[b] = pre[3] + pre[6] * weight;
+        o_fewn[b] = pre[6];
         o_many[b] = pre[4];
         o_kpage[b] = pre[5];
         if (!bad) {
@@ -326,13 +343,16 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
             pre[3] += work.few;
             pre[4] += work.many;
             pre[5] += work.pages;
+            pre[6] += work.few > 0;
         }
     }
     if (tid == 0) {
-        o_seq[p.n] = o_new[p.n] = o_start[p.n] = 0;
+        o_seq[p.n] = o_new[p.n] = 0;
+        o_start[p.n] = run;
         o_row[p.n] = tot[0];
         o_take[p.n] = tot[1];
-        o_few[p.n] = tot[3];
+        o_few[p.n] = tot[3] + tot[6] * weight;
+        o_fewn[p.n] = tot[6];
         o_many[p.n] = tot[4];
         o_kpage[p.n] = tot[5];
         if (blockIdx.x == 0)

@@ -8,7 +8,7 @@
 // What bounds it: every (page, kv head) -- 16 keys and values, 4 d bytes a token -- is read once and
 // meets at most 16 rows, so HBM bounds it and the arithmetic only has to keep out of the way.  One block
 // an SM, twelve warps, each a worker of its own: the units of all requests, in (request, kv head, page)
-// order, are dealt to the workers in equal contiguous runs by pcf_chunk_tables, whatever the lengths.
+// order, are dealt to the workers in contiguous shares of equal weight by pcf_chunk_tables, whatever the lengths.
 // Lane l of a worker holds the table entry of the l-th page ahead and copies it by TMA (128-byte
 // swizzled) with the cos/sin row of the page's first position, into a ring of the worker's own, so no
 // warp waits for another and an SM has more than 100 KB on the way.
@@ -34,8 +34,8 @@
 // rate, the others the way to the first page (2.6), the ramp and the joins (a block's and, behind a fence and
 // a counter, the run's: some 5).  Behind 4 k: 11.7 us for 17 MB, all latency.  64 requests of 17 k tokens on
 // shared spans (64/8 heads): 665 us for 4.8 GB of pages, a third of it found in L2; the copies alone take 609.
-// 48 drafts of up to four tokens behind 100 to 9000 (two row tiles): 146 us for 737 MB, 109 at the copy rate;
-// three warps a sub-partition issue 46 % of the time, their own latencies (shared memory, products) bind.
+// 48 drafts of up to four tokens behind 100 to 9000 (two row tiles): 134 us for 737 MB, 109 at the copy rate;
+// 32 requests behind 16 k: 91 % of the copy rate with one row tile and 93 % with two.
 #pragma once
 #include "chunk_format.h"
 #include "kernel_chunk_tables.cuh"
@@ -274,11 +274,12 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const int worker = blockIdx.x * WARPS + warp;
     const int4* entry = reinterpret_cast<const int4*>(plan + plan_starts(p.n)) + 3 * worker;
     const int4 start = entry[0], first = entry[1];
+    const int32_t end = entry[3].w;                 // units before the next worker
     // {tag; first and last block of the run this block's first unit belongs to, last of its last unit's}
     const int32_t tag = entry[2].x;
     const int4 share = reinterpret_cast<const int4*>(plan + plan_starts(p.n))[3 * blockIdx.x * WARPS + 2];
     if (tag != p.tag) set_dev_error(kDevErrBounds);
-    const int n_units = tag == p.tag ? start.w : 0;
+    const int n_units = tag == p.tag ? end - start.w : 0;
     // cos/sin of 0..15 steps, for everyone, as pairs: (cos, cos', sin, sin') of two frequencies
     for (int i = tid; i < kPage * D / 4; i += THREADS) {
         const int r = i / (D / 4), f = i % (D / 4);

@@ -279,6 +279,25 @@ def poison_excluded(c):
                 c.v_pool[p, :, j % PAGE] = [float("nan"), float("inf"), -float("inf")][j % 3]
 
 
+@pytest.mark.parametrize("n_sms", [1, 2, 5, 23])
+@pytest.mark.parametrize("seq_hi,new_hi,shape", [
+    (90, 3, dict(hq=8, hkv=2, d=64)), (40, 5, dict(hq=8, hkv=4, d=128)), (400, 4, dict(hq=16, hkv=4, d=128)),
+    (90, 60, dict(hq=8, hkv=2, d=64)), (300, 90, dict(hq=32, hkv=4, d=128)), (16, 2, dict(hq=2, hkv=2, d=64))])
+def test_few_blocks_with_many_runs_each(n_sms, seq_hi, new_hi, shape):
+    """Work dealt to few workers: runs of a page or two, several of them in a worker's share, shares that end
+    where a run begins."""
+    rng = np.random.default_rng(100 * n_sms + seq_hi)
+    n = 40
+    c = ChunkCase(rng.integers(0, seq_hi, n).tolist(), rng.integers(0, new_hi, n).tolist(), seed=n_sms, **shape).to_device()
+    c.L.dims.n_sms = n_sms
+    got = c.step()
+    c.check(got)
+    first = c.out.clone()
+    c.attend()
+    pcf.check_device_error()
+    assert torch.equal(c.out, first)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("share", [0.0, 0.2])
 @pytest.mark.parametrize("kinds", [[3, 20, 16, 60, 1], [20, 3], [16, 16, 33], [5]])
