@@ -44,8 +44,8 @@ constexpr int kSums = 7;   // rows, pages taken, pages held afterwards, few-row 
 __device__ __forceinline__ int32_t pages_of(int32_t tokens) { return (tokens + kPage - 1) / kPage; }
 __device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) { return min(a + b, kSumLimit); }
 
-// A request's work in the attention: (page, kv head) units with few rows, else the key tiles all its
-// row pairs visit (every kv head) and the pages whose keys are rotated beforehand.
+// A request's work in the attention: (page, kv head) units with few rows, else the weight of all its row
+// pairs (every kv head) and the pages whose keys are rotated beforehand.
 struct ChunkWork {
     int32_t few, many, pages;
 };
@@ -55,7 +55,7 @@ __device__ __forceinline__ ChunkWork chunk_work(const TablesParams& p, int32_t s
     if (n == 0) return {0, 0, 0};
     if ((int64_t)n * g <= p.few_rows) return {pages * p.hkv, 0, 0};
     const int tpp = 2 * kTileRows / g, last = many_pairs(n, tpp) - 1;
-    const int64_t tiles = (many_before(s, tpp, last) + many_tiles(s, n, tpp, last)) * p.hkv;
+    const int64_t tiles = (many_weight(s, tpp, last) + kPairWeight + many_tiles(s, n, tpp, last)) * p.hkv;
     // (rows that fit one tile: the kernel rotates the keys itself)
     return {0, (int32_t)min(tiles, (int64_t)kSumLimit), n * g <= kTileRows ? 0 : pages};
 }
@@ -173,7 +173,7 @@ __device__ __forceinline__ void write_share(const TablesParams& p, int32_t* arra
     }
 }
 
-// Block w's share of the others' key tiles, in (request, kv head, row pair, tile) order.
+// Block w's share of the others' key tiles, in (request, kv head, row pair, tile) order, by weight.
 __device__ __forceinline__ void write_block(const TablesParams& p, int32_t* arrays, int32_t w) {
     const int32_t* seq = plan_words_of(arrays, CA_SEQ, p.n);
     const int32_t* add = plan_words_of(arrays, CA_NEW, p.n);
@@ -193,10 +193,12 @@ __device__ __forceinline__ void write_block(const TablesParams& p, int32_t* arra
         int lo = 0, hi = many_pairs(add[b], tpp) - 1;   // the pair the tile falls into
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (many_before(seq[b], tpp, mid) <= local) lo = mid; else hi = mid - 1;
+            if (many_weight(seq[b], tpp, mid) <= local) lo = mid; else hi = mid - 1;
         }
+        local -= (int32_t)many_weight(seq[b], tpp, lo);
         e.z = lo;
-        e.w = local - (int32_t)many_before(seq[b], tpp, lo);
+        e.w = max(0, local - kPairWeight);
+        f.z = max(0, kPairWeight - local);
     }
     int4* dst = reinterpret_cast<int4*>(p.plan + plan_many(p.n, p.workers)) + 2 * w;
     dst[0] = e;

@@ -15,7 +15,7 @@
 // many_rows_kernel: one block an SM; a run is two 128-row tiles A and B of one (request, kv head) --
 // row m of a tile is token m / g, query head m % g of the kv head -- against the 128-key tiles its last
 // row sees.  All runs' key tiles, in (request, kv head, row pair, tile) order, are dealt to the blocks
-// in equal contiguous parts by pcf_chunk_tables, whatever the lengths; a block passes on what it has of
+// in contiguous parts of equal weight by pcf_chunk_tables, whatever the lengths; a block passes on what it has of
 // the runs it shares with its neighbours (two at most) and many_join_kernel adds those up in a fixed
 // order.
 //   warps 0-3   softmax of tile A, warps 4-7 of tile B (or the rotation): S row from TMEM, causal cut and exclusion bits,
@@ -29,10 +29,10 @@
 // columns t*128 + {0, 64}, O_A at 256, O_B at 384; P (bf16 pairs) overwrites the S half it came from and
 // is the A operand of O += P V (M = 128, N = d, K = 64 keys).
 //
-// Measured: 2048 tokens behind 32 k (32/8 heads, d 128; 1.13 TFLOP): 840 us a call, 94 % of it this kernel:
-// 1350 TFLOP/s, 71 % of a large product's burst rate.  The chain S -> softmax -> P -> P V -> next Q K^T
+// Measured: 2048 tokens behind 32 k (32/8 heads, d 128; 1.13 TFLOP): 836 us a call, 94 % of it this kernel:
+// 1355 TFLOP/s, 71 % of a large product's burst rate.  The chain S -> softmax -> P -> P V -> next Q K^T
 // through the two halves bounds it (the tensor pipe is busy 62 % of the time), not the exponentials (31 % of
-// their unit) or the copies.  Six chunks of 100 to 700 tokens beside 26 single tokens: 59 % of 288 us.
+// their unit) or the copies.  Six chunks of 100 to 700 tokens beside 26 single tokens: 58 % of 275 us.
 #pragma once
 #include "chunk_format.h"
 #include "kernel_attn.cuh"
@@ -394,7 +394,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     grid_dep_launch();
     const int4* entry = reinterpret_cast<const int4*>(prm.plan + plan_many(prm.n, prm.workers)) + 2 * blockIdx.x;
     const int4 share = entry[1];
-    const int n_tiles = share.y == prm.tag ? share.x : 0;
+    const int weight = share.y == prm.tag ? share.x : 0;
     if (warp == kWarpMma) {
         tmem_alloc(reinterpret_cast<uint32_t*>(misc), 512);
         tmem_relinquish();
@@ -415,7 +415,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         return true;
     };
 
-    if (n_tiles == 0) {            // nothing to do for the whole block
+    if (weight == 0) {             // nothing to do for the whole block
         if (tid == 0) prm.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     } else if (warp == kWarpTma) {
         // ------------------------------------------------------------ runs, Q and K tiles
@@ -425,13 +425,15 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int32_t* many = plan + plan_array(CA_MANY, prm.n);
         const int32_t* kpage = plan + plan_array(CA_KPAGE, prm.n);
         const int4 start = entry[0];
-        int left = n_tiles;
+        int left = weight;
+        int begins = share.z;              // weight of the run's beginning, where that is in this share
         int32_t req = start.x, kvh = start.y, pair = start.z, tile = start.w;
         int kc = 0, last_k[2] = {-1, -1}, last_q = -1, raw_n[2] = {0, 0}, full_n[2] = {0, 0};   // copies of either kind a stage took
         bool ok = true;
         int4 desc = make_int4(0, 0, 0, 0), desc_rows = desc;
         for (int it = 0; ok; ++it) {
             ManyItem w;
+            left -= begins;
             w.req = left > 0 ? req : -1;
             w.kvh = kvh;
             w.pair = pair;
@@ -452,7 +454,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (tile == 0 && w.n_loc < all) {
                     // the block that holds the run's last tile
                     const int32_t u = many[req] + kvh * ((many[req + 1] - many[req]) / prm.hkv) +
-                                      (int32_t)many_before(w.seq, tpp, pair) + all - 1;
+                                      (int32_t)many_weight(w.seq, tpp, pair) + kPairWeight + all - 1;
                     desc = make_int4(Deal(many[prm.n], prm.blocks).owner(u) << 8 | 0xFF, pair * tpp, kvh, 0);
                     desc_rows = make_int4(w.add, w.row_base, 0, 0);
                 }
@@ -527,6 +529,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             // the next run
             tile = 0;
+            begins = kPairWeight;
             if (w.jb + w.n_loc == many_tiles(w.seq, w.add, tpp, pair) && ++pair == many_pairs(w.add, tpp)) {
                 pair = 0;
                 if (++kvh == prm.hkv) {
