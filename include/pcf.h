@@ -401,6 +401,9 @@ pcf_status pcf_chunk_attention_workspace_bytes(const pcf_chunk_dims* dims, size_
  * pcf_chunk_attention_workspace_bytes, contents need not be initialised.  Any number of calls may use
  * one plan, one behind the other (a model's layers); two calls that may overlap need a plan (a
  * pcf_chunk_tables call) and a workspace each, as the plan holds counters that a call moves on.
+ * Dims that allow requests of more than 16 rows (max_chunk * Hq / Hkv) launch the kernels for those too,
+ * some 9 us where there are none: steps of single tokens or drafts do better under dims of their own over
+ * the same tables.
  * Deterministic.  A page outside the pool, a position outside the rope table or a plan of other dims
  * raises PCF_ERR_DEVICE_BOUNDS; a rotated query or key that takes part and is not finite in fp16 (beyond
  * 65504, or NaN), or a value that takes part and is not finite, PCF_ERR_DEVICE_RANGE (a row may share its

@@ -281,7 +281,9 @@ class ChunkLayout:
     what is cached (or starts from ``from_layout``), ``chunk_tables`` adds the pages new tokens start.
     ``slot_map``, ``row_pos`` [max_rows] and ``row_base`` [n_reqs + 1] describe the rows of the last
     ``chunk_tables``, ``plan`` is what the calls after it read.  All are int32 tensors on ``device``
-    that stay where they are, so that a captured step can be replayed.  Calls that may overlap need a
+    that stay where they are, so that a captured step can be replayed.  Steps of single tokens or drafts
+    are quickest under a ChunkLayout of their own with that ``max_chunk``, given another one's
+    ``block_table`` and ``page_pos``.  Calls that may overlap need a
     ChunkLayout and a workspace each."""
 
     def __init__(self, n_reqs: int, hq: int, hkv: int, d: int, n_phys_pages: int, max_pos: int, max_pages: int,
