@@ -210,6 +210,18 @@ struct ManySmem {
     static_assert(kAlloc <= 232448, "more dynamic shared memory than a GB300 block can have");
 };
 
+// A wait sees the parity of a phase only, so a phase may end at most once before each of its waiters has
+// passed it.  What keeps each barrier to that:
+//   Q, K, V, M, ITEM  a copy goes into a stage again only behind the stage's EMPTY, which every waiter on
+//                     its FULL (RAW, ROT) has arrived on, whichever kind of run the tile belongs to;
+//   S_FULL, P_FULL    the next Q K^T into a half waits for the P V that read it, that one for the P of every
+//                     thread that read S;
+//   PV_DONE           waited for by the next Q K^T into the half, and by softmax threads that rescale: those
+//                     have seen S(h), whose Q K^T waited for P V(h - 2), and P V(h + 1) needs their P(h + 1);
+//   O_DONE, O_FREE    take turns: every P V of a run, then every thread's epilogue, then the next run's P V.
+//                     They count the runs their row tile takes part in.  Runs of one row tile are none of tile
+//                     B's: an arrival for it then would be ordered behind V tiles only, not behind the P V of
+//                     the run before, nor the waits for that run's result.
 enum : int {
     MB_Q_FULL = 0, MB_Q_EMPTY = 1,
     MB_K_FULL = 2,      // [2]
@@ -627,7 +639,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const bool qk_role = warp == kWarpMma || warp == kWarpMmaB;
         const int t = (warp == kWarpMma || warp == kWarpPvA) ? 0 : 1;
         const uint32_t leader = lane == 0 ? 1u : 0u;
-        int hq = 0, kc = 0;
+        int hq = 0, kc = 0, own = 0;                     // own: runs the row tile took part in
         int raw_n[2] = {0, 0}, full_n[2] = {0, 0};       // K tiles of either kind a stage held before
         bool ok = true;
         for (int it = 0; ok; ++it) {
@@ -643,7 +655,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                 : mbar_wait(&bars[MB_K_FULL + ks], full_n[ks]++ & 1, abort_flag);
             };
             if (w.single && t == 1) {
-                // tile B is not there: its issuers only take their part in the hand-offs
+                // tile B is not there: its issuers only take their part in the hand-offs of queries, keys and values
                 for (int j = 0; ok && j < w.n_loc; ++j) {
                     const int kt = kc + j;
                     ok = __all_sync(0xffffffffu, qk_role ? wait_k(kt & 1)
@@ -651,7 +663,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     if (ok && leader) mbar_arrive(&bars[(qk_role ? MB_K_EMPTY : MB_V_EMPTY) + (kt & 1)]);
                 }
                 if (ok && qk_role) ok = __all_sync(0xffffffffu, mbar_wait(&bars[MB_Q_FULL], it & 1, abort_flag));
-                if (ok && leader) mbar_arrive(&bars[qk_role ? MB_Q_EMPTY : MB_O_DONE + 1]);
+                if (ok && qk_role && leader) mbar_arrive(&bars[MB_Q_EMPTY]);
                 kc += w.n_loc;
                 continue;
             }
@@ -684,8 +696,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     ok = __all_sync(0xffffffffu,
                                     mbar_wait(&bars[MB_P_FULL + 2 * t + (hg & 1)], (hg >> 1) & 1, abort_flag) &&
                                         (h == 1 || mbar_wait(&bars[MB_V_FULL + (kt & 1)], (kt >> 1) & 1, abort_flag)) &&
-                                        (q > 0 || it == 0 ||
-                                         mbar_wait(&bars[MB_O_FREE + t], (it - 1) & 1, abort_flag)));
+                                        (q > 0 || own == 0 ||
+                                         mbar_wait(&bars[MB_O_FREE + t], (own - 1) & 1, abort_flag)));
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t aV = desc_sw128_lo(smem_u32(sV(kt & 1)) + h * 64 * 128, 16384);
@@ -698,6 +710,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             hq += nq;
             kc += w.n_loc;
+            ++own;
         }
         const int di = (qk_role ? 0 : 2) + t;
         mma_commit_by(leader, &bars[MB_DRAIN + di]);
@@ -708,7 +721,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int m = tid - t * 128;                       // row of the tile = TMEM lane
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tO = tmem + lane_addr + kTmemO + t * 128;
-        int hq = 0, kc = 0;
+        int hq = 0, kc = 0, own = 0;
         int raw_n[2] = {0, 0};
         float nan = 0.f;                                   // NaN where a result is not finite
         bool ok = true;
@@ -722,7 +735,6 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (w.single && t == 1) {
                 ok = rotate_tiles<D>(prm, w, sK(0), SM::kK, s_mask, bars, kc, raw_n, m, lane, abort_flag);
                 if (!ok) break;
-                mbar_arrive(&bars[MB_O_FREE + 1]);
                 kc += w.n_loc;
                 continue;
             }
@@ -812,7 +824,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             if (!ok) break;
             // epilogue: O / l, or the part's sums as they are
-            ok = mbar_wait(&bars[MB_O_DONE + t], it & 1, abort_flag);
+            ok = mbar_wait(&bars[MB_O_DONE + t], own & 1, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
             if (w.slot >= 0) {
@@ -857,6 +869,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_arrive(&bars[MB_O_FREE + t]);
             hq += nq;
             kc += w.n_loc;
+            ++own;
         }
         if (nan != nan) set_dev_error(kDevErrRange);       // (a value that takes part is not finite)
     }
