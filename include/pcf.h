@@ -361,8 +361,8 @@ pcf_status pcf_chunk_plan_words(const pcf_chunk_dims* dims, int64_t* n_words);
  *           plan [pcf_chunk_plan_words] int32
  * Refused on the device, with PCF_ERR_DEVICE_BOUNDS from the next pcf_check_device_error: a negative
  * length, one beyond the dims, positions outside the rope table (of any slot of a page a request
- * writes to), a next_pos that breaks a started page, a free list that runs out or names a page
- * outside the pool, work of about 1<<29 (page, kv head) pairs or key tiles of 128 keys.  Then no table entry is written, the lengths and the list's head stay, slot_map
+ * writes to or goes on behind), a next_pos that breaks a started page, a started page outside the
+ * pool, a free list that runs out or names a page outside the pool, work of about 1<<29 (page, kv head) pairs or key tiles of 128 keys.  Then no table entry is written, the lengths and the list's head stay, slot_map
  * and row_pos are all -1, and calls that use the plan do nothing.
  * One launch, or two where lengths or list head are updated in place. */
 pcf_status pcf_chunk_tables(const pcf_chunk_dims* dims, const int32_t* seq_len, const int32_t* new_len,

@@ -97,21 +97,12 @@ __device__ __forceinline__ void write_row(const TablesParams& p, int32_t* arrays
         const int32_t t = r - base[b], s = seq[b] + t, pg = s / kPage, first = pages_of(seq[b]);
         const int64_t e = (int64_t)b * p.max_pages + pg;
         pos = start[b] + t;
-        int32_t ph;
-        if (pg >= first) {
-            ph = p.free_pages[head + take[b] + pg - first];
-            if (s % kPage == 0) {
-                p.block_table[e] = ph;
-                p.page_pos[e] = pos;
-            }
-        } else {
-            ph = p.block_table[e];
-            if (ph < 0 || ph >= p.n_phys) {
-                set_dev_error(kDevErrBounds);
-                ph = -1;
-            }
+        const int32_t ph = pg >= first ? p.free_pages[head + take[b] + pg - first] : p.block_table[e];
+        if (pg >= first && s % kPage == 0) {
+            p.block_table[e] = ph;
+            p.page_pos[e] = pos;
         }
-        if (ph >= 0) slot = ph * kPage + s % kPage;
+        slot = ph * kPage + s % kPage;
     }
     p.slot_map[r] = slot;
     p.row_pos[r] = pos;
@@ -266,11 +257,17 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         const int32_t before = pages_of(s), after = pages_of(s + n);
         int32_t start = 0;
         if (n > 0) {
-            // a page's slots sit at consecutive positions, so a started page fixes the next one
-            const int32_t last = s > 0 ? p.page_pos[(int64_t)b * p.max_pages + before - 1] : -kPage;
-            start = last < -kPage || last > p.max_pos ? -1 : last + (s % kPage ? s % kPage : kPage);
+            // a page's slots sit at consecutive positions, so a started page fixes the next one; its entries
+            // are checked here, as the call goes on from them
+            const bool started = s % kPage != 0;
+            if (started || (s > 0 && !p.next_pos)) {
+                const int64_t e = (int64_t)b * p.max_pages + before - 1;
+                const int32_t last = p.page_pos[e], ph = started ? p.block_table[e] : 0;
+                if (last < 0 || last > p.max_pos - kPage || ph < 0 || ph >= p.n_phys) bad = true;
+                else start = last + (started ? s % kPage : kPage);
+            }
             if (p.next_pos) {
-                if (s % kPage && want != start) bad = true;
+                if (started && want != start) bad = true;
                 start = want;
             }
             // every slot of the last page has a row in the cos/sin table
