@@ -307,9 +307,10 @@ class ChunkLayout:
         n = ctypes.c_int64(0)
         _lib.check("pcf_chunk_plan_words", lib.pcf_chunk_plan_words(self.dims_ref, ctypes.byref(n)))
         ints = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)
+        # (no row has a slot before the first tables: -1, as behind the last row)
         self._tables = {"block_table": ints(n_reqs, max_pages), "page_pos": ints(n_reqs, max_pages),
-                        "slot_map": ints(max_rows), "row_pos": ints(max_rows), "row_base": ints(n_reqs + 1),
-                        "plan": ints(n.value)}
+                        "slot_map": ints(max_rows).fill_(-1), "row_pos": ints(max_rows).fill_(-1),
+                        "row_base": ints(n_reqs + 1), "plan": ints(n.value)}
 
     def _table(name):
         def put(self, t):

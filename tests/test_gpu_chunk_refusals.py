@@ -65,3 +65,11 @@ def test_idle_requests_and_full_pages_with_next_pos_may_hold_what_they_like():
     c.tables()
     pcf.check_device_error()
     assert np.array_equal(c.L.slot_map.cpu().numpy(), c.slots) and np.array_equal(c.L.row_pos.cpu().numpy(), c.where)
+
+
+def test_rows_of_a_layout_without_tables_go_nowhere():
+    c = ChunkCase([20], [4], stale="normal").to_device()
+    k, v = c.dk.clone(), c.dv.clone()
+    c.append()
+    pcf.check_device_error()
+    assert torch.equal(c.dk, k) and torch.equal(c.dv, v)
