@@ -416,8 +416,8 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
         const int h = (int)(rh % p.hkv);
         const int32_t row = (int32_t)(rh / p.hkv);
         const int32_t slot = p.slot_map[row];
-        if (slot < 0) continue;
-        if (slot >= p.n_phys * kPage) {
+        if (slot == -1) continue;
+        if (slot < 0 || slot >= p.n_phys * kPage) {
             set_dev_error(kDevErrBounds);
             continue;
         }
@@ -428,11 +428,12 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
         uint4 k0 = *reinterpret_cast<const uint4*>(ks + 8 * c);
         uint4 k1 = *reinterpret_cast<const uint4*>(ks + D / 2 + 8 * c);
         if (p.at != nullptr) {
-            const int32_t at = p.at[row], by = at - p.slot_pos[row];
-            if (at < 0 || at >= p.max_pos || by <= -p.max_pos || by >= p.max_pos) {
+            const int32_t at = p.at[row], from = p.slot_pos[row];
+            if (at < 0 || at >= p.max_pos || from < 0 || from >= p.max_pos) {
                 set_dev_error(kDevErrBounds);
                 continue;
             }
+            const int32_t by = at - from;
             if (by != 0) {
                 const float sgn = by < 0 ? -1.f : 1.f;   // cos(-a) = cos a, sin(-a) = -sin a
                 const float4* cs = reinterpret_cast<const float4*>(p.rope + (int64_t)abs(by) * D + 16 * c);

@@ -73,3 +73,31 @@ def test_rows_of_a_layout_without_tables_go_nowhere():
     c.append()
     pcf.check_device_error()
     assert torch.equal(c.dk, k) and torch.equal(c.dv, v)
+
+
+@pytest.mark.parametrize("row_pos", [False, True])
+@pytest.mark.parametrize("slot", [-2, -2 ** 31, "end", 2 ** 31 - 1])
+def test_append_reports_slots_outside_the_pool(slot, row_pos):
+    c = ChunkCase([20, 7], [4, 9], stale="normal").to_device()
+    c.tables()
+    c.L.slot_map[2] = c.n_phys * PAGE if slot == "end" else slot
+    k, page, r = c.dk.clone(), c.slots // PAGE, c.slots % PAGE
+    c.append(row_pos=c.L.row_pos.clone() if row_pos else None)
+    refused()
+    others = np.arange(c.rows) != 2
+    k[page[others], :, r[others]] = c.dkn[: c.rows][torch.from_numpy(others).cuda()]
+    assert torch.equal(c.dk, k)
+
+
+@pytest.mark.parametrize("bad", [-1, "end", -2 ** 31, 2 ** 31 - 1])
+def test_append_reports_slot_positions_outside_the_rope_table(bad):
+    c = ChunkCase([20, 7], [4, 9], stale="normal").to_device()
+    c.tables()
+    at = c.L.row_pos.clone()
+    c.L.row_pos[2] = c.max_pos if bad == "end" else bad
+    k, page, r = c.dk.clone(), c.slots // PAGE, c.slots % PAGE
+    c.append(row_pos=at)
+    refused()
+    others = np.arange(c.rows) != 2
+    k[page[others], :, r[others]] = c.dkn[: c.rows][torch.from_numpy(others).cuda()]
+    assert torch.equal(c.dk, k)
