@@ -57,7 +57,7 @@ struct FewParams {
     float2* block_ml;           // [blocks][2][8 NQ]
     int32_t* count;             // [blocks] parts brought of the run that begins in a block and goes on
     int64_t q_stride;
-    int32_t n, max_pages, max_rows, hq, hkv, n_phys, max_pos, blocks, tag;
+    int32_t n, max_pages, hq, hkv, n_phys, max_pos, tag;
 };
 
 

@@ -190,7 +190,6 @@ struct ManyItem {
     int32_t seq, add, row_base, kpage;
     int32_t slot;               // partial result, or -1: the whole run
     int32_t single;             // all rows fit tile A: keys straight from the pages, rotated here
-    int32_t pad;
 };
 
 template <int D>
@@ -452,7 +451,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             w.jb = tile;
             w.n_loc = w.seq = w.add = w.row_base = w.kpage = 0;
             w.slot = -1;
-            w.single = w.pad = 0;
+            w.single = 0;
             if (left > 0) {
                 w.seq = seq[req];
                 w.add = add[req];

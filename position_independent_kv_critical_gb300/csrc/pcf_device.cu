@@ -1055,8 +1055,8 @@ pcf_status few_rows_impl(const ChunkCall& c, cudaStream_t st) {
     const FewParams p{c.plan, reinterpret_cast<const __nv_bfloat16*>(c.q), c.block_table, c.page_pos, c.excl, c.row_pos,
                       c.rope, reinterpret_cast<__nv_bfloat16*>(c.out), reinterpret_cast<float*>(c.ws + w.worker_o),
                       reinterpret_cast<float*>(c.ws + w.block_o), reinterpret_cast<float2*>(c.ws + w.block_ml),
-                      c.plan + plan_count(d.n_reqs, few_workers(&d), blocks), c.q_stride, d.n_reqs, d.max_pages, d.max_rows,
-                      d.n_q_heads, d.n_kv_heads, d.n_phys_pages, d.max_pos, blocks, plan_tag(&d)};
+                      c.plan + plan_count(d.n_reqs, few_workers(&d), blocks), c.q_stride, d.n_reqs, d.max_pages,
+                      d.n_q_heads, d.n_kv_heads, d.n_phys_pages, d.max_pos, plan_tag(&d)};
     using SM = FewSmem<D, NQ>;
     auto kern = few_rows_kernel<D, NQ>;
     if ((s = set_smem(kern, SM::kAlloc)) != PCF_OK) return s;
