@@ -95,7 +95,7 @@ PCF_HOST_DEVICE inline int64_t many_weight(int32_t seq, int32_t tpp, int32_t pai
 // A request has few rows when its new tokens times the query heads of a kv head are at most this: two
 // 8-row tiles a warp.  Reading the pages then bounds the attention (a key and value of 4 d bytes meet 4 d
 // flops a row).  24 requests of 6 k tokens, 64/8 heads, d 128: 16 rows take 115 us in the few-row kernel
-// and 186 in the other one, 24 rows 206 with four tiles a warp (eight warps of 255 registers) and 191 in
+// and 186 in the other one, 24 rows 206 with four tiles a warp (eight warps of 255 registers) and 185 in
 // the other one.
 constexpr int kFewRows = 16;
 // Warps of a block of the few-row kernel, each a worker: three a sub-partition, of 168 registers.

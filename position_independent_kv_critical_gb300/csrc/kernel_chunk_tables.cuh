@@ -36,8 +36,8 @@ constexpr int kTablesThreads = 512;
 // outputs are buffers of their own, every block of one launch reads the lengths and scans them for
 // itself and then writes its share of the rows (`alone`); where lengths or list head are updated in
 // place, a block must not write them while another still reads, so one block leaves the plan and a
-// second launch writes the rows.  Graph replay, 64 requests of one token: 5.2 us apart, 6.6 in place; 512
-// requests of four: 6.5 and 8.1.
+// second launch writes the rows.  Graph replay, 64 requests of one token: 5.0 us apart (4.7 with next_pos),
+// 6.2 in place; 512 requests of four: 6.3 and 9.0.
 // (Sums of refused lengths may be as large as 4096 x 2^22: they stop at 2^29, above every limit.)
 constexpr int kSumLimit = 1 << 29;
 constexpr int kSums = 7;   // rows, pages taken, pages held afterwards, few-row units, key tiles and pages of the others, few-row requests

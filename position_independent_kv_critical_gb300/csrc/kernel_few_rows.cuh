@@ -22,8 +22,8 @@
 // one or two products a step (rotated operands are fp16, 11 bits instead of bf16's 8: a score's error then
 // stays below that of the inputs; out of its range is reported); the running maximum and sum of the softmax
 // stay in registers (rescaled only when the maximum grows by more than 2^8), P^T in bf16 becomes the B operand of O^T +=
-// V^T P^T by an 8 x 8 transpose in registers (movmatrix).  The sum takes the rounded weights, so a row
-// with one dominant key is exact.  A tcgen05 tile of 128 rows would be nine tenths padding here.
+// V^T P^T by an 8 x 8 transpose in registers (movmatrix).  The sum takes the rounded weights, so here a
+// row with one dominant key is exact.  A tcgen05 tile of 128 rows would be nine tenths padding here.
 //
 // A run of a (request, kv head) that lies within one worker is written out directly.  Otherwise the
 // block joins its warps' partial results through shared memory and passes on at most two (the run
@@ -35,7 +35,8 @@
 // a counter, the run's: some 5).  Behind 4 k: 11.7 us for 17 MB, all latency.  64 requests of 17 k tokens on
 // shared spans (64/8 heads): 665 us for 4.8 GB of pages, a third of it found in L2; the copies alone take 609.
 // 48 drafts of up to four tokens behind 100 to 9000 (two row tiles): 134 us for 737 MB, 109 at the copy rate;
-// 32 requests behind 16 k: 91 % of the copy rate with one row tile and 93 % with two.
+// 32 requests behind 16 k: 91 % of the copy rate with one row tile and 92 % with two; 64 requests at d 64: 90 %
+// and 78 % (half the bytes a key, the same instructions for its softmax).
 #pragma once
 #include "chunk_format.h"
 #include "kernel_chunk_tables.cuh"

@@ -29,10 +29,15 @@
 // columns t*128 + {0, 64}, O_A at 256, O_B at 384; P (bf16 pairs) overwrites the S half it came from and
 // is the A operand of O += P V (M = 128, N = d, K = 64 keys).
 //
-// Measured: 2048 tokens behind 32 k (32/8 heads, d 128; 1.13 TFLOP): 836 us a call, 94 % of it this kernel:
-// 1355 TFLOP/s, 71 % of a large product's burst rate.  The chain S -> softmax -> P -> P V -> next Q K^T
+// The sum of a row's weights takes them unrounded, unlike the few-row kernel's: where one key dominates, the
+// result is its value within half a bf16 step and the final rounding.
+//
+// Measured: 2048 tokens behind 32 k (32/8 heads, d 128; 1.13 TFLOP): 841 us a call of all launches, 1348 TFLOP/s
+// or 71 % of a large product's burst rate, 94 % of the time in this kernel; 907 to 915 us, 1240 TFLOP/s, where
+// such calls run for seconds and the power cap lowers the clock.  The chain S -> softmax -> P -> P V -> next Q K^T
 // through the two halves bounds it (the tensor pipe is busy 62 % of the time), not the exponentials (31 % of
-// their unit) or the copies.  Six chunks of 100 to 700 tokens beside 26 single tokens: 58 % of 275 us.
+// their unit) or the copies.  Six chunks of 100 to 700 tokens beside 26 single tokens: 58 % of 276 us.
+// d = 64: 717 us, 791 TFLOP/s: as many scores, each with half the products.
 #pragma once
 #include "chunk_format.h"
 #include "kernel_attn.cuh"

@@ -29,8 +29,7 @@ def lengths(kinds, n, rng):
     return seq, new
 
 
-@pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("d,masked", [(64, True), (128, False)])
 @pytest.mark.parametrize("n_sms,kinds", [(1, "12"), (2, "12"), (3, "112"), (7, "1222"), (2, "11112"), (152, "12")])
 def test_runs_of_one_key_tile_take_turns(d, masked, n_sms, kinds):
     rng = np.random.default_rng(1000 * n_sms + len(kinds))
