@@ -414,6 +414,88 @@ pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, int32_t* plan, const 
                                const int32_t* page_pos, const uint16_t* excl, const int32_t* row_pos,
                                const float* rope, uint16_t* out, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- trees of drafted tokens
+ * A request may draft a tree instead of a line: its new tokens are the tree's nodes, a parent before its
+ * children, node t going on from node parent[t] of the same request or from the last token held (-1).  The
+ * nodes are the rows of a chunk (pcf_chunk_tables with new_len = the number of nodes; node t takes slot
+ * seq_len + t; pcf_append_kv without row_pos stores their keys unrotated), but a node's position follows from
+ * its depth and it sees, of the nodes, only itself and those it goes on from.  The branch that the model
+ * confirms then moves together in the pages: keys are unrotated, so it moves bit for bit (MiniPIC section 2.1).
+ * A step is: pcf_chunk_tables, pcf_tree_tables; in every layer pcf_append_kv and pcf_tree_attention;
+ * pcf_tree_accept, pcf_tree_keep.  As above: lengths and trees live on the GPU, buffers have the sizes the dims
+ * give, calls can be captured and replayed.  dims as for the chunk calls, with max_chunk at most: */
+#define PCF_TREE_MAX_NODES 256  /* else PCF_ERR_UNSUPPORTED from every call below */
+
+/* Host-only.  int32 words of the plan pcf_tree_tables writes and the calls behind it read. */
+pcf_status pcf_tree_plan_words(const pcf_chunk_dims* dims, int64_t* n_words);
+
+/* Positions and lines of every tree, behind the chunk's pcf_chunk_tables (chunk_plan: its plan).
+ *   in   parent [max_rows] int32: -1 .. t - 1 for node t of a request; not read behind the last row
+ *   out  row_pos [max_rows] int32: position of the request's first new row + the number of nodes the node
+ *          goes on from; -1 behind the last row
+ *        seen [max_rows][W] int32, W = (max_chunk + 31) / 32: bit u % 32 of word u / 32 is set for node u = t
+ *          and the nodes that t goes on from; 0 behind the last row
+ *        tree_plan [pcf_tree_plan_words] int32, 16-byte aligned
+ * Outputs overlap no other buffer of the call (row_pos is not pcf_chunk_tables' row_pos: that one holds the
+ * slots' positions).  A parent out of its range raises PCF_ERR_DEVICE_BOUNDS and counts as -1; lengths that
+ * pcf_chunk_tables refused, a chunk_plan of other dims or work of about 1<<29 units of 64 keys leave a plan
+ * without rows, the latter two with PCF_ERR_DEVICE_BOUNDS.  One launch. */
+pcf_status pcf_tree_tables(const pcf_chunk_dims* dims, const int32_t* chunk_plan, const int32_t* parent,
+                           int32_t* row_pos, int32_t* seen, int32_t* tree_plan, void* stream);
+
+/* Bytes of device workspace pcf_tree_attention needs for these dims. */
+pcf_status pcf_tree_attention_workspace_bytes(const pcf_chunk_dims* dims, size_t* bytes);
+
+/* Attention of the trees' nodes over the pages of their requests and over their own lines (the nodes' keys and
+ * values appended before).  For row i, node t of request b (s tokens held), and q head h:
+ *   out[i][h] = sum_j softmax_j((R_{row_pos[i]} q_{i,h}) . (R_{pos(j)} k_j) / sqrt(d)) v_j
+ * over the slots j < s and the slots s + u with bit u of seen[i] set, without those whose bit in excl is set;
+ * pos(16 p + r) = page_pos[b][p] + r for a slot below s, row_pos of node u for slot s + u.  A row with no slot
+ * left gives zeros.  row_pos and seen are pcf_tree_tables'; the other arguments, strides, alignments, checks
+ * and device errors are those of pcf_chunk_attention, but the plan is only read (slots that no row of the
+ * request sees may hold anything; a node that one row of the request does not see takes part where another
+ * does, so its values must be finite).  ws: device workspace of >= pcf_tree_attention_workspace_bytes, contents
+ * need not be initialised; calls that may overlap need one each.  Deterministic. */
+pcf_status pcf_tree_attention(const pcf_chunk_dims* dims, const int32_t* tree_plan, const uint16_t* q,
+                              int64_t q_row_stride, const uint16_t* k_pool, const uint16_t* v_pool,
+                              const int32_t* block_table, const int32_t* page_pos, const uint16_t* excl,
+                              const int32_t* row_pos, const int32_t* seen, const float* rope, uint16_t* out, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* The branch of every tree that the model's choices confirm, and the requests behind it.  A branch starts at
+ * the held tokens; from where it stands it goes to the node with the lowest number whose parent that is and
+ * whose draft token is the one chosen there, as long as there is one.
+ *   in      draft [max_rows] int32: the nodes' tokens; choice [max_rows]: the token the model chooses behind each
+ *           root_choice [n_reqs] or NULL: the token it chose behind the held tokens.  NULL: node 0 of every
+ *             request (with parent -1) is that token already and is kept; another node with parent -1 never is
+ *           block_table: as pcf_chunk_tables left it
+ *   in/out  free_pages [n_free]: the list the chunk's pages were taken from, with nothing taken since.  The
+ *             pages that the branches do not need, in request order, become the list's next entries (its last
+ *             ones of those taken); entries before the new head are left as they are
+ *   out     path [max_rows]: row row_base[b] + i is the i-th node of request b's branch, -1 behind its last one
+ *           n_kept [n_reqs]: the branches' nodes; next_token [n_reqs]: the choice behind the last of them
+ *             (root_choice, or -1, where there is none)
+ *           seq_len_out [n_reqs]: tokens held before the chunk + n_kept; free_head_out [1]: the list's head.
+ *             Both may be the buffers pcf_chunk_tables moved on, which this call sets right
+ * tree_plan holds a counter that a call moves on: calls that may overlap need a plan each.  A parent out of its
+ * range (never kept) or a free list shorter than what was taken (nothing given back) raises
+ * PCF_ERR_DEVICE_BOUNDS; so does a plan of other dims, with nothing written.  One launch. */
+pcf_status pcf_tree_accept(const pcf_chunk_dims* dims, const int32_t* chunk_plan, int32_t* tree_plan,
+                           const int32_t* parent, const int32_t* draft, const int32_t* choice,
+                           const int32_t* root_choice, const int32_t* block_table, int32_t* free_pages, int32_t n_free,
+                           int32_t* path, int32_t* n_kept, int32_t* next_token, int32_t* seq_len_out,
+                           int32_t* free_head_out, void* stream);
+
+/* Moves the branches' keys and values together, in every layer: in each request the i-th node of its branch from
+ * slot s + path[i] to slot s + i (s tokens held before the chunk), bit for bit; its position there is the one
+ * page_pos gives.  k_pools, v_pools: host arrays of n_layers (1 .. 4096) device pointers, read before the call
+ * returns; the same pool twice is moved twice.  path and n_kept are pcf_tree_accept's, block_table as there.  An
+ * entry of path below its place or not a node, a number kept beyond the tree's nodes, or a page outside the pool
+ * raises PCF_ERR_DEVICE_BOUNDS, and what it names is not moved.  One launch for every 64 layers. */
+pcf_status pcf_tree_keep(const pcf_chunk_dims* dims, const int32_t* tree_plan, const int32_t* path,
+                         const int32_t* n_kept, const int32_t* block_table, int32_t n_layers, uint16_t* const* k_pools,
+                         uint16_t* const* v_pools, void* stream);
+
 /* Synchronizes `stream`, then reads and clears the device error word: PCF_OK,
  * PCF_ERR_DEVICE_TIMEOUT, PCF_ERR_DEVICE_BOUNDS or PCF_ERR_DEVICE_RANGE (the first error raised
  * since the last check; PCF_ERR_CUDA if the sync itself failed).  The rotated queries and keys

@@ -15,6 +15,11 @@ Going on from there, one token or a chunk of tokens at a time, with lengths that
   ``chunk_tables``    block tables, positions and slot map of the new tokens
   ``append_kv``       their keys and values into the pages
   ``chunk_attention`` attention from the new tokens over their requests' pages
+and where the new tokens are a drafted tree, of which the model keeps one branch:
+  ``tree_tables``     the nodes' positions and the nodes each goes on from
+  ``tree_attention``  attention from the nodes over their requests' pages and their own lines
+  ``tree_accept``     the branch that the model's choices confirm, the lengths behind it
+  ``tree_keep``       that branch's keys and values moved together, in every layer
 """
 from __future__ import annotations
 
@@ -29,7 +34,8 @@ from ._lib import PcfError  # noqa: F401
 __all__ = ["Layout", "CacheFusion", "PcfError", "k_from_percent", "rope_table", "score", "select_topk",
            "gather_rows", "fused_attention", "check_device_error", "load_library", "score_noalloc",
            "select_topn_global", "key_norms", "pack_anchor_pages", "prefetch_pool_pages",
-           "wait_limit_check", "score_layers", "ChunkLayout", "chunk_tables", "append_kv", "chunk_attention"]
+           "wait_limit_check", "score_layers", "ChunkLayout", "chunk_tables", "append_kv", "chunk_attention",
+           "DraftTree", "tree_tables", "tree_attention", "tree_accept", "tree_keep"]
 
 
 def load_library():
@@ -417,6 +423,15 @@ def _chunk_rope(L: ChunkLayout, t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+def _chunk_out(L: ChunkLayout, out: torch.Tensor, ws: torch.Tensor):
+    if out.dtype != torch.bfloat16 or not out.is_contiguous():
+        _need(out, torch.bfloat16, "out")
+    if out.shape != (L.max_rows, L.hq, L.d) or out.get_device() != L.index:
+        raise ValueError(f"out: expected [{L.max_rows}, {L.hq}, {L.d}] on {L.device}")
+    if ws.get_device() != L.index or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on {L.device}")
+
+
 def _chunk_call(L: ChunkLayout, fn: str, stream, *args):
     """The call on the layout's device, on that device's current stream unless one is named."""
     call = getattr(_lib.load(), fn)
@@ -468,16 +483,96 @@ def chunk_attention(layout: ChunkLayout, q, k_pool, v_pool, rope, out, ws, excl=
     no part.  ``ws`` sized by ``ChunkLayout.attention_workspace_bytes``."""
     L = layout
     qs = _chunk_rows(L, q, L.hq, "q")
-    if out.dtype != torch.bfloat16 or not out.is_contiguous():
-        _need(out, torch.bfloat16, "out")
-    if out.shape != (L.max_rows, L.hq, L.d) or out.get_device() != L.index:
-        raise ValueError(f"out: expected [{L.max_rows}, {L.hq}, {L.d}] on {L.device}")
-    if ws.get_device() != L.index or not ws.is_contiguous():
-        raise ValueError(f"ws: expected a contiguous tensor on {L.device}")
+    _chunk_out(L, out, ws)
     _chunk_call(L, "pcf_chunk_attention", stream, L.plan.data_ptr(), q.data_ptr(), qs, _chunk_pool(L, k_pool, "k_pool"),
                 _chunk_pool(L, v_pool, "v_pool"), L.block_table.data_ptr(), L.page_pos.data_ptr(),
                 _chunk_ints(L, excl, "excl", L.n_reqs * L.max_pages, torch.int16), L.row_pos.data_ptr(),
                 _chunk_rope(L, rope), out.data_ptr(), ws.data_ptr(), ws.nbytes)
+
+
+class DraftTree:
+    """Trees of drafted tokens on the rows of a ChunkLayout (``max_chunk`` at most 256 nodes a request), and what
+    the tree calls leave: ``row_pos`` [max_rows] and ``seen`` [max_rows, words] (the nodes' positions; bit u % 32
+    of word u // 32: the node is, or goes on from, node u), ``path`` [max_rows], ``n_kept`` and ``next_token``
+    [n_reqs] (the branch that is kept).  All are int32 tensors on the layout's device that stay where they are, so
+    that a captured step can be replayed; steps that may overlap need a DraftTree (and a ChunkLayout) each."""
+
+    def __init__(self, layout: ChunkLayout):
+        n = ctypes.c_int64(0)
+        _lib.check("pcf_tree_plan_words", _lib.load().pcf_tree_plan_words(layout.dims_ref, ctypes.byref(n)))
+        ints = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=layout.device)
+        self.layout = layout
+        self.row_pos = ints(layout.max_rows).fill_(-1)
+        self.seen = ints(layout.max_rows, (layout.max_chunk + 31) // 32)
+        self.path = ints(layout.max_rows).fill_(-1)
+        self.n_kept, self.next_token = ints(layout.n_reqs), ints(layout.n_reqs)
+        self.plan = ints(n.value)
+
+    def attention_workspace_bytes(self) -> int:
+        v = ctypes.c_size_t(0)
+        _lib.check("pcf_tree_attention_workspace_bytes", _lib.load().pcf_tree_attention_workspace_bytes(
+            self.layout.dims_ref, ctypes.byref(v)))
+        return int(v.value)
+
+
+def _tree_of(L: ChunkLayout, tree: DraftTree):
+    if tree.layout is not L:
+        raise ValueError("tree: made for another layout")
+
+
+def tree_tables(layout: ChunkLayout, tree: DraftTree, parent, stream=None):
+    """Positions and lines of the trees on the rows of the last ``chunk_tables``: ``parent`` [max_rows] int32, the
+    number (in its request) of the node each goes on from, -1 for the last token held."""
+    L = layout
+    _tree_of(L, tree)
+    _chunk_call(L, "pcf_tree_tables", stream, L.plan.data_ptr(), _chunk_ints(L, parent, "parent", L.max_rows),
+                tree.row_pos.data_ptr(), tree.seen.data_ptr(), tree.plan.data_ptr())
+
+
+def tree_attention(layout: ChunkLayout, tree: DraftTree, q, k_pool, v_pool, rope, out, ws, excl=None, stream=None):
+    """Attention of the nodes ([max_rows, hq, d], rows may be strided) over their requests' pages and over the
+    nodes each goes on from, into ``out``; the nodes' keys are in their slots (``append_kv`` without ``row_pos``).
+    ``excl`` as in ``chunk_attention``; ``ws`` sized by ``DraftTree.attention_workspace_bytes``."""
+    L = layout
+    _tree_of(L, tree)
+    qs = _chunk_rows(L, q, L.hq, "q")
+    _chunk_out(L, out, ws)
+    _chunk_call(L, "pcf_tree_attention", stream, tree.plan.data_ptr(), q.data_ptr(), qs, _chunk_pool(L, k_pool, "k_pool"),
+                _chunk_pool(L, v_pool, "v_pool"), L.block_table.data_ptr(), L.page_pos.data_ptr(),
+                _chunk_ints(L, excl, "excl", L.n_reqs * L.max_pages, torch.int16), tree.row_pos.data_ptr(),
+                tree.seen.data_ptr(), _chunk_rope(L, rope), out.data_ptr(), ws.data_ptr(), ws.nbytes)
+
+
+def tree_accept(layout: ChunkLayout, tree: DraftTree, parent, draft, choice, free_pages, seq_len_out, free_head_out,
+                root_choice=None, stream=None):
+    """The branch of every tree whose tokens (``draft`` [max_rows]) are the model's choices: ``choice`` [max_rows]
+    behind each node, ``root_choice`` [n_reqs] behind the tokens held (None: every request's first node is that
+    token already).  Fills ``tree.path``, ``tree.n_kept`` and ``tree.next_token``, sets ``seq_len_out`` and
+    ``free_head_out`` to the requests with only their branches, and puts the pages these leave unused back into
+    ``free_pages``, the list ``chunk_tables`` took them from."""
+    L = layout
+    _tree_of(L, tree)
+    n, rows = L.n_reqs, L.max_rows
+    _chunk_call(L, "pcf_tree_accept", stream, L.plan.data_ptr(), tree.plan.data_ptr(),
+                _chunk_ints(L, parent, "parent", rows), _chunk_ints(L, draft, "draft", rows),
+                _chunk_ints(L, choice, "choice", rows), _chunk_ints(L, root_choice, "root_choice", n),
+                L.block_table.data_ptr(), _chunk_ints(L, free_pages, "free_pages"), free_pages.numel(),
+                tree.path.data_ptr(), tree.n_kept.data_ptr(), tree.next_token.data_ptr(),
+                _chunk_ints(L, seq_len_out, "seq_len_out", n), _chunk_ints(L, free_head_out, "free_head_out", 1))
+
+
+def tree_keep(layout: ChunkLayout, tree: DraftTree, k_pools, v_pools, stream=None):
+    """Move the kept branches' keys and values into the slots behind the tokens held, in every layer: ``k_pools``
+    and ``v_pools`` are lists of the layers' pools."""
+    L = layout
+    _tree_of(L, tree)
+    if len(k_pools) != len(v_pools) or not len(k_pools):
+        raise ValueError("k_pools and v_pools: one pool per layer, at least one layer")
+    n = len(k_pools)
+    kp = (ctypes.c_void_p * n)(*[_chunk_pool(L, t, "k_pools") for t in k_pools])
+    vp = (ctypes.c_void_p * n)(*[_chunk_pool(L, t, "v_pools") for t in v_pools])
+    _chunk_call(L, "pcf_tree_keep", stream, tree.plan.data_ptr(), tree.path.data_ptr(), tree.n_kept.data_ptr(),
+                L.block_table.data_ptr(), n, kp, vp)
 
 
 def wait_limit_check(limit_cycles: int, flag, stream=None):

@@ -34,7 +34,8 @@ EXPORTS = (
     "pcf_wait_limit_check", "pcf_score_layers", "pcf_fused_attention_paged",
     "pcf_attention_paged_workspace_bytes", "pcf_score_paged", "pcf_score_paged_workspace_bytes",
     "pcf_chunk_plan_words", "pcf_chunk_tables", "pcf_append_kv", "pcf_chunk_attention_workspace_bytes",
-    "pcf_chunk_attention",
+    "pcf_chunk_attention", "pcf_tree_plan_words", "pcf_tree_tables", "pcf_tree_attention_workspace_bytes",
+    "pcf_tree_attention", "pcf_tree_accept", "pcf_tree_keep",
 )
 
 
@@ -131,6 +132,18 @@ def _declare(lib):
     lib.pcf_append_kv.argtypes = [P(ChunkDims), c_void_p, c_int64, c_void_p, c_int64] + [c_void_p] * 7
     lib.pcf_chunk_attention.restype = c_int32
     lib.pcf_chunk_attention.argtypes = ([P(ChunkDims), c_void_p, c_void_p, c_int64] + [c_void_p] * 9 + [c_size_t, c_void_p])
+    lib.pcf_tree_plan_words.restype = c_int32
+    lib.pcf_tree_plan_words.argtypes = [P(ChunkDims), P(c_int64)]
+    lib.pcf_tree_tables.restype = c_int32
+    lib.pcf_tree_tables.argtypes = [P(ChunkDims)] + [c_void_p] * 6
+    lib.pcf_tree_attention_workspace_bytes.restype = c_int32
+    lib.pcf_tree_attention_workspace_bytes.argtypes = [P(ChunkDims), P(c_size_t)]
+    lib.pcf_tree_attention.restype = c_int32
+    lib.pcf_tree_attention.argtypes = [P(ChunkDims), c_void_p, c_void_p, c_int64] + [c_void_p] * 10 + [c_size_t, c_void_p]
+    lib.pcf_tree_accept.restype = c_int32
+    lib.pcf_tree_accept.argtypes = [P(ChunkDims)] + [c_void_p] * 8 + [c_int32] + [c_void_p] * 6
+    lib.pcf_tree_keep.restype = c_int32
+    lib.pcf_tree_keep.argtypes = [P(ChunkDims)] + [c_void_p] * 4 + [c_int32] + [c_void_p] * 3
     lib.pcf_copy_async.restype = c_int32
     lib.pcf_copy_async.argtypes = [c_int32, c_void_p, c_void_p, c_void_p, c_void_p]
 

@@ -1,0 +1,337 @@
+// Trees of drafted tokens: each node's position and the nodes it goes on from, the branch that the
+// model's choices confirm, and the move of that branch's keys and values.
+//
+// Node t of request b is row row_base[b] + t of the chunk and sits in slot seq + t; parent[t] < t is the
+// node it goes on from, -1 the last token held.
+#pragma once
+#include "kernel_chunk_tables.cuh"
+#include "ptx.cuh"
+#include "tree_format.h"
+
+namespace pcf {
+
+// ------------------------------------------------------------------ tables
+struct TreeTablesParams {
+    const int32_t* chunk;      // plan of the chunk
+    const int32_t* parent;     // [max_rows]
+    int32_t* row_pos;          // [max_rows]
+    uint32_t* seen;            // [max_rows][words]
+    int32_t* plan;
+    int32_t n, max_rows, words, hkv, g, blocks, chunk_tag, tag;
+};
+
+constexpr int kTreeWarps = 8;
+constexpr int kTreeThreads = kTreeWarps * 32;
+
+// Block 0 copies the lengths, scans the requests' weights and writes every block's share of the
+// attention; the others take a request a warp.
+// A warp takes its tree 32 nodes at a time.  Inside the 32 a node's line goes back by pointer doubling
+// over lanes: after step i it reaches 2^i nodes back, five steps reach any (parents come first).  The
+// first node of a line inside the 32 has its parent among the 32s before, whose bits are complete: a
+// copy of those and the line's own word make the node's bits, whatever the depth.
+__global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTablesParams p) {
+    extern __shared__ int32_t s_words[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dep_wait();
+    grid_dep_launch();
+    const bool fits = p.chunk[C_TAG] == p.chunk_tag;
+    const int32_t rows = fits ? p.chunk[C_ROWS] : 0;
+    const int32_t* seq = p.chunk + plan_array(CA_SEQ, p.n);
+    const int32_t* add = p.chunk + plan_array(CA_NEW, p.n);
+    const int32_t* base = p.chunk + plan_array(CA_ROW, p.n);
+    if (blockIdx.x == 0) {
+        __shared__ int s_warp[kTreeWarps];
+        int32_t* s_work = s_words;                     // [n + 1] weight of the requests before
+        if (tid == 0 && !fits) set_dev_error(kDevErrBounds);
+        const int per = (p.n + kTreeThreads - 1) / kTreeThreads;
+        const int b0 = min(p.n, tid * per), b1 = min(p.n, b0 + per);
+        auto weight = [&](int b) {
+            const int32_t n = fits ? add[b] : 0;
+            if (n == 0) return 0;
+            const int64_t w = (int64_t)(tree_units(seq[b] + n) + kTreeRunWeight) * tree_pairs(n, p.g) * p.hkv;
+            return (int)min(w, (int64_t)kSumLimit);
+        };
+        int sum = 0;
+        for (int b = b0; b < b1; ++b) sum = sat_add(sum, weight(b));
+        int x = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x = sat_add(x, y);
+        }
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int w = 0; w < kTreeWarps; ++w) {
+            if (w < warp) before = sat_add(before, s_warp[w]);
+            all = sat_add(all, s_warp[w]);
+        }
+        // (more work than the shares can number: none of it is done)
+        const bool too_much = all >= kSumLimit;
+        if (too_much && tid == 0) set_dev_error(kDevErrBounds);
+        before += x - sum;
+        for (int b = b0; b < b1; ++b) {
+            s_work[b] = too_much ? 0 : before;
+            before = sat_add(before, weight(b));
+        }
+        if (too_much) all = 0;
+        if (tid == 0) s_work[p.n] = all;
+        __syncthreads();
+        for (int b = tid; b <= p.n; b += kTreeThreads) {
+            p.plan[tree_array(TA_SEQ, p.n) + b] = b < p.n && fits ? seq[b] : 0;
+            p.plan[tree_array(TA_NEW, p.n) + b] = b < p.n && fits ? add[b] : 0;
+            p.plan[tree_array(TA_ROW, p.n) + b] = fits ? base[b] : 0;
+            p.plan[tree_array(TA_WORK, p.n) + b] = s_work[b];
+        }
+        if (tid == 0) *reinterpret_cast<int4*>(p.plan) = make_int4(p.tag, too_much ? 0 : rows, 0, 0);   // T_TAG, T_ROWS, T_DONE
+        const Deal deal(all, p.blocks);
+        for (int w = tid; w < p.blocks; w += kTreeThreads) {
+            const int32_t u0 = deal.first(w);
+            int4 e = make_int4(0, 0, 0, 0), f = make_int4(deal.first(w + 1) - u0, p.tag, 0, 0);
+            if (f.x > 0) {
+                const int b = row_request(s_work, p.n, u0);
+                const int32_t pairs = tree_pairs(add[b], p.g), run = tree_units(seq[b] + add[b]) + kTreeRunWeight;
+                const int32_t local = u0 - s_work[b], r = local / run, at = local - r * run;
+                e = make_int4(b, r / pairs, r % pairs, max(0, at - kTreeRunWeight));
+                f.z = max(0, kTreeRunWeight - at);
+            }
+            int4* dst = reinterpret_cast<int4*>(p.plan + tree_shares(p.n)) + 2 * w;
+            dst[0] = e;
+            dst[1] = f;
+        }
+        return;
+    }
+    const int words = p.words;
+    uint32_t* s_bits = reinterpret_cast<uint32_t*>(s_words) + warp * 32 * words * (words + 1);   // [node][word]
+    int32_t* s_depth = reinterpret_cast<int32_t*>(s_bits + 32 * words * words);                  // [node]
+    bool bad = false;
+    for (int b = (blockIdx.x - 1) * kTreeWarps + warp; b < p.n && fits; b += (gridDim.x - 1) * kTreeWarps) {
+        const int32_t n = add[b], first = base[b], pos0 = p.chunk[plan_array(CA_START, p.n) + b];
+        for (int k = 0; 32 * k < n; ++k) {
+            const int t = 32 * k + lane;
+            int32_t up = -1;
+            if (t < n) {
+                up = p.parent[first + t];
+                if (up < -1 || up >= t) {
+                    bad = true;
+                    up = -1;
+                }
+            }
+            // the line inside these 32: its nodes, the lane it has reached
+            uint32_t line = 1u << lane;
+            int at = up >= 32 * k ? up - 32 * k : lane;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                line |= __shfl_sync(0xffffffffu, line, at);
+                at = __shfl_sync(0xffffffffu, at, at);
+            }
+            const int32_t out = __shfl_sync(0xffffffffu, up, at);      // (of the line's first node here)
+            const int32_t depth = __popc(line) + (out >= 0 ? s_depth[out] : 0);
+            if (t < n) {
+                s_depth[t] = depth;
+                uint32_t* dst = p.seen + (int64_t)(first + t) * words;
+                p.row_pos[first + t] = pos0 + depth - 1;
+                for (int w = 0; w < words; ++w) {
+                    const uint32_t v = w == k ? line : w < k && out >= 0 ? s_bits[out * words + w] : 0u;
+                    s_bits[t * words + w] = v;
+                    dst[w] = v;
+                }
+            }
+            __syncwarp();
+        }
+        __syncwarp();
+    }
+    if (bad) set_dev_error(kDevErrBounds);
+    for (int64_t r = rows + (int64_t)(blockIdx.x - 1) * kTreeThreads + tid; r < p.max_rows; r += (int64_t)(gridDim.x - 1) * kTreeThreads) {
+        p.row_pos[r] = -1;
+        for (int w = 0; w < words; ++w) p.seen[r * words + w] = 0;
+    }
+}
+
+// A plan made for other dims (or by no pcf_tree_tables call at all) is refused.
+__device__ __forceinline__ bool tree_fits(const int32_t* plan, int32_t tag) {
+    const bool ok = plan[T_TAG] == tag;
+    if (!ok) set_dev_error(kDevErrBounds);
+    return ok;
+}
+
+// ------------------------------------------------------------------ accept
+struct TreeAcceptParams {
+    const int32_t* chunk;
+    int32_t* plan;
+    const int32_t* parent;     // [max_rows]
+    const int32_t* draft;      // [max_rows] the nodes' tokens
+    const int32_t* choice;     // [max_rows] the model's token behind each node
+    const int32_t* root;       // [n] the model's token behind the held ones, or null: node 0 is kept
+    const int32_t* block_table;
+    int32_t* free_pages;
+    int32_t* path;             // [max_rows]
+    int32_t* kept;             // [n]
+    int32_t* next;             // [n]
+    int32_t* seq_out;          // [n]
+    int32_t* head_out;         // [1]
+    int32_t n, max_rows, max_pages, n_free, chunk_tag, tag;
+};
+
+// A warp walks a request: lane l holds nodes l, l + 32, ..., of each its parent where its token is what the
+// model chose behind that parent; a step is a ballot for the lowest node whose parent is where the branch
+// stands (siblings with the same token: the first one).  The block that is done last scans the pages that
+// the branches need and gives the others back: taken pages lie in the free list in request order, so what
+// is needed stays in front and the rest, in the same order, becomes the list's next entries.
+__global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcceptParams p) {
+    __shared__ int s_last, s_warp[kTreeWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dep_wait();
+    grid_dep_launch();
+    if (p.chunk[C_TAG] != p.chunk_tag || p.plan[T_TAG] != p.tag) {
+        if (tid == 0) set_dev_error(kDevErrBounds);
+        return;
+    }
+    const int32_t rows = p.chunk[C_ROWS], head = p.chunk[C_HEAD], taken = p.chunk[C_TAKEN];
+    const int32_t* seq = p.chunk + plan_array(CA_SEQ, p.n);
+    const int32_t* add = p.chunk + plan_array(CA_NEW, p.n);
+    const int32_t* base = p.chunk + plan_array(CA_ROW, p.n);
+    const int32_t* take = p.chunk + plan_array(CA_TAKE, p.n);
+    bool bad = false;
+    for (int b = blockIdx.x * kTreeWarps + warp; b < p.n; b += gridDim.x * kTreeWarps) {
+        const int32_t n = add[b], first = base[b];
+        const int32_t* choice = p.choice + first;
+        const int32_t root = p.root ? p.root[b] : -1;
+        int32_t up[kTreeMaxWords];                  // -2: not on any branch
+#pragma unroll
+        for (int k = 0; k < kTreeMaxWords; ++k) {
+            const int t = 32 * k + lane;
+            up[k] = -2;
+            if (32 * k < n && t < n) {
+                const int32_t at = p.parent[first + t];
+                if (at < -1 || at >= t) bad = true;
+                else if (at >= 0 ? p.draft[first + t] == choice[at] : p.root ? p.draft[first + t] == root : t == 0) up[k] = at;
+            }
+        }
+        int32_t at = -1, count = 0;
+        while (true) {
+            int32_t to = -1;
+#pragma unroll
+            for (int k = 0; k < kTreeMaxWords; ++k) {
+                if (32 * k < n && to < 0) {
+                    const uint32_t hit = __ballot_sync(0xffffffffu, up[k] == at);
+                    if (hit) to = 32 * k + __ffs(hit) - 1;
+                }
+            }
+            if (to < 0) break;
+            at = to;
+            if (lane == 0) p.path[first + count] = at;
+            ++count;
+        }
+        for (int i = count + lane; i < n; i += 32) p.path[first + i] = -1;
+        if (lane == 0) {
+            p.kept[b] = count;
+            p.next[b] = count > 0 ? choice[at] : root;
+            p.seq_out[b] = seq[b] + count;
+        }
+    }
+    if (bad) set_dev_error(kDevErrBounds);
+    for (int64_t r = rows + (int64_t)blockIdx.x * kTreeThreads + tid; r < p.max_rows; r += (int64_t)gridDim.x * kTreeThreads)
+        p.path[r] = -1;
+    __syncthreads();
+    if (tid == 0) s_last = atomic_inc_acq_rel_gpu(p.plan + T_DONE, gridDim.x - 1) == (int)gridDim.x - 1;
+    __syncthreads();
+    if (!s_last) return;
+    const int per = (p.n + kTreeThreads - 1) / kTreeThreads;
+    const int b0 = min(p.n, tid * per), b1 = min(p.n, b0 + per);
+    auto need = [&](int b) { return pages_of(seq[b] + __ldcg(p.kept + b)) - pages_of(seq[b]); };
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += add[b] > 0 ? need(b) : 0;
+    int x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    int before = x - sum, all = 0;
+    for (int w = 0; w < kTreeWarps; ++w) {
+        if (w < warp) before += s_warp[w];
+        all += s_warp[w];
+    }
+    if (tid == 0) p.head_out[0] = head + all;
+    if (head < 0 || taken < 0 || head > p.n_free - taken) {      // (another list than the chunk's)
+        if (tid == 0) set_dev_error(kDevErrBounds);
+        return;
+    }
+    for (int b = b0; b < b1; ++b) {
+        if (add[b] == 0) continue;
+        const int32_t k = need(b), back = take[b + 1] - take[b] - k;
+        const int32_t* from = p.block_table + (int64_t)b * p.max_pages + pages_of(seq[b]) + k;
+        int32_t* to = p.free_pages + head + all + take[b] - before;
+        for (int i = 0; i < back; ++i) to[i] = from[i];
+        before += k;
+    }
+}
+
+// ------------------------------------------------------------------ keep
+constexpr int kKeepLayers = 64;     // layers of one launch (their pools' addresses are its arguments)
+struct TreeKeepParams {
+    const int32_t* plan;
+    const int32_t* path;
+    const int32_t* kept;
+    const int32_t* block_table;
+    int32_t n, max_pages, hkv, n_phys, layers, tag;
+    uint4* pools[2 * kKeepLayers];  // keys and values of every layer
+};
+
+// The i-th node of the branch moves from slot seq + path[i] to slot seq + i.  path[i] >= i rises, so a slot
+// that is written is never one that a later i reads: a thread takes one 16-byte column of a head and goes
+// through the branch in order, eight loads in flight, and needs no other thread.
+template <int D>
+__global__ void __launch_bounds__(256) tree_keep_kernel(const __grid_constant__ TreeKeepParams p) {
+    constexpr int CH = D / 8;
+    grid_dep_wait();
+    grid_dep_launch();
+    if (!tree_fits(p.plan, p.tag)) return;
+    const int b = blockIdx.x;
+    const int32_t seq = p.plan[tree_array(TA_SEQ, p.n) + b], add = p.plan[tree_array(TA_NEW, p.n) + b];
+    const int32_t first = p.plan[tree_array(TA_ROW, p.n) + b];
+    if (add == 0) return;
+    const int32_t count = p.kept[b];
+    if (count < 0 || count > add) {
+        set_dev_error(kDevErrBounds);
+        return;
+    }
+    const int32_t* table = p.block_table + (int64_t)b * p.max_pages;
+    auto slot = [&](int32_t s, int64_t& at) {            // row of a slot in the pool, head 0
+        const int32_t ph = table[s / kPage];
+        at = (int64_t)ph * p.hkv * kPage + s % kPage;
+        return ph >= 0 && ph < p.n_phys;
+    };
+    for (int c = threadIdx.x; c < p.hkv * CH; c += blockDim.x) {
+        uint4* pool = p.pools[blockIdx.y] + (int64_t)(c / CH) * kPage * CH + c % CH;
+        for (int32_t i0 = 0; i0 < count; i0 += 8) {
+            uint4 v[8];
+            int64_t dst[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dst[i] = -1;
+                if (i0 + i < count) {
+                    const int32_t t = p.path[first + i0 + i];
+                    int64_t from, to;
+                    if (t < i0 + i || t >= add) set_dev_error(kDevErrBounds);
+                    else if (t > i0 + i) {
+                        if (slot(seq + t, from) && slot(seq + i0 + i, to)) {
+                            v[i] = pool[from * CH];
+                            dst[i] = to * CH;
+                        } else {
+                            set_dev_error(kDevErrBounds);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (dst[i] >= 0) pool[dst[i]] = v[i];
+        }
+    }
+}
+
+}  // namespace pcf

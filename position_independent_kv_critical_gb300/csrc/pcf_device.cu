@@ -18,8 +18,11 @@
 #include "kernel_few_rows.cuh"
 #include "kernel_many_rows.cuh"
 #include "kernel_imp.cuh"
+#include "kernel_tree.cuh"
+#include "kernel_tree_tables.cuh"
 #include "kernels_simple.cuh"
 #include "layout_format.h"
+#include "tree_format.h"
 
 using namespace pcf;
 
@@ -1135,4 +1138,118 @@ extern "C" pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, int32_t* p
     const ChunkCall c{dims, plan, q, q_row_stride, k_pool, v_pool, block_table, page_pos, excl, row_pos, rope, out,
                       static_cast<uint8_t*>(ws)};
     return dims->head_dim == 128 ? chunk_attention_impl<128>(c, st) : chunk_attention_impl<64>(c, st);
+}
+
+// ------------------------------------------------------------------ trees of drafted tokens
+namespace {
+bool words_aligned(std::initializer_list<const void*> list) {
+    for (const void* w : list)
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return false;
+    return true;
+}
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+}  // namespace
+
+extern "C" pcf_status pcf_tree_tables(const pcf_chunk_dims* dims, const int32_t* chunk_plan, const int32_t* parent,
+                                      int32_t* row_pos, int32_t* seen, int32_t* tree_plan, void* stream) {
+    pcf_status s = check_tree_dims(dims);
+    if (s != PCF_OK) return s;
+    if (!chunk_plan || !parent || !row_pos || !seen || !tree_plan) return PCF_ERR_INVALID_ARG;
+    if (!words_aligned({chunk_plan, parent, row_pos, seen}) || !aligned16(tree_plan)) return PCF_ERR_INVALID_ARG;
+    if ((s = check_device()) != PCF_OK) return s;
+    const int32_t words = tree_words(dims);
+    const TreeTablesParams p{chunk_plan, parent, row_pos, reinterpret_cast<uint32_t*>(seen), tree_plan, dims->n_reqs,
+                             dims->max_rows, words, dims->n_kv_heads, dims->n_q_heads / dims->n_kv_heads,
+                             chunk_sms(dims->n_sms), plan_tag(dims), tree_tag(dims)};
+    const int smem = 4 * std::max(dims->n_reqs + 1, kTreeWarps * 32 * words * (words + 1));
+    if ((s = set_smem(tree_tables_kernel, smem)) != PCF_OK) return s;
+    const int blocks = std::min((dims->n_reqs + kTreeWarps - 1) / kTreeWarps, device_sms() - 1);
+    return launch(tree_tables_kernel, dim3(1 + std::max(1, blocks)), dim3(kTreeThreads), smem,
+                  static_cast<cudaStream_t>(stream), p);
+}
+
+extern "C" pcf_status pcf_tree_attention(const pcf_chunk_dims* dims, const int32_t* tree_plan, const uint16_t* q,
+                                         int64_t q_row_stride, const uint16_t* k_pool, const uint16_t* v_pool,
+                                         const int32_t* block_table, const int32_t* page_pos, const uint16_t* excl,
+                                         const int32_t* row_pos, const int32_t* seen, const float* rope, uint16_t* out,
+                                         void* ws, size_t ws_bytes, void* stream) {
+    pcf_status s = check_tree_dims(dims);
+    if (s != PCF_OK) return s;
+    if (!tree_plan || !q || !k_pool || !v_pool || !block_table || !page_pos || !row_pos || !seen || !rope || !out || !ws)
+        return PCF_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)dims->n_q_heads * dims->head_dim;
+    if (q_row_stride < row || q_row_stride % 8 != 0) return PCF_ERR_INVALID_ARG;
+    for (const void* a : {(const void*)tree_plan, (const void*)q, (const void*)k_pool, (const void*)v_pool,
+                          (const void*)rope, (const void*)out, (const void*)ws})
+        if (!aligned16(a)) return PCF_ERR_INVALID_ARG;
+    if (!words_aligned({block_table, page_pos, row_pos, seen}) || (reinterpret_cast<uintptr_t>(excl) & 1u))
+        return PCF_ERR_INVALID_ARG;
+    // (a row is read by several blocks, some of them behind the write of its result)
+    if (overlap(q, 2 * (size_t)((dims->max_rows - 1) * q_row_stride + row), out, 2 * (size_t)dims->max_rows * row))
+        return PCF_ERR_INVALID_ARG;
+    if (ws_bytes < tree_ws(dims).total) return PCF_ERR_WORKSPACE_TOO_SMALL;
+    if ((s = check_device()) != PCF_OK) return s;
+    const TreeParams p{tree_plan, reinterpret_cast<const __nv_bfloat16*>(q),
+                       reinterpret_cast<const __nv_bfloat16*>(k_pool), reinterpret_cast<const __nv_bfloat16*>(v_pool),
+                       block_table, page_pos, excl, row_pos, reinterpret_cast<const uint32_t*>(seen), rope,
+                       reinterpret_cast<__nv_bfloat16*>(out), q_row_stride, dims->n_reqs, dims->max_pages,
+                       dims->max_rows, tree_words(dims), dims->n_q_heads, dims->n_kv_heads, dims->n_phys_pages,
+                       dims->max_pos, tree_tag(dims)};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned blocks = (unsigned)(((int64_t)dims->max_rows * dims->n_q_heads + 3) / 4);
+    return dims->head_dim == 128 ? launch(tree_simple_kernel<128>, dim3(blocks), dim3(128), 0, st, p)
+                                 : launch(tree_simple_kernel<64>, dim3(blocks), dim3(128), 0, st, p);
+}
+
+extern "C" pcf_status pcf_tree_accept(const pcf_chunk_dims* dims, const int32_t* chunk_plan, int32_t* tree_plan,
+                                      const int32_t* parent, const int32_t* draft, const int32_t* choice,
+                                      const int32_t* root_choice, const int32_t* block_table, int32_t* free_pages,
+                                      int32_t n_free, int32_t* path, int32_t* n_kept, int32_t* next_token,
+                                      int32_t* seq_len_out, int32_t* free_head_out, void* stream) {
+    pcf_status s = check_tree_dims(dims);
+    if (s != PCF_OK) return s;
+    if (!chunk_plan || !tree_plan || !parent || !draft || !choice || !block_table || n_free < 0 ||
+        (n_free > 0 && !free_pages) || !path || !n_kept || !next_token || !seq_len_out || !free_head_out)
+        return PCF_ERR_INVALID_ARG;
+    if (!words_aligned({chunk_plan, parent, draft, choice, root_choice, block_table, free_pages, path, n_kept, next_token,
+                        seq_len_out, free_head_out}) ||
+        !aligned16(tree_plan))
+        return PCF_ERR_INVALID_ARG;
+    if ((s = check_device()) != PCF_OK) return s;
+    const TreeAcceptParams p{chunk_plan, tree_plan, parent, draft, choice, root_choice, block_table, free_pages, path,
+                             n_kept, next_token, seq_len_out, free_head_out, dims->n_reqs, dims->max_rows,
+                             dims->max_pages, n_free, plan_tag(dims), tree_tag(dims)};
+    const int blocks = std::min((dims->n_reqs + kTreeWarps - 1) / kTreeWarps, device_sms());
+    return launch(tree_accept_kernel, dim3(blocks), dim3(kTreeThreads), 0, static_cast<cudaStream_t>(stream), p);
+}
+
+extern "C" pcf_status pcf_tree_keep(const pcf_chunk_dims* dims, const int32_t* tree_plan, const int32_t* path,
+                                    const int32_t* n_kept, const int32_t* block_table, int32_t n_layers,
+                                    uint16_t* const* k_pools, uint16_t* const* v_pools, void* stream) {
+    pcf_status s = check_tree_dims(dims);
+    if (s != PCF_OK) return s;
+    if (!tree_plan || !path || !n_kept || !block_table || n_layers < 1 || n_layers > 4096 || !k_pools || !v_pools)
+        return PCF_ERR_INVALID_ARG;
+    for (int32_t l = 0; l < n_layers; ++l)
+        if (!k_pools[l] || !v_pools[l] || !aligned16(k_pools[l]) || !aligned16(v_pools[l])) return PCF_ERR_INVALID_ARG;
+    if (!words_aligned({path, n_kept, block_table}) || !aligned16(tree_plan)) return PCF_ERR_INVALID_ARG;
+    if ((s = check_device()) != PCF_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    for (int32_t l0 = 0; l0 < n_layers; l0 += kKeepLayers) {
+        TreeKeepParams p{tree_plan, path, n_kept, block_table, dims->n_reqs, dims->max_pages, dims->n_kv_heads,
+                         dims->n_phys_pages, std::min(kKeepLayers, n_layers - l0), tree_tag(dims), {}};
+        for (int32_t i = 0; i < p.layers; ++i) {
+            p.pools[2 * i] = reinterpret_cast<uint4*>(k_pools[l0 + i]);
+            p.pools[2 * i + 1] = reinterpret_cast<uint4*>(v_pools[l0 + i]);
+        }
+        const dim3 grid(dims->n_reqs, 2 * p.layers);
+        const dim3 threads(std::min(256, (dims->n_kv_heads * dims->head_dim / 8 + 31) / 32 * 32));
+        s = dims->head_dim == 128 ? launch(tree_keep_kernel<128>, grid, threads, 0, st, p)
+                                  : launch(tree_keep_kernel<64>, grid, threads, 0, st, p);
+        if (s != PCF_OK) return s;
+    }
+    return PCF_OK;
 }

@@ -14,6 +14,7 @@
 #include "../../include/pcf.h"
 #include "chunk_format.h"
 #include "layout_format.h"
+#include "tree_format.h"
 
 using namespace pcf;
 
@@ -21,7 +22,7 @@ extern "C" const char* pcf_status_string(pcf_status s) {
     switch (s) {
         case PCF_OK: return "ok";
         case PCF_ERR_INVALID_ARG: return "invalid argument";
-        case PCF_ERR_UNSUPPORTED: return "unsupported shape (head_dim must be 64 or 128; Hq/Hkv must divide 128)";
+        case PCF_ERR_UNSUPPORTED: return "unsupported shape (head_dim must be 64 or 128; Hq/Hkv must divide 128; a tree has at most 256 nodes)";
         case PCF_ERR_CUDA: return "CUDA call failed";
         case PCF_ERR_DEVICE_TIMEOUT: return "a kernel's bounded wait ran out";
         case PCF_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
@@ -541,5 +542,21 @@ extern "C" pcf_status pcf_chunk_attention_workspace_bytes(const pcf_chunk_dims* 
     if (s != PCF_OK) return s;
     if (!bytes) return PCF_ERR_INVALID_ARG;
     *bytes = chunk_ws(dims).total;
+    return PCF_OK;
+}
+
+extern "C" pcf_status pcf_tree_plan_words(const pcf_chunk_dims* dims, int64_t* n_words) {
+    const pcf_status s = check_tree_dims(dims);
+    if (s != PCF_OK) return s;
+    if (!n_words) return PCF_ERR_INVALID_ARG;
+    *n_words = tree_plan_words(dims->n_reqs, chunk_sms(dims->n_sms));
+    return PCF_OK;
+}
+
+extern "C" pcf_status pcf_tree_attention_workspace_bytes(const pcf_chunk_dims* dims, size_t* bytes) {
+    const pcf_status s = check_tree_dims(dims);
+    if (s != PCF_OK) return s;
+    if (!bytes) return PCF_ERR_INVALID_ARG;
+    *bytes = tree_ws(dims).total;
     return PCF_OK;
 }
