@@ -288,8 +288,9 @@ def _own_prepare(s):
     s["seq_out"], s["head_out"] = torch.zeros_like(s["seq"]), torch.zeros_like(s["head"])
     pcf.chunk_tables(L, s["seq"], s["new"], s["free"], s["head"], s["seq_out"], s["head_out"], next_pos=s["start"])
     s["first_of"] = s.get("first") if case.get("roots") else None
-    if op == "attention":
+    if op != "tables":
         pcf.tree_tables(L, tree, s["parent"])
+    if op == "attention":
         s["rope"] = pcf.rope_table(case["d"], s["theta"], s["max_pos"]).to(DEV)
         s["out"] = torch.zeros((max(1, s["rows"]), case["hq"], case["d"]), dtype=torch.bfloat16, device=DEV)
         s["ws"] = torch.empty(max(16, tree.attention_workspace_bytes()), dtype=torch.uint8, device=DEV)
