@@ -5,7 +5,27 @@
 //   out = sum_j softmax_j((R_pos(i) q) . (R_pos(j) k_j) / sqrt(d)) v_j,
 // pos(j) = page_pos + r for a held slot and the node's own position for a node's; a row with no slot left
 // gives zeros.
+//
+// A tree has a few to a few hundred rows a kv head, so a key meets 8 to 256 of them: HBM and the tensor
+// cores bound it about alike at 256 rows (a unit of 64 keys and values, 32 KB at d = 128, takes an SM 1400
+// cycles at the copy rate and its four products of two row tiles 1280), HBM alone below.  So the keys are
+// rotated where they are used, in shared memory: no copy of them is written or read again.  One block an SM,
+// twenty warps; a run is one (request, kv head, row pair) or the part of one that a block has, dealt by
+// pcf_tree_tables in contiguous parts of equal weight.
+//   warps  0-7   softmax of chain 0 (warps 0-3) and 1: S row from TMEM, excluded slots and other branches
+//                hidden, online softmax (lazy rescale), P -> TMEM over the S columns, O epilogue
+//   warps  8-15  two groups of four, units in turn: a run's queries, then the keys, bf16 in, rotated fp16 out
+//   warp  16     runs in order; a unit's four pages of keys and of values (TMA), its hidden slots
+//   warp  17     Q K^T issue (and the TMEM allocation); warps 18, 19  P V issue of chain 0 and 1
+// With more than 128 rows the chains are the pair's two row tiles and both take every unit.  With up to 128
+// there is one tile, and the chains take its units in turn, each with sums of its own that meet in the
+// epilogue: eight softmax warps share what four would do, and a unit's way through the chain
+// (S -> softmax -> P -> P V -> next Q K^T) overlaps the other chain's.
+// TMEM: chain t's two S buffers at columns t*128 + {0, 64}, O of chain 0 at 256, of chain 1 at 384; P (bf16
+// pairs) overwrites the S it came from and is the A operand of O += P V.
 #pragma once
+#include "kernel_few_rows.cuh"
+#include "kernel_many_rows.cuh"
 #include "kernel_tree_tables.cuh"
 #include "ptx.cuh"
 #include "tree_format.h"
@@ -15,8 +35,6 @@ namespace pcf {
 struct TreeParams {
     const int32_t* plan;
     const __nv_bfloat16* q;
-    const __nv_bfloat16* k_pool;
-    const __nv_bfloat16* v_pool;
     const int32_t* block_table;
     const int32_t* page_pos;
     const uint16_t* excl;       // or null
@@ -24,82 +42,802 @@ struct TreeParams {
     const uint32_t* seen;       // [max_rows][words]
     const float* rope;
     __nv_bfloat16* out;
+    float* part_o;              // [blocks][2][256][D]
+    float2* part_ml;            // [blocks][2][256]
+    int4* desc;                 // [blocks][2]: a run begun here that goes on: {last block << 8 | 255, first node, kv head, 0},
+                                //   {nodes, first row, 0, 0}
     int64_t q_stride;
-    int32_t n, max_pages, max_rows, words, hq, hkv, n_phys, max_pos, tag;
+    int32_t n, max_pages, words, hq, hkv, n_phys, max_pos, blocks, tag;
 };
 
-// One warp a (row, query head), slot by slot: lane l has D / 64 pairs of dimensions that turn together.
+constexpr int kTreeAttnThreads = 640;
+constexpr int kTreeReaders = 19;    // warps that read a run: softmax, rotation, issuers
+
+// One run, or the part of one this block has, as warp 16 hands it to the others.
+struct TreeItem {
+    int32_t req;                // < 0: no more
+    int32_t kvh, pair;
+    int32_t jb, n_loc;          // its units
+    int32_t seq, add, row_base;
+    int32_t slot;               // partial result, or -1: the whole run
+    int32_t single;             // its rows fit one tile
+};
+
 template <int D>
-__global__ void __launch_bounds__(128) tree_simple_kernel(const TreeParams p) {
-    constexpr int N = D / 64;
+struct TreeSmem {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kQ = kTileRows * D * 2;
+    static constexpr int kUnit = kTreeUnit * D * 2;
+    static constexpr int kHalfUnit = kTreeUnit * 128;          // 64 rows of 64 elements
+    // (both even: a stage then belongs to units of one parity)
+    static constexpr int NK = D == 128 ? 4 : 8, NV = D == 128 ? 6 : 12;
+    // A unit's hidden slots and nothing else are read behind its key: by the softmax and the P V issuers,
+    // all done with unit u - NV when unit u's value is copied, that is before unit u + 1 is entered here.
+    static constexpr int kMeta = D == 128 ? 8 : 16;
+    static_assert(kMeta >= NV + 2, "a unit's entry lasts until its P V is done");
+    static constexpr int oK = 2 * kQ;
+    static constexpr int oV = oK + NK * kUnit;
+    static constexpr int oMl = oV + NV * kUnit;                // [128] chain 1's maximum and sum
+    static constexpr int oMeta = oMl + kTileRows * 8;          // [kMeta] 64 hidden bits
+    static constexpr int oItem = oMeta + kMeta * 8;
+    static constexpr int oBar = oItem + 2 * (int)sizeof(TreeItem);
+    // barriers
+    static constexpr int B_ITEM_FULL = 0, B_ITEM_EMPTY = 2, B_Q_FULL = 4, B_Q_EMPTY = 5, B_S_FULL = 6, B_P_FULL = 10,
+                         B_PV_DONE = 14, B_O_DONE = 18, B_O_FREE = 20, B_ML = 22, B_DRAIN = 23, B_K_RAW = 26,
+                         B_K_ROT = B_K_RAW + NK, B_K_EMPTY = B_K_ROT + NK, B_V_RAW = B_K_EMPTY + NK,
+                         B_V_CLEAN = B_V_RAW + NV, B_V_EMPTY = B_V_CLEAN + NV, kNumBars = B_V_EMPTY + NV;
+    static constexpr int oMisc = oBar + kNumBars * 8;          // TMEM address, abort flag
+    static constexpr int kBytes = oMisc + 16;
+    static constexpr int kAlloc = kBytes + 1024;
+    static_assert(oBar % 8 == 0 && kAlloc <= 232448, "more dynamic shared memory than a GB300 block can have");
+};
+
+// A wait sees the parity of a phase only, so a phase may end at most once before each of its waiters has
+// passed it.  What keeps each barrier to that:
+//   ITEM, K_ROT     every waiter passes every phase;
+//   K_RAW           a stage belongs to one rotating group (NK is even), which passes every phase of it;
+//   V_RAW, V_CLEAN  both P V issuers pass every phase (of dirty units' for V_CLEAN), a unit of the other chain
+//                   included;
+//   Q, S, P, PV_DONE, O_DONE, O_FREE   as in the many-row kernel: counted by the units and runs that a chain
+//                   takes part in; in a run of one tile the threads of chain 0 arrive on both O_FREE;
+//   ML              chain 1's sums of a run of one tile: written again only behind chain 1's next result, whose
+//                   first P V waited for O_FREE, on which chain 0's threads arrive when they have read them.
+
+// 16 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// odd + 0 x: NaN in a half of `odd` once that half of an x was not finite
+__device__ __forceinline__ uint32_t odd_f16x2(uint32_t x, uint32_t odd) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0), "r"(odd));
+    return r;
+}
+
+// Eight frequencies' cos and sin as packed pairs.
+struct Angles {
+    uint64_t C[4], S[4];
+    __device__ __forceinline__ void set(const float4 (&cs)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            C[e] = f2_pack(cs[e].x, cs[e].z);
+            S[e] = f2_pack(cs[e].y, cs[e].w);
+        }
+    }
+    // further by the angles of `by`, whose negated sines are `ns`
+    __device__ __forceinline__ void advance(const Angles& by, const uint64_t (&ns)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t c = f2_fma(S[e], ns[e], f2_mul(C[e], by.C[e]));
+            S[e] = f2_fma(C[e], by.S[e], f2_mul(S[e], by.C[e]));
+            C[e] = c;
+        }
+    }
+    // 16-byte chunks a and b (dimensions i.. and i + d/2 ..) turned, to fp16; `odd` tells whether they are finite
+    __device__ __forceinline__ void turn(uint4& a, uint4& b, uint32_t& odd) const {
+        const uint64_t minus = f2_pack(-1.f, -1.f);
+        const uint32_t ia[4] = {a.x, a.y, a.z, a.w}, ib[4] = {b.x, b.y, b.z, b.w};
+        uint32_t oa[4], ob[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t A = bf16x2_to_f2(ia[e]), B = bf16x2_to_f2(ib[e]);
+            float y0, y1, z0, z1;
+            f2_unpack(f2_fma(f2_mul(B, S[e]), minus, f2_mul(A, C[e])), y0, y1);   // a cos - b sin
+            f2_unpack(f2_fma(A, S[e], f2_mul(B, C[e])), z0, z1);                   // b cos + a sin
+            oa[e] = pack_f16x2_inf(y0, y1);
+            ob[e] = pack_f16x2_inf(z0, z1);
+            odd = odd_f16x2(ob[e], odd_f16x2(oa[e], odd));
+        }
+        a = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+        b = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+    }
+};
+
+// What a node sees of the 64 slots from slot `first` on, the held ones and those behind the tree included:
+// its bits (`words` of them at `seen`) from node u = first - seq on.
+__device__ __forceinline__ uint64_t tree_window(const uint32_t* seen, int words, int u) {
+    auto word = [&](int w) { return w >= 0 && w < words ? seen[w] : 0u; };
+    if (u >= 0) {
+        const int w = u >> 5, s = u & 31;
+        const uint32_t x = word(w), y = word(w + 1), z = word(w + 2);
+        return (uint64_t)__funnelshift_r(y, z, s) << 32 | __funnelshift_r(x, y, s);
+    }
+    const uint64_t x = (uint64_t)word(1) << 32 | word(0);      // (-64 < u: the slots before node 0 are held ones)
+    return x << -u | ((1ull << -u) - 1);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTreeAttnThreads, 1)
+tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
+    using SM = TreeSmem<D>;
+    constexpr int H = SM::kHalves, NK = SM::NK, NV = SM::NV, CP = D / 16;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::oBar);
+    int32_t* misc = reinterpret_cast<int32_t*>(smem + SM::oMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+    TreeItem* slots = reinterpret_cast<TreeItem*>(smem + SM::oItem);
+    uint2* s_meta = reinterpret_cast<uint2*>(smem + SM::oMeta);
+    float2* s_ml = reinterpret_cast<float2*>(smem + SM::oMl);
+    auto sK = [&](int st) { return smem + SM::oK + st * SM::kUnit; };
+    auto sV = [&](int st) { return smem + SM::oV + st * SM::kUnit; };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars[SM::B_ITEM_FULL + s], 1);
+            mbar_init(&bars[SM::B_ITEM_EMPTY + s], kTreeReaders);
+            mbar_init(&bars[SM::B_O_DONE + s], 1);
+            mbar_init(&bars[SM::B_O_FREE + s], 128);
+        }
+        mbar_init(&bars[SM::B_Q_FULL], 256);
+        mbar_init(&bars[SM::B_Q_EMPTY], 1);
+        mbar_init(&bars[SM::B_ML], 128);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bars[SM::B_S_FULL + i], 1);
+            mbar_init(&bars[SM::B_P_FULL + i], 128);
+            mbar_init(&bars[SM::B_PV_DONE + i], 1);
+        }
+        for (int i = 0; i < 3; ++i) mbar_init(&bars[SM::B_DRAIN + i], 1);
+        for (int s = 0; s < NK; ++s) {
+            mbar_init(&bars[SM::B_K_RAW + s], 1);
+            mbar_init(&bars[SM::B_K_ROT + s], 128);
+            mbar_init(&bars[SM::B_K_EMPTY + s], 1);
+        }
+        for (int s = 0; s < NV; ++s) {
+            mbar_init(&bars[SM::B_V_RAW + s], 1);
+            mbar_init(&bars[SM::B_V_CLEAN + s], 1);
+            mbar_init(&bars[SM::B_V_EMPTY + s], 2);
+        }
+        fence_mbar_init();
+        misc[1] = 0;
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
     grid_dep_wait();
     grid_dep_launch();
-    if (!tree_fits(p.plan, p.tag)) return;
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t row = item / p.hq;
-    const int32_t h = (int32_t)(item % p.hq);
-    if (row >= p.plan[T_ROWS]) return;
-    const int b = row_request(p.plan + tree_array(TA_ROW, p.n), p.n, (int32_t)row);
-    const int32_t seq = p.plan[tree_array(TA_SEQ, p.n) + b], add = p.plan[tree_array(TA_NEW, p.n) + b];
-    const int32_t first = p.plan[tree_array(TA_ROW, p.n) + b];
-    const int kvh = h / (p.hq / p.hkv);
-    const float scale = 1.4426950408889634f * (D == 128 ? 0.08838834764831845f : 0.125f);   // log2(e) / sqrt(d)
-    float a[N], c[N], va[N] = {}, vc[N] = {}, top = -INFINITY, l = 0.f, big = 0.f;
-    auto turn = [&](const __nv_bfloat16* src, int32_t pos, float (&lo)[N], float (&hi)[N]) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int i = lane * N + e;
-            const float x = __bfloat162float(src[i]), y = __bfloat162float(src[i + D / 2]);
-            const float2 cs = reinterpret_cast<const float2*>(p.rope)[(int64_t)pos * (D / 2) + i];
-            lo[e] = x * cs.x - y * cs.y;
-            hi[e] = y * cs.x + x * cs.y;
-            if (!(fabsf(lo[e]) < kF16Limit) || !(fabsf(hi[e]) < kF16Limit)) big = INFINITY;
-        }
-    };
-    const int32_t at = p.row_pos[row];
-    if (at < 0 || at >= p.max_pos) {
-        set_dev_error(kDevErrBounds);
+    const int4* entry = reinterpret_cast<const int4*>(p.plan + tree_shares(p.n)) + 2 * blockIdx.x;
+    const bool fits = p.plan[T_TAG] == p.tag;
+    const int4 share = fits ? entry[1] : make_int4(0, 0, 0, 0);
+    const int weight = share.y == p.tag ? share.x : 0;
+    if (!fits && tid == 0) set_dev_error(kDevErrBounds);
+    if (weight == 0) {             // nothing to do for the whole block
+        if (tid == 0) p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
     }
-    turn(p.q + row * p.q_stride + (int64_t)h * D, at, a, c);
-    for (int32_t j = 0; j < seq + add; ++j) {
-        const int64_t e = (int64_t)b * p.max_pages + j / kPage;
-        const int r = j % kPage, u = j - seq;
-        if (p.excl && p.excl[e] >> r & 1u) continue;
-        if (u >= 0 && !(p.seen[row * p.words + u / 32] >> (u & 31) & 1u)) continue;
-        const int32_t ph = p.block_table[e], pos = u >= 0 ? p.row_pos[first + u] : p.page_pos[e] + r;
-        if (ph < 0 || ph >= p.n_phys || pos < 0 || pos >= p.max_pos) {
-            set_dev_error(kDevErrBounds);
-            continue;
-        }
-        const int64_t src = (((int64_t)ph * p.hkv + kvh) * kPage + r) * D;
-        float x[N], y[N], s = 0.f;
-        turn(p.k_pool + src, pos, x, y);
-#pragma unroll
-        for (int i = 0; i < N; ++i) s += a[i] * x[i] + c[i] * y[i];
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= scale;
-        const float m = fmaxf(top, s), old = ex2(top - m), w = ex2(s - m);
-        top = m;
-        l = l * old + w;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float v0 = __bfloat162float(p.v_pool[src + lane * N + i]);
-            const float v1 = __bfloat162float(p.v_pool[src + D / 2 + lane * N + i]);
-            if (!(fabsf(v0) + fabsf(v1) < INFINITY)) big = INFINITY;
-            va[i] = va[i] * old + w * v0;
-            vc[i] = vc[i] * old + w * v1;
-        }
+    if (warp == 17) {
+        tmem_alloc(reinterpret_cast<uint32_t*>(misc), 512);
+        tmem_relinquish();
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    __nv_bfloat16* dst = p.out + item * D;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+    const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
+    const int tpt = kTileRows >> gs, tpp = 2 * tpt;      // nodes of a row tile, of a pair
+
+    auto take_item = [&](int it, TreeItem& w) -> bool {
+        const bool ok = mbar_wait(&bars[SM::B_ITEM_FULL + (it & 1)], (it >> 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        w = slots[it & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[SM::B_ITEM_EMPTY + (it & 1)]);
+        return true;
+    };
+    // units of a run that a chain takes, unit kc its first one
+    auto chain_units = [&](const TreeItem& w, int kc, int t) { return !w.single ? w.n_loc : (w.n_loc + ((kc & 1) == t ? 1 : 0)) >> 1; };
+
+    if (warp == 16) {
+        // ------------------------------------------------------------ runs, K and V copies
+        const int32_t* seq = p.plan + tree_array(TA_SEQ, p.n);
+        const int32_t* add = p.plan + tree_array(TA_NEW, p.n);
+        const int32_t* row = p.plan + tree_array(TA_ROW, p.n);
+        const int32_t* work = p.plan + tree_array(TA_WORK, p.n);
+        const int4 start = entry[0];
+        int left = weight, begins = share.z;             // weight of the run's beginning, where that is in this share
+        int32_t req = start.x, kvh = start.y, pair = start.z, unit = start.w;
+        int kc = 0, ks = 0, vs = 0, kn = 0, vn = 0;      // units, ring places, turns of the rings
+        bool ok = true;
+        int4 desc = make_int4(0, 0, 0, 0), desc_rows = desc;
+        const int m = lane & 3, hb = lane >> 2 & 1;      // the page and half this lane copies: K lanes 0-7, V lanes 8-15
+        for (int it = 0; ok; ++it) {
+            TreeItem w;
+            left -= begins;
+            w.req = left > 0 ? req : -1;
+            w.kvh = kvh;
+            w.pair = pair;
+            w.jb = unit;
+            w.n_loc = w.seq = w.add = w.row_base = 0;
+            w.slot = -1;
+            w.single = 0;
+            int pairs = 1;
+            if (left > 0) {
+                w.seq = seq[req];
+                w.add = add[req];
+                w.row_base = row[req];
+                w.single = min(tpp, w.add - pair * tpp) << gs <= kTileRows;
+                pairs = tree_pairs(w.add, g);
+                const int all = tree_units(w.seq + w.add);
+                w.n_loc = min(all - unit, left);
+                left -= w.n_loc;
+                if (w.n_loc < all) w.slot = 2 * blockIdx.x + (unit == 0 ? 1 : 0);
+                if (unit == 0 && w.n_loc < all) {
+                    // the block that holds the run's last unit
+                    const int32_t u = work[req] + (kvh * pairs + pair + 1) * (all + kTreeRunWeight) - 1;
+                    desc = make_int4(Deal(work[p.n], p.blocks).owner(u) << 8 | 0xFF, pair * tpp, kvh, 0);
+                    desc_rows = make_int4(w.add, w.row_base, 0, 0);
+                }
+            }
+            if (lane == 0) {
+                ok = it < 2 || mbar_wait(&bars[SM::B_ITEM_EMPTY + (it & 1)], ((it >> 1) - 1) & 1, abort_flag);
+                if (ok) {
+                    slots[it & 1] = w;
+                    mbar_arrive(&bars[SM::B_ITEM_FULL + (it & 1)]);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok || w.req < 0) break;
+            // lane l holds page l of a window of eight units, and of the window behind it
+            const int n_slots = w.seq + w.add, n_pages = pages_of(n_slots);
+            const int64_t table = (int64_t)w.req * p.max_pages;
+            int32_t ph = 0, ph_n = 0;
+            uint32_t gone = 0, gone_n = 0;
+            auto look_up = [&](int u0) {
+                const int pg = u0 * kTreePagesPerUnit + lane;
+                gone_n = 0xFFFFu;
+                ph_n = 0;
+                if (pg < n_pages) {
+                    const int32_t x = p.block_table[table + pg], pos = p.page_pos[table + pg];
+                    const uint32_t ex = p.excl ? p.excl[table + pg] : 0u;
+                    const int have = min(n_slots - pg * kPage, kPage);
+                    gone_n = ex | (0xFFFFu & ~((1u << have) - 1u));
+                    ph_n = x;
+                    // (a page of nodes alone has positions of its own)
+                    if (x < 0 || x >= p.n_phys || (pg * kPage < w.seq && (pos < 0 || pos > p.max_pos - kPage))) {
+                        set_dev_error(kDevErrBounds);
+                        ph_n = 0;
+                        gone_n = 0xFFFFu;                // nothing of it takes part
+                    }
+                }
+            };
+            look_up(w.jb);
+            for (int jj = 0; ok && jj < w.n_loc; ++jj, ++kc) {
+                if ((jj & 7) == 0) {
+                    ph = ph_n;
+                    gone = gone_n;
+                    if (jj + 8 < w.n_loc) look_up(w.jb + jj + 8);
+                }
+                const int at = (jj & 7) * kTreePagesPerUnit;
+                const int32_t y = (__shfl_sync(0xffffffffu, ph, at + m) * p.hkv + w.kvh) * kPage;
+                const uint32_t g0 = __shfl_sync(0xffffffffu, gone, at), g1 = __shfl_sync(0xffffffffu, gone, at + 1),
+                               g2 = __shfl_sync(0xffffffffu, gone, at + 2), g3 = __shfl_sync(0xffffffffu, gone, at + 3);
+                if (lane == 0) {
+                    ok = kn == 0 || mbar_wait(&bars[SM::B_K_EMPTY + ks], (kn - 1) & 1, abort_flag);
+                    if (ok) {
+                        s_meta[kc % SM::kMeta] = make_uint2(g0 | g1 << 16, g2 | g3 << 16);
+                        mbar_arrive_expect_tx(&bars[SM::B_K_RAW + ks], SM::kUnit);
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                if (lane < 4 * H)
+                    tma_load_2d(sK(ks) + hb * SM::kHalfUnit + m * (kPage * 128), &tm_k, &bars[SM::B_K_RAW + ks], hb * 64, y);
+                if (++ks == NK) ks = 0, ++kn;
+                if (lane == 0) {
+                    ok = vn == 0 || mbar_wait(&bars[SM::B_V_EMPTY + vs], (vn - 1) & 1, abort_flag);
+                    if (ok) mbar_arrive_expect_tx(&bars[SM::B_V_RAW + vs], SM::kUnit);
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                if (lane < 4 * H)
+                    tma_load_2d(sV(vs) + hb * SM::kHalfUnit + m * (kPage * 128), &tm_v, &bars[SM::B_V_RAW + vs], hb * 64, y);
+                if (++vs == NV) vs = 0, ++vn;
+            }
+            // the next run
+            unit = 0;
+            begins = kTreeRunWeight;
+            if (++pair == pairs) {
+                pair = 0;
+                if (++kvh == p.hkv) {
+                    kvh = 0;
+                    do { ++req; } while (req < p.n && work[req + 1] == work[req]);
+                }
+            }
+        }
+        if (lane == 0) {
+            p.desc[2 * blockIdx.x] = ok ? desc : make_int4(0, 0, 0, 0);
+            p.desc[2 * blockIdx.x + 1] = desc_rows;
+            // every copy lands before the block exits: each stage's last turn
+            for (int s = 0; s < NK; ++s) {
+                const int turns = kn + (s < ks ? 1 : 0);
+                if (turns > 0) mbar_drain(&bars[SM::B_K_RAW + s], (turns - 1) & 1);
+            }
+            for (int s = 0; s < NV; ++s) {
+                const int turns = vn + (s < vs ? 1 : 0);
+                if (turns > 0) mbar_drain(&bars[SM::B_V_RAW + s], (turns - 1) & 1);
+            }
+        }
+    } else if (warp == 17) {
+        // ------------------------------------------------------------ Q K^T
+        constexpr uint32_t idesc_qk = idesc_f16(128, kTreeUnit);
+        const uint32_t leader = lane == 0 ? 1u : 0u;
+        int kc = 0, hg[2] = {0, 0};
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            TreeItem w;
+            ok = take_item(it, w);
+            if (!ok || w.req < 0) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_Q_FULL], it & 1, abort_flag));
+            for (int jj = 0; ok && jj < w.n_loc; ++jj, ++kc) {
+                const int ks = kc % NK;
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_K_ROT + ks], (kc / NK) & 1, abort_flag));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        dst[lane * N + i] = __float2bfloat16(va[i] * inv);
-        dst[D / 2 + lane * N + i] = __float2bfloat16(vc[i] * inv);
+                for (int t = 0; t < 2; ++t) {
+                    if (!ok || (w.single && (kc & 1) != t)) continue;
+                    ok = __all_sync(0xffffffffu, hg[t] < 2 || mbar_wait(&bars[SM::B_PV_DONE + 2 * t + (hg[t] & 1)],
+                                                                        ((hg[t] - 2) >> 1) & 1, abort_flag));
+                    if (!ok) continue;
+                    tc_fence_after();
+                    const uint32_t aQ = desc_sw128_lo(smem_u32(smem + (w.single ? 0 : t) * SM::kQ), 16);
+                    const uint32_t aK = desc_sw128_lo(smem_u32(sK(ks)), 16);
+                    const uint32_t tS = tmem + t * 128 + (hg[t] & 1) * 64;
+#pragma unroll
+                    for (int k4 = 0; k4 < H; ++k4)
+                        mma_ss_k4(leader, tS, aQ + k4 * 1024, aK + k4 * (SM::kHalfUnit >> 4), kDescSw128Hi, idesc_qk,
+                                  k4 > 0 ? 1u : 0u);
+                    mma_commit_by(leader, &bars[SM::B_S_FULL + 2 * t + (hg[t] & 1)]);
+                    ++hg[t];
+                }
+                if (ok) mma_commit_by(leader, &bars[SM::B_K_EMPTY + ks]);
+            }
+            if (ok) mma_commit_by(leader, &bars[SM::B_Q_EMPTY]);
+        }
+        mma_commit_by(leader, &bars[SM::B_DRAIN]);
+        if (leader) mbar_drain(&bars[SM::B_DRAIN], 0);
+    } else if (warp >= 18) {
+        // ------------------------------------------------------------ P V
+        // The value rows of hidden slots become zeros first (they may hold anything, and a weight of zero
+        // does not silence a NaN): by the issuer whose parity the unit has.
+        constexpr uint32_t idesc_pv = idesc_bf16(128, D, true);
+        const int t = warp - 18;
+        const uint32_t leader = lane == 0 ? 1u : 0u, tO = tmem + kTmemO + t * 128;
+        int kc = 0, vs = 0, vn = 0, hg = 0, own = 0;
+        uint32_t cleaned = 0;                            // parity of the next V_CLEAN phase of every stage
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            TreeItem w;
+            ok = take_item(it, w);
+            if (!ok || w.req < 0) break;
+            const bool part = chain_units(w, kc, t) > 0;
+            bool begun = false;
+            for (int jj = 0; ok && jj < w.n_loc; ++jj, ++kc) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_V_RAW + vs], vn & 1, abort_flag));
+                if (!ok) break;
+                const uint2 gone = s_meta[kc % SM::kMeta];
+                if ((gone.x | gone.y) != 0u) {
+                    if ((kc & 1) == t) {
+                        // (D / 8 lanes a row, the rows in turn)
+                        constexpr int ROWS = 32 / (D / 8);
+                        uint64_t rest = (uint64_t)gone.y << 32 | gone.x;
+                        for (int i = 0; i < lane / (D / 8); ++i) rest &= rest - 1;
+                        while (rest != 0) {
+                            const int row = __ffsll((long long)rest) - 1, ch = lane % (D / 8);
+                            *reinterpret_cast<uint4*>(sV(vs) + (ch >> 3) * SM::kHalfUnit + sw128_off(row, ch & 7)) =
+                                make_uint4(0, 0, 0, 0);
+#pragma unroll
+                            for (int i = 0; i < ROWS; ++i) rest &= rest - 1;
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (leader) mbar_arrive(&bars[SM::B_V_CLEAN + vs]);
+                    }
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_V_CLEAN + vs], cleaned >> vs & 1u, abort_flag));
+                    cleaned ^= 1u << vs;
+                    if (!ok) break;
+                }
+                if (w.single && (kc & 1) != t) {
+                    if (leader) mbar_arrive(&bars[SM::B_V_EMPTY + vs]);
+                } else {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_P_FULL + 2 * t + (hg & 1)], (hg >> 1) & 1, abort_flag) &&
+                                                     (begun || own == 0 ||
+                                                      mbar_wait(&bars[SM::B_O_FREE + t], (own - 1) & 1, abort_flag)));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t aV = desc_sw128_lo(smem_u32(sV(vs)), SM::kHalfUnit);
+                    mma_ts_k4(leader, tO, tmem + t * 128 + (hg & 1) * 64, aV, kDescSw128Hi, idesc_pv, begun ? 1u : 0u);
+                    mma_commit_by(leader, &bars[SM::B_PV_DONE + 2 * t + (hg & 1)]);
+                    mma_commit_by(leader, &bars[SM::B_V_EMPTY + vs]);
+                    begun = true;
+                    ++hg;
+                }
+                if (++vs == NV) vs = 0, ++vn;
+            }
+            if (ok && part) {
+                mma_commit_by(leader, &bars[SM::B_O_DONE + t]);
+                ++own;
+            }
+        }
+        mma_commit_by(leader, &bars[SM::B_DRAIN + 1 + t]);
+        if (leader) mbar_drain(&bars[SM::B_DRAIN + 1 + t], 0);
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ rotation
+        // Thread rt of group r: 16-byte chunk pair c (dimensions 8 c .. and d/2 + 8 c ..) of N consecutive
+        // keys, a warp a page; their angles start from the cos/sin row of the first one's position and
+        // advance by one position, a rotation by table row 1.  Keys of nodes have positions of their own.
+        constexpr int N = 64 * CP / 128;                 // keys a thread
+        const int r = warp >> 2 & 1, rt = tid & 127, c = rt % CP, k0 = rt / CP * N, page = rt >> 5;
+        constexpr uint32_t o_hi = D == 128 ? SM::kHalfUnit : 0u;
+        const int c_hi = D == 128 ? c : c + 4;
+        const float scale = 1.4426950408889634f * (D == 128 ? 0.08838834764831845f : 0.125f);   // log2(e) / sqrt(d)
+        auto load_row = [&](int32_t pos, float4 (&cs)[4]) {
+            const float4* src = reinterpret_cast<const float4*>(p.rope + (int64_t)pos * D + 16 * c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) cs[e] = src[e];
+        };
+        Angles step;
+        uint64_t minus_step[4];
+        {
+            float4 cs[4];
+            load_row(1, cs);
+            step.set(cs);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) minus_step[e] = f2_neg(step.S[e]);
+        }
+        uint32_t odd = 0;                                // NaN where a rotated value is not finite
+        int kc = 0;
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            TreeItem w;
+            ok = take_item(it, w);
+            if (!ok || w.req < 0) break;
+            // a unit's cos/sin row, and the position of the unit behind it, are loaded as soon as the keys before
+            // are handed on: the fence that makes those visible to the tensor cores waits for loads in flight
+            const int n_pages = pages_of(w.seq + w.add);
+            const int32_t* pos_row = p.page_pos + (int64_t)w.req * p.max_pages;
+            auto position = [&](int jj) { return pos_row[min((w.jb + jj) * kTreePagesPerUnit + page, n_pages - 1)] + (k0 & 15); };
+            auto row_of = [&](int32_t pos) { return pos >= 0 && pos < p.max_pos ? pos : 0; };
+            const int j0 = (kc & 1) == r ? 0 : 1;
+            int32_t pos_n = position(j0 + 2);
+            float4 cs[4];
+            load_row(row_of(position(j0)), cs);
+            // ---- the run's queries: chunk pair c of rows th / CP, + 256 / CP, ... (head by head, so that a
+            // thread mostly stays with one node and its cos/sin row)
+            ok = it == 0 || mbar_wait(&bars[SM::B_Q_EMPTY], (it - 1) & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            {
+                const int th = tid - 256;
+                constexpr int STEP = 256 / CP;
+                int32_t last = -1;
+                Angles a;
+                for (int x0 = th / CP; x0 < (w.single ? 1 : 2) * kTileRows; x0 += 4 * STEP) {
+                    uint4 lo[4], hi[4];
+                    int tok[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int x = x0 + i * STEP, y = x % kTileRows;
+                        lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+                        tok[i] = w.pair * tpp + x / kTileRows * tpt + (y & (tpt - 1));
+                        if (x < 2 * kTileRows && tok[i] < w.add) {
+                            const __nv_bfloat16* src = p.q + (w.row_base + tok[i]) * p.q_stride + (int64_t)(w.kvh * g + (y >> (7 - gs))) * D;
+                            lo[i] = *reinterpret_cast<const uint4*>(src + 8 * c);
+                            hi[i] = *reinterpret_cast<const uint4*>(src + D / 2 + 8 * c);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int x = x0 + i * STEP, y = x % kTileRows;
+                        if (tok[i] < w.add) {
+                            if (tok[i] != last) {
+                                last = tok[i];
+                                const int32_t pos = p.row_pos[w.row_base + last];
+                                if (pos < 0 || pos >= p.max_pos) set_dev_error(kDevErrBounds);
+                                float4 f[4];
+                                load_row(row_of(pos), f);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) f[e] = make_float4(f[e].x * scale, f[e].y * scale, f[e].z * scale, f[e].w * scale);
+                                a.set(f);
+                            }
+                            a.turn(lo[i], hi[i], odd);
+                        }
+                        const int row = ((y & (tpt - 1)) << gs) + (y >> (7 - gs));
+                        uint8_t* dst = smem + x / kTileRows * SM::kQ;
+                        *reinterpret_cast<uint4*>(dst + sw128_off(row, c)) = lo[i];
+                        *reinterpret_cast<uint4*>(dst + (D == 128 ? kTileRows * 128 : 0) + sw128_off(row, c_hi)) = hi[i];
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bars[SM::B_Q_FULL]);
+            }
+            // ---- its keys
+            for (int jj = j0; jj < w.n_loc; jj += 2) {
+                const int u = kc + jj, ks = u % NK;
+                const int slot0 = (w.jb + jj) * kTreeUnit;
+                ok = mbar_wait(&bars[SM::B_K_RAW + ks], (u / NK) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                const uint2 meta = s_meta[u % SM::kMeta];
+                const uint32_t gone = ((page & 2 ? meta.y : meta.x) >> (page & 1) * 16) & 0xFFFFu;
+                const bool nodes = slot0 + (page + 1) * kPage > w.seq;       // (the same for the warp)
+                uint8_t* stage = sK(ks);
+                Angles a;
+                a.set(cs);
+#pragma unroll 2
+                for (int i = 0; i < N; ++i) {
+                    const int key = k0 + i;
+                    const bool have = !(gone >> (key & 15) & 1u);
+                    if (nodes && have && slot0 + key >= w.seq) {
+                        const int32_t pos = p.row_pos[w.row_base + slot0 + key - w.seq];
+                        if (pos < 0 || pos >= p.max_pos) set_dev_error(kDevErrBounds);
+                        float4 f[4];
+                        load_row(row_of(pos), f);
+                        a.set(f);
+                    }
+                    uint4* plo = reinterpret_cast<uint4*>(stage + sw128_off(key, c));
+                    uint4* phi = reinterpret_cast<uint4*>(stage + o_hi + sw128_off(key, c_hi));
+                    uint4 lo = *plo, hi = *phi;
+                    if (!have) lo = hi = make_uint4(0, 0, 0, 0);     // (may hold anything)
+                    a.turn(lo, hi, odd);
+                    a.advance(step, minus_step);
+                    *plo = lo;
+                    *phi = hi;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bars[SM::B_K_ROT + ks]);
+                load_row(row_of(pos_n), cs);
+                pos_n = position(jj + 4);
+            }
+            kc += w.n_loc;
+        }
+        if (odd != 0u) set_dev_error(kDevErrRange);
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int t = warp >> 2, m = tid & 127;            // row of the tile = TMEM lane
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tO = tmem + lane_addr + kTmemO;
+        int hg = 0, kc = 0, own[2] = {0, 0}, joined = 0;
+        float nan = 0.f;                                   // NaN where a result is not finite
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            TreeItem w;
+            ok = take_item(it, w);
+            if (!ok || w.req < 0) break;
+            const int tok = w.pair * tpp + (w.single ? 0 : t * tpt) + (m >> gs);
+            const bool valid = tok < w.add;
+            const bool any = __any_sync(0xffffffffu, valid);   // (a warp without rows has no scores to look at)
+            const uint32_t* seen = p.seen + (int64_t)(w.row_base + min(tok, w.add - 1)) * p.words;
+            float m_run = -INFINITY, l_run = 0.f;
+            const int mine = chain_units(w, kc, t), other = chain_units(w, kc, 1 - t);
+            int jj = w.single && (kc & 1) != t ? 1 : 0;
+            for (int q = 0; q < mine; ++q, ++hg, jj += w.single ? 2 : 1) {
+                const int buf = hg & 1;
+                const uint32_t tS = tmem + lane_addr + t * 128 + buf * 64;
+                ok = mbar_wait(&bars[SM::B_S_FULL + 2 * t + buf], (hg >> 1) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                tc_fence_after();
+                if (any) {
+                    const uint2 gone = s_meta[(kc + jj) % SM::kMeta];
+                    const int first = (w.jb + jj) * kTreeUnit;
+                    uint32_t hide0 = gone.x, hide1 = gone.y;
+                    if (first + kTreeUnit > w.seq) {
+                        const uint64_t see = tree_window(seen, p.words, first - w.seq);
+                        hide0 |= ~(uint32_t)see;
+                        hide1 |= ~(uint32_t)(see >> 32);
+                    }
+                    const bool full = __all_sync(0xffffffffu, (hide0 | hide1) == 0u);
+                    uint32_t sv[64];
+                    tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                    tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+                    tmem_ld_wait();
+                    if (!full) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            if (hide0 >> e & 1u) sv[e] = __float_as_uint(-INFINITY);
+                            if (hide1 >> e & 1u) sv[32 + e] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 64; e += 8) {
+                        m4[0] = max3f(m4[0], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                        m4[1] = max3f(m4[1], __uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]));
+                        m4[2] = max3f(m4[2], __uint_as_float(sv[e + 4]), __uint_as_float(sv[e + 5]));
+                        m4[3] = max3f(m4[3], __uint_as_float(sv[e + 6]), __uint_as_float(sv[e + 7]));
+                    }
+                    const float m_new = fmaxf(m_run, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                    const bool need = m_new > m_run + 8.0f;     // lazy rescale: keep P <= 2^8
+                    const float alpha = need ? ex2(m_run - m_new) : 1.0f;
+                    if (need) { l_run *= alpha; m_run = m_new; }
+                    const float msub = m_run == -INFINITY ? 0.f : m_run;
+                    const uint64_t negm2 = f2_pack(-msub, -msub);
+                    uint64_t acc2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float d0, d1;
+                        f2_unpack(f2_add(f2_pack(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), negm2), d0, d1);
+                        const float p0 = ex2(d0), p1 = ex2(d1);
+                        acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(p0, p1));
+                        pk[e] = pack_bf16x2(p0, p1);   // bf16 like the values they meet (an MMA's operands share a type)
+                    }
+                    tmem_st32(tS, pk);
+                    float a0, a1, b0, b1;
+                    f2_unpack(acc2[0], a0, a1);
+                    f2_unpack(acc2[1], b0, b1);
+                    l_run += (a0 + b0) + (a1 + b1);
+                    if (q > 0 && __any_sync(0xffffffffu, need)) {
+                        // every earlier P V of this chain must be done before O is rescaled
+                        ok = mbar_wait(&bars[SM::B_PV_DONE + 2 * t + (1 - buf)], ((hg - 1) >> 1) & 1, abort_flag);
+                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int cc = 0; cc < D / 32; ++cc) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + t * 128 + cc * 32, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st32(tO + t * 128 + cc * 32, o);
+                        }
+                    }
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                mbar_arrive(&bars[SM::B_P_FULL + 2 * t + buf]);
+            }
+            if (!ok) break;
+            // ---- epilogue: O / l, or the part's sums as they are
+            if (mine > 0) ok = mbar_wait(&bars[SM::B_O_DONE + t], own[t]++ & 1, abort_flag);
+            if (w.single && t == 1) {
+                // chain 0 has both results' rows
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                if (mine > 0) {
+                    tc_fence_after();
+                    s_ml[m] = make_float2(m_run, l_run);
+                    tc_fence_before();
+                    mbar_arrive(&bars[SM::B_ML]);
+                }
+                kc += w.n_loc;
+                continue;
+            }
+            const bool two = w.single && other > 0;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (two) {
+                ok = ok && mbar_wait(&bars[SM::B_ML], joined & 1, abort_flag);
+                ++joined;
+            }
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            tc_fence_after();
+            if (two) ml = s_ml[m];
+            const float top = fmaxf(m_run, ml.x), ref = top == -INFINITY ? 0.f : top;
+            float f0 = mine > 0 ? ex2(m_run - ref) : 0.f, f1 = two ? ex2(ml.x - ref) : 0.f;
+            const float l_all = l_run * f0 + ml.y * f1;
+            const int64_t prow = (int64_t)w.slot * (2 * kTileRows) + (w.single ? 0 : t * kTileRows) + m;
+            if (any) {
+                if (w.slot >= 0) {
+                    if (valid) p.part_ml[prow] = make_float2(top, l_all);
+                } else {
+                    const float inv = l_all > 0.f ? 1.0f / l_all : 0.f;
+                    f0 *= inv;
+                    f1 *= inv;
+                }
+#pragma unroll 1
+                for (int cc = 0; cc < D / 16; ++cc) {
+                    float o[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = 0.f;
+                    uint32_t x[16];
+                    if (mine > 0) {
+                        tmem_ld16(tO + t * 128 + cc * 16, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(x[e]) * f0;
+                    }
+                    if (two) {
+                        tmem_ld16(tO + 128 + cc * 16, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(x[e]), f1, o[e]);
+                    }
+                    if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) nan = fmaf(o[e], 0.f, nan);
+                        if (w.slot >= 0) {
+                            float* dst = p.part_o + prow * D + cc * 16;
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        } else {
+                            __nv_bfloat16* dst = p.out + ((int64_t)(w.row_base + tok) * p.hq + w.kvh * g + (m & (g - 1))) * D + cc * 16;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                uint4 v;
+                                v.x = pack_bf16x2(o[8 * e + 0], o[8 * e + 1]);
+                                v.y = pack_bf16x2(o[8 * e + 2], o[8 * e + 3]);
+                                v.z = pack_bf16x2(o[8 * e + 4], o[8 * e + 5]);
+                                v.w = pack_bf16x2(o[8 * e + 6], o[8 * e + 7]);
+                                *reinterpret_cast<uint4*>(dst + 8 * e) = v;
+                            }
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            if (mine > 0) mbar_arrive(&bars[SM::B_O_FREE + t]);
+            if (two) mbar_arrive(&bars[SM::B_O_FREE + 1]);
+            kc += w.n_loc;
+        }
+        if (nan != nan) set_dev_error(kDevErrRange);       // (a value that takes part is not finite)
     }
-    if (!(big < kF16Limit)) set_dev_error(kDevErrRange);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 17) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Blocks (j, y) add up the run that block j of tree_attn_kernel began and left open, some rows of it each: its
+// part, then those of the blocks behind up to the run's last, in their order.
+template <int D>
+__global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p) {
+    constexpr int ROWS = 256 / (D / 4);
+    grid_dep_wait();
+    grid_dep_launch();
+    const int j = blockIdx.x;
+    const int4 d = p.desc[2 * j], rows = p.desc[2 * j + 1];
+    if (d.x == 0) return;
+    const int last = d.x >> 8;
+    const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
+    const int r = blockIdx.y * ROWS + threadIdx.x / (D / 4), f = threadIdx.x % (D / 4);
+    const int tok = d.y + (r >> gs);
+    if (tok >= rows.x) return;
+    float top = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b0 = j; b0 <= last; b0 += 4) {            // four parts' loads in flight
+        float2 ml[4];
+        float4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // (behind the last part: that part again, without weight -- other memory may hold NaN)
+            const int b = min(b0 + i, last);
+            const int64_t row = ((int64_t)b * 2 + (b == j ? 1 : 0)) * (2 * kTileRows) + r;
+            ml[i] = p.part_ml[row];
+            v[i] = *reinterpret_cast<const float4*>(p.part_o + row * D + 4 * f);
+            if (b0 + i > last) ml[i].x = -INFINITY;
+        }
+        add_parts(ml, v, top, l, acc);
+    }
+    const float odd = not_finite(acc, 0.f);
+    if (odd != odd) set_dev_error(kDevErrRange);
+    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const int64_t row = (int64_t)(rows.y + tok) * p.hq + d.z * g + (r & (g - 1));
+    *reinterpret_cast<uint2*>(p.out + row * D + 4 * f) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 }  // namespace pcf

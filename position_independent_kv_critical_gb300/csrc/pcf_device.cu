@@ -1151,6 +1151,22 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + nb && y < x + na;
 }
+
+template <int D>
+pcf_status tree_attention_impl(const pcf_chunk_dims& d, const TreeParams& p, const uint16_t* k_pool,
+                               const uint16_t* v_pool, cudaStream_t st) {
+    CUtensorMap tk, tv;
+    pcf_status s;
+    const uint64_t rows = (uint64_t)d.n_phys_pages * d.n_kv_heads * kPage;
+    if ((s = make_map_2d(&tk, k_pool, D, rows, D * 2, kPage)) != PCF_OK) return s;
+    if ((s = make_map_2d(&tv, v_pool, D, rows, D * 2, kPage)) != PCF_OK) return s;
+    using SM = TreeSmem<D>;
+    auto kern = tree_attn_kernel<D>;
+    if ((s = set_smem(kern, SM::kAlloc)) != PCF_OK) return s;
+    if ((s = launch(kern, dim3(p.blocks), dim3(kTreeAttnThreads), SM::kAlloc, st, tk, tv, p)) != PCF_OK) return s;
+    const int pair_rows = std::min(2 * kTileRows, d.max_chunk * (d.n_q_heads / d.n_kv_heads));
+    return launch(tree_join_kernel<D>, dim3(p.blocks, (pair_rows * (D / 4) + 255) / 256), dim3(256), 0, st, p);
+}
 }  // namespace
 
 extern "C" pcf_status pcf_tree_tables(const pcf_chunk_dims* dims, const int32_t* chunk_plan, const int32_t* parent,
@@ -1192,16 +1208,17 @@ extern "C" pcf_status pcf_tree_attention(const pcf_chunk_dims* dims, const int32
         return PCF_ERR_INVALID_ARG;
     if (ws_bytes < tree_ws(dims).total) return PCF_ERR_WORKSPACE_TOO_SMALL;
     if ((s = check_device()) != PCF_OK) return s;
-    const TreeParams p{tree_plan, reinterpret_cast<const __nv_bfloat16*>(q),
-                       reinterpret_cast<const __nv_bfloat16*>(k_pool), reinterpret_cast<const __nv_bfloat16*>(v_pool),
-                       block_table, page_pos, excl, row_pos, reinterpret_cast<const uint32_t*>(seen), rope,
-                       reinterpret_cast<__nv_bfloat16*>(out), q_row_stride, dims->n_reqs, dims->max_pages,
-                       dims->max_rows, tree_words(dims), dims->n_q_heads, dims->n_kv_heads, dims->n_phys_pages,
-                       dims->max_pos, tree_tag(dims)};
+    const TreeWs w = tree_ws(dims);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    const TreeParams p{tree_plan, reinterpret_cast<const __nv_bfloat16*>(q), block_table, page_pos, excl, row_pos,
+                       reinterpret_cast<const uint32_t*>(seen), rope, reinterpret_cast<__nv_bfloat16*>(out),
+                       reinterpret_cast<float*>(base + w.part_o), reinterpret_cast<float2*>(base + w.part_ml),
+                       reinterpret_cast<int4*>(base + w.desc), q_row_stride, dims->n_reqs, dims->max_pages,
+                       tree_words(dims), dims->n_q_heads, dims->n_kv_heads, dims->n_phys_pages, dims->max_pos,
+                       chunk_sms(dims->n_sms), tree_tag(dims)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned blocks = (unsigned)(((int64_t)dims->max_rows * dims->n_q_heads + 3) / 4);
-    return dims->head_dim == 128 ? launch(tree_simple_kernel<128>, dim3(blocks), dim3(128), 0, st, p)
-                                 : launch(tree_simple_kernel<64>, dim3(blocks), dim3(128), 0, st, p);
+    return dims->head_dim == 128 ? tree_attention_impl<128>(*dims, p, k_pool, v_pool, st)
+                                 : tree_attention_impl<64>(*dims, p, k_pool, v_pool, st);
 }
 
 extern "C" pcf_status pcf_tree_accept(const pcf_chunk_dims* dims, const int32_t* chunk_plan, int32_t* tree_plan,
