@@ -10,13 +10,14 @@
 // cores bound it about alike at 256 rows (a unit of 64 keys and values, 32 KB at d = 128, takes an SM 1400
 // cycles at the copy rate and its four products of two row tiles 1280), HBM alone below.  So the keys are
 // rotated where they are used, in shared memory: no copy of them is written or read again.  One block an SM,
-// twenty warps; a run is one (request, kv head, row pair) or the part of one that a block has, dealt by
+// nineteen warps; a run is one (request, kv head, row pair) or the part of one that a block has, dealt by
 // pcf_tree_tables in contiguous parts of equal weight.
 //   warps  0-7   softmax of chain 0 (warps 0-3) and 1: S row from TMEM, excluded slots and other branches
 //                hidden, online softmax (lazy rescale), P -> TMEM over the S columns, O epilogue
 //   warps  8-15  two groups of four, units in turn: a run's queries, then the keys, bf16 in, rotated fp16 out
 //   warp  16     runs in order; a unit's four pages of keys and of values (TMA), its hidden slots
-//   warp  17     Q K^T issue (and the TMEM allocation); warps 18, 19  P V issue of chain 0 and 1
+//   warp  17     Q K^T issue (and the TMEM allocation)
+//   warp  18     P V issue; value rows of hidden slots become zeros before it
 // With more than 128 rows the chains are the pair's two row tiles and both take every unit.  With up to 128
 // there is one tile, and the chains take its units in turn, each with sums of its own that meet in the
 // epilogue: eight softmax warps share what four would do, and a unit's way through the chain
@@ -50,8 +51,8 @@ struct TreeParams {
     int32_t n, max_pages, words, hq, hkv, n_phys, max_pos, blocks, tag;
 };
 
-constexpr int kTreeAttnThreads = 640;
-constexpr int kTreeReaders = 19;    // warps that read a run: softmax, rotation, issuers
+constexpr int kTreeAttnThreads = 608;
+constexpr int kTreeReaders = 18;    // warps that read a run: softmax, rotation, issuers
 
 // One run, or the part of one this block has, as warp 16 hands it to the others.
 struct TreeItem {
@@ -68,24 +69,30 @@ struct TreeSmem {
     static constexpr int kHalves = D / 64;
     static constexpr int kQ = kTileRows * D * 2;
     static constexpr int kUnit = kTreeUnit * D * 2;
-    static constexpr int kHalfUnit = kTreeUnit * 128;          // 64 rows of 64 elements
+    // A page lands as one box of eight-row groups, a group's halves (64 dimensions, 128-byte rows) one behind the
+    // other: with one box a page, and its groups kGroup bytes apart from page to page too, as the products'
+    // operands want them.  (Boxes of half a page took twice as many copy instructions, some 160 cycles each
+    // in the warp that issues them: 1316 us for 64 shared requests.)
+    static constexpr int kPageBytes = kPage * D * 2, kGroup = 8 * D * 2, kHalf = 1024;
     // (both even: a stage then belongs to units of one parity)
     static constexpr int NK = D == 128 ? 4 : 8, NV = D == 128 ? 6 : 12;
-    // A unit's hidden slots and nothing else are read behind its key: by the softmax and the P V issuers,
-    // all done with unit u - NV when unit u's value is copied, that is before unit u + 1 is entered here.
-    static constexpr int kMeta = D == 128 ? 8 : 16;
-    static_assert(kMeta >= NV + 2, "a unit's entry lasts until its P V is done");
+    // Hidden slots of the units whose keys are here or on the way, read by the rotation and the softmax: unit u
+    // enters its own behind Q K^T of unit u - NK, which came behind P V, and so the softmax, of unit
+    // u - NK - 4 (a chain's two S buffers, units in turn) and before.
+    static constexpr int kMeta = 2 * NK;
+    static_assert(kMeta >= NK + 4, "a unit's entry lasts until its softmax is done");
     static constexpr int oK = 2 * kQ;
     static constexpr int oV = oK + NK * kUnit;
     static constexpr int oMl = oV + NV * kUnit;                // [128] chain 1's maximum and sum
-    static constexpr int oMeta = oMl + kTileRows * 8;          // [kMeta] 64 hidden bits
-    static constexpr int oItem = oMeta + kMeta * 8;
+    static constexpr int oMeta = oMl + kTileRows * 8;          // [kMeta] a unit's 64 hidden bits
+    static constexpr int oMetaV = oMeta + kMeta * 8;           // [NV] the same for a stage's values
+    static constexpr int oItem = oMetaV + NV * 8;
     static constexpr int oBar = oItem + 2 * (int)sizeof(TreeItem);
     // barriers
     static constexpr int B_ITEM_FULL = 0, B_ITEM_EMPTY = 2, B_Q_FULL = 4, B_Q_EMPTY = 5, B_S_FULL = 6, B_P_FULL = 10,
-                         B_PV_DONE = 14, B_O_DONE = 18, B_O_FREE = 20, B_ML = 22, B_DRAIN = 23, B_K_RAW = 26,
+                         B_PV_DONE = 14, B_O_DONE = 18, B_O_FREE = 20, B_ML = 22, B_DRAIN = 23, B_K_RAW = 25,
                          B_K_ROT = B_K_RAW + NK, B_K_EMPTY = B_K_ROT + NK, B_V_RAW = B_K_EMPTY + NK,
-                         B_V_CLEAN = B_V_RAW + NV, B_V_EMPTY = B_V_CLEAN + NV, kNumBars = B_V_EMPTY + NV;
+                         B_V_EMPTY = B_V_RAW + NV, kNumBars = B_V_EMPTY + NV;
     static constexpr int oMisc = oBar + kNumBars * 8;          // TMEM address, abort flag
     static constexpr int kBytes = oMisc + 16;
     static constexpr int kAlloc = kBytes + 1024;
@@ -94,10 +101,8 @@ struct TreeSmem {
 
 // A wait sees the parity of a phase only, so a phase may end at most once before each of its waiters has
 // passed it.  What keeps each barrier to that:
-//   ITEM, K_ROT     every waiter passes every phase;
+//   ITEM, K_ROT, V_RAW   every waiter passes every phase;
 //   K_RAW           a stage belongs to one rotating group (NK is even), which passes every phase of it;
-//   V_RAW, V_CLEAN  both P V issuers pass every phase (of dirty units' for V_CLEAN), a unit of the other chain
-//                   included;
 //   Q, S, P, PV_DONE, O_DONE, O_FREE   as in the many-row kernel: counted by the units and runs that a chain
 //                   takes part in; in a run of one tile the threads of chain 0 arrive on both O_FREE;
 //   ML              chain 1's sums of a run of one tile: written again only behind chain 1's next result, whose
@@ -113,11 +118,82 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
+__device__ __forceinline__ uint4 lds_128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts_128(uint32_t addr, const uint4& v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y, int32_t z,
+                                            int32_t u) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(u)
+        : "memory");
+}
+// high word of a 128-byte-swizzled descriptor whose eight-row groups are `group` bytes apart
+__device__ __forceinline__ constexpr uint32_t desc_sw128_hi(uint32_t group) {
+    return (group >> 4) | (1u << (46 - 32)) | (2u << (61 - 32));
+}
+// As mma_ss_k4, the operands' groups apart by distances of their own.
+__device__ __forceinline__ void mma_ss_k4_by(uint32_t leader, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t a_hi,
+                                             uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred L, p, t;\n\t.reg .b64 da, db;\n\t.reg .b32 la, lb;\n\t"
+        "setp.ne.b32 L, %0, 0;\n\t"
+        "setp.ne.b32 p, %7, 0;\n\t"
+        "setp.eq.b32 t, %0, %0;\n\t"
+        "mov.b64 da, {%2, %4};\n\tmov.b64 db, {%3, %5};\n\t"
+        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], da, db, %6, p;\n\t"
+        "add.u32 la, %2, 2;\n\tadd.u32 lb, %3, 2;\n\t"
+        "mov.b64 da, {la, %4};\n\tmov.b64 db, {lb, %5};\n\t"
+        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], da, db, %6, t;\n\t"
+        "add.u32 la, %2, 4;\n\tadd.u32 lb, %3, 4;\n\t"
+        "mov.b64 da, {la, %4};\n\tmov.b64 db, {lb, %5};\n\t"
+        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], da, db, %6, t;\n\t"
+        "add.u32 la, %2, 6;\n\tadd.u32 lb, %3, 6;\n\t"
+        "mov.b64 da, {la, %4};\n\tmov.b64 db, {lb, %5};\n\t"
+        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], da, db, %6, t;\n\t}\n" ::"r"(leader),
+        "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// As mma_ts_k4, a K = 16 step being a page of `page` (in units of 16 bytes).
+__device__ __forceinline__ void mma_ts_pages(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t page,
+                                             uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred L, p, t;\n\t.reg .b64 db;\n\t.reg .b32 ta, lb;\n\t"
+        "setp.ne.b32 L, %0, 0;\n\t"
+        "setp.ne.b32 p, %7, 0;\n\t"
+        "setp.eq.b32 t, %0, %0;\n\t"
+        "mov.b64 db, {%3, %5};\n\t"
+        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], db, %6, p;\n\t"
+        "add.u32 ta, %2, 8;\n\tadd.u32 lb, %3, %4;\n\tmov.b64 db, {lb, %5};\n\t"
+        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], [ta], db, %6, t;\n\t"
+        "add.u32 ta, %2, 16;\n\tadd.u32 lb, lb, %4;\n\tmov.b64 db, {lb, %5};\n\t"
+        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], [ta], db, %6, t;\n\t"
+        "add.u32 ta, %2, 24;\n\tadd.u32 lb, lb, %4;\n\tmov.b64 db, {lb, %5};\n\t"
+        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], [ta], db, %6, t;\n\t}\n" ::"r"(leader),
+        "r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(page), "r"(hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // odd + 0 x: NaN in a half of `odd` once that half of an x was not finite
 __device__ __forceinline__ uint32_t odd_f16x2(uint32_t x, uint32_t odd) {
     uint32_t r;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0), "r"(odd));
     return r;
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 
 // Eight frequencies' cos and sin as packed pairs.
@@ -184,6 +260,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
     TreeItem* slots = reinterpret_cast<TreeItem*>(smem + SM::oItem);
     uint2* s_meta = reinterpret_cast<uint2*>(smem + SM::oMeta);
+    uint2* s_meta_v = reinterpret_cast<uint2*>(smem + SM::oMetaV);
     float2* s_ml = reinterpret_cast<float2*>(smem + SM::oMl);
     auto sK = [&](int st) { return smem + SM::oK + st * SM::kUnit; };
     auto sV = [&](int st) { return smem + SM::oV + st * SM::kUnit; };
@@ -204,7 +281,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             mbar_init(&bars[SM::B_P_FULL + i], 128);
             mbar_init(&bars[SM::B_PV_DONE + i], 1);
         }
-        for (int i = 0; i < 3; ++i) mbar_init(&bars[SM::B_DRAIN + i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&bars[SM::B_DRAIN + i], 1);
         for (int s = 0; s < NK; ++s) {
             mbar_init(&bars[SM::B_K_RAW + s], 1);
             mbar_init(&bars[SM::B_K_ROT + s], 128);
@@ -212,8 +289,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         for (int s = 0; s < NV; ++s) {
             mbar_init(&bars[SM::B_V_RAW + s], 1);
-            mbar_init(&bars[SM::B_V_CLEAN + s], 1);
-            mbar_init(&bars[SM::B_V_EMPTY + s], 2);
+            mbar_init(&bars[SM::B_V_EMPTY + s], 1);
         }
         fence_mbar_init();
         misc[1] = 0;
@@ -253,8 +329,52 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     // units of a run that a chain takes, unit kc its first one
     auto chain_units = [&](const TreeItem& w, int kc, int t) { return !w.single ? w.n_loc : (w.n_loc + ((kc & 1) == t ? 1 : 0)) >> 1; };
 
+    // Lane l holds page l of a window of eight units, and of the window behind it: its place in the pool, its
+    // slots that no row sees.
+    struct Window {
+        int32_t y = 0, y_n = 0;
+        uint32_t gone = 0, gone_n = 0;
+    };
+    auto look_up = [&](Window& v, const TreeItem& w, int u0) {
+        const int pg = u0 * kTreePagesPerUnit + lane, n_slots = w.seq + w.add;
+        v.gone_n = 0xFFFFu;
+        v.y_n = 0;
+        if (pg < pages_of(n_slots)) {
+            const int64_t e = (int64_t)w.req * p.max_pages + pg;
+            const int32_t x = p.block_table[e], pos = p.page_pos[e];
+            const uint32_t ex = p.excl ? p.excl[e] : 0u;
+            const int have = min(n_slots - pg * kPage, kPage);
+            v.gone_n = ex | (0xFFFFu & ~((1u << have) - 1u));
+            v.y_n = x;
+            // (a page of nodes alone has positions of its own)
+            if (x < 0 || x >= p.n_phys || (pg * kPage < w.seq && (pos < 0 || pos > p.max_pos - kPage))) {
+                set_dev_error(kDevErrBounds);
+                v.y_n = 0;
+                v.gone_n = 0xFFFFu;                      // nothing of it takes part
+            }
+        }
+        v.y_n = (v.y_n * p.hkv + w.kvh) * (D == 128 ? 2 : kPage);      // in the map's rows: groups of eight, or single ones
+    };
+    // unit jj of the run: the window moves on, this lane's page (lanes 0-3) and the unit's hidden bits
+    auto next_unit = [&](Window& v, const TreeItem& w, int jj, int32_t& y) {
+        if ((jj & 7) == 0) {
+            v.y = v.y_n;
+            v.gone = v.gone_n;
+            if (jj + 8 < w.n_loc) look_up(v, w, w.jb + jj + 8);
+        }
+        const int at = (jj & 7) * kTreePagesPerUnit;
+        y = __shfl_sync(0xffffffffu, v.y, at + (lane & 3));
+        const uint32_t g0 = __shfl_sync(0xffffffffu, v.gone, at), g1 = __shfl_sync(0xffffffffu, v.gone, at + 1),
+                       g2 = __shfl_sync(0xffffffffu, v.gone, at + 2), g3 = __shfl_sync(0xffffffffu, v.gone, at + 3);
+        return make_uint2(g0 | g1 << 16, g2 | g3 << 16);
+    };
+    auto copy_page = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int32_t y) {
+        if constexpr (D == 128) tma_load_4d(dst + lane * SM::kPageBytes, map, bar, 0, 0, 0, y);
+        else tma_load_2d(dst + lane * SM::kPageBytes, map, bar, 0, y);
+    };
+
     if (warp == 16) {
-        // ------------------------------------------------------------ runs, K and V copies
+        // ------------------------------------------------------------ runs, K copies
         const int32_t* seq = p.plan + tree_array(TA_SEQ, p.n);
         const int32_t* add = p.plan + tree_array(TA_NEW, p.n);
         const int32_t* row = p.plan + tree_array(TA_ROW, p.n);
@@ -262,10 +382,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         const int4 start = entry[0];
         int left = weight, begins = share.z;             // weight of the run's beginning, where that is in this share
         int32_t req = start.x, kvh = start.y, pair = start.z, unit = start.w;
-        int kc = 0, ks = 0, vs = 0, kn = 0, vn = 0;      // units, ring places, turns of the rings
+        int kc = 0, ks = 0, kn = 0, vs = 0, vn = 0;      // units, places in the rings, their turns
         bool ok = true;
         int4 desc = make_int4(0, 0, 0, 0), desc_rows = desc;
-        const int m = lane & 3, hb = lane >> 2 & 1;      // the page and half this lane copies: K lanes 0-7, V lanes 8-15
         for (int it = 0; ok; ++it) {
             TreeItem w;
             left -= begins;
@@ -303,61 +422,31 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok || w.req < 0) break;
-            // lane l holds page l of a window of eight units, and of the window behind it
-            const int n_slots = w.seq + w.add, n_pages = pages_of(n_slots);
-            const int64_t table = (int64_t)w.req * p.max_pages;
-            int32_t ph = 0, ph_n = 0;
-            uint32_t gone = 0, gone_n = 0;
-            auto look_up = [&](int u0) {
-                const int pg = u0 * kTreePagesPerUnit + lane;
-                gone_n = 0xFFFFu;
-                ph_n = 0;
-                if (pg < n_pages) {
-                    const int32_t x = p.block_table[table + pg], pos = p.page_pos[table + pg];
-                    const uint32_t ex = p.excl ? p.excl[table + pg] : 0u;
-                    const int have = min(n_slots - pg * kPage, kPage);
-                    gone_n = ex | (0xFFFFu & ~((1u << have) - 1u));
-                    ph_n = x;
-                    // (a page of nodes alone has positions of its own)
-                    if (x < 0 || x >= p.n_phys || (pg * kPage < w.seq && (pos < 0 || pos > p.max_pos - kPage))) {
-                        set_dev_error(kDevErrBounds);
-                        ph_n = 0;
-                        gone_n = 0xFFFFu;                // nothing of it takes part
-                    }
-                }
-            };
-            look_up(w.jb);
+            Window v;
+            look_up(v, w, w.jb);
             for (int jj = 0; ok && jj < w.n_loc; ++jj, ++kc) {
-                if ((jj & 7) == 0) {
-                    ph = ph_n;
-                    gone = gone_n;
-                    if (jj + 8 < w.n_loc) look_up(w.jb + jj + 8);
-                }
-                const int at = (jj & 7) * kTreePagesPerUnit;
-                const int32_t y = (__shfl_sync(0xffffffffu, ph, at + m) * p.hkv + w.kvh) * kPage;
-                const uint32_t g0 = __shfl_sync(0xffffffffu, gone, at), g1 = __shfl_sync(0xffffffffu, gone, at + 1),
-                               g2 = __shfl_sync(0xffffffffu, gone, at + 2), g3 = __shfl_sync(0xffffffffu, gone, at + 3);
-                if (lane == 0) {
-                    ok = kn == 0 || mbar_wait(&bars[SM::B_K_EMPTY + ks], (kn - 1) & 1, abort_flag);
+                int32_t y;
+                const uint2 gone = next_unit(v, w, jj, y);
+                // its keys, then its values (one copy of the code: see the note on the instruction cache)
+#pragma unroll 1
+                for (int i = 0; ok && i < 2; ++i) {
+                    const int st = i ? vs : ks, turn = i ? vn : kn;
+                    uint64_t* raw = &bars[(i ? SM::B_V_RAW : SM::B_K_RAW) + st];
+                    if (lane == 0) {
+                        ok = turn == 0 || mbar_wait(&bars[(i ? SM::B_V_EMPTY : SM::B_K_EMPTY) + st], (turn - 1) & 1, abort_flag);
+                        if (ok) {
+                            if (i) s_meta_v[st] = gone;
+                            else s_meta[kc % SM::kMeta] = gone;
+                            mbar_arrive_expect_tx(raw, SM::kUnit);
+                        }
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (ok) {
-                        s_meta[kc % SM::kMeta] = make_uint2(g0 | g1 << 16, g2 | g3 << 16);
-                        mbar_arrive_expect_tx(&bars[SM::B_K_RAW + ks], SM::kUnit);
+                        if (lane < kTreePagesPerUnit) copy_page(i ? sV(st) : sK(st), i ? &tm_v : &tm_k, raw, y);
+                        if (i) vs = vs + 1 == NV ? 0 : vs + 1, vn += vs == 0;
+                        else ks = ks + 1 == NK ? 0 : ks + 1, kn += ks == 0;
                     }
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                if (lane < 4 * H)
-                    tma_load_2d(sK(ks) + hb * SM::kHalfUnit + m * (kPage * 128), &tm_k, &bars[SM::B_K_RAW + ks], hb * 64, y);
-                if (++ks == NK) ks = 0, ++kn;
-                if (lane == 0) {
-                    ok = vn == 0 || mbar_wait(&bars[SM::B_V_EMPTY + vs], (vn - 1) & 1, abort_flag);
-                    if (ok) mbar_arrive_expect_tx(&bars[SM::B_V_RAW + vs], SM::kUnit);
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                if (lane < 4 * H)
-                    tma_load_2d(sV(vs) + hb * SM::kHalfUnit + m * (kPage * 128), &tm_v, &bars[SM::B_V_RAW + vs], hb * 64, y);
-                if (++vs == NV) vs = 0, ++vn;
             }
             // the next run
             unit = 0;
@@ -387,7 +476,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         // ------------------------------------------------------------ Q K^T
         constexpr uint32_t idesc_qk = idesc_f16(128, kTreeUnit);
         const uint32_t leader = lane == 0 ? 1u : 0u;
-        int kc = 0, hg[2] = {0, 0};
+        int kc = 0, hg0 = 0, hg1 = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
             TreeItem w;
@@ -397,22 +486,23 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             for (int jj = 0; ok && jj < w.n_loc; ++jj, ++kc) {
                 const int ks = kc % NK;
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_K_ROT + ks], (kc / NK) & 1, abort_flag));
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (!ok || (w.single && (kc & 1) != t)) continue;
-                    ok = __all_sync(0xffffffffu, hg[t] < 2 || mbar_wait(&bars[SM::B_PV_DONE + 2 * t + (hg[t] & 1)],
-                                                                        ((hg[t] - 2) >> 1) & 1, abort_flag));
-                    if (!ok) continue;
+                const int t0 = w.single ? kc & 1 : 0, t1 = w.single ? t0 : 1;
+#pragma unroll 1
+                for (int t = t0; ok && t <= t1; ++t) {
+                    const int hg = t ? hg1 : hg0;
+                    ok = __all_sync(0xffffffffu, hg < 2 || mbar_wait(&bars[SM::B_PV_DONE + 2 * t + (hg & 1)],
+                                                                     ((hg - 2) >> 1) & 1, abort_flag));
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t aQ = desc_sw128_lo(smem_u32(smem + (w.single ? 0 : t) * SM::kQ), 16);
                     const uint32_t aK = desc_sw128_lo(smem_u32(sK(ks)), 16);
-                    const uint32_t tS = tmem + t * 128 + (hg[t] & 1) * 64;
-#pragma unroll
+                    const uint32_t tS = tmem + t * 128 + (hg & 1) * 64;
+#pragma unroll 1
                     for (int k4 = 0; k4 < H; ++k4)
-                        mma_ss_k4(leader, tS, aQ + k4 * 1024, aK + k4 * (SM::kHalfUnit >> 4), kDescSw128Hi, idesc_qk,
-                                  k4 > 0 ? 1u : 0u);
-                    mma_commit_by(leader, &bars[SM::B_S_FULL + 2 * t + (hg[t] & 1)]);
-                    ++hg[t];
+                        mma_ss_k4_by(leader, tS, aQ + k4 * 1024, aK + k4 * (SM::kHalf >> 4), kDescSw128Hi,
+                                     desc_sw128_hi(SM::kGroup), idesc_qk, k4 > 0 ? 1u : 0u);
+                    mma_commit_by(leader, &bars[SM::B_S_FULL + 2 * t + (hg & 1)]);
+                    if (t) ++hg1; else ++hg0;
                 }
                 if (ok) mma_commit_by(leader, &bars[SM::B_K_EMPTY + ks]);
             }
@@ -420,71 +510,64 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         mma_commit_by(leader, &bars[SM::B_DRAIN]);
         if (leader) mbar_drain(&bars[SM::B_DRAIN], 0);
-    } else if (warp >= 18) {
+    } else if (warp == 18) {
         // ------------------------------------------------------------ P V
         // The value rows of hidden slots become zeros first (they may hold anything, and a weight of zero
-        // does not silence a NaN): by the issuer whose parity the unit has.
+        // does not silence a NaN).
         constexpr uint32_t idesc_pv = idesc_bf16(128, D, true);
-        const int t = warp - 18;
-        const uint32_t leader = lane == 0 ? 1u : 0u, tO = tmem + kTmemO + t * 128;
-        int kc = 0, vs = 0, vn = 0, hg = 0, own = 0;
-        uint32_t cleaned = 0;                            // parity of the next V_CLEAN phase of every stage
+        const uint32_t leader = lane == 0 ? 1u : 0u;
+        int kc = 0, vs = 0, vn = 0, hg0 = 0, hg1 = 0, own0 = 0, own1 = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
             TreeItem w;
             ok = take_item(it, w);
             if (!ok || w.req < 0) break;
-            const bool part = chain_units(w, kc, t) > 0;
-            bool begun = false;
+            bool begun0 = false, begun1 = false;
             for (int jj = 0; ok && jj < w.n_loc; ++jj, ++kc) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_V_RAW + vs], vn & 1, abort_flag));
                 if (!ok) break;
-                const uint2 gone = s_meta[kc % SM::kMeta];
+                const uint2 gone = s_meta_v[vs];
                 if ((gone.x | gone.y) != 0u) {
-                    if ((kc & 1) == t) {
-                        // (D / 8 lanes a row, the rows in turn)
-                        constexpr int ROWS = 32 / (D / 8);
-                        uint64_t rest = (uint64_t)gone.y << 32 | gone.x;
-                        for (int i = 0; i < lane / (D / 8); ++i) rest &= rest - 1;
-                        while (rest != 0) {
-                            const int row = __ffsll((long long)rest) - 1, ch = lane % (D / 8);
-                            *reinterpret_cast<uint4*>(sV(vs) + (ch >> 3) * SM::kHalfUnit + sw128_off(row, ch & 7)) =
-                                make_uint4(0, 0, 0, 0);
+                    // (D / 8 lanes a row, the rows in turn)
+                    constexpr int LANES = D / 8, ROWS = 32 / LANES;
+                    const int ch = lane % LANES;
+                    uint64_t rest = (uint64_t)gone.y << 32 | gone.x;
+                    for (int i = 0; i < lane / LANES; ++i) rest &= rest - 1;
+                    while (rest != 0) {
+                        const int row = __ffsll((long long)rest) - 1;
+                        *reinterpret_cast<uint4*>(sV(vs) + (row >> 3) * SM::kGroup + (ch >> 3) * SM::kHalf +
+                                                  sw128_off(row & 7, ch & 7)) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                            for (int i = 0; i < ROWS; ++i) rest &= rest - 1;
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (leader) mbar_arrive(&bars[SM::B_V_CLEAN + vs]);
+                        for (int i = 0; i < ROWS; ++i) rest &= rest - 1;
                     }
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_V_CLEAN + vs], cleaned >> vs & 1u, abort_flag));
-                    cleaned ^= 1u << vs;
-                    if (!ok) break;
+                    fence_proxy_async_smem();
+                    __syncwarp();
                 }
-                if (w.single && (kc & 1) != t) {
-                    if (leader) mbar_arrive(&bars[SM::B_V_EMPTY + vs]);
-                } else {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_P_FULL + 2 * t + (hg & 1)], (hg >> 1) & 1, abort_flag) &&
-                                                     (begun || own == 0 ||
-                                                      mbar_wait(&bars[SM::B_O_FREE + t], (own - 1) & 1, abort_flag)));
+                const int t0 = w.single ? kc & 1 : 0, t1 = w.single ? t0 : 1;
+#pragma unroll 1
+                for (int t = t0; ok && t <= t1; ++t) {
+                    const int hg = t ? hg1 : hg0, own = t ? own1 : own0;
+                    const bool begun = t ? begun1 : begun0;
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&bars[SM::B_P_FULL + 2 * t + (hg & 1)], (hg >> 1) & 1, abort_flag) &&
+                                        (begun || own == 0 || mbar_wait(&bars[SM::B_O_FREE + t], (own - 1) & 1, abort_flag)));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t aV = desc_sw128_lo(smem_u32(sV(vs)), SM::kHalfUnit);
-                    mma_ts_k4(leader, tO, tmem + t * 128 + (hg & 1) * 64, aV, kDescSw128Hi, idesc_pv, begun ? 1u : 0u);
+                    mma_ts_pages(leader, tmem + kTmemO + t * 128, tmem + t * 128 + (hg & 1) * 64,
+                                 desc_sw128_lo(smem_u32(sV(vs)), SM::kHalf), SM::kPageBytes >> 4,
+                                 desc_sw128_hi(SM::kGroup), idesc_pv, begun ? 1u : 0u);
                     mma_commit_by(leader, &bars[SM::B_PV_DONE + 2 * t + (hg & 1)]);
-                    mma_commit_by(leader, &bars[SM::B_V_EMPTY + vs]);
-                    begun = true;
-                    ++hg;
+                    if (t) begun1 = true, ++hg1;
+                    else begun0 = true, ++hg0;
                 }
+                if (ok) mma_commit_by(leader, &bars[SM::B_V_EMPTY + vs]);
                 if (++vs == NV) vs = 0, ++vn;
             }
-            if (ok && part) {
-                mma_commit_by(leader, &bars[SM::B_O_DONE + t]);
-                ++own;
-            }
+            if (ok && begun0) mma_commit_by(leader, &bars[SM::B_O_DONE]), ++own0;
+            if (ok && begun1) mma_commit_by(leader, &bars[SM::B_O_DONE + 1]), ++own1;
         }
-        mma_commit_by(leader, &bars[SM::B_DRAIN + 1 + t]);
-        if (leader) mbar_drain(&bars[SM::B_DRAIN + 1 + t], 0);
+        mma_commit_by(leader, &bars[SM::B_DRAIN + 1]);
+        if (leader) mbar_drain(&bars[SM::B_DRAIN + 1], 0);
     } else if (warp >= 8) {
         // ------------------------------------------------------------ rotation
         // Thread rt of group r: 16-byte chunk pair c (dimensions 8 c .. and d/2 + 8 c ..) of N consecutive
@@ -492,7 +575,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         // advance by one position, a rotation by table row 1.  Keys of nodes have positions of their own.
         constexpr int N = 64 * CP / 128;                 // keys a thread
         const int r = warp >> 2 & 1, rt = tid & 127, c = rt % CP, k0 = rt / CP * N, page = rt >> 5;
-        constexpr uint32_t o_hi = D == 128 ? SM::kHalfUnit : 0u;
         const int c_hi = D == 128 ? c : c + 4;
         const float scale = 1.4426950408889634f * (D == 128 ? 0.08838834764831845f : 0.125f);   // log2(e) / sqrt(d)
         auto load_row = [&](int32_t pos, float4 (&cs)[4]) {
@@ -500,15 +582,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
             for (int e = 0; e < 4; ++e) cs[e] = src[e];
         };
-        Angles step;
-        uint64_t minus_step[4];
-        {
-            float4 cs[4];
-            load_row(1, cs);
-            step.set(cs);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) minus_step[e] = f2_neg(step.S[e]);
-        }
+        // key k0 + i: 16-byte chunk c of a row sits at c ^ (row & 7), and k0 is a multiple of N
+        const uint32_t a_k = smem_u32(smem + SM::oK) + (k0 >> 3) * SM::kGroup + sw128_off(k0 & 7, c);
+        auto turn_key = [&](uint32_t at, int i, bool have, const Angles& a, uint32_t& odd) {
+            const uint32_t lo_at = (at ^ (i << 4)) + i * 128, hi_at = D == 128 ? lo_at + SM::kHalf : lo_at ^ 64u;
+            uint4 lo = lds_128(lo_at), hi = lds_128(hi_at);
+            if (!have) lo = hi = make_uint4(0, 0, 0, 0);                      // (may hold anything)
+            a.turn(lo, hi, odd);
+            sts_128(lo_at, lo);
+            sts_128(hi_at, hi);
+        };
         uint32_t odd = 0;                                // NaN where a rotated value is not finite
         int kc = 0;
         bool ok = true;
@@ -523,9 +606,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             auto position = [&](int jj) { return pos_row[min((w.jb + jj) * kTreePagesPerUnit + page, n_pages - 1)] + (k0 & 15); };
             auto row_of = [&](int32_t pos) { return pos >= 0 && pos < p.max_pos ? pos : 0; };
             const int j0 = (kc & 1) == r ? 0 : 1;
-            int32_t pos_n = position(j0 + 2);
-            float4 cs[4];
-            load_row(row_of(position(j0)), cs);
+            int32_t pos_n = position(j0);
             // ---- the run's queries: chunk pair c of rows th / CP, + 256 / CP, ... (head by head, so that a
             // thread mostly stays with one node and its cos/sin row)
             ok = it == 0 || mbar_wait(&bars[SM::B_Q_EMPTY], (it - 1) & 1, abort_flag);
@@ -535,11 +616,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 constexpr int STEP = 256 / CP;
                 int32_t last = -1;
                 Angles a;
-                for (int x0 = th / CP; x0 < (w.single ? 1 : 2) * kTileRows; x0 += 4 * STEP) {
-                    uint4 lo[4], hi[4];
-                    int tok[4];
+                for (int x0 = th / CP; x0 < (w.single ? 1 : 2) * kTileRows; x0 += 2 * STEP) {
+                    uint4 lo[2], hi[2];
+                    int tok[2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         const int x = x0 + i * STEP, y = x % kTileRows;
                         lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
                         tok[i] = w.pair * tpp + x / kTileRows * tpt + (y & (tpt - 1));
@@ -550,7 +631,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         const int x = x0 + i * STEP, y = x % kTileRows;
                         if (tok[i] < w.add) {
                             if (tok[i] != last) {
@@ -575,6 +656,15 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 mbar_arrive(&bars[SM::B_Q_FULL]);
             }
             // ---- its keys
+            float4 cs[4];
+            load_row(1, cs);
+            Angles step;
+            uint64_t minus_step[4];
+            step.set(cs);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) minus_step[e] = f2_neg(step.S[e]);
+            load_row(row_of(pos_n), cs);
+            pos_n = position(j0 + 2);
             for (int jj = j0; jj < w.n_loc; jj += 2) {
                 const int u = kc + jj, ks = u % NK;
                 const int slot0 = (w.jb + jj) * kTreeUnit;
@@ -582,29 +672,29 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 const uint2 meta = s_meta[u % SM::kMeta];
                 const uint32_t gone = ((page & 2 ? meta.y : meta.x) >> (page & 1) * 16) & 0xFFFFu;
-                const bool nodes = slot0 + (page + 1) * kPage > w.seq;       // (the same for the warp)
-                uint8_t* stage = sK(ks);
+                const uint32_t at = a_k + ks * SM::kUnit;
                 Angles a;
                 a.set(cs);
-#pragma unroll 2
-                for (int i = 0; i < N; ++i) {
-                    const int key = k0 + i;
-                    const bool have = !(gone >> (key & 15) & 1u);
-                    if (nodes && have && slot0 + key >= w.seq) {
-                        const int32_t pos = p.row_pos[w.row_base + slot0 + key - w.seq];
-                        if (pos < 0 || pos >= p.max_pos) set_dev_error(kDevErrBounds);
-                        float4 f[4];
-                        load_row(row_of(pos), f);
-                        a.set(f);
+                if (slot0 + (page + 1) * kPage <= w.seq) {                    // (the same for the warp)
+#pragma unroll 1
+                    for (int i = 0; i < N; ++i) {
+                        turn_key(at, i, !(gone >> ((k0 & 15) + i) & 1u), a, odd);
+                        a.advance(step, minus_step);
                     }
-                    uint4* plo = reinterpret_cast<uint4*>(stage + sw128_off(key, c));
-                    uint4* phi = reinterpret_cast<uint4*>(stage + o_hi + sw128_off(key, c_hi));
-                    uint4 lo = *plo, hi = *phi;
-                    if (!have) lo = hi = make_uint4(0, 0, 0, 0);     // (may hold anything)
-                    a.turn(lo, hi, odd);
-                    a.advance(step, minus_step);
-                    *plo = lo;
-                    *phi = hi;
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < N; ++i) {
+                        const int key = k0 + i;
+                        const bool have = !(gone >> (key & 15) & 1u);
+                        if (have && slot0 + key >= w.seq) {
+                            const int32_t pos = p.row_pos[w.row_base + slot0 + key - w.seq];
+                            if (pos < 0 || pos >= p.max_pos) set_dev_error(kDevErrBounds);
+                            load_row(row_of(pos), cs);
+                            a.set(cs);
+                        }
+                        turn_key(at, i, have, a, odd);
+                        a.advance(step, minus_step);
+                    }
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bars[SM::B_K_ROT + ks]);
@@ -648,62 +738,73 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         hide0 |= ~(uint32_t)see;
                         hide1 |= ~(uint32_t)(see >> 32);
                     }
-                    const bool full = __all_sync(0xffffffffu, (hide0 | hide1) == 0u);
-                    uint32_t sv[64];
-                    tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-                    tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-                    tmem_ld_wait();
-                    if (!full) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            if (hide0 >> e & 1u) sv[e] = __float_as_uint(-INFINITY);
-                            if (hide1 >> e & 1u) sv[32 + e] = __float_as_uint(-INFINITY);
-                        }
-                    }
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int e = 0; e < 64; e += 8) {
-                        m4[0] = max3f(m4[0], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
-                        m4[1] = max3f(m4[1], __uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]));
-                        m4[2] = max3f(m4[2], __uint_as_float(sv[e + 4]), __uint_as_float(sv[e + 5]));
-                        m4[3] = max3f(m4[3], __uint_as_float(sv[e + 6]), __uint_as_float(sv[e + 7]));
-                    }
-                    const float m_new = fmaxf(m_run, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-                    const bool need = m_new > m_run + 8.0f;     // lazy rescale: keep P <= 2^8
-                    const float alpha = need ? ex2(m_run - m_new) : 1.0f;
-                    if (need) { l_run *= alpha; m_run = m_new; }
-                    const float msub = m_run == -INFINITY ? 0.f : m_run;
-                    const uint64_t negm2 = f2_pack(-msub, -msub);
-                    uint64_t acc2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float d0, d1;
-                        f2_unpack(f2_add(f2_pack(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), negm2), d0, d1);
-                        const float p0 = ex2(d0), p1 = ex2(d1);
-                        acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(p0, p1));
-                        pk[e] = pack_bf16x2(p0, p1);   // bf16 like the values they meet (an MMA's operands share a type)
-                    }
-                    tmem_st32(tS, pk);
-                    float a0, a1, b0, b1;
-                    f2_unpack(acc2[0], a0, a1);
-                    f2_unpack(acc2[1], b0, b1);
-                    l_run += (a0 + b0) + (a1 + b1);
-                    if (q > 0 && __any_sync(0xffffffffu, need)) {
-                        // every earlier P V of this chain must be done before O is rescaled
-                        ok = mbar_wait(&bars[SM::B_PV_DONE + 2 * t + (1 - buf)], ((hg - 1) >> 1) & 1, abort_flag);
-                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                        tc_fence_after();
+                    // Half a unit at a time (a loop body that the instruction cache holds beside the other roles').
 #pragma unroll 1
-                        for (int cc = 0; cc < D / 32; ++cc) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + t * 128 + cc * 32, o);
-                            tmem_ld_wait();
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t sv[32];
+                        tmem_ld32(tS + 32 * h, sv);
+                        tmem_ld_wait();
+                        const uint32_t hide = h ? hide1 : hide0;
+                        if (__any_sync(0xffffffffu, hide != 0u)) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st32(tO + t * 128 + cc * 32, o);
+                            for (int e = 0; e < 32; ++e)
+                                if (hide >> e & 1u) sv[e] = __float_as_uint(-INFINITY);
                         }
+                        float m2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            m2[e & 1] = max3f(m2[e & 1], __uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1]));
+                        const float m_new = fmaxf(m2[0], m2[1]);
+                        // The reference of the exponentials is a whole number, so that what it moves by is a power
+                        // of two and rounds nothing; it moves where a score passes it by more than 2^8.
+                        const bool need = m_new > m_run + 8.0f;
+                        if (__any_sync(0xffffffffu, need)) {
+                            const float to = need ? ceilf(m_new) : m_run, alpha = need ? ex2(m_run - to) : 1.0f;
+                            m_run = to;
+                            l_run *= alpha;
+                            if (q > 0) {       // every earlier P V of this chain must be done before O is rescaled
+                                ok = mbar_wait(&bars[SM::B_PV_DONE + 2 * t + (1 - buf)], ((hg - 1) >> 1) & 1, abort_flag);
+                                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                                tc_fence_after();
+                            }
+#pragma unroll 1
+                            for (int cc = q > 0 ? 0 : D / 16; cc < D / 16; ++cc) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + t * 128 + cc * 16, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st16(tO + t * 128 + cc * 16, o);
+                            }
+                            if (h == 1) {      // and the weights of the first half
+                                uint32_t o[16];
+                                tmem_st_wait();
+                                tmem_ld16(tS, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = pack_bf16x2(bf16_lo(o[e]) * alpha, bf16_hi(o[e]) * alpha);
+                                tmem_st16(tS, o);
+                            }
+                        }
+                        const float msub = m_run == -INFINITY ? 0.f : m_run;
+                        const uint64_t negm2 = f2_pack(-msub, -msub);
+                        uint64_t acc2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float d0, d1;
+                            f2_unpack(f2_add(f2_pack(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), negm2), d0, d1);
+                            const float p0 = ex2(d0), p1 = ex2(d1);
+                            acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(p0, p1));
+                            pk[e] = pack_bf16x2(p0, p1);   // bf16 like the values they meet (an MMA's operands share a type)
+                        }
+                        tmem_st16(tS + 16 * h, pk);
+                        float a0, a1, b0, b1;
+                        f2_unpack(acc2[0], a0, a1);
+                        f2_unpack(acc2[1], b0, b1);
+                        l_run += (a0 + b0) + (a1 + b1);
                     }
+                    if (!ok) break;
                     tmem_st_wait();
                 }
                 tc_fence_before();

@@ -47,8 +47,8 @@ bool get_encode() {
 // encoding off the per-call host path when a caller reuses its buffers from call to call.
 struct MapKey {
     const void* base;
-    uint64_t dims[3], strides[2];
-    uint32_t box[3];
+    uint64_t dims[4], strides[3];
+    uint32_t box[4];
     int32_t rank, dt;
 };
 struct MapEntry {
@@ -66,7 +66,7 @@ pcf_status encode_cached(CUtensorMap* m, const MapKey& k) {
             return PCF_OK;
         }
     if (!get_encode()) return PCF_ERR_CUDA;
-    const cuuint32_t es[3] = {1, 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
     CUresult r = g_encode(m, static_cast<CUtensorMapDataType>(k.dt), k.rank, const_cast<void*>(k.base), k.dims,
                           k.strides, k.box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -115,6 +115,28 @@ pcf_status make_map_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_
     k.box[1] = 1;
     k.box[2] = box2;
     k.rank = 3;
+    k.dt = static_cast<int32_t>(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+    return encode_cached(m, k);
+}
+
+// A pool of rows of 128 bf16 in groups of eight, [rows / 8][half][8][64]: a box of two groups is a page, each
+// half of a group a block of 128-byte rows, 128-byte swizzle.
+pcf_status make_map_pages(CUtensorMap* m, const void* base, uint64_t rows) {
+    MapKey k;
+    std::memset(&k, 0, sizeof(k));
+    k.base = base;
+    k.dims[0] = 64;
+    k.dims[1] = 8;
+    k.dims[2] = 2;
+    k.dims[3] = rows / 8;
+    k.strides[0] = 256;
+    k.strides[1] = 128;
+    k.strides[2] = 8 * 256;
+    k.box[0] = 64;
+    k.box[1] = 8;
+    k.box[2] = 2;
+    k.box[3] = kPage / 8;
+    k.rank = 4;
     k.dt = static_cast<int32_t>(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
     return encode_cached(m, k);
 }
@@ -1158,8 +1180,10 @@ pcf_status tree_attention_impl(const pcf_chunk_dims& d, const TreeParams& p, con
     CUtensorMap tk, tv;
     pcf_status s;
     const uint64_t rows = (uint64_t)d.n_phys_pages * d.n_kv_heads * kPage;
-    if ((s = make_map_2d(&tk, k_pool, D, rows, D * 2, kPage)) != PCF_OK) return s;
-    if ((s = make_map_2d(&tv, v_pool, D, rows, D * 2, kPage)) != PCF_OK) return s;
+    auto map = [&](CUtensorMap* m, const uint16_t* pool) {
+        return D == 128 ? make_map_pages(m, pool, rows) : make_map_2d(m, pool, D, rows, D * 2, kPage);
+    };
+    if ((s = map(&tk, k_pool)) != PCF_OK || (s = map(&tv, v_pool)) != PCF_OK) return s;
     using SM = TreeSmem<D>;
     auto kern = tree_attn_kernel<D>;
     if ((s = set_smem(kern, SM::kAlloc)) != PCF_OK) return s;
