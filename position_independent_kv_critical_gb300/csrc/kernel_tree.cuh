@@ -10,12 +10,12 @@
 // cores bound it about alike at 256 rows (a unit of 64 keys and values, 32 KB at d = 128, takes an SM 1400
 // cycles at the copy rate and its four products of two row tiles 1280), HBM alone below.  So the keys are
 // rotated where they are used, in shared memory: no copy of them is written or read again.  One block an SM,
-// nineteen warps; a run is one (request, kv head, row pair) or the part of one that a block has, dealt by
+// twenty warps; a run is one (request, kv head, row pair) or the part of one that a block has, dealt by
 // pcf_tree_tables in contiguous parts of equal weight.
 //   warps  0-7   softmax of chain 0 (warps 0-3) and 1: S row from TMEM, excluded slots and other branches
 //                hidden, online softmax (lazy rescale), P -> TMEM over the S columns, O epilogue
 //   warps  8-15  two groups of four, units in turn: a run's queries, then the keys, bf16 in, rotated fp16 out
-//   warp  16     runs in order; a unit's four pages of keys and of values (TMA), its hidden slots
+//   warp  16     runs in order; a unit's four pages of keys (TMA), its hidden slots; warp 19 those of values
 //   warp  17     Q K^T issue (and the TMEM allocation)
 //   warp  18     P V issue; value rows of hidden slots become zeros before it
 // With more than 128 rows the chains are the pair's two row tiles and both take every unit.  With up to 128
@@ -51,7 +51,7 @@ struct TreeParams {
     int32_t n, max_pages, words, hq, hkv, n_phys, max_pos, blocks, tag;
 };
 
-constexpr int kTreeAttnThreads = 608;
+constexpr int kTreeAttnThreads = 640;
 constexpr int kTreeReaders = 18;    // warps that read a run: softmax, rotation, issuers
 
 // One run, or the part of one this block has, as warp 16 hands it to the others.
@@ -373,8 +373,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         else tma_load_2d(dst + lane * SM::kPageBytes, map, bar, 0, y);
     };
 
-    if (warp == 16) {
-        // ------------------------------------------------------------ runs, K copies
+    if (warp == 16 || warp == 19) {
+        // ------------------------------------------------------------ runs, K copies (warp 16), V copies (warp 19)
+        const bool val = warp == 19;
+        const int stages = val ? NV : NK;
+        uint8_t* ring = val ? sV(0) : sK(0);
+        const CUtensorMap* map = val ? &tm_v : &tm_k;
+        uint64_t* raw = &bars[val ? SM::B_V_RAW : SM::B_K_RAW];
+        uint64_t* empty = &bars[val ? SM::B_V_EMPTY : SM::B_K_EMPTY];
         const int32_t* seq = p.plan + tree_array(TA_SEQ, p.n);
         const int32_t* add = p.plan + tree_array(TA_NEW, p.n);
         const int32_t* row = p.plan + tree_array(TA_ROW, p.n);
@@ -382,7 +388,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         const int4 start = entry[0];
         int left = weight, begins = share.z;             // weight of the run's beginning, where that is in this share
         int32_t req = start.x, kvh = start.y, pair = start.z, unit = start.w;
-        int kc = 0, ks = 0, kn = 0, vs = 0, vn = 0;      // units, places in the rings, their turns
+        int kc = 0, st = 0, turn = 0;                    // units, place in the ring, its turns
         bool ok = true;
         int4 desc = make_int4(0, 0, 0, 0), desc_rows = desc;
         for (int it = 0; ok; ++it) {
@@ -413,7 +419,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     desc_rows = make_int4(w.add, w.row_base, 0, 0);
                 }
             }
-            if (lane == 0) {
+            if (lane == 0 && !val) {
                 ok = it < 2 || mbar_wait(&bars[SM::B_ITEM_EMPTY + (it & 1)], ((it >> 1) - 1) & 1, abort_flag);
                 if (ok) {
                     slots[it & 1] = w;
@@ -424,29 +430,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if (!ok || w.req < 0) break;
             Window v;
             look_up(v, w, w.jb);
-            for (int jj = 0; ok && jj < w.n_loc; ++jj, ++kc) {
+            for (int jj = 0; jj < w.n_loc; ++jj, ++kc) {
                 int32_t y;
                 const uint2 gone = next_unit(v, w, jj, y);
-                // its keys, then its values (one copy of the code: see the note on the instruction cache)
-#pragma unroll 1
-                for (int i = 0; ok && i < 2; ++i) {
-                    const int st = i ? vs : ks, turn = i ? vn : kn;
-                    uint64_t* raw = &bars[(i ? SM::B_V_RAW : SM::B_K_RAW) + st];
-                    if (lane == 0) {
-                        ok = turn == 0 || mbar_wait(&bars[(i ? SM::B_V_EMPTY : SM::B_K_EMPTY) + st], (turn - 1) & 1, abort_flag);
-                        if (ok) {
-                            if (i) s_meta_v[st] = gone;
-                            else s_meta[kc % SM::kMeta] = gone;
-                            mbar_arrive_expect_tx(raw, SM::kUnit);
-                        }
-                    }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (lane == 0) {
+                    ok = turn == 0 || mbar_wait(empty + st, (turn - 1) & 1, abort_flag);
                     if (ok) {
-                        if (lane < kTreePagesPerUnit) copy_page(i ? sV(st) : sK(st), i ? &tm_v : &tm_k, raw, y);
-                        if (i) vs = vs + 1 == NV ? 0 : vs + 1, vn += vs == 0;
-                        else ks = ks + 1 == NK ? 0 : ks + 1, kn += ks == 0;
+                        (val ? s_meta_v + st : s_meta + kc % SM::kMeta)[0] = gone;
+                        mbar_arrive_expect_tx(raw + st, SM::kUnit);
                     }
                 }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                if (lane < kTreePagesPerUnit) copy_page(ring + st * SM::kUnit, map, raw + st, y);
+                if (++st == stages) st = 0, ++turn;
             }
             // the next run
             unit = 0;
@@ -460,16 +457,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
         }
         if (lane == 0) {
-            p.desc[2 * blockIdx.x] = ok ? desc : make_int4(0, 0, 0, 0);
-            p.desc[2 * blockIdx.x + 1] = desc_rows;
-            // every copy lands before the block exits: each stage's last turn
-            for (int s = 0; s < NK; ++s) {
-                const int turns = kn + (s < ks ? 1 : 0);
-                if (turns > 0) mbar_drain(&bars[SM::B_K_RAW + s], (turns - 1) & 1);
+            if (!val) {
+                p.desc[2 * blockIdx.x] = ok ? desc : make_int4(0, 0, 0, 0);
+                p.desc[2 * blockIdx.x + 1] = desc_rows;
             }
-            for (int s = 0; s < NV; ++s) {
-                const int turns = vn + (s < vs ? 1 : 0);
-                if (turns > 0) mbar_drain(&bars[SM::B_V_RAW + s], (turns - 1) & 1);
+            // every copy lands before the block exits: each stage's last turn
+            for (int s = 0; s < stages; ++s) {
+                const int turns = turn + (s < st ? 1 : 0);
+                if (turns > 0) mbar_drain(raw + s, (turns - 1) & 1);
             }
         }
     } else if (warp == 17) {
