@@ -62,11 +62,11 @@ struct TreeItem {
     int32_t seq, add, row_base;
     int32_t slot;               // partial result, or -1: the whole run
     int32_t single;             // its rows fit one tile
+    int32_t code;               // n_loc * 2 + single, -1: no more
 };
 
 template <int D>
 struct TreeSmem {
-    static constexpr int kHalves = D / 64;
     static constexpr int kQ = kTileRows * D * 2;
     static constexpr int kUnit = kTreeUnit * D * 2;
     // A page lands as one box of eight-row groups, a group's halves (64 dimensions, 128-byte rows) one behind the
@@ -139,45 +139,25 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 __device__ __forceinline__ constexpr uint32_t desc_sw128_hi(uint32_t group) {
     return (group >> 4) | (1u << (46 - 32)) | (2u << (61 - 32));
 }
-// As mma_ss_k4, the operands' groups apart by distances of their own.
-__device__ __forceinline__ void mma_ss_k4_by(uint32_t leader, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t a_hi,
-                                             uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+// One lane of the (whole) warp, the same one every time.  Copies and products are issued in its branch: the
+// compiler then knows that one thread is there, and their operands go to uniform registers without a loop over
+// the lanes (eight products of 64 keys took 1300 cycles with a predicate on lane 0, 600 so).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(r)::"memory");
+    return r != 0;
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred L, p, t;\n\t.reg .b64 da, db;\n\t.reg .b32 la, lb;\n\t"
-        "setp.ne.b32 L, %0, 0;\n\t"
-        "setp.ne.b32 p, %7, 0;\n\t"
-        "setp.eq.b32 t, %0, %0;\n\t"
-        "mov.b64 da, {%2, %4};\n\tmov.b64 db, {%3, %5};\n\t"
-        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], da, db, %6, p;\n\t"
-        "add.u32 la, %2, 2;\n\tadd.u32 lb, %3, 2;\n\t"
-        "mov.b64 da, {la, %4};\n\tmov.b64 db, {lb, %5};\n\t"
-        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], da, db, %6, t;\n\t"
-        "add.u32 la, %2, 4;\n\tadd.u32 lb, %3, 4;\n\t"
-        "mov.b64 da, {la, %4};\n\tmov.b64 db, {lb, %5};\n\t"
-        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], da, db, %6, t;\n\t"
-        "add.u32 la, %2, 6;\n\tadd.u32 lb, %3, 6;\n\t"
-        "mov.b64 da, {la, %4};\n\tmov.b64 db, {lb, %5};\n\t"
-        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], da, db, %6, t;\n\t}\n" ::"r"(leader),
-        "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// As mma_ts_k4, a K = 16 step being a page of `page` (in units of 16 bytes).
-__device__ __forceinline__ void mma_ts_pages(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t page,
-                                             uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred L, p, t;\n\t.reg .b64 db;\n\t.reg .b32 ta, lb;\n\t"
-        "setp.ne.b32 L, %0, 0;\n\t"
-        "setp.ne.b32 p, %7, 0;\n\t"
-        "setp.eq.b32 t, %0, %0;\n\t"
-        "mov.b64 db, {%3, %5};\n\t"
-        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], db, %6, p;\n\t"
-        "add.u32 ta, %2, 8;\n\tadd.u32 lb, %3, %4;\n\tmov.b64 db, {lb, %5};\n\t"
-        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], [ta], db, %6, t;\n\t"
-        "add.u32 ta, %2, 16;\n\tadd.u32 lb, lb, %4;\n\tmov.b64 db, {lb, %5};\n\t"
-        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], [ta], db, %6, t;\n\t"
-        "add.u32 ta, %2, 24;\n\tadd.u32 lb, lb, %4;\n\tmov.b64 db, {lb, %5};\n\t"
-        "@L tcgen05.mma.cta_group::1.kind::f16 [%1], [ta], db, %6, t;\n\t}\n" ::"r"(leader),
-        "r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(page), "r"(hi), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -252,7 +232,7 @@ template <int D>
 __global__ void __launch_bounds__(kTreeAttnThreads, 1)
 tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
     using SM = TreeSmem<D>;
-    constexpr int H = SM::kHalves, NK = SM::NK, NV = SM::NV, CP = D / 16;
+    constexpr int NK = SM::NK, NV = SM::NV, CP = D / 16;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::oBar);
@@ -326,6 +306,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (lane == 0) mbar_arrive(&bars[SM::B_ITEM_EMPTY + (it & 1)]);
         return true;
     };
+    // What an issuer needs of it: n_loc * 2 + single, -1 behind the last one.  (A reduction's result is known to be
+    // the same in all lanes, and so is what follows from it: operands of an MMA that are not go through a loop
+    // over the lanes.)
+    auto take_code = [&](int it) -> int {
+        const bool ok = mbar_wait(&bars[SM::B_ITEM_FULL + (it & 1)], (it >> 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) return -1;
+        const int code = __reduce_max_sync(0xffffffffu, slots[it & 1].code);
+        if (lane == 0) mbar_arrive(&bars[SM::B_ITEM_EMPTY + (it & 1)]);
+        return code;
+    };
     // units of a run that a chain takes, unit kc its first one
     auto chain_units = [&](const TreeItem& w, int kc, int t) { return !w.single ? w.n_loc : (w.n_loc + ((kc & 1) == t ? 1 : 0)) >> 1; };
 
@@ -355,24 +345,21 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         v.y_n = (v.y_n * p.hkv + w.kvh) * (D == 128 ? 2 : kPage);      // in the map's rows: groups of eight, or single ones
     };
-    // unit jj of the run: the window moves on, this lane's page (lanes 0-3) and the unit's hidden bits
-    auto next_unit = [&](Window& v, const TreeItem& w, int jj, int32_t& y) {
+    // unit jj of the run: the window moves on; the unit's pages and hidden bits (a reduction's result is known to be
+    // the same in all lanes)
+    auto next_unit = [&](Window& v, const TreeItem& w, int jj, int32_t (&y)[kTreePagesPerUnit]) {
         if ((jj & 7) == 0) {
             v.y = v.y_n;
             v.gone = v.gone_n;
             if (jj + 8 < w.n_loc) look_up(v, w, w.jb + jj + 8);
         }
         const int at = (jj & 7) * kTreePagesPerUnit;
-        y = __shfl_sync(0xffffffffu, v.y, at + (lane & 3));
+#pragma unroll
+        for (int m = 0; m < kTreePagesPerUnit; ++m) y[m] = __reduce_max_sync(0xffffffffu, lane == at + m ? v.y : 0);
         const uint32_t g0 = __shfl_sync(0xffffffffu, v.gone, at), g1 = __shfl_sync(0xffffffffu, v.gone, at + 1),
                        g2 = __shfl_sync(0xffffffffu, v.gone, at + 2), g3 = __shfl_sync(0xffffffffu, v.gone, at + 3);
         return make_uint2(g0 | g1 << 16, g2 | g3 << 16);
     };
-    auto copy_page = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int32_t y) {
-        if constexpr (D == 128) tma_load_4d(dst + lane * SM::kPageBytes, map, bar, 0, 0, 0, y);
-        else tma_load_2d(dst + lane * SM::kPageBytes, map, bar, 0, y);
-    };
-
     if (warp == 16 || warp == 19) {
         // ------------------------------------------------------------ runs, K copies (warp 16), V copies (warp 19)
         const bool val = warp == 19;
@@ -419,6 +406,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     desc_rows = make_int4(w.add, w.row_base, 0, 0);
                 }
             }
+            w.code = w.req < 0 ? -1 : 2 * w.n_loc + w.single;
             if (lane == 0 && !val) {
                 ok = it < 2 || mbar_wait(&bars[SM::B_ITEM_EMPTY + (it & 1)], ((it >> 1) - 1) & 1, abort_flag);
                 if (ok) {
@@ -431,18 +419,21 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             Window v;
             look_up(v, w, w.jb);
             for (int jj = 0; jj < w.n_loc; ++jj, ++kc) {
-                int32_t y;
+                int32_t y[kTreePagesPerUnit];
                 const uint2 gone = next_unit(v, w, jj, y);
-                if (lane == 0) {
-                    ok = turn == 0 || mbar_wait(empty + st, (turn - 1) & 1, abort_flag);
-                    if (ok) {
-                        (val ? s_meta_v + st : s_meta + kc % SM::kMeta)[0] = gone;
-                        mbar_arrive_expect_tx(raw + st, SM::kUnit);
+                ok = turn == 0 || mbar_wait(empty + st, (turn - 1) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                if (elect_one()) {
+                    (val ? s_meta_v + st : s_meta + kc % SM::kMeta)[0] = gone;
+                    mbar_arrive_expect_tx(raw + st, SM::kUnit);
+#pragma unroll
+                    for (int m = 0; m < kTreePagesPerUnit; ++m) {
+                        uint8_t* dst = ring + st * SM::kUnit + m * SM::kPageBytes;
+                        if constexpr (D == 128) tma_load_4d(dst, map, raw + st, 0, 0, 0, y[m]);
+                        else tma_load_2d(dst, map, raw + st, 0, y[m]);
                     }
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                if (lane < kTreePagesPerUnit) copy_page(ring + st * SM::kUnit, map, raw + st, y);
+                __syncwarp();
                 if (++st == stages) st = 0, ++turn;
             }
             // the next run
@@ -470,18 +461,17 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     } else if (warp == 17) {
         // ------------------------------------------------------------ Q K^T
         constexpr uint32_t idesc_qk = idesc_f16(128, kTreeUnit);
-        const uint32_t leader = lane == 0 ? 1u : 0u;
         int kc = 0, hg0 = 0, hg1 = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
-            TreeItem w;
-            ok = take_item(it, w);
-            if (!ok || w.req < 0) break;
+            const int code = take_code(it), n_loc = code >> 1;
+            const bool single = code & 1;
+            if (code < 0) break;
             ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_Q_FULL], it & 1, abort_flag));
-            for (int jj = 0; ok && jj < w.n_loc; ++jj, ++kc) {
+            for (int jj = 0; ok && jj < n_loc; ++jj, ++kc) {
                 const int ks = kc % NK;
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_K_ROT + ks], (kc / NK) & 1, abort_flag));
-                const int t0 = w.single ? kc & 1 : 0, t1 = w.single ? t0 : 1;
+                const int t0 = single ? kc & 1 : 0, t1 = single ? t0 : 1;
 #pragma unroll 1
                 for (int t = t0; ok && t <= t1; ++t) {
                     const int hg = t ? hg1 : hg0;
@@ -489,36 +479,42 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                                                                      ((hg - 2) >> 1) & 1, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t aQ = desc_sw128_lo(smem_u32(smem + (w.single ? 0 : t) * SM::kQ), 16);
+                    const uint32_t aQ = desc_sw128_lo(smem_u32(smem + (single ? 0 : t) * SM::kQ), 16);
                     const uint32_t aK = desc_sw128_lo(smem_u32(sK(ks)), 16);
                     const uint32_t tS = tmem + t * 128 + (hg & 1) * 64;
-#pragma unroll 1
-                    for (int k4 = 0; k4 < H; ++k4)
-                        mma_ss_k4_by(leader, tS, aQ + k4 * 1024, aK + k4 * (SM::kHalf >> 4), kDescSw128Hi,
-                                     desc_sw128_hi(SM::kGroup), idesc_qk, k4 > 0 ? 1u : 0u);
-                    mma_commit_by(leader, &bars[SM::B_S_FULL + 2 * t + (hg & 1)]);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_ss(tS, desc_of(aQ + (k >> 2) * 1024 + (k & 3) * 2, kDescSw128Hi),
+                                   desc_of(aK + (k >> 2) * (SM::kHalf >> 4) + (k & 3) * 2, desc_sw128_hi(SM::kGroup)), idesc_qk, k);
+                        mma_commit(&bars[SM::B_S_FULL + 2 * t + (hg & 1)]);
+                        if (t == t1) mma_commit(&bars[SM::B_K_EMPTY + ks]);
+                    }
+                    __syncwarp();
                     if (t) ++hg1; else ++hg0;
                 }
-                if (ok) mma_commit_by(leader, &bars[SM::B_K_EMPTY + ks]);
             }
-            if (ok) mma_commit_by(leader, &bars[SM::B_Q_EMPTY]);
+            if (ok && elect_one()) mma_commit(&bars[SM::B_Q_EMPTY]);
+            __syncwarp();
         }
-        mma_commit_by(leader, &bars[SM::B_DRAIN]);
-        if (leader) mbar_drain(&bars[SM::B_DRAIN], 0);
+        if (elect_one()) {
+            mma_commit(&bars[SM::B_DRAIN]);
+            mbar_drain(&bars[SM::B_DRAIN], 0);
+        }
+        __syncwarp();
     } else if (warp == 18) {
         // ------------------------------------------------------------ P V
         // The value rows of hidden slots become zeros first (they may hold anything, and a weight of zero
         // does not silence a NaN).
         constexpr uint32_t idesc_pv = idesc_bf16(128, D, true);
-        const uint32_t leader = lane == 0 ? 1u : 0u;
         int kc = 0, vs = 0, vn = 0, hg0 = 0, hg1 = 0, own0 = 0, own1 = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
-            TreeItem w;
-            ok = take_item(it, w);
-            if (!ok || w.req < 0) break;
+            const int code = take_code(it), n_loc = code >> 1;
+            const bool single = code & 1;
+            if (code < 0) break;
             bool begun0 = false, begun1 = false;
-            for (int jj = 0; ok && jj < w.n_loc; ++jj, ++kc) {
+            for (int jj = 0; ok && jj < n_loc; ++jj, ++kc) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_V_RAW + vs], vn & 1, abort_flag));
                 if (!ok) break;
                 const uint2 gone = s_meta_v[vs];
@@ -538,7 +534,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                const int t0 = w.single ? kc & 1 : 0, t1 = w.single ? t0 : 1;
+                const int t0 = single ? kc & 1 : 0, t1 = single ? t0 : 1;
 #pragma unroll 1
                 for (int t = t0; ok && t <= t1; ++t) {
                     const int hg = t ? hg1 : hg0, own = t ? own1 : own0;
@@ -548,21 +544,35 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                                         (begun || own == 0 || mbar_wait(&bars[SM::B_O_FREE + t], (own - 1) & 1, abort_flag)));
                     if (!ok) break;
                     tc_fence_after();
-                    mma_ts_pages(leader, tmem + kTmemO + t * 128, tmem + t * 128 + (hg & 1) * 64,
-                                 desc_sw128_lo(smem_u32(sV(vs)), SM::kHalf), SM::kPageBytes >> 4,
-                                 desc_sw128_hi(SM::kGroup), idesc_pv, begun ? 1u : 0u);
-                    mma_commit_by(leader, &bars[SM::B_PV_DONE + 2 * t + (hg & 1)]);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kTreePagesPerUnit; ++k)
+                            mma_ts(tmem + kTmemO + t * 128, tmem + t * 128 + (hg & 1) * 64 + 8 * k,
+                                   desc_of(desc_sw128_lo(smem_u32(sV(vs)), SM::kHalf) + k * (SM::kPageBytes >> 4), desc_sw128_hi(SM::kGroup)),
+                                   idesc_pv, k > 0 ? 1u : begun ? 1u : 0u);
+                        mma_commit(&bars[SM::B_PV_DONE + 2 * t + (hg & 1)]);
+                        if (t == t1) mma_commit(&bars[SM::B_V_EMPTY + vs]);
+                    }
+                    __syncwarp();
                     if (t) begun1 = true, ++hg1;
                     else begun0 = true, ++hg0;
                 }
-                if (ok) mma_commit_by(leader, &bars[SM::B_V_EMPTY + vs]);
                 if (++vs == NV) vs = 0, ++vn;
             }
-            if (ok && begun0) mma_commit_by(leader, &bars[SM::B_O_DONE]), ++own0;
-            if (ok && begun1) mma_commit_by(leader, &bars[SM::B_O_DONE + 1]), ++own1;
+            if (!ok) break;
+            if (elect_one()) {
+                if (begun0) mma_commit(&bars[SM::B_O_DONE]);
+                if (begun1) mma_commit(&bars[SM::B_O_DONE + 1]);
+            }
+            __syncwarp();
+            own0 += begun0;
+            own1 += begun1;
         }
-        mma_commit_by(leader, &bars[SM::B_DRAIN + 1]);
-        if (leader) mbar_drain(&bars[SM::B_DRAIN + 1], 0);
+        if (elect_one()) {
+            mma_commit(&bars[SM::B_DRAIN + 1]);
+            mbar_drain(&bars[SM::B_DRAIN + 1], 0);
+        }
+        __syncwarp();
     } else if (warp >= 8) {
         // ------------------------------------------------------------ rotation
         // Thread rt of group r: 16-byte chunk pair c (dimensions 8 c .. and d/2 + 8 c ..) of N consecutive
