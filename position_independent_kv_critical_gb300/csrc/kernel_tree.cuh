@@ -14,10 +14,12 @@
 // pcf_tree_tables in contiguous parts of equal weight.
 //   warps  0-7   softmax of chain 0 (warps 0-3) and 1: S row from TMEM, excluded slots and other branches
 //                hidden, online softmax (lazy rescale), P -> TMEM over the S columns, O epilogue
-//   warps  8-15  two groups of four, units in turn: a run's queries, then the keys, bf16 in, rotated fp16 out
-//   warp  16     runs in order; a unit's four pages of keys (TMA), its hidden slots; warp 19 those of values
+//   warps  8-15  two groups of four, units in turn: a run's queries, then the keys, bf16 in, rotated fp16 out;
+//                values of hidden slots become zeros
+//   warp  16     runs in order; a unit's four pages of keys (TMA), its hidden slots
+//   warp  19     the same pages of values
 //   warp  17     Q K^T issue (and the TMEM allocation)
-//   warp  18     P V issue; value rows of hidden slots become zeros before it
+//   warp  18     P V issue
 // With more than 128 rows the chains are the pair's two row tiles and both take every unit.  With up to 128
 // there is one tile, and the chains take its units in turn, each with sums of its own that meet in the
 // epilogue: eight softmax warps share what four would do, and a unit's way through the chain
@@ -85,8 +87,7 @@ struct TreeSmem {
     static constexpr int oV = oK + NK * kUnit;
     static constexpr int oMl = oV + NV * kUnit;                // [128] chain 1's maximum and sum
     static constexpr int oMeta = oMl + kTileRows * 8;          // [kMeta] a unit's 64 hidden bits
-    static constexpr int oMetaV = oMeta + kMeta * 8;           // [NV] the same for a stage's values
-    static constexpr int oItem = oMetaV + NV * 8;
+    static constexpr int oItem = oMeta + kMeta * 8;
     static constexpr int oBar = oItem + 2 * (int)sizeof(TreeItem);
     // barriers
     static constexpr int B_ITEM_FULL = 0, B_ITEM_EMPTY = 2, B_Q_FULL = 4, B_Q_EMPTY = 5, B_S_FULL = 6, B_P_FULL = 10,
@@ -101,8 +102,8 @@ struct TreeSmem {
 
 // A wait sees the parity of a phase only, so a phase may end at most once before each of its waiters has
 // passed it.  What keeps each barrier to that:
-//   ITEM, K_ROT, V_RAW   every waiter passes every phase;
-//   K_RAW           a stage belongs to one rotating group (NK is even), which passes every phase of it;
+//   ITEM, K_ROT     every waiter passes every phase;
+//   K_RAW, V_RAW    a stage belongs to one rotating group (NK and NV are even), which passes every phase of it;
 //   Q, S, P, PV_DONE, O_DONE, O_FREE   as in the many-row kernel: counted by the units and runs that a chain
 //                   takes part in; in a run of one tile the threads of chain 0 arrive on both O_FREE;
 //   ML              chain 1's sums of a run of one tile: written again only behind chain 1's next result, whose
@@ -240,7 +241,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
     TreeItem* slots = reinterpret_cast<TreeItem*>(smem + SM::oItem);
     uint2* s_meta = reinterpret_cast<uint2*>(smem + SM::oMeta);
-    uint2* s_meta_v = reinterpret_cast<uint2*>(smem + SM::oMetaV);
     float2* s_ml = reinterpret_cast<float2*>(smem + SM::oMl);
     auto sK = [&](int st) { return smem + SM::oK + st * SM::kUnit; };
     auto sV = [&](int st) { return smem + SM::oV + st * SM::kUnit; };
@@ -424,7 +424,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 ok = turn == 0 || mbar_wait(empty + st, (turn - 1) & 1, abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 if (elect_one()) {
-                    (val ? s_meta_v + st : s_meta + kc % SM::kMeta)[0] = gone;
+                    if (!val) s_meta[kc % SM::kMeta] = gone;
                     mbar_arrive_expect_tx(raw + st, SM::kUnit);
 #pragma unroll
                     for (int m = 0; m < kTreePagesPerUnit; ++m) {
@@ -503,11 +503,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         __syncwarp();
     } else if (warp == 18) {
-        // ------------------------------------------------------------ P V
-        // The value rows of hidden slots become zeros first (they may hold anything, and a weight of zero
-        // does not silence a NaN).
+        // ------------------------------------------------------------ P V (a unit's weights come behind its scores,
+        // those behind its values: K_ROT)
         constexpr uint32_t idesc_pv = idesc_bf16(128, D, true);
-        int kc = 0, vs = 0, vn = 0, hg0 = 0, hg1 = 0, own0 = 0, own1 = 0;
+        int kc = 0, vs = 0, hg0 = 0, hg1 = 0, own0 = 0, own1 = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int code = take_code(it), n_loc = code >> 1;
@@ -515,25 +514,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if (code < 0) break;
             bool begun0 = false, begun1 = false;
             for (int jj = 0; ok && jj < n_loc; ++jj, ++kc) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_V_RAW + vs], vn & 1, abort_flag));
-                if (!ok) break;
-                const uint2 gone = s_meta_v[vs];
-                if ((gone.x | gone.y) != 0u) {
-                    // (D / 8 lanes a row, the rows in turn)
-                    constexpr int LANES = D / 8, ROWS = 32 / LANES;
-                    const int ch = lane % LANES;
-                    uint64_t rest = (uint64_t)gone.y << 32 | gone.x;
-                    for (int i = 0; i < lane / LANES; ++i) rest &= rest - 1;
-                    while (rest != 0) {
-                        const int row = __ffsll((long long)rest) - 1;
-                        *reinterpret_cast<uint4*>(sV(vs) + (row >> 3) * SM::kGroup + (ch >> 3) * SM::kHalf +
-                                                  sw128_off(row & 7, ch & 7)) = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                        for (int i = 0; i < ROWS; ++i) rest &= rest - 1;
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
                 const int t0 = single ? kc & 1 : 0, t1 = single ? t0 : 1;
 #pragma unroll 1
                 for (int t = t0; ok && t <= t1; ++t) {
@@ -557,7 +537,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     if (t) begun1 = true, ++hg1;
                     else begun0 = true, ++hg0;
                 }
-                if (++vs == NV) vs = 0, ++vn;
+                if (++vs == NV) vs = 0;
             }
             if (!ok) break;
             if (elect_one()) {
@@ -700,6 +680,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         turn_key(at, i, have, a, odd);
                         a.advance(step, minus_step);
                     }
+                }
+                // the values have landed too when the keys are handed on, the rows of hidden slots zeros (they may
+                // hold anything, and a weight of zero does not silence a NaN)
+                const int vs = u % NV;
+                ok = mbar_wait(&bars[SM::B_V_RAW + vs], (u / NV) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                if ((meta.x | meta.y) != 0u) {
+                    constexpr int LANES = D / 8, ROWS = 128 / LANES;
+                    const int ch = rt % LANES, row0 = rt / LANES;             // (ROWS is a multiple of 8)
+                    uint8_t* dst = sV(vs) + (row0 >> 3) * SM::kGroup + (ch >> 3) * SM::kHalf + sw128_off(row0 & 7, ch & 7);
+#pragma unroll
+                    for (int i = 0; i < kTreeUnit / ROWS; ++i)
+                        if ((row0 + i * ROWS < 32 ? meta.x >> (row0 + i * ROWS) : meta.y >> (row0 + i * ROWS - 32)) & 1u)
+                            *reinterpret_cast<uint4*>(dst + i * ROWS / 8 * SM::kGroup) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bars[SM::B_K_ROT + ks]);
