@@ -45,7 +45,7 @@ struct TreeParams {
     const uint32_t* seen;       // [max_rows][words]
     const float* rope;
     __nv_bfloat16* out;
-    float* part_o;              // [blocks][2][256][D]
+    float4* part_o;             // [blocks][2][D / 4][256]: a warp's rows side by side
     float2* part_ml;            // [blocks][2][256]
     int4* desc;                 // [blocks][2]: a run begun here that goes on: {last block << 8 | 255, first node, kv head, 0},
                                 //   {nodes, first row, 0, 0}
@@ -177,6 +177,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* src) { asm volatile("prefetch.global.L2 [%0];" ::"l"(src)); }
+
 // Eight frequencies' cos and sin as packed pairs.
 struct Angles {
     uint64_t C[4], S[4];
@@ -251,20 +253,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             mbar_init(&bars[SM::B_ITEM_FULL + s], 1);
             mbar_init(&bars[SM::B_ITEM_EMPTY + s], kTreeReaders);
             mbar_init(&bars[SM::B_O_DONE + s], 1);
-            mbar_init(&bars[SM::B_O_FREE + s], 128);
+            mbar_init(&bars[SM::B_O_FREE + s], 4);
         }
-        mbar_init(&bars[SM::B_Q_FULL], 256);
+        mbar_init(&bars[SM::B_Q_FULL], 8);
         mbar_init(&bars[SM::B_Q_EMPTY], 1);
-        mbar_init(&bars[SM::B_ML], 128);
+        mbar_init(&bars[SM::B_ML], 4);
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars[SM::B_S_FULL + i], 1);
-            mbar_init(&bars[SM::B_P_FULL + i], 128);
+            mbar_init(&bars[SM::B_P_FULL + i], 4);
             mbar_init(&bars[SM::B_PV_DONE + i], 1);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&bars[SM::B_DRAIN + i], 1);
         for (int s = 0; s < NK; ++s) {
             mbar_init(&bars[SM::B_K_RAW + s], 1);
-            mbar_init(&bars[SM::B_K_ROT + s], 128);
+            mbar_init(&bars[SM::B_K_ROT + s], 4);
             mbar_init(&bars[SM::B_K_EMPTY + s], 1);
         }
         for (int s = 0; s < NV; ++s) {
@@ -278,7 +280,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
     grid_dep_wait();
     grid_dep_launch();
-    const int4* entry = reinterpret_cast<const int4*>(p.plan + tree_shares(p.n)) + 2 * blockIdx.x;
+    const int4* entry = reinterpret_cast<const int4*>(p.plan + tree_shares(p.n)) + 3 * blockIdx.x;
     const bool fits = p.plan[T_TAG] == p.tag;
     const int4 share = fits ? entry[1] : make_int4(0, 0, 0, 0);
     const int weight = share.y == p.tag ? share.x : 0;
@@ -315,6 +317,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         const int code = __reduce_max_sync(0xffffffffu, slots[it & 1].code);
         if (lane == 0) mbar_arrive(&bars[SM::B_ITEM_EMPTY + (it & 1)]);
         return code;
+    };
+    // An arrival for the whole warp, behind what its lanes did.  (One a thread: 384 of them a unit took as much of
+    // the shared memory's time as the rotation of its keys.)
+    auto arrive_warp = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
     };
     // units of a run that a chain takes, unit kc its first one
     auto chain_units = [&](const TreeItem& w, int kc, int t) { return !w.single ? w.n_loc : (w.n_loc + ((kc & 1) == t ? 1 : 0)) >> 1; };
@@ -360,6 +368,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                        g2 = __shfl_sync(0xffffffffu, v.gone, at + 2), g3 = __shfl_sync(0xffffffffu, v.gone, at + 3);
         return make_uint2(g0 | g1 << 16, g2 | g3 << 16);
     };
+    // Registers: the block has 96 a thread; the rotation takes 112 (its four keys in flight spill in 96), the softmax
+    // 88 and the others 72 (60,416 of 61,440 in all).
+    if (warp >= 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 16 || warp == 19) {
         // ------------------------------------------------------------ runs, K copies (warp 16), V copies (warp 19)
         const bool val = warp == 19;
@@ -372,7 +384,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         const int32_t* add = p.plan + tree_array(TA_NEW, p.n);
         const int32_t* row = p.plan + tree_array(TA_ROW, p.n);
         const int32_t* work = p.plan + tree_array(TA_WORK, p.n);
-        const int4 start = entry[0];
+        const int4 start = entry[0], lens = entry[2];
         int left = weight, begins = share.z;             // weight of the run's beginning, where that is in this share
         int32_t req = start.x, kvh = start.y, pair = start.z, unit = start.w;
         int kc = 0, st = 0, turn = 0;                    // units, place in the ring, its turns
@@ -390,9 +402,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             w.single = 0;
             int pairs = 1;
             if (left > 0) {
-                w.seq = seq[req];
-                w.add = add[req];
-                w.row_base = row[req];
+                const bool first = it == 0;              // (its lengths came with the share)
+                w.seq = first ? lens.x : seq[req];
+                w.add = first ? lens.y : add[req];
+                w.row_base = first ? lens.z : row[req];
                 w.single = min(tpp, w.add - pair * tpp) << gs <= kTileRows;
                 pairs = tree_pairs(w.add, g);
                 const int all = tree_units(w.seq + w.add);
@@ -553,7 +566,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             mbar_drain(&bars[SM::B_DRAIN + 1], 0);
         }
         __syncwarp();
+    }
     } else if (warp >= 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
         // ------------------------------------------------------------ rotation
         // Thread rt of group r: 16-byte chunk pair c (dimensions 8 c .. and d/2 + 8 c ..) of N consecutive
         // keys, a warp a page; their angles start from the cos/sin row of the first one's position and
@@ -592,53 +607,71 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             auto row_of = [&](int32_t pos) { return pos >= 0 && pos < p.max_pos ? pos : 0; };
             const int j0 = (kc & 1) == r ? 0 : 1;
             int32_t pos_n = position(j0);
-            // ---- the run's queries: chunk pair c of rows th / CP, + 256 / CP, ... (head by head, so that a
-            // thread mostly stays with one node and its cos/sin row)
-            ok = it == 0 || mbar_wait(&bars[SM::B_Q_EMPTY], (it - 1) & 1, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            // ---- the run's queries: chunk pair c of rows th / CP, + 256 / CP, ... of a tile (head by head, so that
+            // with four heads and more a thread stays with one node and its cos/sin row)
             {
-                const int th = tid - 256;
-                constexpr int STEP = 256 / CP;
-                int32_t last = -1;
-                Angles a;
-                for (int x0 = th / CP; x0 < (w.single ? 1 : 2) * kTileRows; x0 += 2 * STEP) {
-                    uint4 lo[2], hi[2];
-                    int tok[2];
+                constexpr int STEP = 256 / CP, R = kTileRows / STEP;
+                const int y0 = (tid - 256) / CP, tiles = w.single ? 1 : 2;
+                auto node_of = [&](int tile, int i) { return w.pair * tpp + tile * tpt + ((y0 + i * STEP) & (tpt - 1)); };
+                int32_t at[2];                             // positions of the tiles' first nodes
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int x = x0 + i * STEP, y = x % kTileRows;
+                for (int tile = 0; tile < 2; ++tile) {
+                    const int tok = node_of(tile, 0);
+                    at[tile] = tile < tiles && tok < w.add ? p.row_pos[w.row_base + tok] : 0;
+                }
+                if (tiles > 1) {                           // the second tile's rows are on their way to L2
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const int tok = node_of(1, i);
+                        if (tok < w.add && (c & 1) == 0)
+                            prefetch_l2(p.q + (w.row_base + tok) * p.q_stride + (int64_t)(w.kvh * g + ((y0 + i * STEP) >> (7 - gs))) * D + 16 * c);
+                    }
+                }
+                Angles a;
+                auto angles = [&](int32_t pos) {
+                    if (pos < 0 || pos >= p.max_pos) set_dev_error(kDevErrBounds);
+                    float4 f[4];
+                    load_row(row_of(pos), f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] = make_float4(f[e].x * scale, f[e].y * scale, f[e].z * scale, f[e].w * scale);
+                    a.set(f);
+                };
+#pragma unroll 1
+                for (int tile = 0; tile < tiles; ++tile) {
+                    uint4 lo[R], hi[R];
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const int y = y0 + i * STEP, tok = node_of(tile, i);
                         lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
-                        tok[i] = w.pair * tpp + x / kTileRows * tpt + (y & (tpt - 1));
-                        if (x < 2 * kTileRows && tok[i] < w.add) {
-                            const __nv_bfloat16* src = p.q + (w.row_base + tok[i]) * p.q_stride + (int64_t)(w.kvh * g + (y >> (7 - gs))) * D;
+                        if (tok < w.add) {
+                            const __nv_bfloat16* src = p.q + (w.row_base + tok) * p.q_stride + (int64_t)(w.kvh * g + (y >> (7 - gs))) * D;
                             lo[i] = *reinterpret_cast<const uint4*>(src + 8 * c);
                             hi[i] = *reinterpret_cast<const uint4*>(src + D / 2 + 8 * c);
                         }
                     }
+                    angles(tile ? at[1] : at[0]);
+                    // (the queries of the run before have been read)
+                    if (tile == 0 && it > 0) {
+                        ok = mbar_wait(&bars[SM::B_Q_EMPTY], (it - 1) & 1, abort_flag);
+                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    }
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int x = x0 + i * STEP, y = x % kTileRows;
-                        if (tok[i] < w.add) {
-                            if (tok[i] != last) {
-                                last = tok[i];
-                                const int32_t pos = p.row_pos[w.row_base + last];
-                                if (pos < 0 || pos >= p.max_pos) set_dev_error(kDevErrBounds);
-                                float4 f[4];
-                                load_row(row_of(pos), f);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) f[e] = make_float4(f[e].x * scale, f[e].y * scale, f[e].z * scale, f[e].w * scale);
-                                a.set(f);
-                            }
-                            a.turn(lo[i], hi[i], odd);
+                    for (int i = 0; i < R; ++i) {
+                        const int y = y0 + i * STEP;
+                        if (i > 0 && tpt > STEP) {         // another node
+                            const int tok = node_of(tile, i);
+                            angles(tok < w.add ? p.row_pos[w.row_base + tok] : 0);
                         }
+                        a.turn(lo[i], hi[i], odd);         // (rows behind the last one stay zeros)
                         const int row = ((y & (tpt - 1)) << gs) + (y >> (7 - gs));
-                        uint8_t* dst = smem + x / kTileRows * SM::kQ;
+                        uint8_t* dst = smem + tile * SM::kQ;
                         *reinterpret_cast<uint4*>(dst + sw128_off(row, c)) = lo[i];
                         *reinterpret_cast<uint4*>(dst + (D == 128 ? kTileRows * 128 : 0) + sw128_off(row, c_hi)) = hi[i];
                     }
                 }
+                if (!ok) break;
                 fence_proxy_async_smem();
-                mbar_arrive(&bars[SM::B_Q_FULL]);
+                arrive_warp(&bars[SM::B_Q_FULL]);
             }
             // ---- its keys
             float4 cs[4];
@@ -696,7 +729,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                             *reinterpret_cast<uint4*>(dst + i * ROWS / 8 * SM::kGroup) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&bars[SM::B_K_ROT + ks]);
+                arrive_warp(&bars[SM::B_K_ROT + ks]);
                 load_row(row_of(pos_n), cs);
                 pos_n = position(jj + 4);
             }
@@ -704,6 +737,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         if (odd != 0u) set_dev_error(kDevErrRange);
     } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // ------------------------------------------------------------ softmax
         const int t = warp >> 2, m = tid & 127;            // row of the tile = TMEM lane
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
@@ -740,25 +774,47 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     // Half a unit at a time (a loop body that the instruction cache holds beside the other roles').
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t sv[32];
-                        tmem_ld32(tS + 32 * h, sv);
-                        tmem_ld_wait();
                         const uint32_t hide = h ? hide1 : hide0;
-                        if (__any_sync(0xffffffffu, hide != 0u)) {
+                        const bool masked = __any_sync(0xffffffffu, hide != 0u);
+                        // A row's reference is the largest of the first scores it sees, and stays while the weights
+                        // against it add up to less than 2^16 in 32 keys: their size costs no precision, and most
+                        // halves need no maximum.  It moves by whole numbers: powers of two round nothing.
+                        uint32_t pk[16];
+                        float sum;
+                        for (bool again = false;; again = true) {
+                            uint32_t sv[32];
+                            tmem_ld32(tS + 32 * h, sv);
+                            tmem_ld_wait();
+                            if (masked) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (hide >> e & 1u) sv[e] = __float_as_uint(-INFINITY);
+                            }
+                            const float msub = m_run == -INFINITY ? 0.f : m_run;
+                            const uint64_t negm2 = f2_pack(-msub, -msub);
+                            uint64_t acc2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float d0, d1;
+                                f2_unpack(f2_add(f2_pack(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), negm2), d0, d1);
+                                const float p0 = ex2(d0), p1 = ex2(d1);
+                                acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(p0, p1));
+                                pk[e] = pack_bf16x2(p0, p1);   // bf16 like the values they meet (an MMA's operands share a type)
+                            }
+                            float a0, a1, b0, b1;
+                            f2_unpack(acc2[0], a0, a1);
+                            f2_unpack(acc2[1], b0, b1);
+                            sum = (a0 + b0) + (a1 + b1);
+                            const bool stale = m_run == -INFINITY || sum > 65536.0f;
+                            if (again || !__any_sync(0xffffffffu, stale)) break;
+                            tmem_ld32(tS + 32 * h, sv);
+                            tmem_ld_wait();
+                            float mx = -INFINITY;
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (hide >> e & 1u) sv[e] = __float_as_uint(-INFINITY);
-                        }
-                        float m2[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            m2[e & 1] = max3f(m2[e & 1], __uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1]));
-                        const float m_new = fmaxf(m2[0], m2[1]);
-                        // The reference of the exponentials is a whole number, so that what it moves by is a power
-                        // of two and rounds nothing; it moves where a score passes it by more than 2^8.
-                        const bool need = m_new > m_run + 8.0f;
-                        if (__any_sync(0xffffffffu, need)) {
-                            const float to = need ? ceilf(m_new) : m_run, alpha = need ? ex2(m_run - to) : 1.0f;
+                                if (!(hide >> e & 1u)) mx = fmaxf(mx, __uint_as_float(sv[e]));
+                            const bool need = stale && mx > -INFINITY;
+                            const float to = need ? ceilf(mx) : m_run, alpha = need ? ex2(m_run - to) : 1.0f;
                             m_run = to;
                             l_run *= alpha;
                             if (q > 0) {       // every earlier P V of this chain must be done before O is rescaled
@@ -785,29 +841,15 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                                 tmem_st16(tS, o);
                             }
                         }
-                        const float msub = m_run == -INFINITY ? 0.f : m_run;
-                        const uint64_t negm2 = f2_pack(-msub, -msub);
-                        uint64_t acc2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float d0, d1;
-                            f2_unpack(f2_add(f2_pack(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), negm2), d0, d1);
-                            const float p0 = ex2(d0), p1 = ex2(d1);
-                            acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(p0, p1));
-                            pk[e] = pack_bf16x2(p0, p1);   // bf16 like the values they meet (an MMA's operands share a type)
-                        }
+                        if (!ok) break;
                         tmem_st16(tS + 16 * h, pk);
-                        float a0, a1, b0, b1;
-                        f2_unpack(acc2[0], a0, a1);
-                        f2_unpack(acc2[1], b0, b1);
-                        l_run += (a0 + b0) + (a1 + b1);
+                        l_run += sum;
                     }
                     if (!ok) break;
                     tmem_st_wait();
                 }
                 tc_fence_before();
-                mbar_arrive(&bars[SM::B_P_FULL + 2 * t + buf]);
+                arrive_warp(&bars[SM::B_P_FULL + 2 * t + buf]);
             }
             if (!ok) break;
             // ---- epilogue: O / l, or the part's sums as they are
@@ -819,7 +861,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     tc_fence_after();
                     s_ml[m] = make_float2(m_run, l_run);
                     tc_fence_before();
-                    mbar_arrive(&bars[SM::B_ML]);
+                    arrive_warp(&bars[SM::B_ML]);
                 }
                 kc += w.n_loc;
                 continue;
@@ -836,10 +878,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const float top = fmaxf(m_run, ml.x), ref = top == -INFINITY ? 0.f : top;
             float f0 = mine > 0 ? ex2(m_run - ref) : 0.f, f1 = two ? ex2(ml.x - ref) : 0.f;
             const float l_all = l_run * f0 + ml.y * f1;
-            const int64_t prow = (int64_t)w.slot * (2 * kTileRows) + (w.single ? 0 : t * kTileRows) + m;
+            const int part_row = (w.single ? 0 : t * kTileRows) + m;
             if (any) {
                 if (w.slot >= 0) {
-                    if (valid) p.part_ml[prow] = make_float2(top, l_all);
+                    if (valid) p.part_ml[(int64_t)w.slot * (2 * kTileRows) + part_row] = make_float2(top, l_all);
                 } else {
                     const float inv = l_all > 0.f ? 1.0f / l_all : 0.f;
                     f0 *= inv;
@@ -867,28 +909,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
                         for (int e = 0; e < 16; ++e) nan = fmaf(o[e], 0.f, nan);
                         if (w.slot >= 0) {
-                            float* dst = p.part_o + prow * D + cc * 16;
+                            float4* dst = p.part_o + ((int64_t)w.slot * (D / 4) + cc * 4) * (2 * kTileRows) + part_row;
 #pragma unroll
-                            for (int e = 0; e < 16; e += 4)
-                                *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            for (int e = 0; e < 4; ++e)
+                                dst[e * (2 * kTileRows)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                         } else {
-                            __nv_bfloat16* dst = p.out + ((int64_t)(w.row_base + tok) * p.hq + w.kvh * g + (m & (g - 1))) * D + cc * 16;
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                uint4 v;
-                                v.x = pack_bf16x2(o[8 * e + 0], o[8 * e + 1]);
-                                v.y = pack_bf16x2(o[8 * e + 2], o[8 * e + 3]);
-                                v.z = pack_bf16x2(o[8 * e + 4], o[8 * e + 5]);
-                                v.w = pack_bf16x2(o[8 * e + 6], o[8 * e + 7]);
-                                *reinterpret_cast<uint4*>(dst + 8 * e) = v;
-                            }
+                            uint4* dst = reinterpret_cast<uint4*>(
+                                p.out + ((int64_t)(w.row_base + tok) * p.hq + w.kvh * g + (m & (g - 1))) * D + cc * 16);
+                            dst[0] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                                pack_bf16x2(o[6], o[7]));
+                            dst[1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]), pack_bf16x2(o[12], o[13]),
+                                                pack_bf16x2(o[14], o[15]));
                         }
                     }
                 }
             }
             tc_fence_before();
-            if (mine > 0) mbar_arrive(&bars[SM::B_O_FREE + t]);
-            if (two) mbar_arrive(&bars[SM::B_O_FREE + 1]);
+            if (mine > 0) arrive_warp(&bars[SM::B_O_FREE + t]);
+            if (two) arrive_warp(&bars[SM::B_O_FREE + 1]);
             kc += w.n_loc;
         }
         if (nan != nan) set_dev_error(kDevErrRange);       // (a value that takes part is not finite)
@@ -901,43 +939,117 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
 }
 
-// Blocks (j, y) add up the run that block j of tree_attn_kernel began and left open, some rows of it each: its
-// part, then those of the blocks behind up to the run's last, in their order.
+// Adds up the runs that a block of tree_attn_kernel began and left open: its part, then those of the blocks behind
+// up to the run's last, in a fixed order.  An item is 32 rows and 32 dimensions of such a run: a thread has 8
+// dimensions of a row (a warp 32 rows, as the parts lie); four groups of threads take every fourth part, four parts'
+// loads in flight each, and meet in shared memory.  The items go round the blocks of one launch of two a SM: a grid
+// with a place for every run that a block could begin is nearly all empty blocks (one long request, 8 runs of 20
+// parts of 128 KB: 14 us, and 18 with one group of threads and two parts in flight).
+constexpr int kJoinGroups = 4, kJoinItem = 128, kJoinThreads = kJoinGroups * kJoinItem;
 template <int D>
-__global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p) {
-    constexpr int ROWS = 256 / (D / 4);
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParams p) {
+    __shared__ float s_acc[kJoinGroups - 1][8][kJoinItem];
+    __shared__ float2 s_ml[kJoinGroups - 1][kJoinItem];
+    __shared__ int16_t s_runs[kTreeMaxBlocks];
+    __shared__ int s_warp[kJoinThreads / 32];
     grid_dep_wait();
     grid_dep_launch();
-    const int j = blockIdx.x;
-    const int4 d = p.desc[2 * j], rows = p.desc[2 * j + 1];
-    if (d.x == 0) return;
-    const int last = d.x >> 8;
-    const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
-    const int r = blockIdx.y * ROWS + threadIdx.x / (D / 4), f = threadIdx.x % (D / 4);
-    const int tok = d.y + (r >> gs);
-    if (tok >= rows.x) return;
-    float top = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int b0 = j; b0 <= last; b0 += 4) {            // four parts' loads in flight
-        float2 ml[4];
-        float4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // (behind the last part: that part again, without weight -- other memory may hold NaN)
-            const int b = min(b0 + i, last);
-            const int64_t row = ((int64_t)b * 2 + (b == j ? 1 : 0)) * (2 * kTileRows) + r;
-            ml[i] = p.part_ml[row];
-            v[i] = *reinterpret_cast<const float4*>(p.part_o + row * D + 4 * f);
-            if (b0 + i > last) ml[i].x = -INFINITY;
+    // the runs, in the same order in every block
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int count = 0;
+    for (int b0 = 0; b0 < p.blocks; b0 += kJoinThreads) {
+        const int b = b0 + threadIdx.x;
+        const bool open = b < p.blocks && p.desc[2 * b].x != 0;
+        const uint32_t in_warp = __ballot_sync(0xffffffffu, open);
+        if (lane == 0) s_warp[warp] = __popc(in_warp);
+        __syncthreads();
+        int at = count;
+        for (int w = 0; w < kJoinThreads / 32; ++w) {
+            if (w < warp) at += s_warp[w];
+            count += s_warp[w];
         }
-        add_parts(ml, v, top, l, acc);
+        if (open) s_runs[at + __popc(in_warp & ((1u << lane) - 1))] = (int16_t)b;
+        __syncthreads();
     }
-    const float odd = not_finite(acc, 0.f);
-    if (odd != odd) set_dev_error(kDevErrRange);
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
-    const int64_t row = (int64_t)(rows.y + tok) * p.hq + d.z * g + (r & (g - 1));
-    *reinterpret_cast<uint2*>(p.out + row * D + 4 * f) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    constexpr int COLS = D / 32, CHUNKS = 2 * kTileRows / 32 * COLS;
+    const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
+    const int group = threadIdx.x / kJoinItem, i0 = threadIdx.x % kJoinItem;
+    for (int item = blockIdx.x; item < count * CHUNKS; item += gridDim.x) {
+        const int j = s_runs[item / CHUNKS], chunk = item % CHUNKS;
+        const int4 d = p.desc[2 * j], rows = p.desc[2 * j + 1];
+        const int last = d.x >> 8, r = chunk / COLS * 32 + (i0 & 31), f = chunk % COLS * 4 + (i0 >> 5);
+        const int tok = d.y + (r >> gs);
+        const bool valid = tok < rows.x;
+        if (d.y + (chunk / COLS * 32 >> gs) >= rows.x) continue;                      // (the same for the block)
+        float top = -INFINITY, l = 0.f, acc[8] = {};
+        constexpr int N = 4;
+        for (int b0 = j + group; valid && b0 <= last; b0 += N * kJoinGroups) {
+            float2 ml[N];
+            float4 v[N][2];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                // (behind the last part: that part again, without weight -- other memory may hold NaN)
+                const int b = min(b0 + i * kJoinGroups, last);
+                const int64_t slot = (int64_t)b * 2 + (b == j ? 1 : 0);
+                ml[i] = p.part_ml[slot * (2 * kTileRows) + r];
+                v[i][0] = p.part_o[(slot * (D / 4) + 2 * f) * (2 * kTileRows) + r];
+                v[i][1] = p.part_o[(slot * (D / 4) + 2 * f + 1) * (2 * kTileRows) + r];
+                if (b0 + i * kJoinGroups > last) ml[i].x = -INFINITY;
+            }
+            float now = top;
+#pragma unroll
+            for (int i = 0; i < N; ++i) now = fmaxf(now, ml[i].x);
+            const float ref = now == -INFINITY ? 0.f : now, old = ex2(top - ref);
+            top = now;
+            l *= old;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] *= old;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float w = ex2(ml[i].x - ref);
+                l += w * ml[i].y;
+                acc[0] += w * v[i][0].x;
+                acc[1] += w * v[i][0].y;
+                acc[2] += w * v[i][0].z;
+                acc[3] += w * v[i][0].w;
+                acc[4] += w * v[i][1].x;
+                acc[5] += w * v[i][1].y;
+                acc[6] += w * v[i][1].z;
+                acc[7] += w * v[i][1].w;
+            }
+        }
+        if (group > 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s_acc[group - 1][e][i0] = acc[e];
+            s_ml[group - 1][i0] = make_float2(top, l);
+        }
+        __syncthreads();
+        if (group == 0 && valid) {
+            float all = top;
+#pragma unroll
+            for (int i = 0; i < kJoinGroups - 1; ++i) all = fmaxf(all, s_ml[i][i0].x);
+            const float ref = all == -INFINITY ? 0.f : all, own = ex2(top - ref);
+            l *= own;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] *= own;
+#pragma unroll
+            for (int i = 0; i < kJoinGroups - 1; ++i) {
+                const float w = ex2(s_ml[i][i0].x - ref);
+                l += w * s_ml[i][i0].y;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] += w * s_acc[i][e][i0];
+            }
+            const float inv = l > 0.f ? 1.0f / l : 0.f;
+            float odd = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) odd = fmaf(acc[e], 0.f, odd);
+            if (odd != odd) set_dev_error(kDevErrRange);
+            *reinterpret_cast<uint4*>(p.out + ((int64_t)(rows.y + tok) * p.hq + d.z * g + (r & (g - 1))) * D + 8 * f) =
+                make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                           pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+        }
+        __syncthreads();
+    }
 }
 
 }  // namespace pcf

@@ -87,17 +87,19 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTab
         const Deal deal(all, p.blocks);
         for (int w = tid; w < p.blocks; w += kTreeThreads) {
             const int32_t u0 = deal.first(w);
-            int4 e = make_int4(0, 0, 0, 0), f = make_int4(deal.first(w + 1) - u0, p.tag, 0, 0);
+            int4 e = make_int4(0, 0, 0, 0), f = make_int4(deal.first(w + 1) - u0, p.tag, 0, 0), l = e;
             if (f.x > 0) {
                 const int b = row_request(s_work, p.n, u0);
                 const int32_t pairs = tree_pairs(add[b], p.g), run = tree_units(seq[b] + add[b]) + kTreeRunWeight;
                 const int32_t local = u0 - s_work[b], r = local / run, at = local - r * run;
                 e = make_int4(b, r / pairs, r % pairs, max(0, at - kTreeRunWeight));
                 f.z = max(0, kTreeRunWeight - at);
+                l = make_int4(seq[b], add[b], base[b], 0);
             }
-            int4* dst = reinterpret_cast<int4*>(p.plan + tree_shares(p.n)) + 2 * w;
+            int4* dst = reinterpret_cast<int4*>(p.plan + tree_shares(p.n)) + 3 * w;
             dst[0] = e;
             dst[1] = f;
+            dst[2] = l;
         }
         return;
     }

@@ -1188,8 +1188,7 @@ pcf_status tree_attention_impl(const pcf_chunk_dims& d, const TreeParams& p, con
     auto kern = tree_attn_kernel<D>;
     if ((s = set_smem(kern, SM::kAlloc)) != PCF_OK) return s;
     if ((s = launch(kern, dim3(p.blocks), dim3(kTreeAttnThreads), SM::kAlloc, st, tk, tv, p)) != PCF_OK) return s;
-    const int pair_rows = std::min(2 * kTileRows, d.max_chunk * (d.n_q_heads / d.n_kv_heads));
-    return launch(tree_join_kernel<D>, dim3(p.blocks, (pair_rows * (D / 4) + 255) / 256), dim3(256), 0, st, p);
+    return launch(tree_join_kernel<D>, dim3(2 * p.blocks), dim3(kJoinThreads), 0, st, p);
 }
 }  // namespace
 
@@ -1236,7 +1235,7 @@ extern "C" pcf_status pcf_tree_attention(const pcf_chunk_dims* dims, const int32
     uint8_t* base = static_cast<uint8_t*>(ws);
     const TreeParams p{tree_plan, reinterpret_cast<const __nv_bfloat16*>(q), block_table, page_pos, excl, row_pos,
                        reinterpret_cast<const uint32_t*>(seen), rope, reinterpret_cast<__nv_bfloat16*>(out),
-                       reinterpret_cast<float*>(base + w.part_o), reinterpret_cast<float2*>(base + w.part_ml),
+                       reinterpret_cast<float4*>(base + w.part_o), reinterpret_cast<float2*>(base + w.part_ml),
                        reinterpret_cast<int4*>(base + w.desc), q_row_stride, dims->n_reqs, dims->max_pages,
                        tree_words(dims), dims->n_q_heads, dims->n_kv_heads, dims->n_phys_pages, dims->max_pos,
                        chunk_sms(dims->n_sms), tree_tag(dims)};

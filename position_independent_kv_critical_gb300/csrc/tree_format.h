@@ -15,6 +15,7 @@
 namespace pcf {
 
 constexpr int kTreeMaxNodes = PCF_TREE_MAX_NODES;
+constexpr int kTreeMaxBlocks = 4096;          // blocks of the attention (pcf_chunk_dims.n_sms)
 constexpr int kTreeMaxWords = kTreeMaxNodes / 32;
 constexpr int kTreeUnit = 64;                 // keys of a unit of work (four pages)
 constexpr int kTreePagesPerUnit = kTreeUnit / kPage;
@@ -28,7 +29,9 @@ enum : int {
 // arrays behind the header, n_reqs + 1 words each: tokens held, nodes, first row, weight of the requests
 // before; then kTreeShareWords a block
 enum : int { TA_SEQ = 0, TA_NEW = 1, TA_ROW = 2, TA_WORK = 3, TA_COUNT = 4 };
-constexpr int kTreeShareWords = 8;   // {request, kv head, row pair, unit; weight, tag, weight of the first run's beginning in it, 0}
+// {request, kv head, row pair, unit; weight, tag, weight of the first run's beginning in it, 0; the request's tokens
+// held, nodes, first row, 0}
+constexpr int kTreeShareWords = 12;
 
 PCF_HOST_DEVICE inline int64_t tree_array(int which, int32_t n_reqs) {
     return T_HEADER + (int64_t)which * (n_reqs + 1);

@@ -261,7 +261,7 @@ def test_no_page_is_lost_or_counted_twice(seq, sizes, shape, n_sms):
     blocks = c.L.dims.n_sms
     plan = c.tree.plan.cpu().numpy()
     at = (4 + 4 * (c.n + 1) + 3) // 4 * 4
-    shares = plan[at: at + 8 * blocks].reshape(blocks, 8)
+    shares = plan[at: at + 12 * blocks].reshape(blocks, 12)
     rng = np.random.default_rng(3)
     g = c.hq // c.hkv
     picked = []
