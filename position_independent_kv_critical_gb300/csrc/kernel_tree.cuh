@@ -14,11 +14,11 @@
 // pcf_tree_tables in contiguous parts of equal weight.
 //   warps  0-7   softmax of chain 0 (warps 0-3) and 1: S row from TMEM, excluded slots and other branches
 //                hidden, online softmax (lazy rescale), P -> TMEM over the S columns, O epilogue
-//   warps  8-15  two groups of four, units in turn: a run's queries, then the keys, bf16 in, rotated fp16 out;
-//                values of hidden slots become zeros
+//   warps  8-15  two groups of four, units in turn: keys, bf16 in, rotated fp16 out; values of hidden slots
+//                become zeros
 //   warp  16     runs in order; a unit's four pages of keys (TMA), its hidden slots
 //   warp  19     the same pages of values
-//   warp  17     Q K^T issue (and the TMEM allocation)
+//   warp  17     a run's queries (TMA, rotated by a kernel before), Q K^T issue (and the TMEM allocation)
 //   warp  18     P V issue
 // With more than 128 rows the chains are the pair's two row tiles and both take every unit.  With up to 128
 // there is one tile, and the chains take its units in turn, each with sums of its own that meet in the
@@ -38,6 +38,7 @@ namespace pcf {
 struct TreeParams {
     const int32_t* plan;
     const __nv_bfloat16* q;
+    __half* q_rot;              // [Hkv][max_rows][g][D], scaled by log2(e) / sqrt(d)
     const int32_t* block_table;
     const int32_t* page_pos;
     const uint16_t* excl;       // or null
@@ -50,7 +51,7 @@ struct TreeParams {
     int4* desc;                 // [blocks][2]: a run begun here that goes on: {last block << 8 | 255, first node, kv head, 0},
                                 //   {nodes, first row, 0, 0}
     int64_t q_stride;
-    int32_t n, max_pages, words, hq, hkv, n_phys, max_pos, blocks, tag;
+    int32_t n, max_pages, max_rows, words, hq, hkv, n_phys, max_pos, blocks, tag;
 };
 
 constexpr int kTreeAttnThreads = 640;
@@ -65,6 +66,7 @@ struct TreeItem {
     int32_t slot;               // partial result, or -1: the whole run
     int32_t single;             // its rows fit one tile
     int32_t code;               // n_loc * 2 + single, -1: no more
+    int32_t qy;                 // its first row among the rotated queries
 };
 
 template <int D>
@@ -77,7 +79,7 @@ struct TreeSmem {
     // in the warp that issues them: 1316 us for 64 shared requests.)
     static constexpr int kPageBytes = kPage * D * 2, kGroup = 8 * D * 2, kHalf = 1024;
     // (both even: a stage then belongs to units of one parity)
-    static constexpr int NK = D == 128 ? 4 : 8, NV = D == 128 ? 6 : 12;
+    static constexpr int NK = D == 128 ? 6 : 12, NV = D == 128 ? 4 : 8;
     // Hidden slots of the units whose keys are here or on the way, read by the rotation and the softmax: unit u
     // enters its own behind Q K^T of unit u - NK, which came behind P V, and so the softmax, of unit
     // u - NK - 4 (a chain's two S buffers, units in turn) and before.
@@ -93,7 +95,8 @@ struct TreeSmem {
     static constexpr int B_ITEM_FULL = 0, B_ITEM_EMPTY = 2, B_Q_FULL = 4, B_Q_EMPTY = 5, B_S_FULL = 6, B_P_FULL = 10,
                          B_PV_DONE = 14, B_O_DONE = 18, B_O_FREE = 20, B_ML = 22, B_DRAIN = 23, B_K_RAW = 25,
                          B_K_ROT = B_K_RAW + NK, B_K_EMPTY = B_K_ROT + NK, B_V_RAW = B_K_EMPTY + NK,
-                         B_V_EMPTY = B_V_RAW + NV, kNumBars = B_V_EMPTY + NV;
+                         B_V_FULL = B_V_RAW + NV, B_V_EMPTY = B_V_FULL + NV,
+                         kNumBars = B_V_EMPTY + NV;
     static constexpr int oMisc = oBar + kNumBars * 8;          // TMEM address, abort flag
     static constexpr int kBytes = oMisc + 16;
     static constexpr int kAlloc = kBytes + 1024;
@@ -102,7 +105,7 @@ struct TreeSmem {
 
 // A wait sees the parity of a phase only, so a phase may end at most once before each of its waiters has
 // passed it.  What keeps each barrier to that:
-//   ITEM, K_ROT     every waiter passes every phase;
+//   ITEM, K_ROT, V_FULL   every waiter passes every phase;
 //   K_RAW, V_RAW    a stage belongs to one rotating group (NK and NV are even), which passes every phase of it;
 //   Q, S, P, PV_DONE, O_DONE, O_FREE   as in the many-row kernel: counted by the units and runs that a chain
 //                   takes part in; in a run of one tile the threads of chain 0 arrive on both O_FREE;
@@ -221,7 +224,7 @@ struct Angles {
 // What a node sees of the 64 slots from slot `first` on, the held ones and those behind the tree included:
 // its bits (`words` of them at `seen`) from node u = first - seq on.
 __device__ __forceinline__ uint64_t tree_window(const uint32_t* seen, int words, int u) {
-    auto word = [&](int w) { return w >= 0 && w < words ? seen[w] : 0u; };
+    auto word = [&](int w) { return w >= 0 && w < words ? __ldcg(seen + w) : 0u; };
     if (u >= 0) {
         const int w = u >> 5, s = u & 31;
         const uint32_t x = word(w), y = word(w + 1), z = word(w + 2);
@@ -231,9 +234,53 @@ __device__ __forceinline__ uint64_t tree_window(const uint32_t* seen, int words,
     return x << -u | ((1ull << -u) - 1);
 }
 
+// The nodes' queries rotated, a block 16 rows at a time: thread (r, c) turns the 16-byte chunks c and c + d / 16 of
+// row r's heads, at one angle for all of them, two heads' loads in flight.  A kernel of its own: inside the attention
+// its code (a fifth of it) and its 4000 to 9000 cycles a run cost more; here it runs while that kernel starts and
+// has its first keys copied.
+template <int D>
+__global__ void __launch_bounds__(256) tree_rotate_kernel(const TreeParams p) {
+    constexpr int CP = D / 16, LANES = 256 / (16 * CP);       // heads side by side
+    grid_dep_wait();
+    grid_dep_launch();
+    if (!tree_fits(p.plan, p.tag)) return;
+    const int32_t rows = p.plan[T_ROWS];
+    const int c = threadIdx.x % CP, r = threadIdx.x / CP % 16, h0 = threadIdx.x / (CP * 16);
+    const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
+    const float scale = 1.4426950408889634f * (D == 128 ? 0.08838834764831845f : 0.125f);   // log2(e) / sqrt(d)
+    uint32_t odd = 0;
+    // (blockIdx.y: a share of the heads)
+    const int per = (p.hq + gridDim.y - 1) / gridDim.y, head0 = blockIdx.y * per, head1 = min(p.hq, head0 + per);
+    for (int32_t row = blockIdx.x * 16 + r; row < rows; row += gridDim.x * 16) {
+        const int32_t pos = p.row_pos[row];
+        const bool in_table = pos >= 0 && pos < p.max_pos;
+        if (!in_table) set_dev_error(kDevErrBounds);
+        const float4* src = reinterpret_cast<const float4*>(p.rope + (int64_t)(in_table ? pos : 0) * D + 16 * c);
+        float4 f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f[e] = src[e];
+            f[e] = make_float4(f[e].x * scale, f[e].y * scale, f[e].z * scale, f[e].w * scale);
+        }
+        Angles a;
+        a.set(f);
+#pragma unroll 2
+        for (int h = head0 + h0; h < head1; h += LANES) {
+            const __nv_bfloat16* x = p.q + row * p.q_stride + (int64_t)h * D;
+            uint4 lo = *reinterpret_cast<const uint4*>(x + 8 * c), hi = *reinterpret_cast<const uint4*>(x + D / 2 + 8 * c);
+            a.turn(lo, hi, odd);
+            __half* dst = p.q_rot + (((int64_t)(h >> gs) * p.max_rows + row) * g + (h & (g - 1))) * D;
+            *reinterpret_cast<uint4*>(dst + 8 * c) = lo;
+            *reinterpret_cast<uint4*>(dst + D / 2 + 8 * c) = hi;
+        }
+    }
+    if (odd != 0u) set_dev_error(kDevErrRange);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kTreeAttnThreads, 1)
-tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
+tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
     using SM = TreeSmem<D>;
     constexpr int NK = SM::NK, NV = SM::NV, CP = D / 16;
     extern __shared__ uint8_t smem_raw[];
@@ -255,7 +302,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             mbar_init(&bars[SM::B_O_DONE + s], 1);
             mbar_init(&bars[SM::B_O_FREE + s], 4);
         }
-        mbar_init(&bars[SM::B_Q_FULL], 8);
+        mbar_init(&bars[SM::B_Q_FULL], 1);
         mbar_init(&bars[SM::B_Q_EMPTY], 1);
         mbar_init(&bars[SM::B_ML], 4);
         for (int i = 0; i < 4; ++i) {
@@ -271,24 +318,30 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         for (int s = 0; s < NV; ++s) {
             mbar_init(&bars[SM::B_V_RAW + s], 1);
+            mbar_init(&bars[SM::B_V_FULL + s], 4);
             mbar_init(&bars[SM::B_V_EMPTY + s], 1);
         }
         fence_mbar_init();
         misc[1] = 0;
+        prefetch_tmap(&tm_q);
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    grid_dep_wait();
-    grid_dep_launch();
+    // The kernel before this one in the stream is tree_rotate_kernel, which lets this one start when everything
+    // before it is done: only its own results, the rotated queries, have to be waited for (by warp 17, and below
+    // where there is nothing to do, so that whatever waits for this kernel has waited for that one).  What earlier
+    // kernels wrote is read past L1, which may hold it as it was before them, or behind a wait (the rotation).
     const int4* entry = reinterpret_cast<const int4*>(p.plan + tree_shares(p.n)) + 3 * blockIdx.x;
-    const bool fits = p.plan[T_TAG] == p.tag;
-    const int4 share = fits ? entry[1] : make_int4(0, 0, 0, 0);
+    const bool fits = __ldcg(p.plan + T_TAG) == p.tag;
+    const int4 share = fits ? __ldcg(entry + 1) : make_int4(0, 0, 0, 0);
     const int weight = share.y == p.tag ? share.x : 0;
-    if (!fits && tid == 0) set_dev_error(kDevErrBounds);
     if (weight == 0) {             // nothing to do for the whole block
         if (tid == 0) p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+        grid_dep_wait();
+        grid_dep_launch();
         return;
     }
+    grid_dep_launch();
     if (warp == 17) {
         tmem_alloc(reinterpret_cast<uint32_t*>(misc), 512);
         tmem_relinquish();
@@ -311,10 +364,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     // What an issuer needs of it: n_loc * 2 + single, -1 behind the last one.  (A reduction's result is known to be
     // the same in all lanes, and so is what follows from it: operands of an MMA that are not go through a loop
     // over the lanes.)
-    auto take_code = [&](int it) -> int {
+    auto take_code = [&](int it, int32_t& qy) -> int {
         const bool ok = mbar_wait(&bars[SM::B_ITEM_FULL + (it & 1)], (it >> 1) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) return -1;
         const int code = __reduce_max_sync(0xffffffffu, slots[it & 1].code);
+        qy = __reduce_max_sync(0xffffffffu, slots[it & 1].qy);
         if (lane == 0) mbar_arrive(&bars[SM::B_ITEM_EMPTY + (it & 1)]);
         return code;
     };
@@ -339,8 +393,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         v.y_n = 0;
         if (pg < pages_of(n_slots)) {
             const int64_t e = (int64_t)w.req * p.max_pages + pg;
-            const int32_t x = p.block_table[e], pos = p.page_pos[e];
-            const uint32_t ex = p.excl ? p.excl[e] : 0u;
+            const int32_t x = __ldcg(p.block_table + e), pos = __ldcg(p.page_pos + e);
+            const uint32_t ex = p.excl ? __ldcg(p.excl + e) : 0u;
             const int have = min(n_slots - pg * kPage, kPage);
             v.gone_n = ex | (0xFFFFu & ~((1u << have) - 1u));
             v.y_n = x;
@@ -368,10 +422,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                        g2 = __shfl_sync(0xffffffffu, v.gone, at + 2), g3 = __shfl_sync(0xffffffffu, v.gone, at + 3);
         return make_uint2(g0 | g1 << 16, g2 | g3 << 16);
     };
-    // Registers: the block has 96 a thread; the rotation takes 112 (its four keys in flight spill in 96), the softmax
-    // 88 and the others 72 (60,416 of 61,440 in all).
-    if (warp >= 16) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 16 || warp == 19) {
         // ------------------------------------------------------------ runs, K copies (warp 16), V copies (warp 19)
         const bool val = warp == 19;
@@ -384,7 +434,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         const int32_t* add = p.plan + tree_array(TA_NEW, p.n);
         const int32_t* row = p.plan + tree_array(TA_ROW, p.n);
         const int32_t* work = p.plan + tree_array(TA_WORK, p.n);
-        const int4 start = entry[0], lens = entry[2];
+        const int4 start = __ldcg(entry), lens = __ldcg(entry + 2);
         int left = weight, begins = share.z;             // weight of the run's beginning, where that is in this share
         int32_t req = start.x, kvh = start.y, pair = start.z, unit = start.w;
         int kc = 0, st = 0, turn = 0;                    // units, place in the ring, its turns
@@ -403,9 +453,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             int pairs = 1;
             if (left > 0) {
                 const bool first = it == 0;              // (its lengths came with the share)
-                w.seq = first ? lens.x : seq[req];
-                w.add = first ? lens.y : add[req];
-                w.row_base = first ? lens.z : row[req];
+                w.seq = first ? lens.x : __ldcg(seq + req);
+                w.add = first ? lens.y : __ldcg(add + req);
+                w.row_base = first ? lens.z : __ldcg(row + req);
                 w.single = min(tpp, w.add - pair * tpp) << gs <= kTileRows;
                 pairs = tree_pairs(w.add, g);
                 const int all = tree_units(w.seq + w.add);
@@ -414,12 +464,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 if (w.n_loc < all) w.slot = 2 * blockIdx.x + (unit == 0 ? 1 : 0);
                 if (unit == 0 && w.n_loc < all) {
                     // the block that holds the run's last unit
-                    const int32_t u = work[req] + (kvh * pairs + pair + 1) * (all + kTreeRunWeight) - 1;
-                    desc = make_int4(Deal(work[p.n], p.blocks).owner(u) << 8 | 0xFF, pair * tpp, kvh, 0);
+                    const int32_t u = __ldcg(work + req) + (kvh * pairs + pair + 1) * (all + kTreeRunWeight) - 1;
+                    desc = make_int4(Deal(__ldcg(work + p.n), p.blocks).owner(u) << 8 | 0xFF, pair * tpp, kvh, 0);
                     desc_rows = make_int4(w.add, w.row_base, 0, 0);
                 }
             }
             w.code = w.req < 0 ? -1 : 2 * w.n_loc + w.single;
+            w.qy = (w.kvh * p.max_rows + w.row_base + w.pair * tpp) << gs;
             if (lane == 0 && !val) {
                 ok = it < 2 || mbar_wait(&bars[SM::B_ITEM_EMPTY + (it & 1)], ((it >> 1) - 1) & 1, abort_flag);
                 if (ok) {
@@ -456,7 +507,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 pair = 0;
                 if (++kvh == p.hkv) {
                     kvh = 0;
-                    do { ++req; } while (req < p.n && work[req + 1] == work[req]);
+                    do { ++req; } while (req < p.n && __ldcg(work + req + 1) == __ldcg(work + req));
                 }
             }
         }
@@ -474,12 +525,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     } else if (warp == 17) {
         // ------------------------------------------------------------ Q K^T
         constexpr uint32_t idesc_qk = idesc_f16(128, kTreeUnit);
-        int kc = 0, hg0 = 0, hg1 = 0;
+        int kc = 0, hg0 = 0, hg1 = 0, q_turns = 0;
         bool ok = true;
+        grid_dep_wait();
         for (int it = 0; ok; ++it) {
-            const int code = take_code(it), n_loc = code >> 1;
+            int32_t qy;
+            const int code = take_code(it, qy), n_loc = code >> 1;
             const bool single = code & 1;
             if (code < 0) break;
+            // the run's queries, when those of the run before have been read
+            if (it > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_Q_EMPTY], (it - 1) & 1, abort_flag));
+            if (!ok) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&bars[SM::B_Q_FULL], (single ? 1 : 2) * SM::kQ);
+                for (int x = 0; x < (single ? 1 : 2) * (D / 64); ++x)
+                    tma_load_2d(smem + x * (kTileRows * 128), &tm_q, &bars[SM::B_Q_FULL], x % (D / 64) * 64, qy + x / (D / 64) * kTileRows);
+            }
+            __syncwarp();
+            q_turns = it + 1;
             ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_Q_FULL], it & 1, abort_flag));
             for (int jj = 0; ok && jj < n_loc; ++jj, ++kc) {
                 const int ks = kc % NK;
@@ -513,20 +576,22 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (elect_one()) {
             mma_commit(&bars[SM::B_DRAIN]);
             mbar_drain(&bars[SM::B_DRAIN], 0);
+            if (q_turns > 0) mbar_drain(&bars[SM::B_Q_FULL], (q_turns - 1) & 1);
         }
         __syncwarp();
     } else if (warp == 18) {
-        // ------------------------------------------------------------ P V (a unit's weights come behind its scores,
-        // those behind its values: K_ROT)
+        // ------------------------------------------------------------ P V
         constexpr uint32_t idesc_pv = idesc_bf16(128, D, true);
-        int kc = 0, vs = 0, hg0 = 0, hg1 = 0, own0 = 0, own1 = 0;
+        int kc = 0, vs = 0, vn = 0, hg0 = 0, hg1 = 0, own0 = 0, own1 = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
-            const int code = take_code(it), n_loc = code >> 1;
+            int32_t qy;
+            const int code = take_code(it, qy), n_loc = code >> 1;
             const bool single = code & 1;
             if (code < 0) break;
             bool begun0 = false, begun1 = false;
             for (int jj = 0; ok && jj < n_loc; ++jj, ++kc) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars[SM::B_V_FULL + vs], vn & 1, abort_flag));
                 const int t0 = single ? kc & 1 : 0, t1 = single ? t0 : 1;
 #pragma unroll 1
                 for (int t = t0; ok && t <= t1; ++t) {
@@ -550,7 +615,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     if (t) begun1 = true, ++hg1;
                     else begun0 = true, ++hg0;
                 }
-                if (++vs == NV) vs = 0;
+                if (++vs == NV) vs = 0, ++vn;
             }
             if (!ok) break;
             if (elect_one()) {
@@ -566,9 +631,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             mbar_drain(&bars[SM::B_DRAIN + 1], 0);
         }
         __syncwarp();
-    }
     } else if (warp >= 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
         // ------------------------------------------------------------ rotation
         // Thread rt of group r: 16-byte chunk pair c (dimensions 8 c .. and d/2 + 8 c ..) of N consecutive
         // keys, a warp a page; their angles start from the cos/sin row of the first one's position and
@@ -576,7 +639,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         constexpr int N = 64 * CP / 128;                 // keys a thread
         const int r = warp >> 2 & 1, rt = tid & 127, c = rt % CP, k0 = rt / CP * N, page = rt >> 5;
         const int c_hi = D == 128 ? c : c + 4;
-        const float scale = 1.4426950408889634f * (D == 128 ? 0.08838834764831845f : 0.125f);   // log2(e) / sqrt(d)
         auto load_row = [&](int32_t pos, float4 (&cs)[4]) {
             const float4* src = reinterpret_cast<const float4*>(p.rope + (int64_t)pos * D + 16 * c);
 #pragma unroll
@@ -592,6 +654,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             sts_128(lo_at, lo);
             sts_128(hi_at, hi);
         };
+        grid_dep_wait();
+        float4 cs[4];
+        load_row(1, cs);
+        Angles step;
+        uint64_t minus_step[4];
+        step.set(cs);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) minus_step[e] = f2_neg(step.S[e]);
         uint32_t odd = 0;                                // NaN where a rotated value is not finite
         int kc = 0;
         bool ok = true;
@@ -607,80 +677,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             auto row_of = [&](int32_t pos) { return pos >= 0 && pos < p.max_pos ? pos : 0; };
             const int j0 = (kc & 1) == r ? 0 : 1;
             int32_t pos_n = position(j0);
-            // ---- the run's queries: chunk pair c of rows th / CP, + 256 / CP, ... of a tile (head by head, so that
-            // with four heads and more a thread stays with one node and its cos/sin row)
-            {
-                constexpr int STEP = 256 / CP, R = kTileRows / STEP;
-                const int y0 = (tid - 256) / CP, tiles = w.single ? 1 : 2;
-                auto node_of = [&](int tile, int i) { return w.pair * tpp + tile * tpt + ((y0 + i * STEP) & (tpt - 1)); };
-                int32_t at[2];                             // positions of the tiles' first nodes
-#pragma unroll
-                for (int tile = 0; tile < 2; ++tile) {
-                    const int tok = node_of(tile, 0);
-                    at[tile] = tile < tiles && tok < w.add ? p.row_pos[w.row_base + tok] : 0;
-                }
-                if (tiles > 1) {                           // the second tile's rows are on their way to L2
-#pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        const int tok = node_of(1, i);
-                        if (tok < w.add && (c & 1) == 0)
-                            prefetch_l2(p.q + (w.row_base + tok) * p.q_stride + (int64_t)(w.kvh * g + ((y0 + i * STEP) >> (7 - gs))) * D + 16 * c);
-                    }
-                }
-                Angles a;
-                auto angles = [&](int32_t pos) {
-                    if (pos < 0 || pos >= p.max_pos) set_dev_error(kDevErrBounds);
-                    float4 f[4];
-                    load_row(row_of(pos), f);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) f[e] = make_float4(f[e].x * scale, f[e].y * scale, f[e].z * scale, f[e].w * scale);
-                    a.set(f);
-                };
-#pragma unroll 1
-                for (int tile = 0; tile < tiles; ++tile) {
-                    uint4 lo[R], hi[R];
-#pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        const int y = y0 + i * STEP, tok = node_of(tile, i);
-                        lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
-                        if (tok < w.add) {
-                            const __nv_bfloat16* src = p.q + (w.row_base + tok) * p.q_stride + (int64_t)(w.kvh * g + (y >> (7 - gs))) * D;
-                            lo[i] = *reinterpret_cast<const uint4*>(src + 8 * c);
-                            hi[i] = *reinterpret_cast<const uint4*>(src + D / 2 + 8 * c);
-                        }
-                    }
-                    angles(tile ? at[1] : at[0]);
-                    // (the queries of the run before have been read)
-                    if (tile == 0 && it > 0) {
-                        ok = mbar_wait(&bars[SM::B_Q_EMPTY], (it - 1) & 1, abort_flag);
-                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    }
-#pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        const int y = y0 + i * STEP;
-                        if (i > 0 && tpt > STEP) {         // another node
-                            const int tok = node_of(tile, i);
-                            angles(tok < w.add ? p.row_pos[w.row_base + tok] : 0);
-                        }
-                        a.turn(lo[i], hi[i], odd);         // (rows behind the last one stay zeros)
-                        const int row = ((y & (tpt - 1)) << gs) + (y >> (7 - gs));
-                        uint8_t* dst = smem + tile * SM::kQ;
-                        *reinterpret_cast<uint4*>(dst + sw128_off(row, c)) = lo[i];
-                        *reinterpret_cast<uint4*>(dst + (D == 128 ? kTileRows * 128 : 0) + sw128_off(row, c_hi)) = hi[i];
-                    }
-                }
-                if (!ok) break;
-                fence_proxy_async_smem();
-                arrive_warp(&bars[SM::B_Q_FULL]);
-            }
-            // ---- its keys
-            float4 cs[4];
-            load_row(1, cs);
-            Angles step;
-            uint64_t minus_step[4];
-            step.set(cs);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) minus_step[e] = f2_neg(step.S[e]);
             load_row(row_of(pos_n), cs);
             pos_n = position(j0 + 2);
             for (int jj = j0; jj < w.n_loc; jj += 2) {
@@ -694,7 +690,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 Angles a;
                 a.set(cs);
                 if (slot0 + (page + 1) * kPage <= w.seq) {                    // (the same for the warp)
-#pragma unroll 1
+#pragma unroll
                     for (int i = 0; i < N; ++i) {
                         turn_key(at, i, !(gone >> ((k0 & 15) + i) & 1u), a, odd);
                         a.advance(step, minus_step);
@@ -714,8 +710,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         a.advance(step, minus_step);
                     }
                 }
-                // the values have landed too when the keys are handed on, the rows of hidden slots zeros (they may
-                // hold anything, and a weight of zero does not silence a NaN)
+                fence_proxy_async_smem();
+                arrive_warp(&bars[SM::B_K_ROT + ks]);
+                load_row(row_of(pos_n), cs);
+                pos_n = position(jj + 4);
+                // the unit's values: rows of hidden slots become zeros (they may hold anything, and a weight of zero
+                // does not silence a NaN)
                 const int vs = u % NV;
                 ok = mbar_wait(&bars[SM::B_V_RAW + vs], (u / NV) & 1, abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -727,17 +727,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     for (int i = 0; i < kTreeUnit / ROWS; ++i)
                         if ((row0 + i * ROWS < 32 ? meta.x >> (row0 + i * ROWS) : meta.y >> (row0 + i * ROWS - 32)) & 1u)
                             *reinterpret_cast<uint4*>(dst + i * ROWS / 8 * SM::kGroup) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
                 }
-                fence_proxy_async_smem();
-                arrive_warp(&bars[SM::B_K_ROT + ks]);
-                load_row(row_of(pos_n), cs);
-                pos_n = position(jj + 4);
+                arrive_warp(&bars[SM::B_V_FULL + vs]);
             }
             kc += w.n_loc;
         }
         if (odd != 0u) set_dev_error(kDevErrRange);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // ------------------------------------------------------------ softmax
         const int t = warp >> 2, m = tid & 127;            // row of the tile = TMEM lane
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
@@ -805,7 +802,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                             f2_unpack(acc2[0], a0, a1);
                             f2_unpack(acc2[1], b0, b1);
                             sum = (a0 + b0) + (a1 + b1);
-                            const bool stale = m_run == -INFINITY || sum > 65536.0f;
+                            const bool stale = valid && (m_run == -INFINITY || sum > 65536.0f);    // (other rows hold anything)
                             if (again || !__any_sync(0xffffffffu, stale)) break;
                             tmem_ld32(tS + 32 * h, sv);
                             tmem_ld_wait();

@@ -1177,9 +1177,10 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 template <int D>
 pcf_status tree_attention_impl(const pcf_chunk_dims& d, const TreeParams& p, const uint16_t* k_pool,
                                const uint16_t* v_pool, cudaStream_t st) {
-    CUtensorMap tk, tv;
+    CUtensorMap tq, tk, tv;
     pcf_status s;
     const uint64_t rows = (uint64_t)d.n_phys_pages * d.n_kv_heads * kPage;
+    if ((s = make_map_2d(&tq, p.q_rot, D, (uint64_t)d.max_rows * d.n_q_heads, D * 2, kTileRows, kF16)) != PCF_OK) return s;
     auto map = [&](CUtensorMap* m, const uint16_t* pool) {
         return D == 128 ? make_map_pages(m, pool, rows) : make_map_2d(m, pool, D, rows, D * 2, kPage);
     };
@@ -1187,7 +1188,11 @@ pcf_status tree_attention_impl(const pcf_chunk_dims& d, const TreeParams& p, con
     using SM = TreeSmem<D>;
     auto kern = tree_attn_kernel<D>;
     if ((s = set_smem(kern, SM::kAlloc)) != PCF_OK) return s;
-    if ((s = launch(kern, dim3(p.blocks), dim3(kTreeAttnThreads), SM::kAlloc, st, tk, tv, p)) != PCF_OK) return s;
+    // (a block's sixteen rows, and as many shares of their heads as fill the device)
+    const int row_blocks = std::min((d.max_rows + 15) / 16, 8 * p.blocks);
+    const dim3 rotate(row_blocks, std::max(1, std::min(d.n_q_heads / 4, 4 * p.blocks / row_blocks)));
+    if ((s = launch(tree_rotate_kernel<D>, rotate, dim3(256), 0, st, p)) != PCF_OK) return s;
+    if ((s = launch(kern, dim3(p.blocks), dim3(kTreeAttnThreads), SM::kAlloc, st, tq, tk, tv, p)) != PCF_OK) return s;
     return launch(tree_join_kernel<D>, dim3(2 * p.blocks), dim3(kJoinThreads), 0, st, p);
 }
 }  // namespace
@@ -1233,11 +1238,11 @@ extern "C" pcf_status pcf_tree_attention(const pcf_chunk_dims* dims, const int32
     if ((s = check_device()) != PCF_OK) return s;
     const TreeWs w = tree_ws(dims);
     uint8_t* base = static_cast<uint8_t*>(ws);
-    const TreeParams p{tree_plan, reinterpret_cast<const __nv_bfloat16*>(q), block_table, page_pos, excl, row_pos,
+    const TreeParams p{tree_plan, reinterpret_cast<const __nv_bfloat16*>(q), reinterpret_cast<__half*>(base + w.q_rot), block_table, page_pos, excl, row_pos,
                        reinterpret_cast<const uint32_t*>(seen), rope, reinterpret_cast<__nv_bfloat16*>(out),
                        reinterpret_cast<float4*>(base + w.part_o), reinterpret_cast<float2*>(base + w.part_ml),
                        reinterpret_cast<int4*>(base + w.desc), q_row_stride, dims->n_reqs, dims->max_pages,
-                       tree_words(dims), dims->n_q_heads, dims->n_kv_heads, dims->n_phys_pages, dims->max_pos,
+                       dims->max_rows, tree_words(dims), dims->n_q_heads, dims->n_kv_heads, dims->n_phys_pages, dims->max_pos,
                        chunk_sms(dims->n_sms), tree_tag(dims)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return dims->head_dim == 128 ? tree_attention_impl<128>(*dims, p, k_pool, v_pool, st)

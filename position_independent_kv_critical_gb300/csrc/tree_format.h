@@ -50,19 +50,21 @@ inline int32_t tree_words(const pcf_chunk_dims* c) { return (c->max_chunk + 31) 
 inline pcf_status check_tree_dims(const pcf_chunk_dims* c) {
     const pcf_status s = check_chunk_dims(c);
     if (s != PCF_OK) return s;
+    if ((int64_t)c->max_rows * c->n_q_heads > INT32_MAX) return PCF_ERR_INVALID_ARG;   // rows of the rotated queries
     return c->max_chunk > kTreeMaxNodes ? PCF_ERR_UNSUPPORTED : PCF_OK;
 }
 inline int32_t tree_tag(const pcf_chunk_dims* c) { return (int32_t)((uint32_t)plan_tag(c) * 2654435761u | 1u); }
 
-// Workspace of pcf_tree_attention (byte offsets): the two runs a block shares with its neighbours.
+// Workspace of pcf_tree_attention (byte offsets): rotated queries, the two runs a block shares with its neighbours.
 struct TreeWs {
-    size_t part_o, part_ml, desc, total;
+    size_t q_rot, part_o, part_ml, desc, total;
 };
 inline TreeWs tree_ws(const pcf_chunk_dims* c) {
     TreeWs w;
     const size_t blocks = chunk_sms(c->n_sms);
-    w.part_o = 0;
-    w.part_ml = chunk_align(blocks * 2 * 2 * kTileRows * c->head_dim * 4);
+    w.q_rot = 0;
+    w.part_o = chunk_align((size_t)c->max_rows * c->n_q_heads * c->head_dim * 2);
+    w.part_ml = chunk_align(w.part_o + blocks * 2 * 2 * kTileRows * c->head_dim * 4);
     w.desc = chunk_align(w.part_ml + blocks * 2 * 2 * kTileRows * 8);
     w.total = chunk_align(w.desc + blocks * 32);
     return w;
