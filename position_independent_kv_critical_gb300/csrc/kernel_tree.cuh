@@ -937,22 +937,21 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 }
 
 // Adds up the runs that a block of tree_attn_kernel began and left open: its part, then those of the blocks behind
-// up to the run's last, in a fixed order.  An item is 32 rows and 32 dimensions of such a run: a thread has 8
-// dimensions of a row (a warp 32 rows, as the parts lie); four groups of threads take every fourth part, four parts'
-// loads in flight each, and meet in shared memory.  The items go round the blocks of one launch of two a SM: a grid
-// with a place for every run that a block could begin is nearly all empty blocks (one long request, 8 runs of 20
-// parts of 128 KB: 14 us, and 18 with one group of threads and two parts in flight).
-constexpr int kJoinGroups = 4, kJoinItem = 128, kJoinThreads = kJoinGroups * kJoinItem;
+// up to the run's last, in their order.  A warp takes 32 rows and 8 dimensions of such a run at a time (the parts lie
+// so), four parts' loads in flight, and the warps of one launch go round all of them (a grid with a place for every
+// run that a block could begin is nearly all empty blocks).  Where there are warps enough, four share an item, each
+// with every fourth part, and meet in shared memory: few runs are long ones of many parts (one long request, 8 runs
+// of 20 parts of 128 KB: 8 us so and 14 with a warp an item; 151 runs of two parts: 27 with four and 10 with one).
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParams p) {
-    __shared__ float s_acc[kJoinGroups - 1][8][kJoinItem];
-    __shared__ float2 s_ml[kJoinGroups - 1][kJoinItem];
     __shared__ int16_t s_runs[kTreeMaxBlocks];
-    __shared__ int s_warp[kJoinThreads / 32];
+    __shared__ int s_warp[kJoinWarps];
+    __shared__ float s_acc[kJoinWarps][10][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dep_wait();
     grid_dep_launch();
     // the runs, in the same order in every block
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int count = 0;
     for (int b0 = 0; b0 < p.blocks; b0 += kJoinThreads) {
         const int b = b0 + threadIdx.x;
@@ -961,37 +960,39 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
         if (lane == 0) s_warp[warp] = __popc(in_warp);
         __syncthreads();
         int at = count;
-        for (int w = 0; w < kJoinThreads / 32; ++w) {
+        for (int w = 0; w < kJoinWarps; ++w) {
             if (w < warp) at += s_warp[w];
             count += s_warp[w];
         }
         if (open) s_runs[at + __popc(in_warp & ((1u << lane) - 1))] = (int16_t)b;
         __syncthreads();
     }
-    constexpr int COLS = D / 32, CHUNKS = 2 * kTileRows / 32 * COLS;
+    constexpr int COLS = D / 8, ITEMS = 2 * kTileRows / 32 * COLS, SHARE = 4;
     const int g = p.hq / p.hkv, gs = __ffs(g) - 1;
-    const int group = threadIdx.x / kJoinItem, i0 = threadIdx.x % kJoinItem;
-    for (int item = blockIdx.x; item < count * CHUNKS; item += gridDim.x) {
-        const int j = s_runs[item / CHUNKS], chunk = item % CHUNKS;
+    const bool shared_items = count * ITEMS * SHARE <= (int)gridDim.x * kJoinWarps;
+    const int share = shared_items ? SHARE : 1, mine = warp % share;
+    float odd = 0.f;
+    for (int item = (blockIdx.x * kJoinWarps + warp) / share; item < count * ITEMS || shared_items; item += gridDim.x * kJoinWarps) {
+        const bool there = item < count * ITEMS;
+        const int j = there ? s_runs[item / ITEMS] : 0, at = item % ITEMS;
         const int4 d = p.desc[2 * j], rows = p.desc[2 * j + 1];
-        const int last = d.x >> 8, r = chunk / COLS * 32 + (i0 & 31), f = chunk % COLS * 4 + (i0 >> 5);
+        const int last = d.x >> 8, r = at / COLS * 32 + lane, f = at % COLS;
         const int tok = d.y + (r >> gs);
-        const bool valid = tok < rows.x;
-        if (d.y + (chunk / COLS * 32 >> gs) >= rows.x) continue;                      // (the same for the block)
+        const bool valid = there && tok < rows.x;
         float top = -INFINITY, l = 0.f, acc[8] = {};
         constexpr int N = 4;
-        for (int b0 = j + group; valid && b0 <= last; b0 += N * kJoinGroups) {
+        for (int b0 = j + mine; valid && b0 <= last; b0 += N * share) {
             float2 ml[N];
             float4 v[N][2];
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 // (behind the last part: that part again, without weight -- other memory may hold NaN)
-                const int b = min(b0 + i * kJoinGroups, last);
+                const int b = min(b0 + i * share, last);
                 const int64_t slot = (int64_t)b * 2 + (b == j ? 1 : 0);
                 ml[i] = p.part_ml[slot * (2 * kTileRows) + r];
                 v[i][0] = p.part_o[(slot * (D / 4) + 2 * f) * (2 * kTileRows) + r];
                 v[i][1] = p.part_o[(slot * (D / 4) + 2 * f + 1) * (2 * kTileRows) + r];
-                if (b0 + i * kJoinGroups > last) ml[i].x = -INFINITY;
+                if (b0 + i * share > last) ml[i].x = -INFINITY;
             }
             float now = top;
 #pragma unroll
@@ -1015,38 +1016,37 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
                 acc[7] += w * v[i][1].w;
             }
         }
-        if (group > 0) {
+        if (shared_items) {
+            s_acc[warp][8][lane] = top;
+            s_acc[warp][9][lane] = l;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s_acc[group - 1][e][i0] = acc[e];
-            s_ml[group - 1][i0] = make_float2(top, l);
-        }
-        __syncthreads();
-        if (group == 0 && valid) {
+            for (int e = 0; e < 8; ++e) s_acc[warp][e][lane] = acc[e];
+            __syncthreads();
+            if (mine != 0) break;
             float all = top;
-#pragma unroll
-            for (int i = 0; i < kJoinGroups - 1; ++i) all = fmaxf(all, s_ml[i][i0].x);
+            for (int i = 1; i < SHARE; ++i) all = fmaxf(all, s_acc[warp + i][8][lane]);
             const float ref = all == -INFINITY ? 0.f : all, own = ex2(top - ref);
             l *= own;
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] *= own;
+            for (int i = 1; i < SHARE; ++i) {
+                const float w = ex2(s_acc[warp + i][8][lane] - ref);
+                l += w * s_acc[warp + i][9][lane];
 #pragma unroll
-            for (int i = 0; i < kJoinGroups - 1; ++i) {
-                const float w = ex2(s_ml[i][i0].x - ref);
-                l += w * s_ml[i][i0].y;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] += w * s_acc[i][e][i0];
+                for (int e = 0; e < 8; ++e) acc[e] += w * s_acc[warp + i][e][lane];
             }
+        }
+        if (valid) {
             const float inv = l > 0.f ? 1.0f / l : 0.f;
-            float odd = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) odd = fmaf(acc[e], 0.f, odd);
-            if (odd != odd) set_dev_error(kDevErrRange);
             *reinterpret_cast<uint4*>(p.out + ((int64_t)(rows.y + tok) * p.hq + d.z * g + (r & (g - 1))) * D + 8 * f) =
                 make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
                            pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
         }
-        __syncthreads();
+        if (shared_items) break;
     }
+    if (odd != odd) set_dev_error(kDevErrRange);
 }
 
 }  // namespace pcf

@@ -1193,7 +1193,7 @@ pcf_status tree_attention_impl(const pcf_chunk_dims& d, const TreeParams& p, con
     const dim3 rotate(row_blocks, std::max(1, std::min(d.n_q_heads / 4, 4 * p.blocks / row_blocks)));
     if ((s = launch(tree_rotate_kernel<D>, rotate, dim3(256), 0, st, p)) != PCF_OK) return s;
     if ((s = launch(kern, dim3(p.blocks), dim3(kTreeAttnThreads), SM::kAlloc, st, tq, tk, tv, p)) != PCF_OK) return s;
-    return launch(tree_join_kernel<D>, dim3(2 * p.blocks), dim3(kJoinThreads), 0, st, p);
+    return launch(tree_join_kernel<D>, dim3(4 * p.blocks), dim3(kJoinThreads), 0, st, p);
 }
 }  // namespace
 
