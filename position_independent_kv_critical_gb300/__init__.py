@@ -23,6 +23,7 @@ and where the new tokens are a drafted tree, of which the model keeps one branch
 """
 from __future__ import annotations
 
+import array
 import ctypes
 from typing import Optional, Sequence
 
@@ -561,6 +562,17 @@ def tree_accept(layout: ChunkLayout, tree: DraftTree, parent, draft, choice, fre
                 _chunk_ints(L, seq_len_out, "seq_len_out", n), _chunk_ints(L, free_head_out, "free_head_out", 1))
 
 
+def _pool_list(L: ChunkLayout, pools, name: str):
+    """Addresses of the layers' pools (one condition a tensor, without a call: there are many)."""
+    index, elems, bf16 = L.index, L.pool_elems, torch.bfloat16
+    at = []
+    for t in pools:
+        if t.dtype is not bf16 or not t.is_contiguous() or t.numel() < elems or t.get_device() != index:
+            _chunk_pool(L, t, name)
+        at.append(t.data_ptr())
+    return array.array("Q", at)
+
+
 def tree_keep(layout: ChunkLayout, tree: DraftTree, k_pools, v_pools, stream=None):
     """Move the kept branches' keys and values into the slots behind the tokens held, in every layer: ``k_pools``
     and ``v_pools`` are lists of the layers' pools."""
@@ -568,11 +580,9 @@ def tree_keep(layout: ChunkLayout, tree: DraftTree, k_pools, v_pools, stream=Non
     _tree_of(L, tree)
     if len(k_pools) != len(v_pools) or not len(k_pools):
         raise ValueError("k_pools and v_pools: one pool per layer, at least one layer")
-    n = len(k_pools)
-    kp = (ctypes.c_void_p * n)(*[_chunk_pool(L, t, "k_pools") for t in k_pools])
-    vp = (ctypes.c_void_p * n)(*[_chunk_pool(L, t, "v_pools") for t in v_pools])
+    kp, vp = _pool_list(L, k_pools, "k_pools"), _pool_list(L, v_pools, "v_pools")
     _chunk_call(L, "pcf_tree_keep", stream, tree.plan.data_ptr(), tree.path.data_ptr(), tree.n_kept.data_ptr(),
-                L.block_table.data_ptr(), n, kp, vp)
+                L.block_table.data_ptr(), len(kp), kp.buffer_info()[0], vp.buffer_info()[0])
 
 
 def wait_limit_check(limit_cycles: int, flag, stream=None):

@@ -109,15 +109,17 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTab
     bool bad = false;
     for (int b = (blockIdx.x - 1) * kTreeWarps + warp; b < p.n && fits; b += (gridDim.x - 1) * kTreeWarps) {
         const int32_t n = add[b], first = base[b], pos0 = p.chunk[plan_array(CA_START, p.n) + b];
-        for (int k = 0; 32 * k < n; ++k) {
+        int32_t ups[kTreeMaxWords];                    // (all of a tree's parents on their way at once)
+#pragma unroll
+        for (int k = 0; k < kTreeMaxWords; ++k) ups[k] = 32 * k + lane < n ? p.parent[first + 32 * k + lane] : -1;
+#pragma unroll
+        for (int k = 0; k < kTreeMaxWords; ++k) {
+            if (32 * k >= n) break;
             const int t = 32 * k + lane;
-            int32_t up = -1;
-            if (t < n) {
-                up = p.parent[first + t];
-                if (up < -1 || up >= t) {
-                    bad = true;
-                    up = -1;
-                }
+            int32_t up = ups[k];
+            if (t < n && (up < -1 || up >= t)) {
+                bad = true;
+                up = -1;
             }
             // the line inside these 32: its nodes, the lane it has reached
             uint32_t line = 1u << lane;
@@ -175,14 +177,17 @@ struct TreeAcceptParams {
     int32_t n, max_rows, max_pages, n_free, chunk_tag, tag;
 };
 
-// A warp walks a request: lane l holds nodes l, l + 32, ..., of each its parent where its token is what the
-// model chose behind that parent; a step is a ballot for the lowest node whose parent is where the branch
-// stands (siblings with the same token: the first one).  The block that is done last scans the pages that
-// the branches need and gives the others back: taken pages lie in the free list in request order, so what
-// is needed stays in front and the rest, in the same order, becomes the list's next entries.
+// A warp takes a request: every node whose token is what the model chose behind its parent offers itself to that
+// parent, the lowest one stays (of siblings with the same token the first), and one lane follows the offers from the
+// held tokens on.  (A ballot over all nodes a step instead took 16.5 us for 512 trees of up to 256 nodes.)  The block
+// that is done last scans the pages that the branches need and gives the others back: taken pages lie in the free
+// list in request order, so what is needed stays in front and the rest, in the same order, becomes the list's next
+// entries.
 __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcceptParams p) {
     __shared__ int s_last, s_warp[kTreeWarps];
+    __shared__ int s_next[kTreeWarps][kTreeMaxNodes + 1];     // the lowest node that goes on from node t; [0]: from the held tokens
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int* next = s_next[warp] + 1;
     grid_dep_wait();
     grid_dep_launch();
     if (p.chunk[C_TAG] != p.chunk_tag || p.plan[T_TAG] != p.tag) {
@@ -199,32 +204,37 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
         const int32_t n = add[b], first = base[b];
         const int32_t* choice = p.choice + first;
         const int32_t root = p.root ? p.root[b] : -1;
-        int32_t up[kTreeMaxWords];                  // -2: not on any branch
+        constexpr int kNobody = 1 << 30;
+        for (int i = lane; i <= n; i += 32) next[i - 1] = kNobody;
+        int32_t up[kTreeMaxWords], token[kTreeMaxWords];
 #pragma unroll
         for (int k = 0; k < kTreeMaxWords; ++k) {
             const int t = 32 * k + lane;
-            up[k] = -2;
-            if (32 * k < n && t < n) {
-                const int32_t at = p.parent[first + t];
-                if (at < -1 || at >= t) bad = true;
-                else if (at >= 0 ? p.draft[first + t] == choice[at] : p.root ? p.draft[first + t] == root : t == 0) up[k] = at;
-            }
+            up[k] = t < n ? p.parent[first + t] : -2;
+            token[k] = t < n ? p.draft[first + t] : 0;
         }
-        int32_t at = -1, count = 0;
-        while (true) {
-            int32_t to = -1;
+        uint32_t hit = 0;                              // bit k: node 32 k + lane is what was chosen
 #pragma unroll
-            for (int k = 0; k < kTreeMaxWords; ++k) {
-                if (32 * k < n && to < 0) {
-                    const uint32_t hit = __ballot_sync(0xffffffffu, up[k] == at);
-                    if (hit) to = 32 * k + __ffs(hit) - 1;
-                }
-            }
-            if (to < 0) break;
-            at = to;
-            if (lane == 0) p.path[first + count] = at;
-            ++count;
+        for (int k = 0; k < kTreeMaxWords; ++k) {
+            const int t = 32 * k + lane, at = up[k];
+            const bool fine = t < n && at >= -1 && at < t;
+            bad |= t < n && !fine;
+            const int32_t said = fine && at >= 0 ? choice[at] : root;
+            if (fine && (at >= 0 || p.root ? token[k] == said : t == 0)) hit |= 1u << k;
         }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kTreeMaxWords; ++k)
+            if (hit >> k & 1u) atomicMin(next + up[k], 32 * k + lane);
+        __syncwarp();
+        int32_t at = -1, count = 0;
+        if (lane == 0)
+            for (int32_t to; (to = next[at]) != kNobody; ++count) {
+                at = to;
+                p.path[first + count] = at;
+            }
+        at = __shfl_sync(0xffffffffu, at, 0);
+        count = __shfl_sync(0xffffffffu, count, 0);
         for (int i = count + lane; i < n; i += 32) p.path[first + i] = -1;
         if (lane == 0) {
             p.kept[b] = count;
@@ -239,11 +249,20 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
     if (tid == 0) s_last = atomic_inc_acq_rel_gpu(p.plan + T_DONE, gridDim.x - 1) == (int)gridDim.x - 1;
     __syncthreads();
     if (!s_last) return;
+    // what a request's part of the taken pages begins with and where it goes on, in shared memory for all threads
+    __shared__ int32_t s_to[kMaxReqs], s_from[kMaxReqs];
+    __shared__ uint8_t s_back[kMaxReqs];               // pages it gives back: a tree starts 16 at most
     const int per = (p.n + kTreeThreads - 1) / kTreeThreads;
     const int b0 = min(p.n, tid * per), b1 = min(p.n, b0 + per);
-    auto need = [&](int b) { return pages_of(seq[b] + __ldcg(p.kept + b)) - pages_of(seq[b]); };
     int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += add[b] > 0 ? need(b) : 0;
+#pragma unroll 2
+    for (int b = b0; b < b1; ++b) {
+        const int32_t s = seq[b], held = pages_of(s), enough = add[b] > 0 ? pages_of(s + __ldcg(p.kept + b)) : held;
+        s_to[b] = take[b] - sum;
+        s_from[b] = enough;
+        s_back[b] = (uint8_t)(take[b + 1] - take[b] - (enough - held));
+        sum += enough - held;
+    }
     int x = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -257,18 +276,26 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
         if (w < warp) before += s_warp[w];
         all += s_warp[w];
     }
+    for (int b = b0; b < b1; ++b) s_to[b] -= before;
     if (tid == 0) p.head_out[0] = head + all;
     if (head < 0 || taken < 0 || head > p.n_free - taken) {      // (another list than the chunk's)
         if (tid == 0) set_dev_error(kDevErrBounds);
         return;
     }
-    for (int b = b0; b < b1; ++b) {
-        if (add[b] == 0) continue;
-        const int32_t k = need(b), back = take[b + 1] - take[b] - k;
-        const int32_t* from = p.block_table + (int64_t)b * p.max_pages + pages_of(seq[b]) + k;
-        int32_t* to = p.free_pages + head + all + take[b] - before;
-        for (int i = 0; i < back; ++i) to[i] = from[i];
-        before += k;
+    __syncthreads();
+    constexpr int PLACES = kTreeMaxNodes / kPage;
+    for (int i0 = tid; i0 < p.n * PLACES; i0 += 8 * kTreeThreads) {      // (eight places in flight a thread)
+        int32_t page[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kTreeThreads, b = i / PLACES;
+            if (b < p.n && i % PLACES < s_back[b]) page[k] = p.block_table[(int64_t)b * p.max_pages + s_from[b] + i % PLACES];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kTreeThreads, b = i / PLACES;
+            if (b < p.n && i % PLACES < s_back[b]) p.free_pages[head + all + s_to[b] + i % PLACES] = page[k];
+        }
     }
 }
 
@@ -279,59 +306,79 @@ struct TreeKeepParams {
     const int32_t* path;
     const int32_t* kept;
     const int32_t* block_table;
-    int32_t n, max_pages, hkv, n_phys, layers, tag;
+    int32_t n, max_pages, hkv, n_phys, pools_n, per_block, tag;
     uint4* pools[2 * kKeepLayers];  // keys and values of every layer
 };
 
-// The i-th node of the branch moves from slot seq + path[i] to slot seq + i.  path[i] >= i rises, so a slot
-// that is written is never one that a later i reads: a thread takes one 16-byte column of a head and goes
-// through the branch in order, eight loads in flight, and needs no other thread.
+// The i-th node of the branch moves from slot seq + path[i] to slot seq + i.  path[i] >= i, so a slot that is written
+// is never one that a later i reads: a thread takes one 16-byte column of a head and goes through the branch in
+// order, and needs no other thread.  A block lists a request's moves once, for two to eight pools (as many as leave six
+// blocks a SM; 128 requests in 32 layers: 15.5 us, 20.3 with a block a pool; one request: 2.6 with two, 3.7 with
+// eight); two pools' next four moves are in flight a thread.
+constexpr int kKeepPools = 8, kKeepThreads = 256;   // pools of a block at most
 template <int D>
-__global__ void __launch_bounds__(256) tree_keep_kernel(const __grid_constant__ TreeKeepParams p) {
+__global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const __grid_constant__ TreeKeepParams p) {
     constexpr int CH = D / 8;
+    __shared__ int2 s_move[kTreeMaxNodes];             // rows of head 0 in the pool: from, to
+    __shared__ int s_warp[kKeepThreads / 32];
     grid_dep_wait();
     grid_dep_launch();
     if (!tree_fits(p.plan, p.tag)) return;
-    const int b = blockIdx.x;
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t seq = p.plan[tree_array(TA_SEQ, p.n) + b], add = p.plan[tree_array(TA_NEW, p.n) + b];
     const int32_t first = p.plan[tree_array(TA_ROW, p.n) + b];
     if (add == 0) return;
-    const int32_t count = p.kept[b];
+    int32_t count = p.kept[b];
     if (count < 0 || count > add) {
         set_dev_error(kDevErrBounds);
         return;
     }
-    const int32_t* table = p.block_table + (int64_t)b * p.max_pages;
-    auto slot = [&](int32_t s, int64_t& at) {            // row of a slot in the pool, head 0
-        const int32_t ph = table[s / kPage];
-        at = (int64_t)ph * p.hkv * kPage + s % kPage;
-        return ph >= 0 && ph < p.n_phys;
-    };
-    for (int c = threadIdx.x; c < p.hkv * CH; c += blockDim.x) {
-        uint4* pool = p.pools[blockIdx.y] + (int64_t)(c / CH) * kPage * CH + c % CH;
-        for (int32_t i0 = 0; i0 < count; i0 += 8) {
-            uint4 v[8];
-            int64_t dst[8];
+    // thread i has the i-th node (a tree has no more nodes than the block threads)
+    static_assert(kTreeMaxNodes <= kKeepThreads, "a thread a node");
+    bool moves = false;
+    int2 move = make_int2(0, 0);
+    if (tid < count) {
+        const int32_t* table = p.block_table + (int64_t)b * p.max_pages;
+        const int32_t t = p.path[first + tid];
+        if (t < tid || t >= add) {
+            set_dev_error(kDevErrBounds);
+        } else if (t > tid) {
+            const int32_t from = table[(seq + t) / kPage], to = table[(seq + tid) / kPage];
+            moves = from >= 0 && from < p.n_phys && to >= 0 && to < p.n_phys;
+            if (!moves) set_dev_error(kDevErrBounds);
+            // (pages * heads * 16 is below 2^31)
+            move = make_int2(from * p.hkv * kPage + (seq + t) % kPage, to * p.hkv * kPage + (seq + tid) % kPage);
+        }
+    }
+    const uint32_t in_warp = __ballot_sync(0xffffffffu, moves);
+    if (lane == 0) s_warp[warp] = __popc(in_warp);
+    __syncthreads();
+    int at = 0;
+    count = 0;
+    for (int w = 0; w < kKeepThreads / 32; ++w) {
+        if (w < warp) at += s_warp[w];
+        count += s_warp[w];
+    }
+    if (moves) s_move[at + __popc(in_warp & ((1u << lane) - 1))] = move;
+    __syncthreads();
+    const int p0 = blockIdx.y * p.per_block, pools = min(p.per_block, p.pools_n - p0), columns = p.hkv * CH;
+    // (pools in pairs: a pair and a column a thread)
+    for (int x = tid; x < (pools + 1) / 2 * columns; x += kKeepThreads) {
+        const int c = x % columns, q = p0 + x / columns * 2;
+        const int64_t col = (int64_t)(c / CH) * kPage * CH + c % CH;
+        uint4* pool[2] = {p.pools[q] + col, q + 1 < p0 + pools ? p.pools[q + 1] + col : nullptr};
+        for (int i0 = 0; i0 < count; i0 += 4) {
+            uint4 v[2][4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                dst[i] = -1;
-                if (i0 + i < count) {
-                    const int32_t t = p.path[first + i0 + i];
-                    int64_t from, to;
-                    if (t < i0 + i || t >= add) set_dev_error(kDevErrBounds);
-                    else if (t > i0 + i) {
-                        if (slot(seq + t, from) && slot(seq + i0 + i, to)) {
-                            v[i] = pool[from * CH];
-                            dst[i] = to * CH;
-                        } else {
-                            set_dev_error(kDevErrBounds);
-                        }
-                    }
-                }
-            }
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (dst[i] >= 0) pool[dst[i]] = v[i];
+                for (int i = 0; i < 4; ++i)
+                    if (i0 + i < count && pool[k]) v[k][i] = pool[k][(int64_t)s_move[i0 + i].x * CH];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i0 + i < count && pool[k]) pool[k][(int64_t)s_move[i0 + i].y * CH] = v[k][i];
         }
     }
 }

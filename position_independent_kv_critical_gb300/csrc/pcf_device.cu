@@ -1285,13 +1285,14 @@ extern "C" pcf_status pcf_tree_keep(const pcf_chunk_dims* dims, const int32_t* t
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     for (int32_t l0 = 0; l0 < n_layers; l0 += kKeepLayers) {
         TreeKeepParams p{tree_plan, path, n_kept, block_table, dims->n_reqs, dims->max_pages, dims->n_kv_heads,
-                         dims->n_phys_pages, std::min(kKeepLayers, n_layers - l0), tree_tag(dims), {}};
-        for (int32_t i = 0; i < p.layers; ++i) {
+                         dims->n_phys_pages, 2 * std::min(kKeepLayers, n_layers - l0), 2, tree_tag(dims), {}};
+        const int64_t all = (int64_t)dims->n_reqs * p.pools_n;
+        while (2 * p.per_block <= kKeepPools && all / (2 * p.per_block) >= 6 * device_sms()) p.per_block *= 2;
+        for (int32_t i = 0; i < p.pools_n / 2; ++i) {
             p.pools[2 * i] = reinterpret_cast<uint4*>(k_pools[l0 + i]);
             p.pools[2 * i + 1] = reinterpret_cast<uint4*>(v_pools[l0 + i]);
         }
-        const dim3 grid(dims->n_reqs, 2 * p.layers);
-        const dim3 threads(std::min(256, (dims->n_kv_heads * dims->head_dim / 8 + 31) / 32 * 32));
+        const dim3 grid(dims->n_reqs, (p.pools_n + p.per_block - 1) / p.per_block), threads(kKeepThreads);
         s = dims->head_dim == 128 ? launch(tree_keep_kernel<128>, grid, threads, 0, st, p)
                                   : launch(tree_keep_kernel<64>, grid, threads, 0, st, p);
         if (s != PCF_OK) return s;
