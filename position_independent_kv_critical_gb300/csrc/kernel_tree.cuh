@@ -333,7 +333,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // kernels wrote is read past L1, which may hold it as it was before them, or behind a wait (the rotation).
     const int4* entry = reinterpret_cast<const int4*>(p.plan + tree_shares(p.n)) + 3 * blockIdx.x;
     const bool fits = __ldcg(p.plan + T_TAG) == p.tag;
-    const int4 share = fits ? __ldcg(entry + 1) : make_int4(0, 0, 0, 0);
+    // (all of the share at once: where its first run begins, its weight, the first run's lengths)
+    const int4 start = fits ? __ldcg(entry) : make_int4(0, 0, 0, 0), share = fits ? __ldcg(entry + 1) : start;
+    const int4 lens = fits ? __ldcg(entry + 2) : start;
     const int weight = share.y == p.tag ? share.x : 0;
     if (weight == 0) {             // nothing to do for the whole block
         if (tid == 0) p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -434,12 +436,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int32_t* add = p.plan + tree_array(TA_NEW, p.n);
         const int32_t* row = p.plan + tree_array(TA_ROW, p.n);
         const int32_t* work = p.plan + tree_array(TA_WORK, p.n);
-        const int4 start = __ldcg(entry), lens = __ldcg(entry + 2);
         int left = weight, begins = share.z;             // weight of the run's beginning, where that is in this share
         int32_t req = start.x, kvh = start.y, pair = start.z, unit = start.w;
         int kc = 0, st = 0, turn = 0;                    // units, place in the ring, its turns
         bool ok = true;
-        int4 desc = make_int4(0, 0, 0, 0), desc_rows = desc;
+        int4 open_run = make_int4(-1, 0, 0, 0), open_rows = open_run;    // the run begun here that goes on
         for (int it = 0; ok; ++it) {
             TreeItem w;
             left -= begins;
@@ -463,10 +464,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 left -= w.n_loc;
                 if (w.n_loc < all) w.slot = 2 * blockIdx.x + (unit == 0 ? 1 : 0);
                 if (unit == 0 && w.n_loc < all) {
-                    // the block that holds the run's last unit
-                    const int32_t u = __ldcg(work + req) + (kvh * pairs + pair + 1) * (all + kTreeRunWeight) - 1;
-                    desc = make_int4(Deal(__ldcg(work + p.n), p.blocks).owner(u) << 8 | 0xFF, pair * tpp, kvh, 0);
-                    desc_rows = make_int4(w.add, w.row_base, 0, 0);
+                    open_run = make_int4(req, kvh, pair, all);
+                    open_rows = make_int4(w.add, w.row_base, pairs, 0);
                 }
             }
             w.code = w.req < 0 ? -1 : 2 * w.n_loc + w.single;
@@ -513,8 +512,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         if (lane == 0) {
             if (!val) {
-                p.desc[2 * blockIdx.x] = ok ? desc : make_int4(0, 0, 0, 0);
-                p.desc[2 * blockIdx.x + 1] = desc_rows;
+                int4 desc = make_int4(0, 0, 0, 0);
+                if (ok && open_run.x >= 0) {               // with the block that holds its last unit
+                    const int32_t run = open_run.y * open_rows.z + open_run.z;
+                    const int32_t u = __ldcg(work + open_run.x) + (run + 1) * (open_run.w + kTreeRunWeight) - 1;
+                    desc = make_int4(Deal(__ldcg(work + p.n), p.blocks).owner(u) << 8 | 0xFF, open_run.z * tpp, open_run.y, 0);
+                }
+                p.desc[2 * blockIdx.x] = desc;
+                p.desc[2 * blockIdx.x + 1] = open_rows;
             }
             // every copy lands before the block exits: each stage's last turn
             for (int s = 0; s < stages; ++s) {
