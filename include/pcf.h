@@ -423,7 +423,8 @@ pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, int32_t* plan, const 
  * confirms then moves together in the pages: keys are unrotated, so it moves bit for bit (MiniPIC section 2.1).
  * A step is: pcf_chunk_tables, pcf_tree_tables; in every layer pcf_append_kv and pcf_tree_attention;
  * pcf_tree_accept, pcf_tree_keep.  As above: lengths and trees live on the GPU, buffers have the sizes the dims
- * give, calls can be captured and replayed.  dims as for the chunk calls, with max_chunk at most: */
+ * give, calls can be captured and replayed.  dims as for the chunk calls, with max_rows * n_q_heads < 1<<31 and
+ * max_chunk at most: */
 #define PCF_TREE_MAX_NODES 256  /* else PCF_ERR_UNSUPPORTED from every call below */
 
 /* Host-only.  int32 words of the plan pcf_tree_tables writes and the calls behind it read. */
@@ -489,7 +490,7 @@ pcf_status pcf_tree_accept(const pcf_chunk_dims* dims, const int32_t* chunk_plan
 /* Moves the branches' keys and values together, in every layer: in each request the i-th node of its branch from
  * slot s + path[i] to slot s + i (s tokens held before the chunk), bit for bit; its position there is the one
  * page_pos gives.  k_pools, v_pools: host arrays of n_layers (1 .. 4096) device pointers, read before the call
- * returns; the same pool twice is moved twice.  path and n_kept are pcf_tree_accept's, block_table as there.  An
+ * returns; pools that overlap are refused (PCF_ERR_INVALID_ARG).  path and n_kept are pcf_tree_accept's, block_table as there.  An
  * entry of path below its place or not a node, a number kept beyond the tree's nodes, or a page outside the pool
  * raises PCF_ERR_DEVICE_BOUNDS, and what it names is not moved.  One launch for every 64 layers. */
 pcf_status pcf_tree_keep(const pcf_chunk_dims* dims, const int32_t* tree_plan, const int32_t* path,

@@ -503,11 +503,18 @@ class DraftTree:
         _lib.check("pcf_tree_plan_words", _lib.load().pcf_tree_plan_words(layout.dims_ref, ctypes.byref(n)))
         ints = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=layout.device)
         self.layout = layout
-        self.row_pos = ints(layout.max_rows).fill_(-1)
-        self.seen = ints(layout.max_rows, (layout.max_chunk + 31) // 32)
-        self.path = ints(layout.max_rows).fill_(-1)
-        self.n_kept, self.next_token = ints(layout.n_reqs), ints(layout.n_reqs)
-        self.plan = ints(n.value)
+        self._tables = {"row_pos": ints(layout.max_rows).fill_(-1),
+                        "seen": ints(layout.max_rows, (layout.max_chunk + 31) // 32),
+                        "path": ints(layout.max_rows).fill_(-1), "n_kept": ints(layout.n_reqs),
+                        "next_token": ints(layout.n_reqs), "plan": ints(n.value)}
+
+    # (the calls write them: they are not to be replaced)
+    row_pos = property(lambda self: self._tables["row_pos"])
+    seen = property(lambda self: self._tables["seen"])
+    path = property(lambda self: self._tables["path"])
+    n_kept = property(lambda self: self._tables["n_kept"])
+    next_token = property(lambda self: self._tables["next_token"])
+    plan = property(lambda self: self._tables["plan"])
 
     def attention_workspace_bytes(self) -> int:
         v = ctypes.c_size_t(0)

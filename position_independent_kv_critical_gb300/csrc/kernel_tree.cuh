@@ -180,7 +180,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* src) { asm volatile("prefetch.global.L2 [%0];" ::"l"(src)); }
+__device__ __forceinline__ void prefetch_l1(const void* src) { asm volatile("prefetch.global.L1 [%0];" ::"l"(src)); }
 
 // Eight frequencies' cos and sin as packed pairs.
 struct Angles {
@@ -694,6 +694,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const uint32_t at = a_k + ks * SM::kUnit;
                 Angles a;
                 a.set(cs);
+                // (the next unit's row comes nearer meanwhile; two threads share a line)
+                if (D == 128 && (c & 1) == 0) prefetch_l1(p.rope + (int64_t)row_of(pos_n) * D + 16 * c);
                 if (slot0 + (page + 1) * kPage <= w.seq) {                    // (the same for the warp)
 #pragma unroll
                     for (int i = 0; i < N; ++i) {

@@ -1281,6 +1281,17 @@ extern "C" pcf_status pcf_tree_keep(const pcf_chunk_dims* dims, const int32_t* t
     for (int32_t l = 0; l < n_layers; ++l)
         if (!k_pools[l] || !v_pools[l] || !aligned16(k_pools[l]) || !aligned16(v_pools[l])) return PCF_ERR_INVALID_ARG;
     if (!words_aligned({path, n_kept, block_table}) || !aligned16(tree_plan)) return PCF_ERR_INVALID_ARG;
+    // (a pool named twice would be moved by two blocks at once)
+    std::vector<uintptr_t> at;
+    at.reserve(2 * (size_t)n_layers);
+    for (int32_t l = 0; l < n_layers; ++l) {
+        at.push_back(reinterpret_cast<uintptr_t>(k_pools[l]));
+        at.push_back(reinterpret_cast<uintptr_t>(v_pools[l]));
+    }
+    std::sort(at.begin(), at.end());
+    const uintptr_t bytes = (uintptr_t)dims->n_phys_pages * dims->n_kv_heads * kPage * dims->head_dim * 2;
+    for (size_t i = 1; i < at.size(); ++i)
+        if (at[i] - at[i - 1] < bytes) return PCF_ERR_INVALID_ARG;
     if ((s = check_device()) != PCF_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     for (int32_t l0 = 0; l0 < n_layers; l0 += kKeepLayers) {

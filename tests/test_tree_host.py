@@ -15,7 +15,8 @@ from tree_util import chain, random_tree, star
 
 @pytest.mark.parametrize("kw,status", [
     (dict(n_reqs=0), INVALID), (dict(max_rows=0), INVALID), (dict(max_chunk=21), INVALID), (dict(head_dim=96), UNSUPPORTED),
-    (dict(n_q_heads=6), UNSUPPORTED), (dict(max_rows=257, max_chunk=257), UNSUPPORTED)])
+    (dict(n_q_heads=6), UNSUPPORTED), (dict(max_rows=257, max_chunk=257), UNSUPPORTED),
+    (dict(max_rows=1 << 22, max_chunk=2, n_q_heads=512, n_kv_heads=512), INVALID)])     # rows of the rotated queries
 def test_dims_out_of_range_are_refused(lib, kw, status):
     n, size = ctypes.c_int64(0), ctypes.c_size_t(0)
     d = ctypes.byref(dims(**kw))
@@ -105,8 +106,9 @@ def test_accept_refuses_null_and_misaligned_pointers(lib):
 
 def test_keep_refuses_bad_pointers_and_numbers_of_layers(lib):
     d = ctypes.byref(dims())
-    pools = (ctypes.c_void_p * 2)(P, P)
-    args = [P, P, P, P, 2, pools, pools, None]
+    size = 40 * 2 * 16 * 64 * 2                            # of a pool of these dims
+    pools = [(ctypes.c_void_p * 2)(*[P + size * (2 * i + j) for i in range(2)]) for j in range(2)]
+    args = [P, P, P, P, 2, *pools, None]
     for i in (0, 1, 2, 3, 5, 6):
         bad = list(args)
         bad[i] = None
@@ -121,8 +123,12 @@ def test_keep_refuses_bad_pointers_and_numbers_of_layers(lib):
     for wrong in (None, P + 8):
         for which in (5, 6):
             bad = list(args)
-            bad[which] = (ctypes.c_void_p * 2)(P, wrong)
+            bad[which] = (ctypes.c_void_p * 2)(args[which][0], wrong)
             assert lib.pcf_tree_keep(d, *bad) == INVALID
+    for k, v in (((0, 2), (1, 2)), ((0, 0), (1, 2)), ((0, 1), (0, 3)), ((0, 1.5), (2, 4))):       # pools that overlap
+        bad = list(args)
+        bad[5], bad[6] = ((ctypes.c_void_p * 2)(*[P + int(size * x) for x in w]) for w in (k, v))
+        assert lib.pcf_tree_keep(d, *bad) == INVALID, (k, v)
     if not torch.cuda.is_available():
         assert lib.pcf_tree_keep(d, *args) == NO_DEVICE
 
@@ -156,8 +162,10 @@ def test_binding_refuses_tensors_of_other_shapes_types_and_layouts():
     for k, v in (([pool], [pool, pool]), ([], []), ([pool[:39]], [pool]), ([pool], [pool.float()])):
         with pytest.raises(ValueError, match="pools"):
             pcf.tree_keep(L, T, k, v)
+    with pytest.raises(AttributeError):
+        T.row_pos = i32(20)
     for call in (lambda: pcf.tree_tables(L, T, i32(20)), lambda: pcf.tree_accept(L, T, **ok),
-                 lambda: pcf.tree_keep(L, T, [pool], [pool])):
+                 lambda: pcf.tree_keep(L, T, [pool], [pool.clone()])):
         with pytest.raises(ValueError, match="not on a GPU"):
             call()
 
