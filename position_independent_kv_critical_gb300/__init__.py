@@ -25,6 +25,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 from typing import Optional, Sequence
 
 import torch
@@ -569,15 +570,17 @@ def tree_accept(layout: ChunkLayout, tree: DraftTree, parent, draft, choice, fre
                 _chunk_ints(L, seq_len_out, "seq_len_out", n), _chunk_ints(L, free_head_out, "free_head_out", 1))
 
 
+_dtype = operator.attrgetter("dtype")
+
+
 def _pool_list(L: ChunkLayout, pools, name: str):
-    """Addresses of the layers' pools (one condition a tensor, without a call: there are many)."""
-    index, elems, bf16 = L.index, L.pool_elems, torch.bfloat16
-    at = []
-    for t in pools:
-        if t.dtype is not bf16 or not t.is_contiguous() or t.numel() < elems or t.get_device() != index:
+    """Addresses of the layers' pools (checked a property at a time, which is quicker for many tensors)."""
+    T = torch.Tensor
+    if (set(map(_dtype, pools)) != {torch.bfloat16} or not all(map(T.is_contiguous, pools))
+            or min(map(T.numel, pools)) < L.pool_elems or set(map(T.get_device, pools)) != {L.index}):
+        for t in pools:
             _chunk_pool(L, t, name)
-        at.append(t.data_ptr())
-    return array.array("Q", at)
+    return array.array("Q", map(T.data_ptr, pools))
 
 
 def tree_keep(layout: ChunkLayout, tree: DraftTree, k_pools, v_pools, stream=None):

@@ -26,6 +26,16 @@
 // (S -> softmax -> P -> P V -> next Q K^T) overlaps the other chain's.
 // TMEM: chain t's two S buffers at columns t*128 + {0, 64}, O of chain 0 at 256, of chain 1 at 384; P (bf16
 // pairs) overwrites the S it came from and is the A operand of O += P V.
+//
+// Measured (32/8 heads, d 128, graph replay): 24 requests behind 16 k tokens: 16 nodes 292 us, 5.4 TB/s or 80 % of a
+// plain copy; 64 nodes (two row tiles) 396 us, 1019 TFLOP/s.  48 trees of 1 to 64 nodes behind 100 to 9000 tokens:
+// 233 us for 872 MB.  64 requests of 16 nodes on shared spans (64/8 heads, 10 % of the slots excluded): 845 us for
+// 4.75 GB, a third of it found in L2.  12 trees of 200 to 256 nodes (64/8 heads): 304 us, 736 TFLOP/s.
+// What bounds it: with one row tile the copies and, next, the rotation (24 requests: 276 us without its arithmetic);
+// with two the chain of hand-offs through two S buffers (issue slots 52 % used, tensor pipe 40 %; 337 of 352 us
+// without the rotation's arithmetic, 332 with one product a unit).  The five roles' loops also compete for the
+// instruction cache: unrolled further here and there they took 1316 us instead of 1149 on the shared requests, with
+// 3.2 cycles an instruction waited for the next one instead of 0.7.  So loops are rolled where latency allows it.
 #pragma once
 #include "kernel_few_rows.cuh"
 #include "kernel_many_rows.cuh"
@@ -74,9 +84,8 @@ struct TreeSmem {
     static constexpr int kQ = kTileRows * D * 2;
     static constexpr int kUnit = kTreeUnit * D * 2;
     // A page lands as one box of eight-row groups, a group's halves (64 dimensions, 128-byte rows) one behind the
-    // other: with one box a page, and its groups kGroup bytes apart from page to page too, as the products'
-    // operands want them.  (Boxes of half a page took twice as many copy instructions, some 160 cycles each
-    // in the warp that issues them: 1316 us for 64 shared requests.)
+    // other: half the copies of boxes of half a page, and groups kGroup bytes apart from page to page too, as the
+    // products' operands want them.
     static constexpr int kPageBytes = kPage * D * 2, kGroup = 8 * D * 2, kHalf = 1024;
     // (both even: a stage then belongs to units of one parity)
     static constexpr int NK = D == 128 ? 6 : 12, NV = D == 128 ? 4 : 8;
@@ -235,9 +244,9 @@ __device__ __forceinline__ uint64_t tree_window(const uint32_t* seen, int words,
 }
 
 // The nodes' queries rotated, a block 16 rows at a time: thread (r, c) turns the 16-byte chunks c and c + d / 16 of
-// row r's heads, at one angle for all of them, two heads' loads in flight.  A kernel of its own: inside the attention
-// its code (a fifth of it) and its 4000 to 9000 cycles a run cost more; here it runs while that kernel starts and
-// has its first keys copied.
+// row r's heads, at one angle for all of them, two heads' loads in flight.  A kernel of its own, which runs while the
+// attention starts and has its first keys copied: there it was a fifth of the code and 4000 to 9000 cycles a run
+// (64 shared requests 1006 us so, 965 with this kernel; the largest trees 350 and 347, for 12 us of it).
 template <int D>
 __global__ void __launch_bounds__(256) tree_rotate_kernel(const TreeParams p) {
     constexpr int CP = D / 16, LANES = 256 / (16 * CP);       // heads side by side
@@ -374,8 +383,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (lane == 0) mbar_arrive(&bars[SM::B_ITEM_EMPTY + (it & 1)]);
         return code;
     };
-    // An arrival for the whole warp, behind what its lanes did.  (One a thread: 384 of them a unit took as much of
-    // the shared memory's time as the rotation of its keys.)
+    // An arrival for the whole warp, behind what its lanes did (one a thread would be 384 operations on shared memory
+    // a unit).
     auto arrive_warp = [&](uint64_t* bar) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);

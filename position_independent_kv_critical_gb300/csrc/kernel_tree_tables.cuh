@@ -28,7 +28,9 @@ constexpr int kTreeThreads = kTreeWarps * 32;
 // A warp takes its tree 32 nodes at a time.  Inside the 32 a node's line goes back by pointer doubling
 // over lanes: after step i it reaches 2^i nodes back, five steps reach any (parents come first).  The
 // first node of a line inside the 32 has its parent among the 32s before, whose bits are complete: a
-// copy of those and the line's own word make the node's bits, whatever the depth.
+// copy of those and the line's own word make the node's bits, whatever the depth.  Bound by dependent loads and
+// barriers: 64 trees of 16 nodes 2.8 us in a replayed graph, 512 of up to 256 nodes 6.2 (9.4 with a tree's parents
+// loaded 32 at a time).
 __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTablesParams p) {
     extern __shared__ int32_t s_words[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -179,7 +181,8 @@ struct TreeAcceptParams {
 
 // A warp takes a request: every node whose token is what the model chose behind its parent offers itself to that
 // parent, the lowest one stays (of siblings with the same token the first), and one lane follows the offers from the
-// held tokens on.  (A ballot over all nodes a step instead took 16.5 us for 512 trees of up to 256 nodes.)  The block
+// held tokens on.  (512 trees of up to 256 nodes: 9.6 us; 16.5 with a ballot over all nodes a step and pages given
+// back one behind the other.)  The block
 // that is done last scans the pages that the branches need and gives the others back: taken pages lie in the free
 // list in request order, so what is needed stays in front and the rest, in the same order, becomes the list's next
 // entries.
