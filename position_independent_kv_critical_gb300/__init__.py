@@ -24,6 +24,7 @@ and where the new tokens are a drafted tree, of which the model keeps one branch
 from __future__ import annotations
 
 import array
+import collections
 import ctypes
 import operator
 from typing import Optional, Sequence
@@ -492,6 +493,9 @@ def chunk_attention(layout: ChunkLayout, q, k_pool, v_pool, rope, out, ws, excl=
                 _chunk_rope(L, rope), out.data_ptr(), ws.data_ptr(), ws.nbytes)
 
 
+_TreeAddresses = collections.namedtuple("_TreeAddresses", "row_pos seen path n_kept next_token plan")
+
+
 class DraftTree:
     """Trees of drafted tokens on the rows of a ChunkLayout (``max_chunk`` at most 256 nodes a request), and what
     the tree calls leave: ``row_pos`` [max_rows] and ``seen`` [max_rows, words] (the nodes' positions; bit u % 32
@@ -508,6 +512,8 @@ class DraftTree:
                         "seen": ints(layout.max_rows, (layout.max_chunk + 31) // 32),
                         "path": ints(layout.max_rows).fill_(-1), "n_kept": ints(layout.n_reqs),
                         "next_token": ints(layout.n_reqs), "plan": ints(n.value)}
+        # (their addresses, which stay: a step's calls are bound by their host side)
+        self._at = _TreeAddresses(**{name: t.data_ptr() for name, t in self._tables.items()})
 
     # (the calls write them: they are not to be replaced)
     row_pos = property(lambda self: self._tables["row_pos"])
@@ -535,7 +541,7 @@ def tree_tables(layout: ChunkLayout, tree: DraftTree, parent, stream=None):
     L = layout
     _tree_of(L, tree)
     _chunk_call(L, "pcf_tree_tables", stream, L.plan.data_ptr(), _chunk_ints(L, parent, "parent", L.max_rows),
-                tree.row_pos.data_ptr(), tree.seen.data_ptr(), tree.plan.data_ptr())
+                tree._at.row_pos, tree._at.seen, tree._at.plan)
 
 
 def tree_attention(layout: ChunkLayout, tree: DraftTree, q, k_pool, v_pool, rope, out, ws, excl=None, stream=None):
@@ -546,10 +552,10 @@ def tree_attention(layout: ChunkLayout, tree: DraftTree, q, k_pool, v_pool, rope
     _tree_of(L, tree)
     qs = _chunk_rows(L, q, L.hq, "q")
     _chunk_out(L, out, ws)
-    _chunk_call(L, "pcf_tree_attention", stream, tree.plan.data_ptr(), q.data_ptr(), qs, _chunk_pool(L, k_pool, "k_pool"),
+    _chunk_call(L, "pcf_tree_attention", stream, tree._at.plan, q.data_ptr(), qs, _chunk_pool(L, k_pool, "k_pool"),
                 _chunk_pool(L, v_pool, "v_pool"), L.block_table.data_ptr(), L.page_pos.data_ptr(),
-                _chunk_ints(L, excl, "excl", L.n_reqs * L.max_pages, torch.int16), tree.row_pos.data_ptr(),
-                tree.seen.data_ptr(), _chunk_rope(L, rope), out.data_ptr(), ws.data_ptr(), ws.nbytes)
+                _chunk_ints(L, excl, "excl", L.n_reqs * L.max_pages, torch.int16), tree._at.row_pos,
+                tree._at.seen, _chunk_rope(L, rope), out.data_ptr(), ws.data_ptr(), ws.nbytes)
 
 
 def tree_accept(layout: ChunkLayout, tree: DraftTree, parent, draft, choice, free_pages, seq_len_out, free_head_out,
@@ -562,11 +568,12 @@ def tree_accept(layout: ChunkLayout, tree: DraftTree, parent, draft, choice, fre
     L = layout
     _tree_of(L, tree)
     n, rows = L.n_reqs, L.max_rows
-    _chunk_call(L, "pcf_tree_accept", stream, L.plan.data_ptr(), tree.plan.data_ptr(),
+    at = tree._at
+    _chunk_call(L, "pcf_tree_accept", stream, L.plan.data_ptr(), at.plan,
                 _chunk_ints(L, parent, "parent", rows), _chunk_ints(L, draft, "draft", rows),
                 _chunk_ints(L, choice, "choice", rows), _chunk_ints(L, root_choice, "root_choice", n),
                 L.block_table.data_ptr(), _chunk_ints(L, free_pages, "free_pages"), free_pages.numel(),
-                tree.path.data_ptr(), tree.n_kept.data_ptr(), tree.next_token.data_ptr(),
+                at.path, at.n_kept, at.next_token,
                 _chunk_ints(L, seq_len_out, "seq_len_out", n), _chunk_ints(L, free_head_out, "free_head_out", 1))
 
 
@@ -591,7 +598,7 @@ def tree_keep(layout: ChunkLayout, tree: DraftTree, k_pools, v_pools, stream=Non
     if len(k_pools) != len(v_pools) or not len(k_pools):
         raise ValueError("k_pools and v_pools: one pool per layer, at least one layer")
     kp, vp = _pool_list(L, k_pools, "k_pools"), _pool_list(L, v_pools, "v_pools")
-    _chunk_call(L, "pcf_tree_keep", stream, tree.plan.data_ptr(), tree.path.data_ptr(), tree.n_kept.data_ptr(),
+    _chunk_call(L, "pcf_tree_keep", stream, tree._at.plan, tree._at.path, tree._at.n_kept,
                 L.block_table.data_ptr(), len(kp), kp.buffer_info()[0], vp.buffer_info()[0])
 
 
