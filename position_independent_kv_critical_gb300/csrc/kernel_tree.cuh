@@ -27,10 +27,10 @@
 // TMEM: chain t's two S buffers at columns t*128 + {0, 64}, O of chain 0 at 256, of chain 1 at 384; P (bf16
 // pairs) overwrites the S it came from and is the A operand of O += P V.
 //
-// Measured (32/8 heads, d 128, graph replay): 24 requests behind 16 k tokens: 16 nodes 292 us, 5.4 TB/s or 80 % of a
-// plain copy; 64 nodes (two row tiles) 396 us, 1019 TFLOP/s.  48 trees of 1 to 64 nodes behind 100 to 9000 tokens:
-// 233 us for 872 MB.  64 requests of 16 nodes on shared spans (64/8 heads, 10 % of the slots excluded): 845 us for
-// 4.75 GB, a third of it found in L2.  12 trees of 200 to 256 nodes (64/8 heads): 304 us, 736 TFLOP/s.
+// Measured (32/8 heads, d 128, graph replay): 24 requests behind 16 k tokens: 16 nodes 291 us, 5.4 TB/s or 80 % of a
+// plain copy; 64 nodes (two row tiles) 393 us, 1024 TFLOP/s.  48 trees of 1 to 64 nodes behind 100 to 9000 tokens:
+// 232 us for 872 MB.  64 requests of 16 nodes on shared spans (64/8 heads, 10 % of the slots excluded): 841 us for
+// 4.75 GB, a third of it found in L2.  12 trees of 200 to 256 nodes (64/8 heads): 303 us, 738 TFLOP/s.
 // What bounds it: with one row tile the copies and, next, the rotation (24 requests: 276 us without its arithmetic);
 // with two the chain of hand-offs through two S buffers (issue slots 52 % used, tensor pipe 40 %; 337 of 352 us
 // without the rotation's arithmetic, 332 with one product a unit).  The five roles' loops also compete for the
@@ -59,7 +59,7 @@ struct TreeParams {
     float4* part_o;             // [blocks][2][D / 4][256]: a warp's rows side by side
     float2* part_ml;            // [blocks][2][256]
     int4* desc;                 // [blocks][2]: a run begun here that goes on: {last block << 8 | 255, first node, kv head, 0},
-                                //   {nodes, first row, 0, 0}
+                                //   {nodes, first row, row pairs of its request, 0}
     int64_t q_stride;
     int32_t n, max_pages, max_rows, words, hq, hkv, n_phys, max_pos, blocks, tag;
 };
@@ -117,9 +117,9 @@ struct TreeSmem {
 //   ITEM, K_ROT, V_FULL   every waiter passes every phase;
 //   K_RAW, V_RAW    a stage belongs to one rotating group (NK and NV are even), which passes every phase of it;
 //   Q, S, P, PV_DONE, O_DONE, O_FREE   as in the many-row kernel: counted by the units and runs that a chain
-//                   takes part in; in a run of one tile the threads of chain 0 arrive on both O_FREE;
+//                   takes part in; in a run of one tile the warps of chain 0 arrive on both O_FREE;
 //   ML              chain 1's sums of a run of one tile: written again only behind chain 1's next result, whose
-//                   first P V waited for O_FREE, on which chain 0's threads arrive when they have read them.
+//                   first P V waited for O_FREE, on which chain 0's warps arrive when they have read them.
 
 // 16 columns of this thread's TMEM lane
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -784,7 +784,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         hide0 |= ~(uint32_t)see;
                         hide1 |= ~(uint32_t)(see >> 32);
                     }
-                    // Half a unit at a time (a loop body that the instruction cache holds beside the other roles').
+                    // Half a unit at a time: 24 requests of 64 nodes behind 16 k tokens 392 us, 516 with a quarter (twice
+                    // the votes and branches), 435 to 452 with the whole (more code than the instruction cache holds
+                    // beside the other roles', and registers that these have to give).
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t hide = h ? hide1 : hide0;

@@ -1276,21 +1276,20 @@ extern "C" pcf_status pcf_tree_keep(const pcf_chunk_dims* dims, const int32_t* t
                                     uint16_t* const* k_pools, uint16_t* const* v_pools, void* stream) {
     pcf_status s = check_tree_dims(dims);
     if (s != PCF_OK) return s;
-    if (!tree_plan || !path || !n_kept || !block_table || n_layers < 1 || n_layers > 4096 || !k_pools || !v_pools)
+    if (!tree_plan || !path || !n_kept || !block_table || n_layers < 1 || n_layers > kMaxKeepLayers || !k_pools || !v_pools)
         return PCF_ERR_INVALID_ARG;
     for (int32_t l = 0; l < n_layers; ++l)
         if (!k_pools[l] || !v_pools[l] || !aligned16(k_pools[l]) || !aligned16(v_pools[l])) return PCF_ERR_INVALID_ARG;
     if (!words_aligned({path, n_kept, block_table}) || !aligned16(tree_plan)) return PCF_ERR_INVALID_ARG;
     // (a pool named twice would be moved by two blocks at once)
-    std::vector<uintptr_t> at;
-    at.reserve(2 * (size_t)n_layers);
+    uintptr_t at[2 * kMaxKeepLayers];
     for (int32_t l = 0; l < n_layers; ++l) {
-        at.push_back(reinterpret_cast<uintptr_t>(k_pools[l]));
-        at.push_back(reinterpret_cast<uintptr_t>(v_pools[l]));
+        at[2 * l] = reinterpret_cast<uintptr_t>(k_pools[l]);
+        at[2 * l + 1] = reinterpret_cast<uintptr_t>(v_pools[l]);
     }
-    std::sort(at.begin(), at.end());
+    std::sort(at, at + 2 * n_layers);
     const uintptr_t bytes = (uintptr_t)dims->n_phys_pages * dims->n_kv_heads * kPage * dims->head_dim * 2;
-    for (size_t i = 1; i < at.size(); ++i)
+    for (int32_t i = 1; i < 2 * n_layers; ++i)
         if (at[i] - at[i - 1] < bytes) return PCF_ERR_INVALID_ARG;
     if ((s = check_device()) != PCF_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

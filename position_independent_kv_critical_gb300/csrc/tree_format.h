@@ -56,6 +56,8 @@ inline pcf_status check_tree_dims(const pcf_chunk_dims* c) {
 }
 inline int32_t tree_tag(const pcf_chunk_dims* c) { return (int32_t)((uint32_t)plan_tag(c) * 2654435761u | 1u); }
 
+constexpr int kMaxKeepLayers = 4096;     // layers of one pcf_tree_keep
+
 // Workspace of pcf_tree_attention (byte offsets): rotated queries, the two runs a block shares with its neighbours.
 struct TreeWs {
     size_t q_rot, part_o, part_ml, desc, total;
