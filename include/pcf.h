@@ -490,9 +490,10 @@ pcf_status pcf_tree_accept(const pcf_chunk_dims* dims, const int32_t* chunk_plan
 /* Moves the branches' keys and values together, in every layer: in each request the i-th node of its branch from
  * slot s + path[i] to slot s + i (s tokens held before the chunk), bit for bit; its position there is the one
  * page_pos gives.  k_pools, v_pools: host arrays of n_layers (1 .. 4096) device pointers, read before the call
- * returns; pools that overlap are refused (PCF_ERR_INVALID_ARG).  path and n_kept are pcf_tree_accept's, block_table as there.  An
- * entry of path below its place or not a node, a number kept beyond the tree's nodes, or a page outside the pool
- * raises PCF_ERR_DEVICE_BOUNDS, and what it names is not moved.  One launch for every 64 layers. */
+ * returns; pools that overlap are refused (PCF_ERR_INVALID_ARG).  path and n_kept are pcf_tree_accept's,
+ * block_table as there.  Once for every pcf_tree_accept: a second call would move what has moved.  An entry of path
+ * below its place or not a node, a number kept beyond the tree's nodes, or a page outside the pool raises
+ * PCF_ERR_DEVICE_BOUNDS, and what it names is not moved.  One launch for every 64 layers. */
 pcf_status pcf_tree_keep(const pcf_chunk_dims* dims, const int32_t* tree_plan, const int32_t* path,
                          const int32_t* n_kept, const int32_t* block_table, int32_t n_layers, uint16_t* const* k_pools,
                          uint16_t* const* v_pools, void* stream);
