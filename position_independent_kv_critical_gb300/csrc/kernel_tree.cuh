@@ -846,9 +846,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                 for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                                 tmem_st16(tO + t * 128 + cc * 16, o);
                             }
+                            // (stored, before O is loaded again: another row's reference may move in the second half)
+                            tmem_st_wait();
                             if (h == 1) {      // and the weights of the first half
                                 uint32_t o[16];
-                                tmem_st_wait();
                                 tmem_ld16(tS, o);
                                 tmem_ld_wait();
 #pragma unroll
