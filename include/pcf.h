@@ -479,8 +479,9 @@ pcf_status pcf_tree_attention(const pcf_chunk_dims* dims, const int32_t* tree_pl
  *           seq_len_out [n_reqs]: tokens held before the chunk + n_kept; free_head_out [1]: the list's head.
  *             Both may be the buffers pcf_chunk_tables moved on, which this call sets right
  * tree_plan holds a counter that a call moves on: calls that may overlap need a plan each.  A parent out of its
- * range (never kept) or a free list shorter than what was taken (nothing given back) raises
- * PCF_ERR_DEVICE_BOUNDS; so does a plan of other dims, with nothing written.  One launch. */
+ * range (never kept) raises PCF_ERR_DEVICE_BOUNDS; so does a free list shorter than what was taken: then nothing is
+ * given back, free_head_out is the head as pcf_chunk_tables moved it on, and pages that the branches do not need stay
+ * out of the list until a call with the right one.  So does a plan of other dims, with nothing written.  One launch. */
 pcf_status pcf_tree_accept(const pcf_chunk_dims* dims, const int32_t* chunk_plan, int32_t* tree_plan,
                            const int32_t* parent, const int32_t* draft, const int32_t* choice,
                            const int32_t* root_choice, const int32_t* block_table, int32_t* free_pages, int32_t n_free,

@@ -280,8 +280,11 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
         all += s_warp[w];
     }
     for (int b = b0; b < b1; ++b) s_to[b] -= before;
-    if (tid == 0) p.head_out[0] = head + all;
-    if (head < 0 || taken < 0 || head > p.n_free - taken) {      // (another list than the chunk's)
+    // (another list than the chunk's: all that was taken stays taken, for the list's order does not change and pages that
+    // the branches hold lie behind its first ones)
+    const bool refused = head < 0 || taken < 0 || head > p.n_free - taken;
+    if (tid == 0) p.head_out[0] = head + (refused ? taken : all);
+    if (refused) {
         if (tid == 0) set_dev_error(kDevErrBounds);
         return;
     }
