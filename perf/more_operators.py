@@ -270,7 +270,8 @@ def prepare(case, seed):
                          + i * case["span_len"]] = 1
             word = (bits << torch.arange(PAGE, dtype=torch.int32)).sum(-1)
             s["excl"] = torch.where(word >= 32768, word - 65536, word).to(torch.int16).to(DEV)
-    # what a program keeps from call to call: the layout with the step's tables, the tree's buffers
+    # what a program has before these calls: the layout with the chunk's tables, the tree's buffers, the model's
+    # cos/sin rows (which the plain form works out within its pass)
     if own:
         _own_prepare(s)
     return s
@@ -288,8 +289,6 @@ def _own_prepare(s):
     s["seq_out"], s["head_out"] = torch.zeros_like(s["seq"]), torch.zeros_like(s["head"])
     pcf.chunk_tables(L, s["seq"], s["new"], s["free"], s["head"], s["seq_out"], s["head_out"], next_pos=s["start"])
     s["first_of"] = s.get("first") if case.get("roots") else None
-    if op != "tables":
-        pcf.tree_tables(L, tree, s["parent"])
     if op == "attention":
         s["rope"] = pcf.rope_table(case["d"], s["theta"], s["max_pos"]).to(DEV)
         s["out"] = torch.zeros((max(1, s["rows"]), case["hq"], case["d"]), dtype=torch.bfloat16, device=DEV)
@@ -312,6 +311,8 @@ def run(state):
         if op == "keep":
             pcf.tree_keep(L, tree, state["k_pools"], state["v_pools"])
             return {"k": state["k_all"], "v": state["v_all"]}
+        # (a step's tables and its first layer: like the plain form, the pass starts from the trees' parents)
+        pcf.tree_tables(L, tree, state["parent"])
         pcf.tree_attention(L, tree, state["q"], state["k_pool"], state["v_pool"], state["rope"], state["out"], state["ws"],
                            excl=state["excl"])
         return {"out": state["out"]}
@@ -323,7 +324,9 @@ def run(state):
 
 
 def _own_accept(s):
+    # (from the trees' parents too)
     tree = s["tree"]
+    s["pcf"].tree_tables(s["L"], tree, s["parent"])
     s["pcf"].tree_accept(s["L"], tree, s["parent"], s["draft"], s["choice"], s["free"], s["seq_out"], s["head_out"],
                          root_choice=s["first_of"])
     return {"path": tree.path, "kept": tree.n_kept, "next": tree.next_token, "seq": s["seq_out"], "free": s["free"],
