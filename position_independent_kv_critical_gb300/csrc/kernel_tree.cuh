@@ -791,9 +791,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t hide = h ? hide1 : hide0;
                         const bool masked = __any_sync(0xffffffffu, hide != 0u);
-                        // A row's reference is the largest of the first scores it sees, and stays while the weights
-                        // against it add up to less than 2^16 in 32 keys: their size costs no precision, and most
-                        // halves need no maximum.  It moves by whole numbers: powers of two round nothing.
+                        // A row's reference is 16 above the largest of the first scores it sees, and stays while the
+                        // weights against it add up to no more than 1 in 32 keys: how small they are costs no precision
+                        // (the largest is 2^-16 at least, and what is lost below 2^-126 is 2^-110 of it), and most
+                        // halves need no maximum.  Weights of 1 at most leave the sums of weights times values the
+                        // whole range of fp32: below slots / 32 times the largest value (with the largest score itself as
+                        // the reference weights went up to 2^16, and values of 5e33 to infinity).  It moves by whole
+                        // numbers: powers of two round nothing.
                         uint32_t pk[16];
                         float sum;
                         for (bool again = false;; again = true) {
@@ -820,7 +824,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             f2_unpack(acc2[0], a0, a1);
                             f2_unpack(acc2[1], b0, b1);
                             sum = (a0 + b0) + (a1 + b1);
-                            const bool stale = valid && (m_run == -INFINITY || sum > 65536.0f);    // (other rows hold anything)
+                            const bool stale = valid && (m_run == -INFINITY || sum > 1.0f);    // (other rows hold anything)
                             if (again || !__any_sync(0xffffffffu, stale)) break;
                             tmem_ld32(tS + 32 * h, sv);
                             tmem_ld_wait();
@@ -829,7 +833,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             for (int e = 0; e < 32; ++e)
                                 if (!(hide >> e & 1u)) mx = fmaxf(mx, __uint_as_float(sv[e]));
                             const bool need = stale && mx > -INFINITY;
-                            const float to = need ? ceilf(mx) : m_run, alpha = need ? ex2(m_run - to) : 1.0f;
+                            const float to = need ? ceilf(mx) + 16.0f : m_run, alpha = need ? ex2(m_run - to) : 1.0f;
                             m_run = to;
                             l_run *= alpha;
                             if (q > 0) {       // every earlier P V of this chain must be done before O is rescaled
