@@ -423,8 +423,11 @@ pcf_status pcf_chunk_attention(const pcf_chunk_dims* dims, int32_t* plan, const 
  * confirms then moves together in the pages: keys are unrotated, so it moves bit for bit (MiniPIC section 2.1).
  * A step is: pcf_chunk_tables, pcf_tree_tables; in every layer pcf_append_kv and pcf_tree_attention;
  * pcf_tree_accept, pcf_tree_keep.  As above: lengths and trees live on the GPU, buffers have the sizes the dims
- * give, calls can be captured and replayed.  dims as for the chunk calls, with max_rows * n_q_heads < 1<<31 and
- * max_chunk at most: */
+ * give, calls can be captured and replayed.  pcf_chunk_tables knows no trees and checks the positions of the nodes'
+ * slots: the rope table must reach as far behind the held tokens as a line of all the nodes would, to the end of its
+ * last page, however flat the tree.  A request that does not fit refuses the batch, so a tree near the table's end is
+ * drafted with fewer nodes.
+ * dims as for the chunk calls, with max_rows * n_q_heads < 1<<31 and max_chunk at most: */
 #define PCF_TREE_MAX_NODES 256  /* else PCF_ERR_UNSUPPORTED from every call below */
 
 /* Host-only.  int32 words of the plan pcf_tree_tables writes and the calls behind it read. */

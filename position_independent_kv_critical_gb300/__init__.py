@@ -501,7 +501,9 @@ class DraftTree:
     the tree calls leave: ``row_pos`` [max_rows] and ``seen`` [max_rows, words] (the nodes' positions; bit u % 32
     of word u // 32: the node is, or goes on from, node u), ``path`` [max_rows], ``n_kept`` and ``next_token``
     [n_reqs] (the branch that is kept).  All are int32 tensors on the layout's device that stay where they are, so
-    that a captured step can be replayed; steps that may overlap need a DraftTree (and a ChunkLayout) each."""
+    that a captured step can be replayed; steps that may overlap need a DraftTree (and a ChunkLayout) each.  The
+    layout's ``max_pos`` must reach as far as a line of all a tree's nodes would, to the end of its last page:
+    ``chunk_tables`` refuses the batch otherwise."""
 
     def __init__(self, layout: ChunkLayout):
         n = ctypes.c_int64(0)
