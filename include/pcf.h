@@ -485,7 +485,9 @@ pcf_status pcf_tree_attention(const pcf_chunk_dims* dims, const int32_t* tree_pl
  * tree_plan holds a counter that a call moves on: calls that may overlap need a plan each.  A parent out of its
  * range (never kept) raises PCF_ERR_DEVICE_BOUNDS; so does a free list shorter than what was taken: then nothing is
  * given back, free_head_out is the head as pcf_chunk_tables moved it on, and pages that the branches do not need stay
- * out of the list until a call with the right one.  So does a plan of other dims, with nothing written.  One launch. */
+ * out of the list until a call with the right one.  So does a plan of other dims, with nothing written, and a tree_plan
+ * that is not of chunk_plan's last pcf_chunk_tables, with n_kept 0 and nothing else written (pcf_tree_keep then moves
+ * nothing; pcf_tree_attention, which has no chunk_plan, attended over the earlier chunk's lengths).  One launch. */
 pcf_status pcf_tree_accept(const pcf_chunk_dims* dims, const int32_t* chunk_plan, int32_t* tree_plan,
                            const int32_t* parent, const int32_t* draft, const int32_t* choice,
                            const int32_t* root_choice, const int32_t* block_table, int32_t* free_pages, int32_t n_free,

@@ -30,6 +30,8 @@ enum : int {
 // before the request, position of its first row; of the requests before it that have few rows their
 // weight (their (page, kv head) units and run_weight for each of their runs) and their number; of those with
 // more the weight of their row pairs (many_weight) and the pages they hold.  Behind the first positions: run_weight.
+// Behind the tokens held: the step, a number that every call adds one to (from whatever the plan held), by which
+// a plan that was made from this one is known to be of the same call.
 // Behind them the work split of both kinds: kStartWords words a worker, then kManyWords a block.
 enum : int { CA_SEQ = 0, CA_NEW = 1, CA_ROW = 2, CA_TAKE = 3, CA_START = 4, CA_FEW = 5, CA_MANY = 6, CA_KPAGE = 7, CA_FEWN = 8, CA_COUNT = 9 };
 // {request, kv head, page, units before; its pages, tokens held, new tokens, first row; tag, and for a block's
@@ -39,6 +41,7 @@ constexpr int kStartWords = 12;
 PCF_HOST_DEVICE inline int64_t plan_array(int which, int32_t n_reqs) {
     return C_HEADER + (int64_t)which * (n_reqs + 1);
 }
+PCF_HOST_DEVICE inline int64_t plan_step(int32_t n_reqs) { return plan_array(CA_SEQ, n_reqs) + n_reqs; }
 PCF_HOST_DEVICE inline int64_t plan_starts(int32_t n_reqs) {
     return (plan_array(CA_COUNT, n_reqs) + 3) / 4 * 4;
 }

@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
     int32_t* o_kpage = plan_words_of(s_arrays, CA_KPAGE, p.n);
     int32_t* o_fewn = plan_words_of(s_arrays, CA_FEWN, p.n);
     const int32_t head = p.free_head[0];
+    const uint32_t step = tid == 0 && blockIdx.x == 0 ? (uint32_t)plan[plan_step(p.n)] + 1u : 0u;
     bool bad = head < 0 || head > p.n_free;
     int sum[kSums] = {};
     for (int b = b0; b < b1; ++b) {
@@ -346,7 +347,8 @@ __global__ void __launch_bounds__(kTablesThreads) chunk_plan_kernel(const Tables
         }
     }
     if (tid == 0) {
-        o_seq[p.n] = o_new[p.n] = 0;
+        o_seq[p.n] = (int32_t)step;                    // (plan_step)
+        o_new[p.n] = 0;
         o_start[p.n] = run;
         o_row[p.n] = tot[0];
         o_take[p.n] = tot[1];

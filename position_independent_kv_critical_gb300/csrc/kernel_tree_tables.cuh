@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTab
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dep_wait();
     grid_dep_launch();
+    const int32_t step = p.chunk[plan_step(p.n)];
     const bool fits = p.chunk[C_TAG] == p.chunk_tag;
     const int32_t rows = fits ? p.chunk[C_ROWS] : 0;
     const int32_t* seq = p.chunk + plan_array(CA_SEQ, p.n);
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTab
             p.plan[tree_array(TA_ROW, p.n) + b] = fits ? base[b] : 0;
             p.plan[tree_array(TA_WORK, p.n) + b] = s_work[b];
         }
-        if (tid == 0) *reinterpret_cast<int4*>(p.plan) = make_int4(p.tag, too_much ? 0 : rows, 0, 0);   // T_TAG, T_ROWS, T_DONE
+        if (tid == 0) *reinterpret_cast<int4*>(p.plan) = make_int4(p.tag, too_much ? 0 : rows, 0, step);   // T_TAG, T_ROWS, T_DONE, T_STEP
         const Deal deal(all, p.blocks);
         for (int w = tid; w < p.blocks; w += kTreeThreads) {
             const int32_t u0 = deal.first(w);
@@ -193,11 +194,19 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
     int* next = s_next[warp] + 1;
     grid_dep_wait();
     grid_dep_launch();
-    if (p.chunk[C_TAG] != p.chunk_tag || p.plan[T_TAG] != p.tag) {
+    const int4 of_plan = *reinterpret_cast<const int4*>(p.plan);
+    const int32_t step = p.chunk[plan_step(p.n)], rows = p.chunk[C_ROWS], head = p.chunk[C_HEAD], taken = p.chunk[C_TAKEN];
+    if (p.chunk[C_TAG] != p.chunk_tag || of_plan.x != p.tag) {
         if (tid == 0) set_dev_error(kDevErrBounds);
         return;
     }
-    const int32_t rows = p.chunk[C_ROWS], head = p.chunk[C_HEAD], taken = p.chunk[C_TAKEN];
+    // Trees of an earlier chunk: what was attended over and what tree_keep would move are that chunk's.  Nothing is
+    // kept, so that nothing moves.
+    if (step != of_plan.w) {                           // (T_STEP)
+        if (tid == 0) set_dev_error(kDevErrBounds);
+        for (int b = blockIdx.x * kTreeThreads + tid; b < p.n; b += gridDim.x * kTreeThreads) p.kept[b] = 0;
+        return;
+    }
     const int32_t* seq = p.chunk + plan_array(CA_SEQ, p.n);
     const int32_t* add = p.chunk + plan_array(CA_NEW, p.n);
     const int32_t* base = p.chunk + plan_array(CA_ROW, p.n);

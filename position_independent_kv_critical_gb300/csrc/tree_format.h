@@ -24,6 +24,7 @@ enum : int {
     T_TAG = 0,       // of the dims the plan was made for (tree_tag)
     T_ROWS = 1,      // nodes of all requests together; 0 also where the chunk's lengths were refused
     T_DONE = 2,      // blocks of pcf_tree_accept that are done (0 between calls)
+    T_STEP = 3,      // the chunk plan's step (plan_step)
     T_HEADER = 4
 };
 // arrays behind the header, n_reqs + 1 words each: tokens held, nodes, first row, weight of the requests
