@@ -36,7 +36,6 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTab
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dep_wait();
     grid_dep_launch();
-    const int32_t step = p.chunk[plan_step(p.n)];
     const bool fits = p.chunk[C_TAG] == p.chunk_tag;
     const int32_t rows = fits ? p.chunk[C_ROWS] : 0;
     const int32_t* seq = p.chunk + plan_array(CA_SEQ, p.n);
@@ -86,7 +85,8 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTab
             p.plan[tree_array(TA_ROW, p.n) + b] = fits ? base[b] : 0;
             p.plan[tree_array(TA_WORK, p.n) + b] = s_work[b];
         }
-        if (tid == 0) *reinterpret_cast<int4*>(p.plan) = make_int4(p.tag, too_much ? 0 : rows, 0, step);   // T_TAG, T_ROWS, T_DONE, T_STEP
+        if (tid == kTreeThreads - 1)
+            *reinterpret_cast<int4*>(p.plan) = make_int4(p.tag, too_much ? 0 : rows, 0, fits ? p.chunk[plan_step(p.n)] : 0);   // T_TAG, T_ROWS, T_DONE, T_STEP
         const Deal deal(all, p.blocks);
         for (int w = tid; w < p.blocks; w += kTreeThreads) {
             const int32_t u0 = deal.first(w);
@@ -195,18 +195,14 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
     grid_dep_wait();
     grid_dep_launch();
     const int4 of_plan = *reinterpret_cast<const int4*>(p.plan);
-    const int32_t step = p.chunk[plan_step(p.n)], rows = p.chunk[C_ROWS], head = p.chunk[C_HEAD], taken = p.chunk[C_TAKEN];
     if (p.chunk[C_TAG] != p.chunk_tag || of_plan.x != p.tag) {
         if (tid == 0) set_dev_error(kDevErrBounds);
         return;
     }
     // Trees of an earlier chunk: what was attended over and what tree_keep would move are that chunk's.  Nothing is
-    // kept, so that nothing moves.
-    if (step != of_plan.w) {                           // (T_STEP)
-        if (tid == 0) set_dev_error(kDevErrBounds);
-        for (int b = blockIdx.x * kTreeThreads + tid; b < p.n; b += gridDim.x * kTreeThreads) p.kept[b] = 0;
-        return;
-    }
+    // kept, so that nothing moves.  (Looked at below, behind the requests' own loads.)
+    const int32_t rows = p.chunk[C_ROWS], head = p.chunk[C_HEAD], taken = p.chunk[C_TAKEN];
+    const bool stale = p.chunk[plan_step(p.n)] != of_plan.w;           // (T_STEP)
     const int32_t* seq = p.chunk + plan_array(CA_SEQ, p.n);
     const int32_t* add = p.chunk + plan_array(CA_NEW, p.n);
     const int32_t* base = p.chunk + plan_array(CA_ROW, p.n);
@@ -239,6 +235,10 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
         for (int k = 0; k < kTreeMaxWords; ++k)
             if (hit >> k & 1u) atomicMin(next + up[k], 32 * k + lane);
         __syncwarp();
+        if (stale) {
+            if (lane == 0) p.kept[b] = 0;
+            continue;
+        }
         int32_t at = -1, count = 0;
         if (lane == 0)
             for (int32_t to; (to = next[at]) != kNobody; ++count) {
@@ -254,7 +254,8 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
             p.seq_out[b] = seq[b] + count;
         }
     }
-    if (bad) set_dev_error(kDevErrBounds);
+    if (bad || stale) set_dev_error(kDevErrBounds);
+    if (stale) return;
     for (int64_t r = rows + (int64_t)blockIdx.x * kTreeThreads + tid; r < p.max_rows; r += (int64_t)gridDim.x * kTreeThreads)
         p.path[r] = -1;
     __syncthreads();
