@@ -459,7 +459,8 @@ pcf_status pcf_tree_attention_workspace_bytes(const pcf_chunk_dims* dims, size_t
  * and device errors are those of pcf_chunk_attention, but the plan is only read (slots that no row of the
  * request sees may hold anything; a node that one row of the request does not see takes part where another
  * does, so its values must be finite).  Values may be as large as 2^112 (5e33) in any context, and as slots * |v| < 2^132
- * allows in a shorter one: beyond it a row's weighted sum may leave fp32, which raises PCF_ERR_DEVICE_RANGE.  ws: device workspace of >= pcf_tree_attention_workspace_bytes, contents
+ * allows in a shorter one: beyond it a row's weighted sum may leave fp32, which raises PCF_ERR_DEVICE_RANGE.  Rotated
+ * queries and keys are rounded to fp16 and weights to bf16 before their products; scores and sums are fp32.  ws: device workspace of >= pcf_tree_attention_workspace_bytes, contents
  * need not be initialised; calls that may overlap need one each.  Deterministic. */
 pcf_status pcf_tree_attention(const pcf_chunk_dims* dims, const int32_t* tree_plan, const uint16_t* q,
                               int64_t q_row_stride, const uint16_t* k_pool, const uint16_t* v_pool,

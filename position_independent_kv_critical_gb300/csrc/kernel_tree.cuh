@@ -29,11 +29,12 @@
 //
 // Measured (32/8 heads, d 128, graph replay): 24 requests behind 16 k tokens: 16 nodes 291 us, 5.4 TB/s or 80 % of a
 // plain copy; 64 nodes (two row tiles) 393 us, 1024 TFLOP/s.  48 trees of 1 to 64 nodes behind 100 to 9000 tokens:
-// 232 us for 872 MB.  64 requests of 16 nodes on shared spans (64/8 heads, 10 % of the slots excluded): 841 us for
+// 232 us for 872 MB.  64 requests of 16 nodes on shared spans (64/8 heads, 10 % of the slots excluded): 833 us for
 // 4.75 GB, a third of it found in L2.  12 trees of 200 to 256 nodes (64/8 heads): 303 us, 738 TFLOP/s.
-// What bounds it: with one row tile the copies and, next, the rotation (24 requests: 276 us without its arithmetic);
-// with two the chain of hand-offs through two S buffers (issue slots 52 % used, tensor pipe 40 %; 337 of 352 us
-// without the rotation's arithmetic, 332 with one product a unit).  The five roles' loops also compete for the
+// What bounds it: with one row tile the copies and, next, the rotation (24 requests of 16 nodes: 276 us without its
+// arithmetic); with two the chain of hand-offs through two S buffers (issue slots 52 % used, tensor pipe 40 %; 24
+// requests of 64 nodes, 391 us in that run: 398 without the rotation's arithmetic, 385 without the softmax's, 368 with
+// one product of each kind a unit).  The five roles' loops also compete for the
 // instruction cache: unrolled further here and there they took 1316 us instead of 1149 on the shared requests, with
 // 3.2 cycles an instruction waited for the next one instead of 0.7.  So loops are rolled where latency allows it.
 #pragma once

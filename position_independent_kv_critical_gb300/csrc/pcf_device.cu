@@ -1231,7 +1231,7 @@ extern "C" pcf_status pcf_tree_attention(const pcf_chunk_dims* dims, const int32
         if (!aligned16(a)) return PCF_ERR_INVALID_ARG;
     if (!words_aligned({block_table, page_pos, row_pos, seen}) || (reinterpret_cast<uintptr_t>(excl) & 1u))
         return PCF_ERR_INVALID_ARG;
-    // (a row is read by several blocks, some of them behind the write of its result)
+    // (a result is not written over the queries, as in pcf_chunk_attention: what the call reads stays as it was)
     if (overlap(q, 2 * (size_t)((dims->max_rows - 1) * q_row_stride + row), out, 2 * (size_t)dims->max_rows * row))
         return PCF_ERR_INVALID_ARG;
     if (ws_bytes < tree_ws(dims).total) return PCF_ERR_WORKSPACE_TOO_SMALL;
