@@ -566,7 +566,8 @@ def tree_accept(layout: ChunkLayout, tree: DraftTree, parent, draft, choice, fre
     behind each node, ``root_choice`` [n_reqs] behind the tokens held (None: every request's first node is that
     token already).  Fills ``tree.path``, ``tree.n_kept`` and ``tree.next_token``, sets ``seq_len_out`` and
     ``free_head_out`` to the requests with only their branches, and puts the pages these leave unused back into
-    ``free_pages``, the list ``chunk_tables`` took them from."""
+    ``free_pages``, the list ``chunk_tables`` took them from.  Trees that are not of the last ``chunk_tables`` are
+    refused (``check_device_error``), and none of their nodes is kept."""
     L = layout
     _tree_of(L, tree)
     n, rows = L.n_reqs, L.max_rows

@@ -794,8 +794,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         const bool masked = __any_sync(0xffffffffu, hide != 0u);
                         // A row's reference is 16 above the largest of the first scores it sees, and stays while the
                         // weights against it add up to no more than 1 in 32 keys: how small they are costs no precision
-                        // (the largest is 2^-16 at least, and what is lost below 2^-126 is 2^-110 of it), and most
-                        // halves need no maximum.  Weights of 1 at most leave the sums of weights times values the
+                        // (the largest is above 2^-17, and what is lost lies below 2^-126), and most halves need no
+                        // maximum.  Weights of 1 at most leave the sums of weights times values the
                         // whole range of fp32: below slots / 32 times the largest value (with the largest score itself as
                         // the reference weights went up to 2^16, and values of 5e33 to infinity).  It moves by whole
                         // numbers: powers of two round nothing.

@@ -1,7 +1,7 @@
 """Requests whose scores grow along the context, so that a row's reference moves behind its first unit.
 
 The attention of a tree keeps a row's softmax reference from the first scores it sees and moves it when 32 weights
-against it add up to more than 2^16; what the row has summed up by then is scaled down by a power of two.  Normal
+add up to more than 2^16 times that of the first scores' largest (rounded up to a power of two); what the row has summed up by then is scaled down by a power of two.  Normal
 draws never get there.  Here two dimensions that hardly turn (the two lowest frequencies) carry a chosen level, in
 bits, from a slot to the rows of three kinds: kind 0 sees level a, kind 1 level b, kind 2 the sum of both.  A node's
 query heads go through the kinds in turn, so the rows of one warp move at different places.
